@@ -65,6 +65,45 @@ class VerifyArgs(ctypes.Structure):
                 ("next_anchor", ctypes.c_void_p)]
 
 
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+KV_PAGE = 64
+DEV_TIMEOUT, DEV_BOUNDS, DEV_NONFINITE = 1, 2, 4
+
+
+class RopeConfig(ctypes.Structure):
+    """dlite_rope_config (include/dlite.h)."""
+    _fields_ = [("rot", ctypes.c_int), ("scaling", ctypes.c_int)] + \
+               [(n, ctypes.c_double) for n in ("theta", "factor", "orig_len", "beta_fast", "beta_slow", "attn_factor")]
+
+
+class RopeArgs(ctypes.Structure):
+    """dlite_rope_args."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "heads", "d_h", "rot", "layout", "dtype", "n_pos")] + \
+               [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("pos", ctypes.c_void_p), ("n_rows", ctypes.c_void_p), ("table", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """dlite_kv_cache."""
+    _fields_ = [("pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int) for n in ("n_pages", "n_kv", "d_h", "max_pages", "k_exp", "v_exp")]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """dlite_kv_append_args."""
+    _fields_ = [("cache", KvCacheDesc)] + [(n, ctypes.c_int) for n in ("B", "T", "dtype", "rot", "layout", "n_pos")] + \
+               [("k", ctypes.c_void_p), ("k_stride", ctypes.c_int64), ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64),
+                ("pos", ctypes.c_void_p), ("n_rows", ctypes.c_void_p), ("table", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class KvReadArgs(ctypes.Structure):
+    """dlite_kv_read_args."""
+    _fields_ = [("cache", KvCacheDesc)] + [(n, ctypes.c_int) for n in ("B", "T", "dtype")] + \
+               [("k_out", ctypes.c_void_p), ("k_stride", ctypes.c_int64), ("v_out", ctypes.c_void_p), ("v_stride", ctypes.c_int64),
+                ("pos", ctypes.c_void_p), ("n_rows", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
 class Taps(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("z", "x", "b", "hs")]
 
@@ -95,6 +134,10 @@ _SIGS = {
                                         _P, _P, _P]),
     "dlite_round_host": (_I, [_P, _I, _P, _P, _P, _P, _P, _F, _U64, _P, _P, _P, _P, _P]),
     "dlite_synthetic_target": (_I, [_I, _I, _I, _P, _P, _I, _P, _U64, _P, _P, _P]),
+    "dlite_rope_table": (_I, [ctypes.POINTER(RopeConfig), _I, _P, _P]),
+    "dlite_rope": (_I, [ctypes.POINTER(RopeArgs), _P]),
+    "dlite_kv_append": (_I, [ctypes.POINTER(KvAppendArgs), _P]),
+    "dlite_kv_read": (_I, [ctypes.POINTER(KvReadArgs), _P]),
     "dlite_selftest_wait": (_I, [_P, _U64, _P, _P]),
     "dlite_device_status": (_I, [_P, _I, ctypes.POINTER(_I), _P]),
     "dlite_status_string": (ctypes.c_char_p, [_I]),
@@ -218,6 +261,169 @@ def synthetic_target(cand, accept_c, seed, pos, target_tokens, V, round_counter=
     _check(lib.dlite_synthetic_target(B, K, V, _ptr(cand), _ptr(accept_c), accept_c.shape[0],
                                       _ptr(round_counter), seed, _ptr(pos), _ptr(target_tokens),
                                       _stream(stream)), "dlite_synthetic_target")
+
+
+# ---------------------------------------------------------------- target-side operators
+# (no handle; tensors and stream of the current device; see include/dlite.h)
+
+_DTYPES = {torch.float32: DLITE_F32, torch.bfloat16: DLITE_BF16}
+
+
+def _dtype(t, what):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what}: float32 or bfloat16 expected, got {t.dtype}")
+    return code
+
+
+def _here(stream, *tensors):
+    """The stream to launch on; every tensor has to be on the current CUDA device."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("device tensor expected")
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, current device cuda:{dev}")
+    if stream is None:
+        return torch.cuda.current_stream()
+    if stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, current device cuda:{dev}")
+    return stream
+
+
+def _vec(t, dtype, shape, what):
+    """Pointer of a dense tensor of this type and shape (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} {list(shape)} expected, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _row_stride(t, what):
+    """Elements between the rows (b, t) of [B, T, H, d]: dense columns, evenly spaced rows."""
+    if t.dim() != 4:
+        raise ValueError(f"{what}: [B, T, heads, d_h] expected, got {list(t.shape)}")
+    B, T, H, d = t.shape
+    sb, st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d):
+        raise ValueError(f"{what}: the heads of a row have to be dense")
+    row = st if T > 1 else (sb if B > 1 else H * d)
+    if T > 1 and B > 1 and sb != T * st:
+        raise ValueError(f"{what}: rows (b, t) have to be evenly spaced")
+    if row < H * d:
+        raise ValueError(f"{what}: rows overlap")
+    return row
+
+
+def _like_on(stream, shape, dtype, device):
+    """A new tensor that belongs to the stream it is written on."""
+    if stream == torch.cuda.current_stream():
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def rope_table(n_pos, rot, theta=1e6, scaling="plain", factor=1.0, orig_len=0.0, beta_fast=32.0, beta_slow=1.0,
+               attn_factor=0.0, stream=None):
+    """(cos, sin) of positions 0..n_pos-1, float32 [n_pos, rot / 2, 2] on the current device
+    (dlite_rope_table). scaling: "plain", "linear", "ntk" or "yarn"."""
+    lib = load()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: one of {sorted(ROPE_SCALINGS)} expected")
+    s = _here(stream)
+    table = _like_on(s, (max(int(n_pos), 0), max(int(rot), 0) // 2, 2), torch.float32, "cuda")
+    cfg = RopeConfig(int(rot), ROPE_SCALINGS[scaling], theta, factor, orig_len, beta_fast, beta_slow, attn_factor)
+    _check(lib.dlite_rope_table(ctypes.byref(cfg), int(n_pos), table.data_ptr() or None, s.cuda_stream), "dlite_rope_table")
+    return table
+
+
+def _table(table, layout):
+    """(rotated columns, layout code, positions) of a rope_table."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout: one of {sorted(ROPE_LAYOUTS)} expected")
+    if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
+        raise ValueError("table: contiguous float32 [n_pos, rot / 2, 2] expected")
+    return 2 * table.shape[1], ROPE_LAYOUTS[layout], table.shape[0]
+
+
+def rope(x, pos, table, layout="half", n_rows=None, out=None, status=None, stream=None):
+    """x [B, T, heads, d_h] with the first columns of every head rotated by the angles of
+    position pos[b] + t (dlite_rope). out: None (a new tensor), x itself, or another tensor of
+    x's shape; rows t >= n_rows[b] of it are left as they were. Returns out."""
+    lib = load()
+    s = _here(stream, x, pos, table, n_rows, out, status)
+    xs = _row_stride(x, "x")
+    B, T, H, d = x.shape
+    if out is None:
+        out = _like_on(s, x.shape, x.dtype, x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out: x's shape and type expected")
+    rot, lay, n_pos = _table(table, layout)
+    a = RopeArgs(B, T, H, d, rot, lay, _dtype(x, "x"), n_pos, x.data_ptr(), xs, out.data_ptr(), _row_stride(out, "out"),
+                 _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"), table.data_ptr(),
+                 _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_rope(ctypes.byref(a), s.cuda_stream), "dlite_rope")
+    return out
+
+
+def kv_pages(n_pages, n_kv, d_h, device="cuda"):
+    """Memory of a paged 4-bit cache: uint8 [n_pages, n_kv, 72 d_h], one record of 64 tokens per
+    (page, head). The zeros it starts with stand for zero keys and values."""
+    return torch.zeros(n_pages, n_kv, 72 * d_h, dtype=torch.uint8, device=device)
+
+
+def _kv_desc(pages, block_table, B, k_exp, v_exp):
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
+        raise ValueError("pages: contiguous uint8 [n_pages, n_kv, 72 d_h] expected")
+    n_pages, n_kv, rec = pages.shape
+    if rec % 72:
+        raise ValueError("pages: records of 72 d_h bytes expected")
+    if block_table.dim() != 2:
+        raise ValueError("block_table: int32 [B, max_pages] expected")
+    bt = _vec(block_table, torch.int32, (B, block_table.shape[1]), "block_table")
+    return KvCacheDesc(pages.data_ptr(), bt, n_pages, n_kv, rec // 72, block_table.shape[1], k_exp, v_exp)
+
+
+def kv_append(pages, block_table, k, v, pos, table=None, layout="half", n_rows=None, k_exp=0, v_exp=0, status=None, stream=None):
+    """Append k, v [B, T, n_kv, d_h] to the cache at positions pos[b] + t, the keys rotated on
+    the way when a rope_table is given (dlite_kv_append). block_table is int32 [B, max_pages]."""
+    lib = load()
+    s = _here(stream, pages, block_table, k, v, pos, table, n_rows, status)
+    ks, vs = _row_stride(k, "k"), _row_stride(v, "v")
+    B, T, H, d = k.shape
+    desc = _kv_desc(pages, block_table, B, k_exp, v_exp)
+    if v.shape != k.shape or v.dtype != k.dtype or H != desc.n_kv or d != desc.d_h:
+        raise ValueError("k, v: [B, T, n_kv, d_h] of the cache's heads and one type expected")
+    rot, lay, n_pos = _table(table, layout) if table is not None else (0, 0, 0)
+    a = KvAppendArgs(desc, B, T, _dtype(k, "k"), rot, lay, n_pos, k.data_ptr(), ks, v.data_ptr(), vs,
+                     _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"),
+                     table.data_ptr() if table is not None else None, _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_kv_append(ctypes.byref(a), s.cuda_stream), "dlite_kv_append")
+
+
+def kv_read(pages, block_table, pos, T, n_rows=None, k_exp=0, v_exp=0, dtype=torch.bfloat16, k_out=None, v_out=None,
+            status=None, stream=None):
+    """The values the cache holds at positions pos[b] + t, t < T: (k, v) [B, T, n_kv, d_h]
+    (dlite_kv_read). New outputs start as zeros where rows are not read."""
+    lib = load()
+    s = _here(stream, pages, block_table, pos, n_rows, k_out, v_out, status)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out: both or neither expected")
+    B = block_table.shape[0]
+    desc = _kv_desc(pages, block_table, B, k_exp, v_exp)
+    shape = (B, T, desc.n_kv, desc.d_h)
+    if k_out is None:
+        with torch.cuda.stream(s):
+            k_out, v_out = (torch.zeros(shape, dtype=dtype, device=pages.device) for _ in range(2))
+    elif tuple(k_out.shape) != shape or tuple(v_out.shape) != shape or v_out.dtype != k_out.dtype:
+        raise ValueError(f"k_out, v_out: {list(shape)} of one type expected")
+    a = KvReadArgs(desc, B, T, _dtype(k_out, "k_out"), k_out.data_ptr(), _row_stride(k_out, "k_out"), v_out.data_ptr(),
+                   _row_stride(v_out, "v_out"), _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"),
+                   _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_kv_read(ctypes.byref(a), s.cuda_stream), "dlite_kv_read")
+    return k_out, v_out
 
 
 def config_struct(cfg, B_max):

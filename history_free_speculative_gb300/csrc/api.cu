@@ -844,6 +844,12 @@ int check_round_args(dlite_handle* h, int B, const void* hidden, const int32_t* 
 
 // ================================================================ C ABI
 
+int dlite::launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return DLITE_OK;
+  g_last_cuda_error = e;
+  return DLITE_ERR_CUDA;
+}
+
 extern "C" {
 
 const char* dlite_status_string(int st) {

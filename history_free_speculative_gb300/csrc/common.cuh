@@ -12,6 +12,7 @@ typedef __nv_bfloat16 bf16;
 // Sticky device status bits (mirrors DLITE_DEV_* in dlite.h).
 constexpr int kDevTimeout = 1;
 constexpr int kDevBounds = 2;
+constexpr int kDevNonfinite = 4;
 
 __device__ __forceinline__ void flag_status(int* st, int bits) {
   if (st) atomicOr(st, bits);

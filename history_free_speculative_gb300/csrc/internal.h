@@ -26,6 +26,9 @@ inline int device_sms() {
   return n;
 }
 
+// Status code of a launch; an error is kept for dlite_last_cuda_error (api.cu).
+int launch_status(cudaError_t e);
+
 // Launch with programmatic stream serialization (see pdl_trigger / pdl_wait).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,

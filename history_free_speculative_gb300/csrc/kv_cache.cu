@@ -1,0 +1,384 @@
+// Append to and read from the paged 4-bit cache of the target side.
+//
+// Append: one CTA per (page a request's new rows touch, KV head, request). Its
+// items are (token, 16 columns) for keys and for values: one thread loads 16
+// columns (and, for rotated keys, their partners), rotates, quantises and has the
+// scale byte and eight code bytes of that token. Keys go straight out (8 bytes
+// of a token's row). Value codes are transposed through shared memory, because
+// a byte holds two neighbouring tokens of a column: a page that is filled whole
+// leaves as 16-byte stores, else each byte is one thread's, and a byte whose
+// other token is old is read and merged. Bound: HBM for prompts (values in, 9/16
+// byte out); launch latency and two dependent loads (position, page id) for a token.
+//
+// Read: the CTA fetches its record with one bulk copy (9 KB at d_h 128) and decodes the
+// rows asked for out of shared memory.
+#include <algorithm>
+
+#include "kv_page.cuh"
+#include "rope.cuh"
+#include "tc_device.cuh"
+
+namespace dlite {
+namespace {
+
+struct AppendArgs {
+  uint8_t* pages;
+  const int32_t* bt;
+  int n_pages, n_kv, max_pages;
+  int T, half, inter, n_pos;
+  float k_inv, v_inv;  // 2^-exp
+  const void *k, *v;
+  long long ks, vs;
+  const int64_t* pos;
+  const int32_t* n_rows;
+  const float2* table;  // null: no rotation
+  int* status;
+};
+
+// 8 consecutive values as float: 16-byte accesses (VEC) or one by one
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+
+// Columns c .. c + 7 of a key row after the rotation. VEC: 8 columns lie on one side of
+// every border (the halves and the rotated part are multiples of 8 columns).
+template <typename T, bool VEC>
+__device__ __forceinline__ void rotated8(const T* row, int c, int half, bool inter, const float2* tab, float* y) {
+  if constexpr (VEC) {
+    load8<T, VEC>(row + c, y);
+    if (!tab || c >= 2 * half) return;
+    if (inter) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) rope_pair(y[2 * j], y[2 * j + 1], tab[c / 2 + j], y[2 * j], y[2 * j + 1]);
+    } else {
+      const bool first = c < half;
+      float o[8];
+      load8<T, VEC>(row + (first ? c + half : c - half), o);
+      const float2* tb = tab + (first ? c : c - half);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 cs = tb[j];
+        float y0, y1;
+        rope_pair(first ? y[j] : o[j], first ? o[j] : y[j], cs, y0, y1);
+        y[j] = first ? y0 : y1;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int cc = c + j;
+      y[j] = to_f32(row[cc]);
+      if (!tab || cc >= 2 * half) continue;
+      const int i = inter ? cc >> 1 : (cc < half ? cc : cc - half);
+      const bool first = inter ? !(cc & 1) : cc < half;
+      const float o = to_f32(row[inter ? cc ^ 1 : (first ? cc + half : cc - half)]);
+      float y0, y1;
+      rope_pair(first ? y[j] : o, first ? o : y[j], tab[i], y0, y1);
+      y[j] = first ? y0 : y1;
+    }
+  }
+}
+
+// The rows of request b in page `page` (the request's page_i-th touched one): tokens [lo, hi)
+// of the page, from row t0 of the call on. False: none.
+struct Span {
+  long long page;
+  int lo, hi, t0;
+};
+__device__ __forceinline__ bool page_span(const int64_t* pos, const int32_t* n_rows, int T, int b, int page_i, Span& s) {
+  const long long p0 = pos[b];
+  const int n = n_rows ? min(max(n_rows[b], 0), T) : T;
+  s.page = (p0 >> 6) + page_i;
+  const long long first = max(p0, s.page * 64), last = min(p0 + n, s.page * 64 + 64);
+  if (first >= last) return false;
+  s.lo = (int)(first - s.page * 64);
+  s.hi = (int)(last - s.page * 64);
+  s.t0 = (int)(first - p0);
+  return true;
+}
+
+template <typename T, int DH, bool VEC>
+__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
+  constexpr int NB = DH / 16;
+  __shared__ __align__(16) uint8_t vc[DH][kv::kPage];  // value codes, one byte each
+  pdl_trigger();
+  pdl_wait();
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, nthr = blockDim.x;
+  Span sp;
+  if (!page_span(a.pos, a.n_rows, a.T, b, blockIdx.x, sp)) return;
+  int id = -1;
+  if (sp.page >= 0 && sp.page < a.max_pages) id = a.bt[(size_t)b * a.max_pages + sp.page];
+  if (id < 0 || id >= a.n_pages) {
+    if (tid == 0) flag_status(a.status, kDevBounds);
+    return;
+  }
+  uint8_t* rec = a.pages + ((size_t)id * a.n_kv + h) * kv::rec_bytes(DH);
+  const int nt = sp.hi - sp.lo, items = nt * NB;
+  bool bad = false;
+  for (int u = tid; u < 2 * items; u += nthr) {
+    float v[16];
+    uint2 codes;
+    uint32_t scale;
+    if (u < items) {  // keys: the blocks of a token side by side
+      const int i = u / NB, j = u % NB;
+      const T* row = static_cast<const T*>(a.k) + ((long long)b * a.T + sp.t0 + i) * a.ks + (long long)h * DH;
+      const float2* tab = nullptr;
+      if (a.table) {
+        long long p = sp.page * 64 + sp.lo + i;
+        if (p >= a.n_pos) {
+          p = a.n_pos - 1;
+          flag_status(a.status, kDevBounds);
+        }
+        tab = a.table + p * a.half;
+      }
+      rotated8<T, VEC>(row, 16 * j, a.half, a.inter, tab, v);
+      rotated8<T, VEC>(row, 16 * j + 8, a.half, a.inter, tab, v + 8);
+      bad |= kv::quantise16(v, a.k_inv, codes, scale);
+      const int tok = sp.lo + i;
+      *reinterpret_cast<uint2*>(rec + tok * (DH / 2) + 8 * j) = codes;
+      rec[kv::ks_off(DH) + tok * NB + j] = (uint8_t)scale;
+    } else {  // values: the tokens of a block side by side
+      const int j = (u - items) / nt, i = (u - items) - j * nt, tok = sp.lo + i;
+      const T* row = static_cast<const T*>(a.v) + ((long long)b * a.T + sp.t0 + i) * a.vs + (long long)h * DH + 16 * j;
+      load8<T, VEC>(row, v);
+      load8<T, VEC>(row + 8, v + 8);
+      bad |= kv::quantise16(v, a.v_inv, codes, scale);
+      rec[kv::vs_off(DH) + j * 64 + tok] = (uint8_t)scale;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) vc[16 * j + e][tok] = (uint8_t)(((e < 8 ? codes.x : codes.y) >> ((e & 7) * 4)) & 15u);
+    }
+  }
+  if (bad) flag_status(a.status, kDevNonfinite);
+  __syncthreads();
+  uint8_t* vd = rec + kv::v_off(DH);
+  if (nt == 64) {
+    for (int u = tid; u < DH * 2; u += nthr) {  // 32 tokens of a column
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(&vc[u >> 1][(u & 1) * 32]);
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // four code bytes c0 c1 c2 c3 -> c0 | c1 << 4, c2 | c3 << 4
+        const uint32_t x0 = src[2 * q] | (src[2 * q] >> 4), x1 = src[2 * q + 1] | (src[2 * q + 1] >> 4);
+        w[q] = __byte_perm(x0, x1, 0x6420);
+      }
+      *reinterpret_cast<uint4*>(vd + u * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    const int b0 = sp.lo >> 1, nb = ((sp.hi + 1) >> 1) - b0;
+    for (int u = tid; u < DH * nb; u += nthr) {
+      const int d = u / nb, by = b0 + (u - d * nb), t = 2 * by;
+      uint8_t* dst = vd + d * 32 + by;
+      const bool n0 = t >= sp.lo, n1 = t + 1 < sp.hi;  // which of the byte's tokens are new
+      uint32_t w = n0 && n1 ? 0u : *dst;
+      if (n0) w = (w & 0xf0u) | vc[d][t];
+      if (n1) w = (w & 0x0fu) | ((uint32_t)vc[d][t + 1] << 4);
+      *dst = (uint8_t)w;
+    }
+  }
+}
+
+struct ReadArgs {
+  const uint8_t* pages;
+  const int32_t* bt;
+  int n_pages, n_kv, max_pages, T;
+  float k_scale, v_scale;  // 2^exp
+  void *k, *v;
+  long long ks, vs;
+  const int64_t* pos;
+  const int32_t* n_rows;
+  int* status;
+};
+
+__device__ __forceinline__ void put(float x, float& y) { y = x; }
+__device__ __forceinline__ void put(float x, bf16& y) { y = __float2bfloat16_rn(x); }
+
+// 16 decoded values to p: 16-byte stores where p allows them
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float (&v)[16], bool vec) {
+  T o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) put(v[i], o[i]);
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(o)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = o[i];
+  }
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(256) kv_read_kernel(ReadArgs a, bool vec) {
+  constexpr int NB = DH / 16;
+  __shared__ __align__(128) uint8_t rec[kv::rec_bytes(DH)];
+  __shared__ __align__(8) uint64_t bar;
+  pdl_trigger();
+  pdl_wait();
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, nthr = blockDim.x;
+  Span sp;
+  if (!page_span(a.pos, a.n_rows, a.T, b, blockIdx.x, sp)) return;
+  int id = -1;
+  if (sp.page >= 0 && sp.page < a.max_pages) id = a.bt[(size_t)b * a.max_pages + sp.page];
+  if (id < 0 || id >= a.n_pages) {
+    if (tid == 0) flag_status(a.status, kDevBounds);
+    return;
+  }
+  const uint32_t bs = tc::su32(&bar);
+  if (tid == 0) {
+    tc::mbar_init(bs, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tc::mbar_expect_tx(bs, kv::rec_bytes(DH));
+    tc::bulk_load(tc::su32(rec), a.pages + ((size_t)id * a.n_kv + h) * kv::rec_bytes(DH), kv::rec_bytes(DH), bs);
+  }
+  __syncthreads();
+  if (!__syncthreads_and(tc::mbar_wait(bs, 0, a.status))) {  // the copy never landed: give it one more bounded wait, leave
+    if (tid == 0) tc::mbar_wait(bs, 0, a.status);
+    __syncthreads();
+    return;
+  }
+  const int nt = sp.hi - sp.lo, items = nt * NB;
+  for (int u = tid; u < 2 * items; u += nthr) {
+    float v[16];
+    uint32_t by[8];
+    float s;
+    const bool key = u < items;
+    int i, j;
+    if (key) {
+      i = u / NB, j = u % NB;
+      const int tok = sp.lo + i;
+      const uint2 w = *reinterpret_cast<const uint2*>(rec + tok * (DH / 2) + 8 * j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) by[e] = ((e < 4 ? w.x : w.y) >> ((e & 3) * 8)) & 0xffu;
+      s = kv::fp8_to_f32(rec[kv::ks_off(DH) + tok * NB + j]) * a.k_scale;
+    } else {
+      j = (u - items) / nt, i = (u - items) - j * nt;
+      const int tok = sp.lo + i, sh = (tok & 1) * 4;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint8_t* col = rec + kv::v_off(DH) + (16 * j + 2 * e) * 32 + (tok >> 1);
+        by[e] = ((col[0] >> sh) & 15u) | (((col[32] >> sh) & 15u) << 4);
+      }
+      s = kv::fp8_to_f32(rec[kv::vs_off(DH) + j * 64 + tok]) * a.v_scale;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t p = kv::fp4x2_to_f16x2(by[e]);
+      v[2 * e] = __half2float(__ushort_as_half((unsigned short)(p & 0xffffu))) * s;
+      v[2 * e + 1] = __half2float(__ushort_as_half((unsigned short)(p >> 16))) * s;
+    }
+    const long long r = (long long)b * a.T + sp.t0 + i, c = (long long)h * DH + 16 * j;
+    store16(key ? static_cast<T*>(a.k) + r * a.ks + c : static_cast<T*>(a.v) + r * a.vs + c, v, vec);
+  }
+}
+
+// Host checks shared by the cache's calls.
+int check_cache(const dlite_kv_cache& c, int B, int T, const int64_t* pos) {
+  if (!c.pages || !c.block_table || !pos) return DLITE_ERR_INVALID_ARG;
+  if (((uintptr_t)c.pages & 15) || ((uintptr_t)c.block_table & 3) || ((uintptr_t)pos & 7)) return DLITE_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || c.n_pages < 1 || c.n_kv < 1 || c.max_pages < 1) return DLITE_ERR_INVALID_ARG;
+  if (c.k_exp < -64 || c.k_exp > 64 || c.v_exp < -64 || c.v_exp > 64) return DLITE_ERR_INVALID_ARG;
+  if ((c.d_h != 64 && c.d_h != 128) || c.n_kv > 65535 || B > 65535 || c.max_pages >= (1 << 25) || T >= (1 << 30))
+    return DLITE_ERR_UNSUPPORTED_SHAPE;
+  return DLITE_OK;
+}
+
+// CTAs along the pages: as many as T rows can touch from any first position
+inline unsigned touched_pages(int T) { return (unsigned)((T + 2 * kv::kPage - 2) / kv::kPage); }
+// Threads: 256 once a page holds more items than 128 threads take in a turn
+inline unsigned cta_threads(int T, int d_h) { return std::min(T, kv::kPage) * (d_h / 16) * 2 > 128 ? 256 : 128; }
+
+}  // namespace
+}  // namespace dlite
+
+extern "C" int dlite_kv_append(const dlite_kv_append_args* g, dlite_stream_t stream) {
+  using namespace dlite;
+  if (!g || !g->k || !g->v) return DLITE_ERR_INVALID_ARG;
+  const dlite_kv_cache& c = g->cache;
+  if (const int rc = check_cache(c, g->B, g->T, g->pos)) return rc;
+  if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
+  const int es = g->dtype == DLITE_F32 ? 4 : 2;
+  const long long cols = (long long)c.n_kv * c.d_h;
+  if (g->k_stride < cols || g->v_stride < cols || ((uintptr_t)g->k | (uintptr_t)g->v) % es) return DLITE_ERR_INVALID_ARG;
+  if (g->table) {
+    if ((g->layout != DLITE_ROPE_HALF && g->layout != DLITE_ROPE_INTERLEAVED) || g->n_pos < 1 || (uintptr_t)g->table % 8)
+      return DLITE_ERR_INVALID_ARG;
+    if (g->rot < 2 || g->rot % 2 || g->rot > c.d_h) return DLITE_ERR_UNSUPPORTED_SHAPE;
+  }
+  AppendArgs a = {};
+  a.pages = static_cast<uint8_t*>(c.pages);
+  a.bt = c.block_table;
+  a.n_pages = c.n_pages;
+  a.n_kv = c.n_kv;
+  a.max_pages = c.max_pages;
+  a.T = g->T;
+  a.half = g->table ? g->rot / 2 : 0;
+  a.inter = g->layout == DLITE_ROPE_INTERLEAVED;
+  a.n_pos = g->n_pos;
+  a.k_inv = ldexpf(1.f, -c.k_exp);
+  a.v_inv = ldexpf(1.f, -c.v_exp);
+  a.k = g->k;
+  a.ks = g->k_stride;
+  a.v = g->v;
+  a.vs = g->v_stride;
+  a.pos = g->pos;
+  a.n_rows = g->n_rows;
+  a.table = reinterpret_cast<const float2*>(g->table);
+  a.status = g->status;
+  // 16-byte loads: rows on 16 bytes, and (rotated keys) borders at multiples of 8 columns
+  const int V = 16 / es;
+  const bool vec = !(((uintptr_t)g->k | (uintptr_t)g->v) & 15) && g->k_stride % V == 0 && g->v_stride % V == 0 &&
+                   (!g->table || g->rot % (a.inter ? 8 : 16) == 0);
+  void (*fn)(AppendArgs);
+  if (g->dtype == DLITE_F32)
+    fn = c.d_h == 128 ? (vec ? kv_append_kernel<float, 128, true> : kv_append_kernel<float, 128, false>)
+                      : (vec ? kv_append_kernel<float, 64, true> : kv_append_kernel<float, 64, false>);
+  else
+    fn = c.d_h == 128 ? (vec ? kv_append_kernel<bf16, 128, true> : kv_append_kernel<bf16, 128, false>)
+                      : (vec ? kv_append_kernel<bf16, 64, true> : kv_append_kernel<bf16, 64, false>);
+  return launch_status(launch_pdl(fn, dim3(touched_pages(g->T), c.n_kv, g->B), dim3(cta_threads(g->T, c.d_h)), 0,
+                                  (cudaStream_t)stream, a));
+}
+
+extern "C" int dlite_kv_read(const dlite_kv_read_args* g, dlite_stream_t stream) {
+  using namespace dlite;
+  if (!g || !g->k_out || !g->v_out) return DLITE_ERR_INVALID_ARG;
+  const dlite_kv_cache& c = g->cache;
+  if (const int rc = check_cache(c, g->B, g->T, g->pos)) return rc;
+  if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
+  const int es = g->dtype == DLITE_F32 ? 4 : 2, V = 16 / es;
+  const long long cols = (long long)c.n_kv * c.d_h;
+  if (g->k_stride < cols || g->v_stride < cols || ((uintptr_t)g->k_out | (uintptr_t)g->v_out) % es) return DLITE_ERR_INVALID_ARG;
+  ReadArgs a = {};
+  a.pages = static_cast<const uint8_t*>(c.pages);
+  a.bt = c.block_table;
+  a.n_pages = c.n_pages;
+  a.n_kv = c.n_kv;
+  a.max_pages = c.max_pages;
+  a.T = g->T;
+  a.k_scale = ldexpf(1.f, c.k_exp);
+  a.v_scale = ldexpf(1.f, c.v_exp);
+  a.k = g->k_out;
+  a.ks = g->k_stride;
+  a.v = g->v_out;
+  a.vs = g->v_stride;
+  a.pos = g->pos;
+  a.n_rows = g->n_rows;
+  a.status = g->status;
+  const bool vec = !(((uintptr_t)g->k_out | (uintptr_t)g->v_out) & 15) && g->k_stride % V == 0 && g->v_stride % V == 0;
+  void (*fn)(ReadArgs, bool) = g->dtype == DLITE_F32 ? (c.d_h == 128 ? kv_read_kernel<float, 128> : kv_read_kernel<float, 64>)
+                                                     : (c.d_h == 128 ? kv_read_kernel<bf16, 128> : kv_read_kernel<bf16, 64>);
+  return launch_status(launch_pdl(fn, dim3(touched_pages(g->T), c.n_kv, g->B), dim3(cta_threads(g->T, c.d_h)), 0,
+                                  (cudaStream_t)stream, a, vec));
+}

@@ -1,0 +1,95 @@
+// The paged 4-bit cache's record of one (page, KV head): layout and conversions.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
+namespace dlite {
+namespace kv {
+
+constexpr int kPage = DLITE_KV_PAGE;
+
+// Byte offsets inside a record of 72 d_h bytes.
+__host__ __device__ constexpr int rec_bytes(int d_h) { return 72 * d_h; }
+__host__ __device__ constexpr int v_off(int d_h) { return 32 * d_h; }
+__host__ __device__ constexpr int ks_off(int d_h) { return 64 * d_h; }
+__host__ __device__ constexpr int vs_off(int d_h) { return 68 * d_h; }
+
+// Two e2m1 codes (byte: low nibble first) / two e4m3 numbers as an f16 pair. Both are
+// exact, and so is the product of a code and a scale (2 + 4 significant bits, 2^-10..2688).
+__device__ __forceinline__ uint32_t fp4x2_to_f16x2(uint32_t byte) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(byte));
+  return r;
+}
+// byte B of a word
+template <int B>
+__device__ __forceinline__ uint32_t fp4x2_of(uint32_t w) {
+  uint32_t r;
+  if constexpr (B == 0)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+  else if constexpr (B == 1)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+  else if constexpr (B == 2)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
+  else
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t fp8x2_to_f16x2(uint16_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+  return r;
+}
+// Nearest e4m3 of s (0 <= s <= 448), as a byte, and its value.
+__device__ __forceinline__ uint32_t f32_to_fp8(float s) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(s));
+  return r & 0xffu;
+}
+__device__ __forceinline__ float fp8_to_f32(uint32_t byte) {
+  const uint32_t h = fp8x2_to_f16x2((uint16_t)byte);
+  return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+}
+// Nearest e2m1 codes of (lo, hi), ties to even, saturating: one byte.
+__device__ __forceinline__ uint32_t f32x2_to_fp4(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, t, t, t};\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+  return r & 0xffu;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Codes (nibble e of the pair lo, hi: column e) and scale byte of 16 columns.
+// v is overwritten. Returns whether a value was NaN or infinite.
+__device__ __forceinline__ bool quantise16(float (&v)[16], float inv_exp, uint2& codes, uint32_t& scale) {
+  float amax = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] *= inv_exp;
+    const float m = fabsf(v[i]);
+    if (m <= 3.402823466e38f)
+      amax = fmaxf(amax, m);
+    else
+      bad = true;
+    if (v[i] != v[i]) v[i] = 0.f;
+  }
+  scale = f32_to_fp8(fminf(__fdiv_rn(amax, 6.f), 448.f));
+  const float s = fp8_to_f32(scale);
+  uint32_t w[2] = {0u, 0u};
+  if (s > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+      w[i >> 3] |= f32x2_to_fp4(__fdiv_rn(v[i], s), __fdiv_rn(v[i + 1], s)) << ((i & 7) * 4);
+  }
+  codes = make_uint2(w[0], w[1]);
+  return bad;
+}
+
+}  // namespace kv
+}  // namespace dlite

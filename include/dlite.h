@@ -52,6 +52,7 @@ enum dlite_status {
 /* Device status word bits (dlite_device_status). */
 #define DLITE_DEV_TIMEOUT 1
 #define DLITE_DEV_BOUNDS 2
+#define DLITE_DEV_NONFINITE 4 /* target-side calls: a NaN or infinity met a format that cannot hold it */
 
 /* Drafter shape. Positions: block = anchor + K placeholders ([P1] §"草稿块长与
  * 验证块长不是一个参数": block_size 8 = 1 anchor + 7 drafts). */
@@ -382,6 +383,148 @@ int dlite_synthetic_target(int B, int K, int V, const int32_t *candidates, const
  * Afterwards dlite_device_status returns DLITE_ERR_DEVICE_TIMEOUT (and clears
  * the flag if asked). Errors: INVALID_ARG, CUDA. */
 int dlite_selftest_wait(dlite_handle *h, uint64_t limit_ns, int32_t *result, dlite_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Target-side operators of the round. Between the draft and its verification
+ * the target runs one causal forward over [a, d_1..d_K] ([P1] §"一次因果前向评估整条候选"):
+ * T = K + 1 rows per request at positions pos[b] + t, against the target's own
+ * KV cache, whose length after the round is cropped to the committed tokens
+ * ([P1] §"一轮执行后..." step 4). These calls are the parts of that
+ * forward that touch positions, the cache and the scores; the target's weights
+ * stay with the caller. pos [B] int64 (device) is the number of tokens of
+ * request b already in the cache: dlite_advance moves it by n_commit, which is
+ * the crop (rows past it are overwritten by the next append).
+ *
+ * They need no handle. Common to all of them:
+ *   rows      row (b, t) of x [B, T, ...] starts at element (b T + t) stride; the
+ *             columns of a row are dense. stride >= the row's columns.
+ *   n_rows    [B] int32 (device) or NULL: request b has n_rows[b] valid rows
+ *             (values are taken into [0, T]); rows behind them are not read and
+ *             their outputs are left as they were. NULL: all T.
+ *   status    device int32 or NULL: receives DLITE_DEV_* bits (sticky, atomically or-ed).
+ *   Pointers must be aligned to their element type; 16-byte aligned rows take
+ *   the vector paths (attention's cache pages must be 16-byte aligned).
+ * Errors: INVALID_ARG (NULL, misaligned, stride too small, bad enum, sizes below 1),
+ * UNSUPPORTED_SHAPE (sizes outside those stated), CUDA. */
+
+enum dlite_rope_layout {
+    DLITE_ROPE_HALF = 0,        /* column i of the rotated part pairs with i + rot / 2 */
+    DLITE_ROPE_INTERLEAVED = 1  /* column 2i pairs with 2i + 1 */
+};
+enum dlite_rope_scaling {
+    DLITE_ROPE_PLAIN = 0,  /* f_i = theta^(-2i / rot) */
+    DLITE_ROPE_LINEAR = 1, /* position interpolation: f_i / factor */
+    DLITE_ROPE_NTK = 2,    /* base change: theta factor^(rot / (rot - 2)) in place of theta (rot >= 4) */
+    DLITE_ROPE_YARN = 3    /* by parts (Peng et al., "YaRN", 2023): f_i (1 - r_i) + f_i / factor r_i with the ramp
+                            * r_i = clamp((i - lo) / (hi - lo), 0, 1), lo = max(floor(c(beta_fast)), 0),
+                            * hi = min(ceil(c(beta_slow)), rot - 1), c(b) = rot ln(orig_len / (2 pi b)) / (2 ln theta);
+                            * hi <= lo: a step behind lo */
+};
+typedef struct {
+    int rot;          /* rotated columns of a head (its first ones); even, 2..256 */
+    int scaling;      /* dlite_rope_scaling */
+    double theta;     /* base, > 1 */
+    double factor;    /* context extension, >= 1 (LINEAR, NTK, YARN) */
+    double orig_len;  /* YARN: the context length before extension */
+    double beta_fast, beta_slow; /* YARN: rotations at the ramp's ends (32, 1); beta_fast > beta_slow > 0 */
+    double attn_factor; /* > 0: factor m on cos and sin; 0: m = 1, or 0.1 ln(factor) + 1 with YARN */
+} dlite_rope_config;
+
+/* table [n_pos, rot / 2, 2] float32 (out): (m cos, m sin)(p f_i), the angle, its
+ * cosine and sine in float64 and rounded once, so far positions keep their phase. */
+int dlite_rope_table(const dlite_rope_config *cfg, int n_pos, float *table, dlite_stream_t stream);
+
+/* Rotary positions: out = x with the first rot columns of every head rotated by
+ * the angles of position pos[b] + t: (x0, x1) -> (x0 c - x1 s, x1 c + x0 s), the
+ * four products rounded to float32, then each sum, then the result once to
+ * dtype; the other columns are copied. out may be x itself (same stride),
+ * otherwise the two do not overlap. A position outside [0, n_pos) is
+ * taken to the nearest end and flags DLITE_DEV_BOUNDS. */
+typedef struct {
+    int B, T, heads, d_h; /* d_h 2..1024 */
+    int rot, layout;      /* even, 2..min(256, d_h); dlite_rope_layout */
+    int dtype;            /* dlite_dtype of x and out */
+    int n_pos;
+    const void *x;        /* [B, T, heads, d_h] */
+    int64_t x_stride;
+    void *out;
+    int64_t out_stride;
+    const int64_t *pos;   /* [B] */
+    const int32_t *n_rows;
+    const float *table;   /* dlite_rope_table's, of the same rot */
+    int *status;
+} dlite_rope_args;
+int dlite_rope(const dlite_rope_args *args, dlite_stream_t stream);
+
+/* Paged 4-bit cache. A page holds DLITE_KV_PAGE tokens of every KV head; token p
+ * of request b is row p % 64 of page block_table[b, p / 64]. pages is
+ * [n_pages][n_kv][72 d_h] bytes, one record per (page, head):
+ *   key codes   [64][d_h / 2]   byte j of a token: column 2j low nibble, 2j + 1 high
+ *   value codes [d_h][32]       byte i of a column: token 2i low nibble, 2i + 1 high
+ *   key scales  [64][d_h / 16], value scales [d_h / 16][64]   e4m3, one per (token, 16 columns)
+ * A code is an e2m1 number (sign, two exponent bits, one mantissa bit: 0, .5, 1,
+ * 1.5, 2, 3, 4, 6); the value is code x scale x 2^exp, exact in bf16. Values are
+ * stored with the tokens of a column side by side because the attention's second
+ * product reads them along the tokens. Quantisation of 16 columns y = x 2^-exp:
+ * scale = e4m3(max |y| / 6) to nearest, at most 448; code = e2m1(y / scale) to
+ * nearest, ties to even, magnitudes above 6 to 6; float32 arithmetic. A scale
+ * that rounds to 0 makes the 16 values 0. The format holds no NaN or infinity: the
+ * scale is taken over the finite y, NaN is stored as 0, an infinity as +-6 scale,
+ * and DLITE_DEV_NONFINITE is flagged. Scale bytes are non-negative and finite
+ * (0x00..0x7e); pages written by other means keep to that. Code and scale bytes
+ * of rows not yet appended may hold anything. */
+#define DLITE_KV_PAGE 64
+typedef struct {
+    void *pages;                 /* 16-byte aligned */
+    const int32_t *block_table;  /* [B, max_pages] page ids */
+    int n_pages, n_kv, d_h;      /* d_h 64 or 128 */
+    int max_pages;               /* columns of block_table: requests hold up to 64 max_pages tokens (< 2^31) */
+    int k_exp, v_exp;            /* -64..64: a power of two taken out of keys / values before their e4m3
+                                  * scales (2^-9..448), so that the largest |x| / 6 lies well inside */
+} dlite_kv_cache;
+
+/* Append keys and values to the cache: rows t < n_rows[b] of request b go to
+ * positions pos[b] + t. With a table the keys are rotated on the way, by the
+ * arithmetic of dlite_rope without its last rounding to dtype; NULL: keys are
+ * stored as they come (already rotated). Any T: a decoded token, a
+ * verification block, a prompt. No other row of the cache changes. Two requests
+ * of a call must not append into the same page (a shared page is copied first). A row at a
+ * position outside [0, 64 max_pages) or in a page whose id is outside [0, n_pages)
+ * is not stored and flags DLITE_DEV_BOUNDS; so does a position the table does not
+ * hold (taken to its nearest end, as dlite_rope does). */
+typedef struct {
+    dlite_kv_cache cache;
+    int B, T;
+    int dtype;            /* of k and v */
+    int rot, layout;      /* with a table: even rot, 2..d_h; dlite_rope_layout */
+    int n_pos;            /* rows of the table */
+    const void *k;        /* [B, T, n_kv, d_h] */
+    int64_t k_stride;
+    const void *v;
+    int64_t v_stride;
+    const int64_t *pos;   /* [B] */
+    const int32_t *n_rows;
+    const float *table;   /* [n_pos, rot / 2, 2] or NULL */
+    int *status;
+} dlite_kv_append_args;
+int dlite_kv_append(const dlite_kv_append_args *args, dlite_stream_t stream);
+
+/* Read cached rows back as the values they stand for: row (b, t) of k_out and
+ * v_out is position pos[b] + t (exact in both dtypes). A row outside the table or in a
+ * page outside [0, n_pages) is left as it was and flags DLITE_DEV_BOUNDS. */
+typedef struct {
+    dlite_kv_cache cache;
+    int B, T;
+    int dtype;            /* of k_out and v_out */
+    void *k_out;          /* [B, T, n_kv, d_h] */
+    int64_t k_stride;
+    void *v_out;
+    int64_t v_stride;
+    const int64_t *pos;   /* [B] */
+    const int32_t *n_rows;
+    int *status;
+} dlite_kv_read_args;
+int dlite_kv_read(const dlite_kv_read_args *args, dlite_stream_t stream);
 
 /* Read (and with clear != 0, reset) the sticky device status word.
  * Synchronises `stream`. *status_out gets DLITE_DEV_* bits. Returns

@@ -6,3 +6,4 @@ binding) never imports, links or runs anything here.
 """
 from . import philox  # noqa: F401
 from . import dlite_oracle  # noqa: F401
+from . import target_oracle  # noqa: F401
