@@ -104,6 +104,14 @@ class KvReadArgs(ctypes.Structure):
                 ("pos", ctypes.c_void_p), ("n_rows", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
+class KvAttentionArgs(ctypes.Structure):
+    """dlite_kv_attention_args."""
+    _fields_ = [("cache", KvCacheDesc)] + [(n, ctypes.c_int) for n in ("B", "T", "n_q", "dtype", "window")] + \
+               [("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("lse", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("n_rows", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)]
+
+
 class Taps(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("z", "x", "b", "hs")]
 
@@ -138,6 +146,8 @@ _SIGS = {
     "dlite_rope": (_I, [ctypes.POINTER(RopeArgs), _P]),
     "dlite_kv_append": (_I, [ctypes.POINTER(KvAppendArgs), _P]),
     "dlite_kv_read": (_I, [ctypes.POINTER(KvReadArgs), _P]),
+    "dlite_kv_attention_workspace": (ctypes.c_size_t, [ctypes.POINTER(KvAttentionArgs)]),
+    "dlite_kv_attention": (_I, [ctypes.POINTER(KvAttentionArgs), _P]),
     "dlite_selftest_wait": (_I, [_P, _U64, _P, _P]),
     "dlite_device_status": (_I, [_P, _I, ctypes.POINTER(_I), _P]),
     "dlite_status_string": (ctypes.c_char_p, [_I]),
@@ -317,12 +327,13 @@ def _row_stride(t, what):
     return row
 
 
-def _like_on(stream, shape, dtype, device):
-    """A new tensor that belongs to the stream it is written on."""
+def _new(stream, shape, dtype, zero=False):
+    """A new tensor that belongs to the stream it is written on (zeros where a call leaves rows out)."""
+    make = torch.zeros if zero else torch.empty
     if stream == torch.cuda.current_stream():
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device="cuda")
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device="cuda")
 
 
 def rope_table(n_pos, rot, theta=1e6, scaling="plain", factor=1.0, orig_len=0.0, beta_fast=32.0, beta_slow=1.0,
@@ -333,7 +344,7 @@ def rope_table(n_pos, rot, theta=1e6, scaling="plain", factor=1.0, orig_len=0.0,
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling: one of {sorted(ROPE_SCALINGS)} expected")
     s = _here(stream)
-    table = _like_on(s, (max(int(n_pos), 0), max(int(rot), 0) // 2, 2), torch.float32, "cuda")
+    table = _new(s, (max(int(n_pos), 0), max(int(rot), 0) // 2, 2), torch.float32)
     cfg = RopeConfig(int(rot), ROPE_SCALINGS[scaling], theta, factor, orig_len, beta_fast, beta_slow, attn_factor)
     _check(lib.dlite_rope_table(ctypes.byref(cfg), int(n_pos), table.data_ptr() or None, s.cuda_stream), "dlite_rope_table")
     return table
@@ -351,13 +362,13 @@ def _table(table, layout):
 def rope(x, pos, table, layout="half", n_rows=None, out=None, status=None, stream=None):
     """x [B, T, heads, d_h] with the first columns of every head rotated by the angles of
     position pos[b] + t (dlite_rope). out: None (a new tensor), x itself, or another tensor of
-    x's shape; rows t >= n_rows[b] of it are left as they were. Returns out."""
+    x's shape; rows t >= n_rows[b] of it are left as they were (zeros in a new one). Returns out."""
     lib = load()
     s = _here(stream, x, pos, table, n_rows, out, status)
     xs = _row_stride(x, "x")
     B, T, H, d = x.shape
     if out is None:
-        out = _like_on(s, x.shape, x.dtype, x.device)
+        out = _new(s, x.shape, x.dtype, zero=n_rows is not None)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out: x's shape and type expected")
     rot, lay, n_pos = _table(table, layout)
@@ -415,8 +426,7 @@ def kv_read(pages, block_table, pos, T, n_rows=None, k_exp=0, v_exp=0, dtype=tor
     desc = _kv_desc(pages, block_table, B, k_exp, v_exp)
     shape = (B, T, desc.n_kv, desc.d_h)
     if k_out is None:
-        with torch.cuda.stream(s):
-            k_out, v_out = (torch.zeros(shape, dtype=dtype, device=pages.device) for _ in range(2))
+        k_out, v_out = (_new(s, shape, dtype, zero=True) for _ in range(2))
     elif tuple(k_out.shape) != shape or tuple(v_out.shape) != shape or v_out.dtype != k_out.dtype:
         raise ValueError(f"k_out, v_out: {list(shape)} of one type expected")
     a = KvReadArgs(desc, B, T, _dtype(k_out, "k_out"), k_out.data_ptr(), _row_stride(k_out, "k_out"), v_out.data_ptr(),
@@ -424,6 +434,46 @@ def kv_read(pages, block_table, pos, T, n_rows=None, k_exp=0, v_exp=0, dtype=tor
                    _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_kv_read(ctypes.byref(a), s.cuda_stream), "dlite_kv_read")
     return k_out, v_out
+
+
+def kv_attention(q, pages, block_table, pos, scale=None, window=0, n_rows=None, k_exp=0, v_exp=0, out=None, lse=None,
+                 workspace=None, status=None, stream=None):
+    """Attention of q [B, T, n_q, d_h] (rows at positions pos[b] + t, their keys already
+    appended) over the cache (dlite_kv_attention); scale None: d_h^-1/2. lse: None (not wanted), True (a new
+    tensor) or float32 [B, T, n_q]. workspace: None (a new one for this call) or a uint8 tensor of at least
+    kv_attention_workspace(...) bytes. Returns (out, lse); rows t >= n_rows[b] are left as
+    they were (zeros in new outputs)."""
+    lib = load()
+    s = _here(stream, q, pages, block_table, pos, n_rows, out, None if lse is True else lse, workspace, status)
+    qs = _row_stride(q, "q")
+    B, T, H, d = q.shape
+    desc = _kv_desc(pages, block_table, B, k_exp, v_exp)
+    if d != desc.d_h:
+        raise ValueError(f"q: heads of {desc.d_h} columns expected")
+    if out is None:
+        out = _new(s, q.shape, q.dtype, zero=n_rows is not None)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out: q's shape and type expected")
+    if lse is True:
+        lse = _new(s, (B, T, H), torch.float32, zero=n_rows is not None)
+    a = KvAttentionArgs(desc, B, T, H, _dtype(q, "q"), window, d ** -0.5 if scale is None else scale, q.data_ptr(), qs,
+                        out.data_ptr(), _row_stride(out, "out"), _vec(lse, torch.float32, (B, T, H), "lse"),
+                        _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"), None, 0,
+                        _vec(status, torch.int32, (1,), "status"))
+    need = lib.dlite_kv_attention_workspace(ctypes.byref(a))
+    if need:
+        if workspace is None:
+            workspace = _new(s, (need,), torch.uint8)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.dlite_kv_attention(ctypes.byref(a), s.cuda_stream), "dlite_kv_attention")
+    return out, lse
+
+
+def kv_attention_workspace(B, T, n_q, n_kv, d_h, max_pages, dtype=torch.bfloat16):
+    """Bytes of workspace a kv_attention call of these sizes needs on the current device (0: none)."""
+    a = KvAttentionArgs(KvCacheDesc(16, 16, 1, n_kv, d_h, max_pages, 0, 0), B, T, n_q, _DTYPES[dtype], 0, 1.0, 16, n_q * d_h,
+                        16, n_q * d_h, None, 16, None, None, 0, None)
+    return load().dlite_kv_attention_workspace(ctypes.byref(a))
 
 
 def config_struct(cfg, B_max):

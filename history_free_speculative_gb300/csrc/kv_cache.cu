@@ -283,17 +283,6 @@ __global__ void __launch_bounds__(256) kv_read_kernel(ReadArgs a, bool vec) {
   }
 }
 
-// Host checks shared by the cache's calls.
-int check_cache(const dlite_kv_cache& c, int B, int T, const int64_t* pos) {
-  if (!c.pages || !c.block_table || !pos) return DLITE_ERR_INVALID_ARG;
-  if (((uintptr_t)c.pages & 15) || ((uintptr_t)c.block_table & 3) || ((uintptr_t)pos & 7)) return DLITE_ERR_INVALID_ARG;
-  if (B < 1 || T < 1 || c.n_pages < 1 || c.n_kv < 1 || c.max_pages < 1) return DLITE_ERR_INVALID_ARG;
-  if (c.k_exp < -64 || c.k_exp > 64 || c.v_exp < -64 || c.v_exp > 64) return DLITE_ERR_INVALID_ARG;
-  if ((c.d_h != 64 && c.d_h != 128) || c.n_kv > 65535 || B > 65535 || c.max_pages >= (1 << 25) || T >= (1 << 30))
-    return DLITE_ERR_UNSUPPORTED_SHAPE;
-  return DLITE_OK;
-}
-
 // CTAs along the pages: as many as T rows can touch from any first position
 inline unsigned touched_pages(int T) { return (unsigned)((T + 2 * kv::kPage - 2) / kv::kPage); }
 // Threads: 256 once a page holds more items than 128 threads take in a turn
@@ -306,7 +295,7 @@ extern "C" int dlite_kv_append(const dlite_kv_append_args* g, dlite_stream_t str
   using namespace dlite;
   if (!g || !g->k || !g->v) return DLITE_ERR_INVALID_ARG;
   const dlite_kv_cache& c = g->cache;
-  if (const int rc = check_cache(c, g->B, g->T, g->pos)) return rc;
+  if (const int rc = kv::check_cache(c, g->B, g->T, g->pos)) return rc;
   if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
   const int es = g->dtype == DLITE_F32 ? 4 : 2;
   const long long cols = (long long)c.n_kv * c.d_h;
@@ -355,7 +344,7 @@ extern "C" int dlite_kv_read(const dlite_kv_read_args* g, dlite_stream_t stream)
   using namespace dlite;
   if (!g || !g->k_out || !g->v_out) return DLITE_ERR_INVALID_ARG;
   const dlite_kv_cache& c = g->cache;
-  if (const int rc = check_cache(c, g->B, g->T, g->pos)) return rc;
+  if (const int rc = kv::check_cache(c, g->B, g->T, g->pos)) return rc;
   if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
   const int es = g->dtype == DLITE_F32 ? 4 : 2, V = 16 / es;
   const long long cols = (long long)c.n_kv * c.d_h;

@@ -526,6 +526,42 @@ typedef struct {
 } dlite_kv_read_args;
 int dlite_kv_read(const dlite_kv_read_args *args, dlite_stream_t stream);
 
+/* Attention of the T rows of each request over the cache, grouped queries: query
+ * head i reads KV head i / (n_q / n_kv). Row t of request b sees key j iff
+ *   max(0, pos[b] + t - window + 1) <= j <= pos[b] + t   (window 0: from key 0 on)
+ * and j lies below 64 max_pages in a page whose id is in [0, n_pages): the rows' own
+ * keys (positions pos[b] .. pos[b] + T - 1) are appended before this call, and a
+ * negative page id is a hole (an evicted page). Then
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  lse = ln sum_j p_j,
+ * with float32 scores, statistics and sums. A row that sees no key gets zeros and
+ * lse = -inf; a row whose query holds a NaN or infinity gets NaN. An id >= n_pages or a block
+ * past the cache's end flags DLITE_DEV_BOUNDS. Rows of other requests and of
+ * tokens not yet appended never reach a result, whatever their bytes hold.
+ * workspace: device memory of at least dlite_kv_attention_workspace(args) bytes, 16-byte
+ * aligned (NULL if that is 0), written and read by this call alone: calls that may overlap
+ * (other streams, captured graphs) need one each. The need depends on B, T, n_q,
+ * the cache's n_kv, d_h and max_pages and the device's SM count only. */
+typedef struct {
+    dlite_kv_cache cache;
+    int B, T;
+    int n_q;              /* a multiple of n_kv; n_q / n_kv * T <= 2^20 */
+    int dtype;            /* of q and out */
+    int window;           /* >= 0 */
+    float scale;          /* > 0, finite */
+    const void *q;        /* [B, T, n_q, d_h] */
+    int64_t q_stride;
+    void *out;            /* [B, T, n_q, d_h] */
+    int64_t out_stride;
+    float *lse;           /* [B, T, n_q] dense, or NULL */
+    const int64_t *pos;   /* [B] */
+    const int32_t *n_rows;
+    void *workspace;
+    size_t workspace_bytes;
+    int *status;
+} dlite_kv_attention_args;
+size_t dlite_kv_attention_workspace(const dlite_kv_attention_args *args); /* 0 also for invalid args */
+int dlite_kv_attention(const dlite_kv_attention_args *args, dlite_stream_t stream);
+
 /* Read (and with clear != 0, reset) the sticky device status word.
  * Synchronises `stream`. *status_out gets DLITE_DEV_* bits. Returns
  * DLITE_ERR_DEVICE_TIMEOUT or DLITE_ERR_BOUNDS when those bits are set. */

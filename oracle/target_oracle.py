@@ -167,3 +167,57 @@ def append(pages, block_table, k, v, pos, table=None, layout="half", n_rows=None
                              k_exp, v_exp):
                     flags.add("nonfinite")
     return flags
+
+
+# ---------------------------------------------------------------- attention
+
+def read_record(rec, k_exp, v_exp):
+    """(keys, values) float64 [64, d] of a record."""
+    kd, vd, ks, vs = rec_parts(rec)
+    d = vd.shape[0]
+    kc, vc = np.empty((64, d), dtype=np.uint8), np.empty((64, d), dtype=np.uint8)
+    kc[:, 0::2], kc[:, 1::2] = kd & 15, kd >> 4
+    vc[0::2], vc[1::2] = vd.T & 15, vd.T >> 4
+    sc = np.append(E4M3, np.nan)      # 0x7f, and every byte with the sign bit, is not a scale
+    pick = lambda b: sc[np.minimum(b, 0x7F)]  # noqa: E731
+    val = lambda c, s: np.where(c & 8, -1.0, 1.0) * E2M1[c & 7] * np.repeat(s, 16, axis=1)  # noqa: E731
+    return val(kc, pick(ks)) * 2.0 ** k_exp, val(vc, pick(vs.T)) * 2.0 ** v_exp
+
+
+def attention(q, pages, block_table, pos, scale, window=0, n_rows=None, k_exp=0, v_exp=0, out=None, lse=None):
+    """q [B, T, n_q, d]. Returns (out, lse, reach, eps): reach = sum p |v| / sum p bounds how far weights off by a
+    relative amount move an output; eps = the largest scale sum |q| |k| of a row, the size of a score's terms."""
+    B, T, nq, d = q.shape
+    nkv = pages.shape[1]
+    out = np.zeros((B, T, nq, d)) if out is None else np.array(out, dtype=np.float64)
+    lse = np.zeros((B, T, nq)) if lse is None else np.array(lse, dtype=np.float64)
+    reach, eps = np.zeros((B, T, nq, d)), np.zeros((B, T, nq))
+    for b in range(B):
+        n = T if n_rows is None else min(max(int(n_rows[b]), 0), T)
+        last = min(max(int(pos[b]) + n, 0), block_table.shape[1] * PAGE)
+        ids = block_table[b, :(last + PAGE - 1) // PAGE]
+        for h in range(nkv if n else 0):
+            ks, vs, js = [np.zeros((0, d))], [np.zeros((0, d))], [np.zeros(0, dtype=np.int64)]
+            for i, pid in enumerate(ids):
+                if 0 <= pid < len(pages):
+                    k, v = read_record(pages[pid, h], k_exp, v_exp)
+                    ks.append(k), vs.append(v), js.append(i * PAGE + np.arange(PAGE))
+            k, v, j = np.concatenate(ks), np.concatenate(vs), np.concatenate(js)
+            for t in range(n):
+                p = int(pos[b]) + t
+                see = (j <= p) & (j < block_table.shape[1] * PAGE)
+                if window:
+                    see &= j > p - window
+                for i in range(h * (nq // nkv), (h + 1) * (nq // nkv)):
+                    qq = q[b, t, i].astype(np.float64)
+                    if not see.any():
+                        out[b, t, i], lse[b, t, i] = 0, -np.inf
+                        continue
+                    s = scale * (k[see] @ qq)
+                    m = s.max()
+                    w = np.exp(s - m)
+                    lse[b, t, i] = m + np.log(w.sum())
+                    out[b, t, i] = (w[:, None] * v[see]).sum(0) / w.sum()
+                    reach[b, t, i] = (w[:, None] * np.abs(v[see])).sum(0) / w.sum()
+                    eps[b, t, i] = scale * (np.abs(k[see]) @ np.abs(qq)).max()
+    return out, lse, reach, eps

@@ -125,3 +125,40 @@ def test_append_places_rows_by_the_table():
         kk, vv = TO.read_row(pages[page, 1], row, 0, 0)
         assert np.abs(kk - k[b, t, 1]).max() < 0.18 * np.abs(k[b, t, 1]).max() and np.abs(vv - v[b, t, 1]).max() < 0.18 * np.abs(v[b, t, 1]).max()
     assert not pages[2].any() and not pages[3].any() and not pages[5].any()
+
+
+def test_attention_is_torchs_on_the_decoded_cache():
+    rng = np.random.default_rng(11)
+    B, T, nq, nkv, d = 2, 3, 4, 2, 64
+    pages = rng.integers(0, 256, (7, nkv, 72 * d), dtype=np.uint8)
+    pages[..., 64 * d:] = 0x28 + pages[..., 64 * d:] % 24
+    bt = np.array([[3, 0, 5], [1, 6, 2]])
+    pos, q = [100, 130], rng.normal(size=(B, T, nq, d)) * 0.2
+    out, lse, reach, eps = TO.attention(q, pages, bt, pos, 0.125, k_exp=1, v_exp=-1)
+    win = TO.attention(q, pages, bt, pos, 0.125, window=40, k_exp=1, v_exp=-1)[0]
+    for b in range(B):
+        for h in range(nkv):
+            kk, vv = (np.concatenate([TO.read_record(pages[i, h], 1, -1)[w] for i in bt[b]]) for w in (0, 1))
+            r, rv = TO.read_row(pages[bt[b, 1], h], 9, 1, -1)
+            assert np.array_equal(kk[73], r) and np.array_equal(vv[73], rv)
+            key, row = torch.arange(192), pos[b] + torch.arange(T)[:, None]
+            for mask, got in ((key <= row, out), ((key <= row) & (key > row - 40), win)):
+                want = torch.nn.functional.scaled_dot_product_attention(
+                    torch.from_numpy(q[b, :, 2 * h:2 * h + 2]).transpose(0, 1), torch.from_numpy(kk).expand(2, -1, -1),
+                    torch.from_numpy(vv).expand(2, -1, -1), attn_mask=mask, scale=0.125)
+                assert np.abs(got[b, :, 2 * h:2 * h + 2] - want.transpose(0, 1).numpy()).max() < 1e-10
+            s = 0.125 * torch.from_numpy(q[b, 1, 2 * h] @ kk.T)
+            assert math.isclose(float(torch.logsumexp(s[:pos[b] + 2], 0)), lse[b, 1, 2 * h], rel_tol=1e-12)
+    assert (reach >= np.abs(out) - 1e-12).all() and (eps > 0).all()
+
+
+def test_attention_holes_and_empty_rows():
+    rng = np.random.default_rng(12)
+    pages = rng.integers(0, 0x70, (3, 1, 72 * 64), dtype=np.uint8)
+    q = rng.normal(size=(3, 2, 1, 64)) * 0.05
+    bt = np.array([[0, 1], [-1, 1], [-1, 7]])
+    out, lse, _, _ = TO.attention(q, pages, bt, [80, 63, 100], 0.1, n_rows=[1, 2, 2], out=np.full(q.shape, 5.0), lse=np.full((3, 2, 1), 5.0))
+    assert (out[0, 1] == 5).all() and lse[0, 1] == 5                 # a row behind the last valid one
+    assert not out[1, 0].any() and lse[1, 0] == -np.inf               # keys 0..63 lie in a hole
+    assert np.allclose(out[1, 1], TO.read_row(pages[1, 0], 0, 0, 0)[1])   # one key left
+    assert not out[2].any() and (lse[2] == -np.inf).all()
