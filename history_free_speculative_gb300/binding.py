@@ -112,6 +112,13 @@ class KvAttentionArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)]
 
 
+class LogprobsArgs(ctypes.Structure):
+    """dlite_logprobs_args."""
+    _fields_ = [(n, ctypes.c_int) for n in ("rows", "V", "n_top", "dtype")] + \
+               [("temperature", ctypes.c_float), ("logits", ctypes.c_void_p), ("stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_void_p) for n in ("tokens", "logprob", "entropy", "top_ids", "top_logprobs", "status")]
+
+
 class Taps(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("z", "x", "b", "hs")]
 
@@ -148,6 +155,7 @@ _SIGS = {
     "dlite_kv_read": (_I, [ctypes.POINTER(KvReadArgs), _P]),
     "dlite_kv_attention_workspace": (ctypes.c_size_t, [ctypes.POINTER(KvAttentionArgs)]),
     "dlite_kv_attention": (_I, [ctypes.POINTER(KvAttentionArgs), _P]),
+    "dlite_token_logprobs": (_I, [ctypes.POINTER(LogprobsArgs), _P]),
     "dlite_selftest_wait": (_I, [_P, _U64, _P, _P]),
     "dlite_device_status": (_I, [_P, _I, ctypes.POINTER(_I), _P]),
     "dlite_status_string": (ctypes.c_char_p, [_I]),
@@ -474,6 +482,39 @@ def kv_attention_workspace(B, T, n_q, n_kv, d_h, max_pages, dtype=torch.bfloat16
     a = KvAttentionArgs(KvCacheDesc(16, 16, 1, n_kv, d_h, max_pages, 0, 0), B, T, n_q, _DTYPES[dtype], 0, 1.0, 16, n_q * d_h,
                         16, n_q * d_h, None, 16, None, None, 0, None)
     return load().dlite_kv_attention_workspace(ctypes.byref(a))
+
+
+def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entropy=None, top_ids=None, top_logprobs=None,
+                   status=None, stream=None):
+    """ln softmax(logits / temperature) of one token per row, the row's entropy and its n_top most
+    likely alternatives (dlite_token_logprobs). logits [..., V] with dense, evenly spaced rows, tokens int32
+    of the leading shape. Rows whose token is negative are not read: zeros, ids -1.
+    Returns dict(logprob, entropy [...] float32, top_ids [..., n_top] int32, top_logprobs [..., n_top] float32)."""
+    lib = load()
+    s = _here(stream, logits, tokens, logprob, entropy, top_ids, top_logprobs, status)
+    if logits.dim() < 1 or logits.shape[:-1] != tokens.shape:
+        raise ValueError("logits [..., V] and tokens of the leading shape expected")
+    lead, V = tuple(tokens.shape), logits.shape[-1]
+    rows = tokens.numel()
+    if V > 1 and logits.stride(-1) != 1:
+        raise ValueError("logits: the ids of a row have to be dense")
+    stride, span = V, None
+    for n, st in reversed(list(zip(lead, logits.stride()))):
+        if n > 1:
+            if span is None:
+                stride = st
+            elif st != span:
+                raise ValueError("logits: rows have to be evenly spaced")
+            span = st * n
+    n_top = int(n_top)
+    want = ((logprob, lead, torch.float32), (entropy, lead, torch.float32), (top_ids, lead + (max(n_top, 0),), torch.int32),
+            (top_logprobs, lead + (max(n_top, 0),), torch.float32))
+    got = [_new(s, shape, dt) if t is None else t for t, shape, dt in want]
+    ptr = [_vec(t, dt, shape, "output") for t, (_, shape, dt) in zip(got, want)]
+    a = LogprobsArgs(rows, V, n_top, _dtype(logits, "logits"), temperature, logits.data_ptr(), stride,
+                     _vec(tokens, torch.int32, lead, "tokens"), *ptr, _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_token_logprobs(ctypes.byref(a), s.cuda_stream), "dlite_token_logprobs")
+    return dict(zip(("logprob", "entropy", "top_ids", "top_logprobs"), got))
 
 
 def config_struct(cfg, B_max):

@@ -562,6 +562,33 @@ typedef struct {
 size_t dlite_kv_attention_workspace(const dlite_kv_attention_args *args); /* 0 also for invalid args */
 int dlite_kv_attention(const dlite_kv_attention_args *args, dlite_stream_t stream);
 
+/* Log probabilities of given tokens under softmax(logits / temperature), with the
+ * entropy and the most likely alternatives of their rows (e.g. the committed tokens of
+ * a round against the target's rows: tokens = commits [B, K+1], whose entries past the
+ * acceptance are -1). Row r with tokens[r] < 0 is not read; it gets zeros and the ids -1.
+ *   logprob [rows]              ln p(tokens[r]); an id >= V gives NaN and flags DLITE_DEV_BOUNDS
+ *   entropy [rows]              -sum p ln p
+ *   top_ids, top_logprobs [rows, n_top]   the n_top largest logits in descending order, the lower
+ *                               id first among equals (-0 = +0)
+ * logprob and entropy may be NULL. A logit of -inf is an impossible token (ln p = -inf, no
+ * part in the entropy); a row of -inf alone gives ln p = -inf and entropy 0. A row with a
+ * NaN or +inf gives NaN; its alternatives rank NaN as -inf. Sums are float32. */
+#define DLITE_MAX_TOP 32
+typedef struct {
+    int rows, V;          /* V up to 2^30 */
+    int n_top;            /* 0..min(V, DLITE_MAX_TOP) */
+    int dtype;            /* of logits */
+    float temperature;    /* > 0, finite */
+    const void *logits;   /* [rows, V] */
+    int64_t stride;       /* elements between rows, >= V */
+    const int32_t *tokens; /* [rows] */
+    float *logprob, *entropy;
+    int32_t *top_ids;
+    float *top_logprobs;
+    int *status;
+} dlite_logprobs_args;
+int dlite_token_logprobs(const dlite_logprobs_args *args, dlite_stream_t stream);
+
 /* Read (and with clear != 0, reset) the sticky device status word.
  * Synchronises `stream`. *status_out gets DLITE_DEV_* bits. Returns
  * DLITE_ERR_DEVICE_TIMEOUT or DLITE_ERR_BOUNDS when those bits are set. */

@@ -221,3 +221,23 @@ def attention(q, pages, block_table, pos, scale, window=0, n_rows=None, k_exp=0,
                     reach[b, t, i] = (w[:, None] * np.abs(v[see])).sum(0) / w.sum()
                     eps[b, t, i] = scale * (np.abs(k[see]) @ np.abs(qq)).max()
     return out, lse, reach, eps
+
+
+# ---------------------------------------------------------------- token log probabilities
+
+def token_logprobs(x, token, temperature=1.0, n_top=0):
+    """(ln p(token), entropy, top ids, their ln p) of one row of logits."""
+    x = np.asarray(x, dtype=np.float64)
+    order = np.lexsort((np.arange(len(x)), -np.where(np.isnan(x), -np.inf, x)))[:n_top]
+    if np.isnan(x).any() or (x == np.inf).any():
+        return np.nan, np.nan, order, np.full(n_top, np.nan)
+    m = x.max()
+    if m == -np.inf:
+        return -np.inf if token < len(x) else np.nan, 0.0, order, np.full(n_top, -np.inf)
+    d = (m - x) / temperature
+    e = np.exp(-d)
+    others = np.sort(np.delete(e, x.argmax()))     # S - 1, small terms first
+    lp = -d - np.log1p(others.sum())
+    p = np.exp(lp)
+    h = -np.sum(np.where(p > 0, p * np.where(p > 0, lp, 0), 0))
+    return lp[token] if token < len(x) else np.nan, h, order, lp[order]

@@ -270,3 +270,31 @@ def test_append_token_by_token_equals_a_prompt():
             graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(whole, single)
+
+
+def test_the_binding_refuses_what_it_does_not_take():
+    x, pos, table = _rows((2, 3, 2, 64), "f32", 1), torch.zeros(2, dtype=torch.int64, device=DEV), binding.rope_table(8, 64)
+    pages, bt = binding.kv_pages(4, 2, 64), torch.zeros(2, 2, dtype=torch.int32, device=DEV)
+    V = ValueError
+    for err, call in [
+            (V, lambda: binding.rope(x, pos.int(), table)), (V, lambda: binding.rope(x, pos[:1], table)),
+            (V, lambda: binding.rope(x.half(), pos, table)), (V, lambda: binding.rope(x, pos, table, layout="pairs")),
+            (V, lambda: binding.rope(x, pos, table.double())), (V, lambda: binding.rope(x, pos, table, out=x[:1])),
+            (V, lambda: binding.rope(x, pos, table, n_rows=pos)), (V, lambda: binding.rope(x.transpose(1, 2), pos, table)),
+            (V, lambda: binding.rope(x, pos, table, status=torch.zeros(2, dtype=torch.int32, device=DEV))),
+            (V, lambda: binding.rope_table(8, 64, scaling="other")), (binding.DliteError, lambda: binding.rope_table(0, 64)),
+            (binding.DliteError, lambda: binding.rope(x[..., :32].contiguous(), pos, table)),
+            (V, lambda: binding.kv_append(pages, bt, x, x[:, :, :1], pos)), (V, lambda: binding.kv_append(pages, bt.long(), x, x, pos)),
+            (V, lambda: binding.kv_append(pages[:, :1], bt, x, x, pos)), (V, lambda: binding.kv_append(pages, bt[:1], x, x, pos)),
+            (V, lambda: binding.kv_append(pages, bt, x, x.bfloat16(), pos)), (V, lambda: binding.kv_append(pages.int(), bt, x, x, pos)),
+            (V, lambda: binding.kv_read(pages, bt, pos, 1, k_out=x)), (V, lambda: binding.kv_read(pages, bt, pos, 2, k_out=x, v_out=x)),
+            (V, lambda: binding.kv_attention(x[..., :32], pages, bt, pos)), (V, lambda: binding.kv_attention(x, pages, bt, pos, lse=pos)),
+            (V, lambda: binding.kv_attention(x, pages, bt, pos, out=x.bfloat16())),
+            (binding.DliteError, lambda: binding.kv_attention(x[:, :, :1], pages, bt, pos)),
+            (binding.DliteError, lambda: binding.kv_attention(x, pages, bt, pos, scale=-1.0)),
+            (V, lambda: binding.token_logprobs(x, bt)), (V, lambda: binding.token_logprobs(x[0, 0], pos)),
+            (V, lambda: binding.token_logprobs(x[0, 0].half(), bt[0])), (V, lambda: binding.token_logprobs(x[0, 0].t().contiguous().t(), bt[0])),
+            (binding.DliteError, lambda: binding.token_logprobs(x[0, 0], bt[0], temperature=0.0)),
+            (binding.DliteError, lambda: binding.token_logprobs(x[0, 0], bt[0], n_top=33))]:
+        with pytest.raises(err):
+            call()

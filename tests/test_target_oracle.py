@@ -162,3 +162,23 @@ def test_attention_holes_and_empty_rows():
     assert not out[1, 0].any() and lse[1, 0] == -np.inf               # keys 0..63 lie in a hole
     assert np.allclose(out[1, 1], TO.read_row(pages[1, 0], 0, 0, 0)[1])   # one key left
     assert not out[2].any() and (lse[2] == -np.inf).all()
+
+
+def test_logprobs_are_torchs():
+    rng = np.random.default_rng(15)
+    x = rng.normal(size=500) * 3
+    x[7], x[100:110] = x[3], -np.inf
+    for T in (1.0, 0.7):
+        lp = torch.log_softmax(torch.from_numpy(x) / T, 0)
+        got, h, ids, top = TO.token_logprobs(x, 42, T, 6)
+        assert math.isclose(got, float(lp[42]), rel_tol=1e-13)
+        assert math.isclose(h, float(torch.distributions.Categorical(logits=torch.from_numpy(x[np.isfinite(x)]) / T).entropy()), rel_tol=1e-12)
+        want = torch.from_numpy(x).sort(descending=True, stable=True).indices[:6]
+        assert np.array_equal(ids, want.numpy()) and np.allclose(top, lp[want].numpy())
+    assert TO.token_logprobs(x, 100)[0] == -np.inf and np.isnan(TO.token_logprobs(x, 500)[0])
+    # a near-certain row: H = sum q (1 + ln 1/q ...) for one other token of probability q
+    q = 1e-9
+    h = TO.token_logprobs(np.array([0.0, math.log(q)]), 0)[1]
+    assert math.isclose(h, q * (1 - math.log(q)), rel_tol=1e-6)
+    lp, h, ids, top = TO.token_logprobs(np.full(4, -np.inf), 1, 1.0, 2)
+    assert lp == -np.inf and h == 0 and list(ids) == [0, 1] and (top == -np.inf).all()
