@@ -295,19 +295,20 @@ def _dtype(t, what):
 
 
 def _here(stream, *tensors):
-    """The stream to launch on; every tensor has to be on the current CUDA device."""
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("device tensor expected")
+    """(pointer, stream or None) of the stream to launch on: None for the current one. Every tensor
+    has to be on the current CUDA device."""
+    if tensors and tensors[0].get_device() < 0:
+        raise ValueError("device tensor expected")
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, current device cuda:{dev}")
-    if stream is None:
-        return torch.cuda.current_stream()
+            raise ValueError(f"tensor on {t.device}, current device cuda:{dev}")
+    cur = torch._C._cuda_getCurrentRawStream(dev)   # torch.cuda.current_stream().cuda_stream without the Stream object
+    if stream is None or (stream.cuda_stream == cur and stream.device.index == dev):
+        return cur, None
     if stream.device.index != dev:
         raise ValueError(f"stream on {stream.device}, current device cuda:{dev}")
-    return stream
+    return stream.cuda_stream, stream
 
 
 def _vec(t, dtype, shape, what):
@@ -338,7 +339,7 @@ def _row_stride(t, what):
 def _new(stream, shape, dtype, zero=False):
     """A new tensor that belongs to the stream it is written on (zeros where a call leaves rows out)."""
     make = torch.zeros if zero else torch.empty
-    if stream == torch.cuda.current_stream():
+    if stream is None:
         return make(shape, dtype=dtype, device="cuda")
     with torch.cuda.stream(stream):
         return make(shape, dtype=dtype, device="cuda")
@@ -351,10 +352,10 @@ def rope_table(n_pos, rot, theta=1e6, scaling="plain", factor=1.0, orig_len=0.0,
     lib = load()
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling: one of {sorted(ROPE_SCALINGS)} expected")
-    s = _here(stream)
+    ptr, s = _here(stream)
     table = _new(s, (max(int(n_pos), 0), max(int(rot), 0) // 2, 2), torch.float32)
     cfg = RopeConfig(int(rot), ROPE_SCALINGS[scaling], theta, factor, orig_len, beta_fast, beta_slow, attn_factor)
-    _check(lib.dlite_rope_table(ctypes.byref(cfg), int(n_pos), table.data_ptr() or None, s.cuda_stream), "dlite_rope_table")
+    _check(lib.dlite_rope_table(ctypes.byref(cfg), int(n_pos), table.data_ptr() or None, ptr), "dlite_rope_table")
     return table
 
 
@@ -372,7 +373,7 @@ def rope(x, pos, table, layout="half", n_rows=None, out=None, status=None, strea
     position pos[b] + t (dlite_rope). out: None (a new tensor), x itself, or another tensor of
     x's shape; rows t >= n_rows[b] of it are left as they were (zeros in a new one). Returns out."""
     lib = load()
-    s = _here(stream, x, pos, table, n_rows, out, status)
+    ptr, s = _here(stream, x, pos, table, n_rows, out, status)
     xs = _row_stride(x, "x")
     B, T, H, d = x.shape
     if out is None:
@@ -383,7 +384,7 @@ def rope(x, pos, table, layout="half", n_rows=None, out=None, status=None, strea
     a = RopeArgs(B, T, H, d, rot, lay, _dtype(x, "x"), n_pos, x.data_ptr(), xs, out.data_ptr(), _row_stride(out, "out"),
                  _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"), table.data_ptr(),
                  _vec(status, torch.int32, (1,), "status"))
-    _check(lib.dlite_rope(ctypes.byref(a), s.cuda_stream), "dlite_rope")
+    _check(lib.dlite_rope(ctypes.byref(a), ptr), "dlite_rope")
     return out
 
 
@@ -409,7 +410,7 @@ def kv_append(pages, block_table, k, v, pos, table=None, layout="half", n_rows=N
     """Append k, v [B, T, n_kv, d_h] to the cache at positions pos[b] + t, the keys rotated on
     the way when a rope_table is given (dlite_kv_append). block_table is int32 [B, max_pages]."""
     lib = load()
-    s = _here(stream, pages, block_table, k, v, pos, table, n_rows, status)
+    ptr, s = _here(stream, pages, block_table, k, v, pos, table, n_rows, status)
     ks, vs = _row_stride(k, "k"), _row_stride(v, "v")
     B, T, H, d = k.shape
     desc = _kv_desc(pages, block_table, B, k_exp, v_exp)
@@ -419,7 +420,7 @@ def kv_append(pages, block_table, k, v, pos, table=None, layout="half", n_rows=N
     a = KvAppendArgs(desc, B, T, _dtype(k, "k"), rot, lay, n_pos, k.data_ptr(), ks, v.data_ptr(), vs,
                      _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"),
                      table.data_ptr() if table is not None else None, _vec(status, torch.int32, (1,), "status"))
-    _check(lib.dlite_kv_append(ctypes.byref(a), s.cuda_stream), "dlite_kv_append")
+    _check(lib.dlite_kv_append(ctypes.byref(a), ptr), "dlite_kv_append")
 
 
 def kv_read(pages, block_table, pos, T, n_rows=None, k_exp=0, v_exp=0, dtype=torch.bfloat16, k_out=None, v_out=None,
@@ -427,7 +428,7 @@ def kv_read(pages, block_table, pos, T, n_rows=None, k_exp=0, v_exp=0, dtype=tor
     """The values the cache holds at positions pos[b] + t, t < T: (k, v) [B, T, n_kv, d_h]
     (dlite_kv_read). New outputs start as zeros where rows are not read."""
     lib = load()
-    s = _here(stream, pages, block_table, pos, n_rows, k_out, v_out, status)
+    ptr, s = _here(stream, pages, block_table, pos, n_rows, k_out, v_out, status)
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out: both or neither expected")
     B = block_table.shape[0]
@@ -440,7 +441,7 @@ def kv_read(pages, block_table, pos, T, n_rows=None, k_exp=0, v_exp=0, dtype=tor
     a = KvReadArgs(desc, B, T, _dtype(k_out, "k_out"), k_out.data_ptr(), _row_stride(k_out, "k_out"), v_out.data_ptr(),
                    _row_stride(v_out, "v_out"), _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"),
                    _vec(status, torch.int32, (1,), "status"))
-    _check(lib.dlite_kv_read(ctypes.byref(a), s.cuda_stream), "dlite_kv_read")
+    _check(lib.dlite_kv_read(ctypes.byref(a), ptr), "dlite_kv_read")
     return k_out, v_out
 
 
@@ -452,7 +453,7 @@ def kv_attention(q, pages, block_table, pos, scale=None, window=0, n_rows=None, 
     kv_attention_workspace(...) bytes. Returns (out, lse); rows t >= n_rows[b] are left as
     they were (zeros in new outputs)."""
     lib = load()
-    s = _here(stream, q, pages, block_table, pos, n_rows, out, None if lse is True else lse, workspace, status)
+    ptr, s = _here(stream, q, pages, block_table, pos, n_rows, out, None if lse is True else lse, workspace, status)
     qs = _row_stride(q, "q")
     B, T, H, d = q.shape
     desc = _kv_desc(pages, block_table, B, k_exp, v_exp)
@@ -473,7 +474,7 @@ def kv_attention(q, pages, block_table, pos, scale=None, window=0, n_rows=None, 
         if workspace is None:
             workspace = _new(s, (need,), torch.uint8)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib.dlite_kv_attention(ctypes.byref(a), s.cuda_stream), "dlite_kv_attention")
+    _check(lib.dlite_kv_attention(ctypes.byref(a), ptr), "dlite_kv_attention")
     return out, lse
 
 
@@ -491,7 +492,7 @@ def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entro
     of the leading shape. Rows whose token is negative are not read: zeros, ids -1.
     Returns dict(logprob, entropy [...] float32, top_ids [..., n_top] int32, top_logprobs [..., n_top] float32)."""
     lib = load()
-    s = _here(stream, logits, tokens, logprob, entropy, top_ids, top_logprobs, status)
+    ptr, s = _here(stream, logits, tokens, logprob, entropy, top_ids, top_logprobs, status)
     if logits.dim() < 1 or logits.shape[:-1] != tokens.shape:
         raise ValueError("logits [..., V] and tokens of the leading shape expected")
     lead, V = tuple(tokens.shape), logits.shape[-1]
@@ -510,10 +511,10 @@ def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entro
     want = ((logprob, lead, torch.float32), (entropy, lead, torch.float32), (top_ids, lead + (max(n_top, 0),), torch.int32),
             (top_logprobs, lead + (max(n_top, 0),), torch.float32))
     got = [_new(s, shape, dt) if t is None else t for t, shape, dt in want]
-    ptr = [_vec(t, dt, shape, "output") for t, (_, shape, dt) in zip(got, want)]
+    outs = [_vec(t, dt, shape, "output") for t, (_, shape, dt) in zip(got, want)]
     a = LogprobsArgs(rows, V, n_top, _dtype(logits, "logits"), temperature, logits.data_ptr(), stride,
-                     _vec(tokens, torch.int32, lead, "tokens"), *ptr, _vec(status, torch.int32, (1,), "status"))
-    _check(lib.dlite_token_logprobs(ctypes.byref(a), s.cuda_stream), "dlite_token_logprobs")
+                     _vec(tokens, torch.int32, lead, "tokens"), *outs, _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_token_logprobs(ctypes.byref(a), ptr), "dlite_token_logprobs")
     return dict(zip(("logprob", "entropy", "top_ids", "top_logprobs"), got))
 
 
