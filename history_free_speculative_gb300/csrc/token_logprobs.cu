@@ -7,12 +7,14 @@
 // a row that is nearly certain keeps its small entropy to full precision.
 //
 // A row is read by a cluster of CTAs (one when there are many rows), each a slice, each thread
-// every blockDim-th 16-byte piece of the slice, in four pieces in flight. A thread keeps
-// (m, n, s, w = sum e^-d d) online and the place of its largest element. The thread maxima,
-// as 64-bit keys (value, then lower id first, all distinct), give the alternatives: at most n_top
-// threads can own one, namely those with the n_top largest keys, and an alternative is never below
-// the n_top-th of those keys. Each warp takes some of those threads, reads their elements
-// again (L2) and keeps the best 32 across its lanes; a tournament over the warps, then one over the CTAs, ends it.
+// every blockDim-th 16-byte piece of the slice, four pieces in flight. A thread keeps
+// (m, n, s, w = sum e^-d d) online and the place of its largest element. Alternatives are ordered by 64-bit keys
+// (value, then lower id first), all distinct. The largest keys of 64 groups of threads give a floor: their n_top-th
+// is the key of an element that n_top - 1 others exceed, so no alternative lies below it. Only threads whose largest
+// key reaches the floor can own one; their elements are read again (L2), the few
+// that reach the floor are listed, and a key's place is the number of keys above it. (64 groups and
+// n_top = 20: about -64 ln(1 - 20 / 64) = 24 elements.) A list that would not fit, which takes
+// over a thousand large elements in the same few threads, is replaced by sorted merges.
 // Bound: HBM for many rows, a dependent chain of a few microseconds for a few.
 #include <math.h>
 
@@ -24,9 +26,9 @@
 namespace dlite {
 namespace {
 
-constexpr int kMaxTop = DLITE_MAX_TOP;
-constexpr int kThreads = 512;
-constexpr int kNW = kThreads / 32;
+constexpr int kGroups = 64;  // groups of threads behind the floor
+constexpr int kList = 1024;  // listed elements
+constexpr int kMaxCluster = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct LpArgs {
@@ -113,9 +115,10 @@ __device__ __forceinline__ void unpack(const uint4& w, float* v) {
   }
 }
 
-// Takes N elements with ids id0 .. id0 + N - 1 into the statistics; idx: id of the first largest.
-template <int N>
-__device__ __forceinline__ void take(const float (&v)[N], int id0, float k, Stat& st, int& idx) {
+// Takes the N elements of P pieces of E (ids id0 + p step + e) into the statistics; idx: id of the first largest.
+template <int P, int E>
+__device__ __forceinline__ void take(const float (&v)[P * E], int id0, int step, float k, Stat& st, int& idx) {
+  constexpr int N = P * E;
   float cm = v[0], cn = v[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) {
@@ -136,9 +139,17 @@ __device__ __forceinline__ void take(const float (&v)[N], int id0, float k, Stat
     st.m = cm;
 #pragma unroll
     for (int i = N - 1; i >= 0; --i)
-      if (v[i] == cm) idx = id0 + i;
+      if (v[i] == cm) idx = id0 + (i / E) * step + i % E;
   }
-  if (cm >= st.m || cn == -INFINITY) {  // the largest is among them, or an excluded id
+  float s = 0.f, w = 0.f;
+  if (cm < st.m && (st.m - cn) * k < 1e30f) {  // neither the largest is among them nor an excluded id
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float d = (st.m - v[i]) * k, e = tc::ex2_approx(-d);
+      s += e;
+      w = fmaf(e, d, w);
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (v[i] == -INFINITY) continue;
@@ -146,38 +157,33 @@ __device__ __forceinline__ void take(const float (&v)[N], int id0, float k, Stat
         st.n += 1.f;
         continue;
       }
-      const float d = (st.m - v[i]) * k;
-      const float e = tc::ex2_approx(-d);
-      st.s += e;
-      st.w += e * fminf(d, 1e30f);  // d may overflow where e = 0
-    }
-  } else {
-    float s = 0.f, w = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
       const float d = (st.m - v[i]) * k, e = tc::ex2_approx(-d);
       s += e;
-      w = fmaf(e, fminf(d, 1e30f), w);
+      w = fmaf(e, fminf(d, 1e30f), w);  // d may overflow where e = 0; a NaN e stays
     }
-    st.s += s;
-    st.w += w;
   }
+  st.s += s;
+  st.w += w;
 }
 
-__device__ __forceinline__ uint64_t ld_cluster_u64(const uint64_t* local, uint32_t rank) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(tc::map_to_rank(tc::su32(local), rank)) : "memory");
-  return v;
+// Store to the same shared-memory variable of CTA `rank` of the cluster.
+__device__ __forceinline__ void st_cluster_u64(uint64_t* local, uint32_t rank, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tc::map_to_rank(tc::su32(local), rank)), "l"(v) : "memory");
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LpArgs a, int C) {
-  constexpr int E = 16 / sizeof(T);
-  __shared__ uint64_t lists[kNW * 32];   // sorted keys of the warps
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
+  constexpr int E = 16 / sizeof(T), NW = NT / 32, GS = NT / kGroups;
+  static_assert(kList >= NT, "the merges' lists share the list's memory");
+  __shared__ uint64_t list[kList];       // elements that reach the floor
+  __shared__ uint64_t group_key[kGroups];
   __shared__ uint64_t result[32];        // this CTA's alternatives
-  __shared__ Stat stats[kNW];
-  __shared__ __align__(16) Stat cta_stat;
-  __shared__ int owners[kMaxTop];
+  __shared__ Stat stats[NW];
+  // of rank 0: what the CTAs of the cluster send
+  __shared__ uint64_t gather_key[kMaxCluster * 32];
+  __shared__ __align__(16) Stat gather_stat[kMaxCluster];
+  __shared__ uint16_t owner[NT];
+  __shared__ int n_owner, n_list;
   __shared__ uint64_t s_floor;
   pdl_trigger();
   pdl_wait();
@@ -195,40 +201,45 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LpArgs a
     }
     return;
   }
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // waited for before the first remote store
   const T* x = static_cast<const T*>(a.x) + row * a.stride;
   // elements before the first 16-byte border, whole pieces, the rest
   const int head = min(a.V, (int)(((16 - ((uintptr_t)x & 15)) & 15) / sizeof(T)));
   const int nv = (a.V - head) / E, tail = head + nv * E;
   const int v0 = (int)((long long)nv * rank / C), v1 = (int)((long long)nv * (rank + 1) / C);
   const uint4* body = reinterpret_cast<const uint4*>(x + head);
+  const bool has_head = rank == 0 && tid < head, has_tail = rank == C - 1 && tail + tid < a.V;
 
   Stat st = {-INFINITY, 0.f, 0.f, 0.f};
-  int idx = -1;
-  auto single = [&](int id) {
-    const float v[1] = {to_f32(x[id])};
-    if (idx < 0) idx = id;
-    take<1>(v, id, a.k, st, idx);
-  };
-  if (rank == 0 && tid < head) single(tid);
   int p = v0 + tid;
-  if (idx < 0 && p < v1) idx = head + p * E;
-  for (; p + 3 * kThreads < v1; p += 4 * kThreads) {
+  // the thread's first element, the lowest of its ids, stands for a thread without a larger one than -inf
+  int idx = has_head ? tid : p < v1 ? head + p * E : has_tail ? tail + tid : -1;
+  if (has_head) {
+    const float v[1] = {to_f32(x[tid])};
+    take<1, 1>(v, tid, 0, a.k, st, idx);
+  }
+  constexpr int P = 16 / E;  // pieces taken at once: 16 elements
+  for (; p + 3 * NT < v1; p += 4 * NT) {
     uint4 w[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) w[u] = __ldcs(body + p + u * kThreads);
+    for (int u = 0; u < 4; ++u) w[u] = __ldcs(body + p + u * NT);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float v[E];
-      unpack<T>(w[u], v);
-      take<E>(v, head + (p + u * kThreads) * E, a.k, st, idx);
+    for (int u = 0; u < 4; u += P) {
+      float v[P * E];
+#pragma unroll
+      for (int q = 0; q < P; ++q) unpack<T>(w[u + q], v + q * E);
+      take<P, E>(v, head + (p + u * NT) * E, NT * E, a.k, st, idx);
     }
   }
-  for (; p < v1; p += kThreads) {
+  for (; p < v1; p += NT) {
     float v[E];
     unpack<T>(__ldcs(body + p), v);
-    take<E>(v, head + p * E, a.k, st, idx);
+    take<1, E>(v, head + p * E, 0, a.k, st, idx);
   }
-  if (rank == C - 1 && tail + tid < a.V) single(tail + tid);
+  if (has_tail) {
+    const float v[1] = {to_f32(x[tail + tid])};
+    take<1, 1>(v, tail + tid, 0, a.k, st, idx);
+  }
 
   Stat all = st;
 #pragma unroll
@@ -241,100 +252,154 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LpArgs a
   if (lane == 0) stats[warp] = all;
 
   if (a.n_top) {
-    // the n_top threads with the largest keys, and the n_top-th of those keys
     const uint64_t mine = idx < 0 ? 0 : key_of(st.m, idx);
-    lists[tid] = warp_sort_desc(mine, lane);
-    __syncthreads();
-    if (warp == 0) {
-      const uint64_t best = warp_merge_lists(lists, kNW, lane);
-      const uint64_t fl = shfl64(best, a.n_top - 1);
-      if (lane == 0) s_floor = fl ? fl : 1;  // 0: fewer threads with elements than n_top
+    uint64_t gk = mine;
+#pragma unroll
+    for (int o = GS / 2; o > 0; o >>= 1) {
+      const uint64_t b = shfl64_xor(gk, o);
+      gk = b > gk ? b : gk;
     }
-    if (tid < kMaxTop) owners[tid] = -1;
+    if (tid % GS == 0) group_key[tid / GS] = gk;
+    if (tid == 0) {
+      s_floor = 1;  // fewer than n_top groups with elements: every element
+      n_owner = n_list = 0;
+    }
+    if (tid < 32) result[tid] = 0;
+    __syncthreads();
+    if (tid < kGroups) {
+      const uint64_t g = group_key[tid];
+      int above = 0;
+#pragma unroll 16
+      for (int i = 0; i < kGroups; ++i) above += group_key[i] > g;
+      if (g && above == a.n_top - 1) s_floor = g;
+    }
     __syncthreads();
     const uint64_t floor_key = s_floor;
-    // keys are distinct, so a thread's place among the winners is its key's rank
-    if (mine >= floor_key) {
-      int place = 0;
-      for (int w = 0; w < kNW; ++w)
-        for (int i = 0; i < a.n_top; ++i) {
-          if (lists[w * 32 + i] <= mine) break;
-          ++place;
-        }
-      owners[place] = tid;
-    }
+    if (mine >= floor_key) owner[atomicAdd(&n_owner, 1)] = (uint16_t)tid;
     __syncthreads();
-    uint64_t best = 0;
-    auto batch = [&](uint64_t key) {
-      if (key < floor_key) key = 0;
-      if (!__any_sync(0xffffffffu, key != 0)) return;
-      best = warp_merge_desc(best, warp_sort_desc(key, lane), lane);
+    // the owners' elements: item = (owner, one of its places; the last two are its head and tail elements)
+    const int places = (v1 - v0 + NT - 1) / NT + 2, items = n_owner * places;
+    auto offer = [&](float v, int id) {
+      const uint64_t key = key_of(v, id);
+      if (key < floor_key) return;
+      const int at = atomicAdd(&n_list, 1);
+      if (at < kList) list[at] = key;
     };
-    for (int o = warp; o < a.n_top; o += kNW) {
-      const int t = owners[o];
-      if (t < 0) break;
-      if (rank == 0 && t < head) batch(lane == 0 ? key_of(to_f32(x[t]), t) : 0);
-      if (rank == C - 1 && tail + t < a.V) batch(lane == 0 ? key_of(to_f32(x[tail + t]), tail + t) : 0);
-      for (int q0 = v0 + t; q0 < v1; q0 += 32 * kThreads) {
-        const int q = q0 + lane * kThreads;
-        float v[E];
-        if (q < v1) unpack<T>(body[q], v);
+    for (int i0 = tid; i0 < items; i0 += 4 * NT) {
+      uint4 w[4];
+      int q[4];
 #pragma unroll
-        for (int i = 0; i < E; ++i) batch(q < v1 ? key_of(v[i], head + q * E + i) : 0);
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * NT, o = i / places, t = i < items ? owner[o] : 0, j = i - o * places;
+        q[u] = -1;
+        if (i >= items) continue;
+        if (j < places - 2) {
+          q[u] = v0 + t + j * NT;
+          if (q[u] < v1)
+            w[u] = body[q[u]];
+          else
+            q[u] = -1;
+        } else if (j == places - 2) {
+          if (rank == 0 && t < head) offer(to_f32(x[t]), t);
+        } else if (rank == C - 1 && tail + t < a.V) {
+          offer(to_f32(x[tail + t]), tail + t);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (q[u] < 0) continue;
+        float v[E];
+        unpack<T>(w[u], v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) offer(v[e], head + q[u] * E + e);
       }
     }
-    __syncthreads();  // every thread is done with the lists
-    lists[tid] = best;
+    __syncthreads();
+    if (n_list <= kList) {
+      const int n = n_list;
+      for (int i = tid; i < n; i += NT) {
+        const uint64_t key = list[i];
+        int above = 0;
+        for (int j = 0; j < n; ++j) above += list[j] > key;
+        if (above < a.n_top) result[above] = key;
+      }
+    } else {  // too many: each warp keeps the best 32 of its owners' elements, and the warps' lists are merged
+      uint64_t best = 0;
+      auto batch = [&](uint64_t key) {
+        if (key < floor_key) key = 0;
+        if (!__any_sync(0xffffffffu, key != 0)) return;
+        best = warp_merge_desc(best, warp_sort_desc(key, lane), lane);
+      };
+      for (int o = warp; o < n_owner; o += NW) {
+        const int t = owner[o];
+        if (rank == 0 && t < head) batch(lane == 0 ? key_of(to_f32(x[t]), t) : 0);
+        if (rank == C - 1 && tail + t < a.V) batch(lane == 0 ? key_of(to_f32(x[tail + t]), tail + t) : 0);
+        for (int q0 = v0 + t; q0 < v1; q0 += 32 * NT) {
+          const int q = q0 + lane * NT;
+          float v[E];
+          if (q < v1) unpack<T>(body[q], v);
+#pragma unroll
+          for (int e = 0; e < E; ++e) batch(q < v1 ? key_of(v[e], head + q * E + e) : 0);
+        }
+      }
+      __syncthreads();  // every thread has seen n_list
+      list[tid] = best;
+      __syncthreads();
+      if (warp == 0) result[lane] = warp_merge_lists(list, NW, lane);
+    }
   }
   __syncthreads();
+  if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // rank 0 runs
   if (warp == 0) {
-    if (a.n_top) result[lane] = warp_merge_lists(lists, kNW, lane);
-    Stat b = lane < kNW ? stats[lane] : Stat{-INFINITY, 0.f, 0.f, 0.f};
+    Stat b = lane < NW ? stats[lane] : Stat{-INFINITY, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const Stat c = {__shfl_xor_sync(0xffffffffu, b.m, o), __shfl_xor_sync(0xffffffffu, b.n, o),
                       __shfl_xor_sync(0xffffffffu, b.s, o), __shfl_xor_sync(0xffffffffu, b.w, o)};
       b = lane & o ? join(c, b, a.k) : join(b, c, a.k);
     }
-    if (lane == 0) cta_stat = b;
-  }
-  __syncthreads();
-  if (C > 1) tc::cluster_sync_all();
-  if (rank == 0 && warp == 0) {
-    Stat all_st = cta_stat;
-    uint64_t best = a.n_top ? result[lane] : 0;
-    for (int c = 1; c < C; ++c) {
-      const uint64_t* q = reinterpret_cast<const uint64_t*>(&cta_stat);
-      const uint64_t lo = ld_cluster_u64(q, c), hi = ld_cluster_u64(q + 1, c);
-      all_st = join(all_st, Stat{__uint_as_float((uint32_t)lo), __uint_as_float((uint32_t)(lo >> 32)),
-                                 __uint_as_float((uint32_t)hi), __uint_as_float((uint32_t)(hi >> 32))}, a.k);
-      if (a.n_top) best = warp_merge_desc(best, ld_cluster_u64(result + lane, c), lane);
-    }
-    const float S1 = all_st.s + (all_st.n - 1.f);  // S - 1
-    // a row of -inf alone: every token impossible; +inf or NaN: no distribution
-    const bool none = all_st.n == 0.f && all_st.s == 0.f, bad = all_st.m == INFINITY || all_st.s != all_st.s;
-    const float logS = bad ? NAN : log1pf(S1);
-    if (lane == 0) {
-      if (a.lp) {
-        float r = NAN;
-        if (tok < a.V) {
-          const float xv = to_f32(x[tok]);
-          r = none || (xv == -INFINITY && !bad) ? -INFINITY : -((all_st.m - xv) / a.T) - logS;
-        } else {
-          flag_status(a.status, kDevBounds);
-        }
-        a.lp[row] = r;
+    if (C > 1) {
+      if (lane < 2) {
+        const uint64_t v = lane ? ((uint64_t)__float_as_uint(b.w) << 32) | __float_as_uint(b.s)
+                                : ((uint64_t)__float_as_uint(b.n) << 32) | __float_as_uint(b.m);
+        st_cluster_u64(reinterpret_cast<uint64_t*>(&gather_stat[rank]) + lane, 0, v);
       }
-      if (a.ent) a.ent[row] = none ? 0.f : logS + all_st.w * kLn2 / (all_st.n + all_st.s);
-    }
-    if (lane < a.n_top) {
-      const int id = id_of(best);
-      const float xv = to_f32(x[id]);
-      a.ids[(size_t)row * a.n_top + lane] = id;
-      a.top[(size_t)row * a.n_top + lane] = none || (xv == -INFINITY && !bad) ? -INFINITY : -((all_st.m - xv) / a.T) - logS;
+      if (a.n_top) st_cluster_u64(&gather_key[rank * 32 + lane], 0, result[lane]);
+    } else if (lane == 0) {
+      gather_stat[0] = b;
     }
   }
-  if (C > 1) tc::cluster_sync_all();  // no CTA leaves while another reads its shared memory
+  if (C > 1) {
+    tc::cluster_sync_all();
+    if (rank) return;  // nothing reads this CTA's memory
+  } else {
+    __syncthreads();
+  }
+  Stat all_st = gather_stat[0];
+  for (int c = 1; c < C; ++c) all_st = join(all_st, gather_stat[c], a.k);
+  // a row of -inf alone: every token impossible; +inf or NaN: no distribution
+  const bool none = all_st.n == 0.f && all_st.s == 0.f, bad = all_st.m == INFINITY || all_st.s != all_st.s;
+  const float logS = bad ? NAN : log1pf(all_st.s + (all_st.n - 1.f));
+  auto ln_p = [&](float xv) { return none || (xv == -INFINITY && !bad) ? -INFINITY : -((all_st.m - xv) / a.T) - logS; };
+  if (tid == NT - 1) {
+    if (a.lp) a.lp[row] = tok < a.V ? ln_p(to_f32(x[tok])) : NAN;
+    if (tok >= a.V) flag_status(a.status, kDevBounds);
+    if (a.ent) a.ent[row] = none ? 0.f : logS + all_st.w * kLn2 / (all_st.n + all_st.s);
+  }
+  if (tid < (a.n_top ? 32 * C : 0)) {
+    uint64_t key = result[lane];
+    int above = lane;
+    if (C > 1) {
+      key = gather_key[tid];
+      above = 0;
+      for (int j = 0; j < 32 * C; ++j) above += gather_key[j] > key;
+    }
+    if (key && above < a.n_top) {
+      const int id = id_of(key);
+      a.ids[(size_t)row * a.n_top + above] = id;
+      a.top[(size_t)row * a.n_top + above] = ln_p(to_f32(x[id]));
+    }
+  }
 }
 
 }  // namespace
@@ -362,13 +427,14 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
   a.ids = g->top_ids;
   a.top = g->top_logprobs;
   a.status = g->status;
-  // few rows: a cluster per row, so that every SM reads; a slice keeps a piece for every thread
+  // few rows: a cluster per row, so that every SM reads; a slice keeps four pieces for every thread. Many rows:
+  // CTAs of 256 threads, of which an SM holds several at different places of their rows.
   const int es = g->dtype == DLITE_F32 ? 4 : 2;
   int C = 1;
-  while (C < 8 && 2LL * C * g->rows <= 2LL * device_sms() && (long long)g->V * es >= 2LL * C * kThreads * 16) C *= 2;
+  while (C < kMaxCluster && 2LL * C * g->rows <= 2LL * device_sms() && (long long)g->V * es >= 2LL * C * 512 * 16 * 4) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C * g->rows);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C > 1 ? 512 : 256);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -379,6 +445,7 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  return launch_status(g->dtype == DLITE_F32 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<float>, a, C)
-                                             : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<bf16>, a, C));
+  void (*fn)(LpArgs, int) = g->dtype == DLITE_F32 ? (C > 1 ? token_logprobs_kernel<float, 512> : token_logprobs_kernel<float, 256>)
+                                                  : (C > 1 ? token_logprobs_kernel<bf16, 512> : token_logprobs_kernel<bf16, 256>);
+  return launch_status(cudaLaunchKernelEx(&cfg, fn, a, C));
 }

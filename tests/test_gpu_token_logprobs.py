@@ -144,3 +144,15 @@ def test_graph_replay_and_streams():
             graph.replay()
             s.synchronize()
             _check(x[i].double().numpy(), tok[i], 0.8, 10, got)
+
+
+@pytest.mark.parametrize("V,rows", [(262144, 1), (65536, 200)])
+def test_large_elements_in_the_same_threads(V, rows):
+    """Thousands of large logits at ids a multiple of 4096 (+ 0..7) apart: a few threads own them all."""
+    x = torch.randn(rows, V, generator=_gen(8)) * 0.1
+    i = torch.arange(V)
+    for mod, width in ((4096, 8), (4096, 64), (2048, 1500)):
+        y = x + torch.where(i % mod < width, 20.0 + (i * 7919 % 100003).float() / 1e4, torch.tensor(0.0))
+        tok = torch.full((rows,), 5, dtype=torch.int32)
+        got = binding.token_logprobs(y.to(DEV), tok.to(DEV), 1.0, 32)
+        _check(y[:2].double().numpy(), tok[:2], 1.0, 32, {k: v[:2] for k, v in got.items()})
