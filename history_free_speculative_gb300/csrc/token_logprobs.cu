@@ -7,14 +7,16 @@
 // a row that is nearly certain keeps its small entropy to full precision.
 //
 // A row is read by a cluster of CTAs (one when there are many rows), each a slice, each thread
-// every blockDim-th 16-byte piece of the slice, four pieces in flight. A thread keeps
-// (m, n, s, w = sum e^-d d) online and the place of its largest element. Alternatives are ordered by 64-bit keys
-// (value, then lower id first), all distinct. The largest keys of 64 groups of threads give a floor: their n_top-th
-// is the key of an element that n_top - 1 others exceed, so no alternative lies below it. Only threads whose largest
-// key reaches the floor can own one; their elements are read again (L2), the few
-// that reach the floor are listed, and a key's place is the number of keys above it. (64 groups and
-// n_top = 20: about -64 ln(1 - 20 / 64) = 24 elements.) A list that would not fit, which takes
-// over a thousand large elements in the same few threads, is replaced by sorted merges.
+// every blockDim-th 16-byte piece of the slice, four pieces in flight. A warp shares its running maximum m (one
+// warp-wide maximum per 16 elements a lane), so that rescaling is a branch the whole warp takes, about ln(steps) times:
+// with a maximum per thread some lane of a warp rescaled in most steps (512 bf16 rows of 151,936: 93.5 us). A thread
+// keeps (n, s, w = sum e^-d d) and the largest of its own elements.
+// Alternatives are ordered by 64-bit keys (value, then lower id first), all distinct. The n_top-th largest of the maxima of 64
+// groups of threads is a floor: n_top elements reach it. Only threads whose own maximum reaches the floor can hold an
+// alternative; their elements are read again (L2), those that reach the floor are listed, and an
+// element's place is the number of larger keys. (64 groups, n_top = 20: about -64 ln(1 - 20 / 64) = 24 elements and
+// the floor's equals.) A list that does not fit (many equals, or a thousand large elements in the same few
+// threads) is replaced by each warp's best 32, merged.
 // Bound: HBM for many rows, a dependent chain of a few microseconds for a few.
 #include <math.h>
 
@@ -115,51 +117,50 @@ __device__ __forceinline__ void unpack(const uint4& w, float* v) {
   }
 }
 
-// Takes the N elements of P pieces of E (ids id0 + p step + e) into the statistics; idx: id of the first largest.
-template <int P, int E>
-__device__ __forceinline__ void take(const float (&v)[P * E], int id0, int step, float k, Stat& st, int& idx) {
-  constexpr int N = P * E;
-  float cm = v[0], cn = v[0];
+__device__ __forceinline__ float warp_max_f32(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// One warp takes N elements a lane (-inf where a lane has fewer). st.m is the warp's running
+// maximum, the same in every lane; own: the lane's largest element.
+template <int N>
+__device__ __forceinline__ void take(const float (&v)[N], float k, Stat& st, float& own) {
+  float cm = v[0];
 #pragma unroll
-  for (int i = 1; i < N; ++i) {
-    cm = fmaxf(cm, v[i]);
-    cn = fminf(cn, v[i]);
-  }
-  if (cm > st.m) {
-    const float t = st.n + st.s;
-    if (st.m == -INFINITY) {
-      st.w = st.w + 0.f * t;  // no weight so far; a NaN stays one
-      st.s = 0.f * t;
-    } else {
-      const float d = fminf((cm - st.m) * k, 1e4f), f = tc::ex2_approx(-d);
-      st.w = f * (st.w + d * t);
-      st.s = f * t;
-    }
-    st.n = 0.f;
-    st.m = cm;
-#pragma unroll
-    for (int i = N - 1; i >= 0; --i)
-      if (v[i] == cm) idx = id0 + (i / E) * step + i % E;
-  }
+  for (int i = 1; i < N; ++i) cm = fmaxf(cm, v[i]);
+  own = fmaxf(own, cm);
+  const float wm = warp_max_f32(cm);
   float s = 0.f, w = 0.f;
-  if (cm < st.m && (st.m - cn) * k < 1e30f) {  // neither the largest is among them nor an excluded id
+  if (wm < st.m) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float d = (st.m - v[i]) * k, e = tc::ex2_approx(-d);
       s += e;
-      w = fmaf(e, d, w);
+      w = fmaf(e, fminf(d, 1e30f), w);  // d = inf, or overflown, where e = 0; a NaN e stays
     }
-  } else {
+  } else {  // the largest so far is among them
+    if (wm > st.m) {
+      const float t = st.n + st.s;
+      if (st.m == -INFINITY) {
+        st.w = st.w + 0.f * t;  // no weight so far; a NaN stays one
+        st.s = 0.f * t;
+      } else {
+        const float d = fminf((wm - st.m) * k, 1e4f), f = tc::ex2_approx(-d);
+        st.w = f * (st.w + d * t);
+        st.s = f * t;
+      }
+      st.n = 0.f;
+      st.m = wm;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (v[i] == -INFINITY) continue;
-      if (v[i] == st.m) {
-        st.n += 1.f;
-        continue;
-      }
-      const float d = (st.m - v[i]) * k, e = tc::ex2_approx(-d);
+      const bool top = v[i] == st.m;
+      const float d = (st.m - v[i]) * k, e = top ? 0.f : tc::ex2_approx(-d);
       s += e;
-      w = fmaf(e, fminf(d, 1e30f), w);  // d may overflow where e = 0; a NaN e stays
+      w = fmaf(e, fminf(d, 1e30f), w);
+      st.n += top && st.m > -INFINITY ? 1.f : 0.f;
     }
   }
   st.s += s;
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
   constexpr int E = 16 / sizeof(T), NW = NT / 32, GS = NT / kGroups;
   static_assert(kList >= NT, "the merges' lists share the list's memory");
   __shared__ uint64_t list[kList];       // elements that reach the floor
-  __shared__ uint64_t group_key[kGroups];
+  __shared__ float group_max[kGroups];
   __shared__ uint64_t result[32];        // this CTA's alternatives
   __shared__ Stat stats[NW];
   // of rank 0: what the CTAs of the cluster send
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
   __shared__ __align__(16) Stat gather_stat[kMaxCluster];
   __shared__ uint16_t owner[NT];
   __shared__ int n_owner, n_list;
-  __shared__ uint64_t s_floor;
+  __shared__ float s_floor;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -208,18 +209,17 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
   const int nv = (a.V - head) / E, tail = head + nv * E;
   const int v0 = (int)((long long)nv * rank / C), v1 = (int)((long long)nv * (rank + 1) / C);
   const uint4* body = reinterpret_cast<const uint4*>(x + head);
-  const bool has_head = rank == 0 && tid < head, has_tail = rank == C - 1 && tail + tid < a.V;
 
   Stat st = {-INFINITY, 0.f, 0.f, 0.f};
-  int p = v0 + tid;
-  // the thread's first element, the lowest of its ids, stands for a thread without a larger one than -inf
-  int idx = has_head ? tid : p < v1 ? head + p * E : has_tail ? tail + tid : -1;
-  if (has_head) {
-    const float v[1] = {to_f32(x[tid])};
-    take<1, 1>(v, tid, 0, a.k, st, idx);
+  float own = -INFINITY;
+  const int first = tid & ~31;  // the warp's first thread: all loops are the warp's
+  if (rank == 0 && first < head) {
+    const float v[1] = {tid < head ? to_f32(x[tid]) : -INFINITY};
+    take<1>(v, a.k, st, own);
   }
   constexpr int P = 16 / E;  // pieces taken at once: 16 elements
-  for (; p + 3 * NT < v1; p += 4 * NT) {
+  int p = v0 + tid, pw = v0 + first;
+  for (; pw + 31 + 3 * NT < v1; p += 4 * NT, pw += 4 * NT) {
     uint4 w[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) w[u] = __ldcs(body + p + u * NT);
@@ -228,17 +228,22 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
       float v[P * E];
 #pragma unroll
       for (int q = 0; q < P; ++q) unpack<T>(w[u + q], v + q * E);
-      take<P, E>(v, head + (p + u * NT) * E, NT * E, a.k, st, idx);
+      take<P * E>(v, a.k, st, own);
     }
   }
-  for (; p < v1; p += NT) {
+  for (; pw < v1; p += NT, pw += NT) {
     float v[E];
-    unpack<T>(__ldcs(body + p), v);
-    take<1, E>(v, head + p * E, 0, a.k, st, idx);
+    if (p < v1) {
+      unpack<T>(__ldcs(body + p), v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = -INFINITY;
+    }
+    take<E>(v, a.k, st, own);
   }
-  if (has_tail) {
-    const float v[1] = {to_f32(x[tail + tid])};
-    take<1, 1>(v, tail + tid, 0, a.k, st, idx);
+  if (rank == C - 1 && tail + first < a.V) {
+    const float v[1] = {tail + tid < a.V ? to_f32(x[tail + tid]) : -INFINITY};
+    take<1>(v, a.k, st, own);
   }
 
   Stat all = st;
@@ -252,38 +257,33 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
   if (lane == 0) stats[warp] = all;
 
   if (a.n_top) {
-    const uint64_t mine = idx < 0 ? 0 : key_of(st.m, idx);
-    uint64_t gk = mine;
+    float gm = own;
 #pragma unroll
-    for (int o = GS / 2; o > 0; o >>= 1) {
-      const uint64_t b = shfl64_xor(gk, o);
-      gk = b > gk ? b : gk;
-    }
-    if (tid % GS == 0) group_key[tid / GS] = gk;
-    if (tid == 0) {
-      s_floor = 1;  // fewer than n_top groups with elements: every element
-      n_owner = n_list = 0;
-    }
+    for (int o = GS / 2; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+    if (tid % GS == 0) group_max[tid / GS] = gm;
+    if (tid == 0) n_owner = n_list = 0;
     if (tid < 32) result[tid] = 0;
     __syncthreads();
     if (tid < kGroups) {
-      const uint64_t g = group_key[tid];
-      int above = 0;
+      const float g = group_max[tid];
+      int above = 0, reach = 0;
 #pragma unroll 16
-      for (int i = 0; i < kGroups; ++i) above += group_key[i] > g;
-      if (g && above == a.n_top - 1) s_floor = g;
+      for (int i = 0; i < kGroups; ++i) {
+        above += group_max[i] > g;
+        reach += group_max[i] >= g;
+      }
+      if (above < a.n_top && reach >= a.n_top) s_floor = g;  // equal groups write the same
     }
     __syncthreads();
-    const uint64_t floor_key = s_floor;
-    if (mine >= floor_key) owner[atomicAdd(&n_owner, 1)] = (uint16_t)tid;
+    const float floor = s_floor;
+    if (!(own < floor)) owner[atomicAdd(&n_owner, 1)] = (uint16_t)tid;
     __syncthreads();
     // the owners' elements: item = (owner, one of its places; the last two are its head and tail elements)
     const int places = (v1 - v0 + NT - 1) / NT + 2, items = n_owner * places;
     auto offer = [&](float v, int id) {
-      const uint64_t key = key_of(v, id);
-      if (key < floor_key) return;
+      if (v < floor || (v != v && floor > -INFINITY)) return;
       const int at = atomicAdd(&n_list, 1);
-      if (at < kList) list[at] = key;
+      if (at < kList) list[at] = key_of(v, id);
     };
     for (int i0 = tid; i0 < items; i0 += 4 * NT) {
       uint4 w[4];
@@ -326,8 +326,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
     } else {  // too many: each warp keeps the best 32 of its owners' elements, and the warps' lists are merged
       uint64_t best = 0;
       auto batch = [&](uint64_t key) {
-        if (key < floor_key) key = 0;
-        if (!__any_sync(0xffffffffu, key != 0)) return;
+        if (!__any_sync(0xffffffffu, key > shfl64(best, 31))) return;
         best = warp_merge_desc(best, warp_sort_desc(key, lane), lane);
       };
       for (int o = warp; o < n_owner; o += NW) {
