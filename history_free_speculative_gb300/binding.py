@@ -508,14 +508,19 @@ def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entro
                 raise ValueError("logits: rows have to be evenly spaced")
             span = st * n
     n_top = int(n_top)
-    want = ((logprob, lead, torch.float32), (entropy, lead, torch.float32), (top_ids, lead + (max(n_top, 0),), torch.int32),
-            (top_logprobs, lead + (max(n_top, 0),), torch.float32))
-    got = [_new(s, shape, dt) if t is None else t for t, shape, dt in want]
-    outs = [_vec(t, dt, shape, "output") for t, (_, shape, dt) in zip(got, want)]
+    at = lead + (max(n_top, 0),)
+    outs = []
+    for name, t, shape, dt in (("logprob", logprob, lead, torch.float32), ("entropy", entropy, lead, torch.float32),
+                               ("top_ids", top_ids, at, torch.int32), ("top_logprobs", top_logprobs, at, torch.float32)):
+        if t is None:
+            t = _new(s, shape, dt)
+        else:
+            _vec(t, dt, shape, name)
+        outs.append(t)
     a = LogprobsArgs(rows, V, n_top, _dtype(logits, "logits"), temperature, logits.data_ptr(), stride,
-                     _vec(tokens, torch.int32, lead, "tokens"), *outs, _vec(status, torch.int32, (1,), "status"))
+                     _vec(tokens, torch.int32, lead, "tokens"), *(t.data_ptr() for t in outs), _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_token_logprobs(ctypes.byref(a), ptr), "dlite_token_logprobs")
-    return dict(zip(("logprob", "entropy", "top_ids", "top_logprobs"), got))
+    return dict(logprob=outs[0], entropy=outs[1], top_ids=outs[2], top_logprobs=outs[3])
 
 
 def config_struct(cfg, B_max):

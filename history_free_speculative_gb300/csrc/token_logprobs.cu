@@ -7,16 +7,21 @@
 // a row that is nearly certain keeps its small entropy to full precision.
 //
 // A row is read by a cluster of CTAs (one when there are many rows), each a slice, each thread
-// every blockDim-th 16-byte piece of the slice, four pieces in flight. A warp shares its running maximum m (one
+// every blockDim-th 16-byte piece of the slice. The slice comes by bulk copies through a ring of shared-memory
+// stages (four pieces a thread each), so that loads are in flight while a warp computes. A warp shares its running maximum m (one
 // warp-wide maximum per 16 elements a lane), so that rescaling is a branch the whole warp takes, about ln(steps) times:
 // with a maximum per thread some lane of a warp rescaled in most steps (512 bf16 rows of 151,936: 93.5 us). A thread
 // keeps (n, s, w = sum e^-d d) and the largest of its own elements.
-// Alternatives are ordered by 64-bit keys (value, then lower id first), all distinct. The n_top-th largest of the maxima of 64
-// groups of threads is a floor: n_top elements reach it. Only threads whose own maximum reaches the floor can hold an
-// alternative; their elements are read again (L2), those that reach the floor are listed, and an
-// element's place is the number of larger keys. (64 groups, n_top = 20: about -64 ln(1 - 20 / 64) = 24 elements and
-// the floor's equals.) A list that does not fit (many equals, or a thousand large elements in the same few
-// threads) is replaced by each warp's best 32, merged.
+// Alternatives are ordered by 64-bit keys (value, then lower id first), all distinct. Whenever a thread's 16 elements reach a
+// floor, their place and maximum are listed; the floor is the n_top-th largest of the running maxima of 64 groups of threads: n_top
+// elements reach it, so no alternative is left out. It is first taken over the first stage alone and then raised by one
+// warp a stage in turn, without a barrier: a maximum that another warp has not yet written only leaves the floor lower. About
+// 24 (ln stages + 2) places are listed at n_top = 20. At the end the places that reach the last floor are read again, their
+// elements that reach it are listed, and a key's place is the number of larger keys. A list that does not fit (many
+// equal elements, or rows that rise towards their end) is given up: the threads whose own maximum
+// reaches the floor have all their elements read again, each warp keeps its best 32 and these are merged.
+// (512 bf16 rows of 151,936, n_top 20: reading all elements of the owning threads again costs 12 to 20 us of 55, listing single
+// elements as they pass 28.)
 // Bound: HBM for many rows, a dependent chain of a few microseconds for a few.
 #include <math.h>
 
@@ -29,9 +34,8 @@ namespace dlite {
 namespace {
 
 constexpr int kGroups = 64;  // groups of threads behind the floor
-constexpr int kList = 1024;  // listed elements
+constexpr int kList = 512;   // listed places, and listed elements, at most
 constexpr int kMaxCluster = 8;
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct LpArgs {
   int V, n_top;
@@ -46,17 +50,39 @@ struct LpArgs {
 };
 
 // Softmax statistics of a set of elements: the largest, how often it occurs, and over the
-// others s = sum 2^-d, w = sum 2^-d d with d = (m - x) k.
+// others s = sum 2^(-d k), w = sum 2^(-d k) d with d = m - x.
 struct Stat {
   float m, n, s, w;
 };
+// Weight of a distance d >= 0; one beyond 2^-200 is 0, and its d (perhaps infinite) is taken as 0.
+__device__ __forceinline__ float weight(float& d, float k) {
+  const float e = d * k;
+  if (e > 200.f) {
+    d = 0.f;
+    return 0.f;
+  }
+  return tc::ex2_approx(-e);
+}
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float k) {
   const bool up = b.m > a.m;
   const Stat hi = up ? b : a, lo = up ? a : b;
   if (lo.m == hi.m) return {hi.m, hi.n + lo.n, hi.s + lo.s, hi.w + lo.w};
   // lo.n = 0 and lo.s = 0 (no element, or only -inf): nothing to take along. A NaN sum stays.
-  const float d = fminf((hi.m - lo.m) * k, 1e4f), f = tc::ex2_approx(-d), t = lo.n + lo.s;
+  float d = hi.m - lo.m;
+  const float f = weight(d, k), t = lo.n + lo.s;
   return {hi.m, hi.n, hi.s + f * t, hi.w + f * (lo.w + d * t)};
+}
+
+// The statistics of a warp's lanes together, the same bits in every lane
+__device__ __forceinline__ Stat warp_join(Stat v, float k, int lane) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    const Stat b = {__shfl_xor_sync(0xffffffffu, v.m, o), __shfl_xor_sync(0xffffffffu, v.n, o),
+                    __shfl_xor_sync(0xffffffffu, v.s, o), __shfl_xor_sync(0xffffffffu, v.w, o)};
+    const bool up = lane & o;  // the same order of the two on both lanes
+    v = join(up ? b : v, up ? v : b, k);
+  }
+  return v;
 }
 
 // Order of the alternatives: larger logit first (-0 = +0, NaN as -inf), then the lower id; 0 = no element.
@@ -67,6 +93,10 @@ __device__ __forceinline__ uint64_t key_of(float x, int id) {
   return ((uint64_t)u << 32) | (uint32_t)~id;
 }
 __device__ __forceinline__ int id_of(uint64_t key) { return (int)~(uint32_t)key; }
+__device__ __forceinline__ float value_of(uint64_t key) {
+  const uint32_t u = (uint32_t)(key >> 32);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
 
 __device__ __forceinline__ uint64_t shfl64(uint64_t v, int src) { return __shfl_sync(0xffffffffu, v, src); }
 __device__ __forceinline__ uint64_t shfl64_xor(uint64_t v, int mask) { return __shfl_xor_sync(0xffffffffu, v, mask); }
@@ -102,19 +132,62 @@ __device__ __forceinline__ uint64_t warp_merge_lists(const uint64_t* keys, int l
   return best;
 }
 
-// E elements of type T at p as float: one 16-byte access
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// The elements of a 16-byte piece as float
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4& w, float* v) {
-  if constexpr (sizeof(T) == 4) {
-    v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
-  } else {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __uint_as_float(u[i]);
+    } else {
+      v[2 * i] = lo_f32(u[i]);
+      v[2 * i + 1] = hi_f32(u[i]);
     }
   }
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Two fp32 at a time
+__device__ __forceinline__ uint64_t pack2f(float lo, float hi) {
+  return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float lo2f(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2f(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 __device__ __forceinline__ float warp_max_f32(float v) {
@@ -123,60 +196,153 @@ __device__ __forceinline__ float warp_max_f32(float v) {
   return r;
 }
 
-// One warp takes N elements a lane (-inf where a lane has fewer). st.m is the warp's running
-// maximum, the same in every lane; own: the lane's largest element.
-template <int N>
-__device__ __forceinline__ void take(const float (&v)[N], float k, Stat& st, float& own) {
-  float cm = v[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) cm = fmaxf(cm, v[i]);
-  own = fmaxf(own, cm);
-  const float wm = warp_max_f32(cm);
-  float s = 0.f, w = 0.f;
-  if (wm < st.m) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = (st.m - v[i]) * k, e = tc::ex2_approx(-d);
-      s += e;
-      w = fmaf(e, fminf(d, 1e30f), w);  // d = inf, or overflown, where e = 0; a NaN e stays
-    }
-  } else {  // the largest so far is among them
-    if (wm > st.m) {
-      const float t = st.n + st.s;
-      if (st.m == -INFINITY) {
-        st.w = st.w + 0.f * t;  // no weight so far; a NaN stays one
-        st.s = 0.f * t;
-      } else {
-        const float d = fminf((wm - st.m) * k, 1e4f), f = tc::ex2_approx(-d);
-        st.w = f * (st.w + d * t);
-        st.s = f * t;
-      }
-      st.n = 0.f;
-      st.m = wm;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool top = v[i] == st.m;
-      const float d = (st.m - v[i]) * k, e = top ? 0.f : tc::ex2_approx(-d);
-      s += e;
-      w = fmaf(e, fminf(d, 1e30f), w);
-      st.n += top && st.m > -INFINITY ? 1.f : 0.f;
-    }
+// A list of keys of a CTA
+struct Top {
+  bool on;
+  float floor;
+  uint64_t* list;
+  int* n;
+  __device__ __forceinline__ void add(float v, int id) const {
+    if (*(volatile int*)n > kList) return;  // given up
+    const int at = atomicAdd(n, 1);
+    if (at < kList) list[at] = key_of(v, id);
   }
-  st.s += s;
-  st.w += w;
+};
+
+constexpr float kTame = 1.2676506002282294e30f;  // 2^100
+constexpr uint32_t kFloorBf16x2 = 0xF200F200u;   // -2^101, twice
+
+// out[i] = the i-th largest of n distinct keys, i < n_top (the block's threads, no barrier here)
+template <int NT>
+__device__ __forceinline__ void place(const uint64_t* keys, int n, int n_top, uint64_t* out) {
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const uint64_t key = keys[i];
+    int above = 0;
+    for (int j = 0; j < n; ++j) above += keys[j] > key;
+    if (above < n_top) out[above] = key;
+  }
 }
 
+// The n-th largest (from 1) of 64 values, by one warp (bitonic sort of two a lane).
+__device__ __forceinline__ float nth_largest64(const volatile float* g, int n, int lane) {
+  float v[2] = {g[lane], g[32 + lane]};
+#pragma unroll
+  for (int size = 2; size <= 64; size <<= 1)
+#pragma unroll
+    for (int j = size >> 1; j > 0; j >>= 1) {
+      if (j == 32) {
+        const float hi = fmaxf(v[0], v[1]), lo = fminf(v[0], v[1]);
+        v[0] = hi, v[1] = lo;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float o = __shfl_xor_sync(0xffffffffu, v[r], j);
+          const bool desc = size == 64 || (size == 32 ? r == 0 : (lane & size) == 0);
+          v[r] = ((lane & j) == 0) == desc ? fmaxf(v[r], o) : fminf(v[r], o);
+        }
+      }
+    }
+  const float a = __shfl_sync(0xffffffffu, v[0], (n - 1) & 31), b = __shfl_sync(0xffffffffu, v[1], (n - 1) & 31);
+  return n <= 32 ? a : b;
+}
+
+// The largest of N words of elements of type T (NaN ignored)
+template <typename T, int N>
+__device__ __forceinline__ float max_of(const uint32_t (&x)[N]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t c = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) c = max_bf16x2(c, x[i]);
+    return fmaxf(lo_f32(c), hi_f32(c));
+  } else {
+    float c = __uint_as_float(x[0]);
+#pragma unroll
+    for (int i = 1; i < N; ++i) c = fmaxf(c, __uint_as_float(x[i]));
+    return c;
+  }
+}
+
+// One warp takes N words a lane of elements of type T (-inf where a lane has fewer). st.m is the
+// warp's running maximum, the same in every lane; own: the lane's largest element.
+// The usual step, all elements below a maximum of moderate size, runs two elements an
+// instruction: elements below -2^101 (excluded ones: -inf, the type's lowest) become
+// -2^101, whose weight is 0 too and whose distance stays finite.
+// Elements whose maximum reaches the floor of `top` go to its list, as the place id0 of the first.
+template <typename T, int N>
+__device__ __forceinline__ void take(const uint32_t (&x)[N], int id0, bool real, float k, Stat& st, float& own,
+                                     const Top& top) {
+  constexpr int E = sizeof(T) == 4 ? 1 : 2;
+  const float cm = max_of<T>(x);
+  own = fmaxf(own, cm);
+  if (top.on && real && (cm >= top.floor || top.floor == -INFINITY)) top.add(cm, id0);
+  const float wm = warp_max_f32(cm);
+  if (wm < st.m && fabsf(st.m) < kTame && k > 1e-20f && N * E % 2 == 0) {
+    const uint64_t m2 = pack2f(st.m, st.m), k2 = pack2f(-k, -k);
+    uint64_t s2 = 0, w2 = 0;
+#pragma unroll
+    for (int i = 0; i < N * E / 2; ++i) {
+      uint64_t v;
+      if constexpr (E == 2) {
+        const uint32_t c = max_nan_bf16x2(x[i], kFloorBf16x2);
+        v = pack2f(lo_f32(c), hi_f32(c));
+      } else {
+        v = pack2f(max_nan(__uint_as_float(x[2 * i]), -2.f * kTame), max_nan(__uint_as_float(x[2 * i + 1]), -2.f * kTame));
+      }
+      const uint64_t d = sub2(m2, v), t = mul2(d, k2);
+      const uint64_t e = pack2f(tc::ex2_approx(lo2f(t)), tc::ex2_approx(hi2f(t)));
+      s2 = add2(s2, e);
+      w2 = fma2(e, d, w2);
+    }
+    st.s += lo2f(s2) + hi2f(s2);
+    st.w += lo2f(w2) + hi2f(w2);
+    return;
+  }
+  if (wm > st.m) {
+    const float t = st.n + st.s;
+    float d = wm - st.m;
+    const float f = weight(d, k);   // nothing yet (m = -inf): 0
+    st.w = f * (st.w + d * t);
+    st.s = f * t;
+    st.n = 0.f;
+    st.m = wm;
+  }
+#pragma unroll
+  for (int i = 0; i < N * E; ++i) {
+    const float v = E == 2 ? (i & 1 ? hi_f32(x[i / 2]) : lo_f32(x[i / 2])) : __uint_as_float(x[i]);
+    // no branches: the maximum itself is counted, an element too far below it (or -inf) is nothing, a NaN stays
+    const bool top = v == st.m;
+    const float d = st.m - v, t = d * k;
+    const bool none = top || t > 200.f;
+    const float e = none ? 0.f : tc::ex2_approx(-t);
+    st.n += top && v > -INFINITY ? 1.f : 0.f;
+    st.s += e;
+    st.w = fmaf(e, none ? 0.f : d, st.w);
+  }
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // Store to the same shared-memory variable of CTA `rank` of the cluster.
 __device__ __forceinline__ void st_cluster_u64(uint64_t* local, uint32_t rank, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tc::map_to_rank(tc::su32(local), rank)), "l"(v) : "memory");
 }
 
+// Stages of four pieces a thread; their number is the launch's.
+template <int NT>
+struct Ring {
+  static constexpr int PIECES = 4 * NT, BYTES = PIECES * 16, MAX_STAGES = 8;
+  static constexpr int smem(int stages) { return stages * BYTES; }
+};
+
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
+__global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C, int stages) {
+  using R = Ring<NT>;
   constexpr int E = 16 / sizeof(T), NW = NT / 32, GS = NT / kGroups;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[R::MAX_STAGES], empty[R::MAX_STAGES];
   static_assert(kList >= NT, "the merges' lists share the list's memory");
-  __shared__ uint64_t list[kList];       // elements that reach the floor
+  __shared__ uint64_t list[kList], cand[kList];  // places, and elements, that reach the floor
   __shared__ float group_max[kGroups];
   __shared__ uint64_t result[32];        // this CTA's alternatives
   __shared__ Stat stats[NW];
@@ -184,8 +350,8 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
   __shared__ uint64_t gather_key[kMaxCluster * 32];
   __shared__ __align__(16) Stat gather_stat[kMaxCluster];
   __shared__ uint16_t owner[NT];
-  __shared__ int n_owner, n_list;
-  __shared__ float s_floor;
+  __shared__ int n_owner, n_list, n_cand;
+  __shared__ float s_floor, s_ref;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -210,120 +376,176 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
   const int v0 = (int)((long long)nv * rank / C), v1 = (int)((long long)nv * (rank + 1) / C);
   const uint4* body = reinterpret_cast<const uint4*>(x + head);
 
-  Stat st = {-INFINITY, 0.f, 0.f, 0.f};
-  float own = -INFINITY;
+  if (tid < 32) result[tid] = 0;
+  if (tid < kGroups) group_max[tid] = -INFINITY;
+  if (tid == 0) {
+    n_list = n_cand = n_owner = 0;
+    s_floor = -INFINITY;  // stays where fewer than n_top groups hold elements
+    for (int i = 0; i < stages; ++i) {
+      tc::mbar_init(tc::su32(full + i), 1);
+      tc::mbar_init(tc::su32(empty + i), NW);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  auto issue = [&](int c, int st) {  // thread 0: chunk c of the slice into stage st
+    const uint32_t bar = tc::su32(full + st), bytes = 16 * min(R::PIECES, v1 - v0 - c * R::PIECES);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc::mbar_expect_tx(bar, bytes);
+    tc::bulk_load(tc::su32(ring + st * R::BYTES), body + v0 + c * R::PIECES, bytes, bar);
+  };
+  if (tid == 0)
+    for (int c = 0; c < stages && v0 + c * R::PIECES < v1; ++c) issue(c, c);
+
+  T x_tok = T(0.f);
+  if (tid == NT - 1 && tok < a.V) x_tok = x[tok];  // early: its latency passes under the row's
+  const int chunks = (v1 - v0 + R::PIECES - 1) / R::PIECES;
   const int first = tid & ~31;  // the warp's first thread: all loops are the warp's
+  bool ok = true;
+  float ref = -INFINITY;
+  Top top = {a.n_top > 0, -INFINITY, list, &n_list};
+  if (chunks) {
+    // the first stage alone: its maximum is every warp's first reference (later rescales are rare then), the
+    // maxima of groups of threads give the first floor
+    ok = tc::mbar_wait(tc::su32(full), 0, a.status);
+    float cm = -INFINITY;
+    const int n = ok ? min(R::PIECES, v1 - v0) : 0;
+    for (int q = tid; q < n; q += NT) {
+      uint32_t v[4];
+      *reinterpret_cast<uint4*>(v) = reinterpret_cast<const uint4*>(ring)[q];
+      cm = fmaxf(cm, max_of<T>(v));
+    }
+#pragma unroll
+    for (int o = GS / 2; o > 0; o >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
+    if (tid % GS == 0) group_max[tid / GS] = cm;
+    __syncthreads();
+    if (warp == 0) {
+      const float g = warp_max_f32(fmaxf(group_max[lane], group_max[32 + lane]));
+      const float f = a.n_top ? nth_largest64(group_max, a.n_top, lane) : 0.f;
+      if (lane == 0) {
+        s_ref = g;
+        s_floor = f;
+      }
+    }
+    __syncthreads();
+    ref = s_ref;
+    top.floor = s_floor;
+  }
+
+  Stat st = {ref, 0.f, 0.f, 0.f};
+  float own = -INFINITY;
+  auto group_maxima = [&](float v) {
+#pragma unroll
+    for (int o = GS / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    // the first stage's maxima, of the same threads' elements, stand until these reach them
+    if (tid % GS == 0) *(volatile float*)&group_max[tid / GS] = fmaxf(v, *(volatile float*)&group_max[tid / GS]);
+  };
   if (rank == 0 && first < head) {
-    const float v[1] = {tid < head ? to_f32(x[tid]) : -INFINITY};
-    take<1>(v, a.k, st, own);
+    const uint32_t v[1] = {__float_as_uint(tid < head ? to_f32(x[tid]) : -INFINITY)};
+    take<float>(v, tid, tid < head, a.k, st, own, top);
   }
-  constexpr int P = 16 / E;  // pieces taken at once: 16 elements
-  int p = v0 + tid, pw = v0 + first;
-  for (; pw + 31 + 3 * NT < v1; p += 4 * NT, pw += 4 * NT) {
-    uint4 w[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) w[u] = __ldcs(body + p + u * NT);
-#pragma unroll
-    for (int u = 0; u < 4; u += P) {
-      float v[P * E];
-#pragma unroll
-      for (int q = 0; q < P; ++q) unpack<T>(w[u + q], v + q * E);
-      take<P * E>(v, a.k, st, own);
+  constexpr int P = sizeof(T) == 4 ? 4 : 2;  // pieces taken at once: 16 elements
+  int stage = 0;
+  uint32_t phase = 0;  // of the stage's turn
+  for (int c = 0; c < chunks; ++c) {
+    // the stage of chunk c - 1 is refilled now: the other warps have had a chunk's time to leave it
+    if (tid == 0 && c >= 1 && c - 1 + stages < chunks) {
+      ok &= tc::mbar_wait(tc::su32(empty + (stage ? stage : stages) - 1), stage ? phase : phase ^ 1u, a.status);
+      if (ok) issue(c - 1 + stages, (stage ? stage : stages) - 1);
     }
-  }
-  for (; pw < v1; p += NT, pw += NT) {
-    float v[E];
-    if (p < v1) {
-      unpack<T>(__ldcs(body + p), v);
+    ok = ok && tc::mbar_wait(tc::su32(full + stage), phase, a.status);
+    // a copy never landed: the status says so, the row's outputs mean nothing; the barriers below are kept
+    const int n = __all_sync(0xffffffffu, ok) ? min(R::PIECES, v1 - v0 - c * R::PIECES) : 0;
+    const uint4* src = reinterpret_cast<const uint4*>(ring + stage * R::BYTES);
+    if (n == R::PIECES) {
+#pragma unroll
+      for (int u = 0; u < 4; u += P) {
+        uint32_t v[4 * P];
+#pragma unroll
+        for (int q = 0; q < P; ++q) *reinterpret_cast<uint4*>(v + 4 * q) = src[tid + (u + q) * NT];
+        take<T>(v, head + (v0 + c * R::PIECES + tid + u * NT) * E, true, a.k, st, own, top);
+      }
     } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = -INFINITY;
+      constexpr uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+      for (int q = tid, qw = first; qw < n; q += NT, qw += NT) {
+        uint32_t v[4];
+        *reinterpret_cast<uint4*>(v) = q < n ? src[q] : make_uint4(none, none, none, none);
+        take<T>(v, head + (v0 + c * R::PIECES + q) * E, q < n, a.k, st, own, top);
+      }
     }
-    take<E>(v, a.k, st, own);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(tc::su32(empty + stage));
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    if (a.n_top) {
+      group_maxima(own);
+      if (c % NW == warp) {
+        const float f = nth_largest64(group_max, a.n_top, lane);
+        if (lane == 0 && f > *(volatile float*)&s_floor) *(volatile float*)&s_floor = f;  // lower ones are floors too
+      }
+      top.floor = fmaxf(top.floor, *(volatile float*)&s_floor);
+    }
   }
+  if (tid == 0 && !ok)  // let the copies in flight end (bounded) before the memory is given back
+    for (int i = 0; i < stages && i < chunks; ++i)
+      for (uint32_t ph = 0; ph < 2; ++ph) tc::mbar_wait(tc::su32(full + i), ph, a.status);
   if (rank == C - 1 && tail + first < a.V) {
-    const float v[1] = {tail + tid < a.V ? to_f32(x[tail + tid]) : -INFINITY};
-    take<1>(v, a.k, st, own);
+    const uint32_t v[1] = {__float_as_uint(tail + tid < a.V ? to_f32(x[tail + tid]) : -INFINITY)};
+    take<float>(v, tail + tid, tail + tid < a.V, a.k, st, own, top);
   }
 
-  Stat all = st;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Stat b = {__shfl_xor_sync(0xffffffffu, all.m, o), __shfl_xor_sync(0xffffffffu, all.n, o),
-                    __shfl_xor_sync(0xffffffffu, all.s, o), __shfl_xor_sync(0xffffffffu, all.w, o)};
-    // the same order of the two on both lanes: bits agree
-    all = lane & o ? join(b, all, a.k) : join(all, b, a.k);
-  }
+  const Stat all = warp_join(st, a.k, lane);
   if (lane == 0) stats[warp] = all;
-
+  if (a.n_top) group_maxima(own);
+  __syncthreads();
+  if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // rank 0 runs
+  if (warp == NW - 1) {  // the last warp joins the warps' statistics while the others look for alternatives
+    Stat b = lane < NW ? stats[lane] : Stat{-INFINITY, 0.f, 0.f, 0.f};
+    b = warp_join(b, a.k, lane);
+    if (C > 1) {
+      if (lane < 2) {
+        const uint64_t v = lane ? ((uint64_t)__float_as_uint(b.w) << 32) | __float_as_uint(b.s)
+                                : ((uint64_t)__float_as_uint(b.n) << 32) | __float_as_uint(b.m);
+        st_cluster_u64(reinterpret_cast<uint64_t*>(&gather_stat[rank]) + lane, 0, v);
+      }
+    } else if (lane == 0) {
+      gather_stat[0] = b;
+    }
+  }
   if (a.n_top) {
-    float gm = own;
-#pragma unroll
-    for (int o = GS / 2; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-    if (tid % GS == 0) group_max[tid / GS] = gm;
-    if (tid == 0) n_owner = n_list = 0;
-    if (tid < 32) result[tid] = 0;
-    __syncthreads();
-    if (tid < kGroups) {
-      const float g = group_max[tid];
-      int above = 0, reach = 0;
-#pragma unroll 16
-      for (int i = 0; i < kGroups; ++i) {
-        above += group_max[i] > g;
-        reach += group_max[i] >= g;
-      }
-      if (above < a.n_top && reach >= a.n_top) s_floor = g;  // equal groups write the same
-    }
-    __syncthreads();
-    const float floor = s_floor;
-    if (!(own < floor)) owner[atomicAdd(&n_owner, 1)] = (uint16_t)tid;
-    __syncthreads();
-    // the owners' elements: item = (owner, one of its places; the last two are its head and tail elements)
-    const int places = (v1 - v0 + NT - 1) / NT + 2, items = n_owner * places;
-    auto offer = [&](float v, int id) {
-      if (v < floor || (v != v && floor > -INFINITY)) return;
-      const int at = atomicAdd(&n_list, 1);
-      if (at < kList) list[at] = key_of(v, id);
-    };
-    for (int i0 = tid; i0 < items; i0 += 4 * NT) {
-      uint4 w[4];
-      int q[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * NT, o = i / places, t = i < items ? owner[o] : 0, j = i - o * places;
-        q[u] = -1;
-        if (i >= items) continue;
-        if (j < places - 2) {
-          q[u] = v0 + t + j * NT;
-          if (q[u] < v1)
-            w[u] = body[q[u]];
-          else
-            q[u] = -1;
-        } else if (j == places - 2) {
-          if (rank == 0 && t < head) offer(to_f32(x[t]), t);
-        } else if (rank == C - 1 && tail + t < a.V) {
-          offer(to_f32(x[tail + t]), tail + t);
+    // the last floor, and the elements of the places that reach it
+    top.floor = nth_largest64(group_max, a.n_top, lane);
+    const int places = n_list;
+    if (places <= kList) {
+      const Top found = {true, top.floor, cand, &n_cand};
+      auto offer = [&](float v, int id) {
+        if (v >= found.floor || found.floor == -INFINITY) found.add(v, id);
+      };
+      for (int i = tid; i < places * P; i += NT) {
+        const uint64_t key = list[i / P];
+        if (value_of(key) < top.floor) continue;
+        const int id = id_of(key), u = i % P;
+        if (id < head || id >= tail) {
+          if (u == 0) offer(to_f32(x[id]), id);
+          continue;
         }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (q[u] < 0) continue;
+        const int q = (id - head) / E, chunk = (q - v0) / R::PIECES;
+        const bool whole = (chunk + 1) * R::PIECES <= v1 - v0;  // taken P pieces at a time, NT apart
+        if (u && !whole) continue;
         float v[E];
-        unpack<T>(w[u], v);
+        unpack<T>(body[q + u * NT], v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) offer(v[e], head + q[u] * E + e);
+        for (int e = 0; e < E; ++e) offer(v[e], id + u * NT * E + e);
       }
+      __syncthreads();
     }
-    __syncthreads();
-    if (n_list <= kList) {
-      const int n = n_list;
-      for (int i = tid; i < n; i += NT) {
-        const uint64_t key = list[i];
-        int above = 0;
-        for (int j = 0; j < n; ++j) above += list[j] > key;
-        if (above < a.n_top) result[above] = key;
-      }
+    if (places <= kList && n_cand <= kList) {
+      place<NT>(cand, n_cand, a.n_top, result);
     } else {  // too many: each warp keeps the best 32 of its owners' elements, and the warps' lists are merged
+      if (!(own < top.floor)) owner[atomicAdd(&n_owner, 1)] = (uint16_t)tid;
+      __syncthreads();
       uint64_t best = 0;
       auto batch = [&](uint64_t key) {
         if (!__any_sync(0xffffffffu, key > shfl64(best, 31))) return;
@@ -348,55 +570,31 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C) {
     }
   }
   __syncthreads();
-  if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // rank 0 runs
-  if (warp == 0) {
-    Stat b = lane < NW ? stats[lane] : Stat{-INFINITY, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Stat c = {__shfl_xor_sync(0xffffffffu, b.m, o), __shfl_xor_sync(0xffffffffu, b.n, o),
-                      __shfl_xor_sync(0xffffffffu, b.s, o), __shfl_xor_sync(0xffffffffu, b.w, o)};
-      b = lane & o ? join(c, b, a.k) : join(b, c, a.k);
-    }
-    if (C > 1) {
-      if (lane < 2) {
-        const uint64_t v = lane ? ((uint64_t)__float_as_uint(b.w) << 32) | __float_as_uint(b.s)
-                                : ((uint64_t)__float_as_uint(b.n) << 32) | __float_as_uint(b.m);
-        st_cluster_u64(reinterpret_cast<uint64_t*>(&gather_stat[rank]) + lane, 0, v);
-      }
-      if (a.n_top) st_cluster_u64(&gather_key[rank * 32 + lane], 0, result[lane]);
-    } else if (lane == 0) {
-      gather_stat[0] = b;
-    }
-  }
+  if (warp == 0 && C > 1 && a.n_top) st_cluster_u64(&gather_key[rank * 32 + lane], 0, result[lane]);
   if (C > 1) {
     tc::cluster_sync_all();
     if (rank) return;  // nothing reads this CTA's memory
   } else {
     __syncthreads();
   }
-  Stat all_st = gather_stat[0];
-  for (int c = 1; c < C; ++c) all_st = join(all_st, gather_stat[c], a.k);
+  const Stat all_st = C > 1 ? warp_join(lane < C ? gather_stat[lane] : Stat{-INFINITY, 0.f, 0.f, 0.f}, a.k, lane) : gather_stat[0];
   // a row of -inf alone: every token impossible; +inf or NaN: no distribution
   const bool none = all_st.n == 0.f && all_st.s == 0.f, bad = all_st.m == INFINITY || all_st.s != all_st.s;
   const float logS = bad ? NAN : log1pf(all_st.s + (all_st.n - 1.f));
   auto ln_p = [&](float xv) { return none || (xv == -INFINITY && !bad) ? -INFINITY : -((all_st.m - xv) / a.T) - logS; };
   if (tid == NT - 1) {
-    if (a.lp) a.lp[row] = tok < a.V ? ln_p(to_f32(x[tok])) : NAN;
+    if (a.lp) a.lp[row] = tok < a.V ? ln_p(to_f32(x_tok)) : NAN;
     if (tok >= a.V) flag_status(a.status, kDevBounds);
-    if (a.ent) a.ent[row] = none ? 0.f : logS + all_st.w * kLn2 / (all_st.n + all_st.s);
+    if (a.ent) a.ent[row] = none ? 0.f : logS + all_st.w / a.T / (all_st.n + all_st.s);
   }
-  if (tid < (a.n_top ? 32 * C : 0)) {
-    uint64_t key = result[lane];
-    int above = lane;
-    if (C > 1) {
-      key = gather_key[tid];
-      above = 0;
-      for (int j = 0; j < 32 * C; ++j) above += gather_key[j] > key;
-    }
+  if (tid < (a.n_top ? 32 * C : 0) && lane < a.n_top) {
+    const uint64_t key = C > 1 ? gather_key[tid] : result[lane];
+    int above = C > 1 ? 0 : lane;
+    for (int c = 0; c < C && C > 1 && above < a.n_top; ++c)  // descending lists
+      for (int i = 0; i < a.n_top && above < a.n_top && gather_key[c * 32 + i] > key; ++i) ++above;
     if (key && above < a.n_top) {
-      const int id = id_of(key);
-      a.ids[(size_t)row * a.n_top + above] = id;
-      a.top[(size_t)row * a.n_top + above] = ln_p(to_f32(x[id]));
+      a.ids[(size_t)row * a.n_top + above] = id_of(key);
+      a.top[(size_t)row * a.n_top + above] = ln_p(value_of(key));
     }
   }
 }
@@ -426,14 +624,26 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
   a.ids = g->top_ids;
   a.top = g->top_logprobs;
   a.status = g->status;
-  // few rows: a cluster per row, so that every SM reads; a slice keeps four pieces for every thread. Many rows:
-  // CTAs of 256 threads, of which an SM holds several at different places of their rows.
+  // Rows are split among a cluster until there are two CTAs an SM, as long as a slice keeps two stages; CTAs of 512
+  // threads where even then an SM has only one. (bf16 rows of 151,936, n_top 20: 64 rows 17.0 us with one CTA an SM, 19.3 with
+  // two; 200 rows 32.9, 28.8, and 38.7 with three: what a CTA does apart from reading takes about 6 us.)
   const int es = g->dtype == DLITE_F32 ? 4 : 2;
   int C = 1;
-  while (C < kMaxCluster && 2LL * C * g->rows <= 2LL * device_sms() && (long long)g->V * es >= 2LL * C * 512 * 16 * 4) C *= 2;
+  while (C < kMaxCluster && (long long)C * g->rows < 2LL * device_sms() && (long long)g->V * es >= 4LL * C * Ring<256>::BYTES) C *= 2;
+  const bool wide = (long long)C * g->rows <= device_sms();
+  void (*fn)(LpArgs, int, int) = g->dtype == DLITE_F32 ? (wide ? token_logprobs_kernel<float, 512> : token_logprobs_kernel<float, 256>)
+                                                       : (wide ? token_logprobs_kernel<bf16, 512> : token_logprobs_kernel<bf16, 256>);
+  // Residency: as many CTAs an SM as the rows come to (at most 5), no more: with room for more the rows are spread unevenly
+  // (456 rows, three an SM, took as long as 608). What shared memory that leaves holds stages.
+  const int res = (int)std::min(5LL, std::max(1LL, ((long long)C * g->rows + device_sms() - 1) / device_sms()));
+  const int budget = 228 * 1024 / res - 1024 - 13 * 1024;  // the kernel's own shared memory is below 13 KB
+  const int stage_bytes = wide ? Ring<512>::BYTES : Ring<256>::BYTES;
+  const int stages = std::min(budget / stage_bytes, (int)Ring<256>::MAX_STAGES);
+  const int smem = budget / 1024 * 1024;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C * g->rows);
-  cfg.blockDim = dim3(C > 1 ? 512 : 256);
+  cfg.blockDim = dim3(wide ? 512 : 256);
+  cfg.dynamicSmemBytes = (size_t)std::min(smem, 227 * 1024 - 13 * 1024);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -444,7 +654,7 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  void (*fn)(LpArgs, int) = g->dtype == DLITE_F32 ? (C > 1 ? token_logprobs_kernel<float, 512> : token_logprobs_kernel<float, 256>)
-                                                  : (C > 1 ? token_logprobs_kernel<bf16, 512> : token_logprobs_kernel<bf16, 256>);
-  return launch_status(cudaLaunchKernelEx(&cfg, fn, a, C));
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, fn, a, C, stages);
+  return launch_status(e);
 }
