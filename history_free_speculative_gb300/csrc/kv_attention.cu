@@ -1,10 +1,11 @@
 // Attention of a verification block (or a decoded token) over the paged 4-bit cache.
 //
 // The query rows of one KV head, (n_q / n_kv) heads x T tokens in token order, are cut into
-// tiles of 16 MT rows; a CTA takes one tile of one (head, request) and a run of its
-// pages. A page's record (9 KB at d_h 128) comes with one bulk copy into a ring of shared-memory
-// slots; a warp takes every NW-th page of the run whole, with its own slots, running maximum, sum and output
-// (16 MT x d_h fp32 in registers), so warps meet only at the end.
+// tiles of 16 MT rows; how tiles and pages go to CTAs is in kv_attention.cuh. This file has the kernel for
+// float32 queries and for heads of 64; bf16 queries with heads of 128 take the tcgen05 kernel (kv_attention_tc.cu).
+// A page's record (9 KB at d_h 128) comes with one bulk copy into a ring of shared-memory
+// slots; a warp takes every NW-th page of a piece whole, with its own slots, running maximum, sum and output
+// (16 MT x d_h fp32 in registers), so warps meet only at a piece's end.
 //
 // Codes become f16 operands exactly: e2m1 x e4m3 has 6 significant bits between 2^-10 and 2688. Queries are scaled by a power
 // of two per row (largest element in [2^14, 2^15)), so a bf16 query is exact in f16 too; a float32 query
@@ -23,8 +24,11 @@
 
 #include <algorithm>
 
-#include "kv_page.cuh"
-#include "tc_device.cuh"
+#ifndef KV_TC
+#define KV_TC 0
+#endif
+
+#include "kv_attention.cuh"
 
 namespace dlite {
 namespace {
@@ -32,25 +36,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr float kWeightExp = 14.f;  // weights are kept as 2^(s - m + 14)
 
-struct KvAttnArgs {
-  const uint8_t* pages;
-  const int32_t* bt;
-  int n_pages, n_kv, max_pages;
-  int T, n_q, group, row_tiles, window, nsplit;
-  float scale_log2;  // scale log2(e) 2^k_exp
-  float v_scale;     // 2^v_exp
-  const void* q;
-  long long qs;
-  void* out;
-  long long os;
-  float* lse;
-  const int64_t* pos;
-  const int32_t* n_rows;
-  float* part_o;   // [segment][split][row][d_h]
-  float2* part_ml; // [segment][split][row]: running maximum (log2 units) and sum
-  int vec;         // q and out rows on 16 bytes
-  int* status;
-};
+using kv::AttnArgs;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -76,11 +62,11 @@ struct Shape {
   static constexpr int NP = sizeof(T) == 4 ? 2 : 1;  // f16 planes of a query / a weight
   static constexpr int R = 16 * MT;                  // rows of a tile
   static constexpr int REC = kv::rec_bytes(DH);
-  static constexpr int SLOTS = (NP == 1 && DH == 128 ? 3 : DH == 64 ? 4 : 2) * kWarps;
+  static constexpr int SLOTS = (DH == 64 ? 4 : 2) * kWarps;
   static constexpr int STEPS = DH / 16;
   static constexpr int QF = NP * MT * STEPS * 512;   // query fragments, bytes
   static constexpr int LDO = DH + 8;                 // row pitch of the warps' outputs (conflict-free float2 stores)
-  static constexpr int SMEM = SLOTS * REC + QF + R * 12 + 2 * kWarps * R * 4 + SLOTS * 12;
+  static constexpr int SMEM = SLOTS * REC + QF + R * 12 + 2 * kWarps * R * 4 + SLOTS * 12 + (kv::kMaxList + 1) * 4;
   static_assert(kWarps * R * LDO * 4 <= SLOTS * REC, "the warps' outputs share the ring's memory");
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 };
@@ -271,217 +257,235 @@ __device__ __forceinline__ void half_page(const uint8_t* rec, int hf, const uint
 }
 
 template <typename T, int DH, int MT>
-__global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const KvAttnArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const AttnArgs a) {
   using S = Shape<T, DH, MT>;
-  constexpr int R = S::R, REC = S::REC, SLOTS = S::SLOTS, STEPS = S::STEPS, NP = S::NP, LDO = S::LDO;
+  constexpr int R = S::R, REC = S::REC, STEPS = S::STEPS, NP = S::NP, LDO = S::LDO, PER = S::SLOTS / kWarps;
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t* ring = sm;
-  uint4* qf = reinterpret_cast<uint4*>(sm + SLOTS * REC);
-  float* row_sc = reinterpret_cast<float*>(sm + SLOTS * REC + S::QF);
+  uint4* qf = reinterpret_cast<uint4*>(sm + S::SLOTS * REC);
+  float* row_sc = reinterpret_cast<float*>(sm + S::SLOTS * REC + S::QF);
   int2* row_keys = reinterpret_cast<int2*>(row_sc + R);
   float* sm_m = reinterpret_cast<float*>(row_keys + R);  // [warp][row]
   float* sm_l = sm_m + kWarps * R;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm_l + kWarps * R);
-  int* slot_ok = reinterpret_cast<int*>(full + SLOTS);
+  int* slot_ok = reinterpret_cast<int*>(full + S::SLOTS);
+  int* prefix = slot_ok + S::SLOTS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int split = blockIdx.x, h = blockIdx.y / a.row_tiles, rt = blockIdx.y % a.row_tiles, b = blockIdx.z;
   pdl_wait();  // no early trigger: the grid fills the SMs, and a dependent would only take their slots
-
-  const int n = a.n_rows ? min(max(a.n_rows[b], 0), a.T) : a.T;
-  const int r0 = rt * R, r1 = min(r0 + R, n * a.group);
-  if (r0 >= r1) return;
-  const long long p0 = a.pos[b];
-  const long long cap = (long long)a.max_pages * kv::kPage;
-  const int t_lo = r0 / a.group, t_hi = (r1 - 1) / a.group;
-  if (tid == 0 && rt == 0 && split == 0 && (p0 < 0 || p0 + n > cap)) flag_status(a.status, kDevBounds);
-  const int key_end = (int)min(max(p0 + t_hi + 1, 0LL), cap);
-  const int key_beg = a.window ? (int)min(max(p0 + t_lo - a.window + 1, 0LL), cap) : 0;
-  const int pg0 = key_beg / kv::kPage, np = key_end > key_beg ? (key_end + kv::kPage - 1) / kv::kPage - pg0 : 0;
-  const int pa = pg0 + (int)((long long)np * split / a.nsplit), cnt = pg0 + (int)((long long)np * (split + 1) / a.nsplit) - pa;
-  const int32_t* bt = a.bt + (size_t)b * a.max_pages + pa;
-
-  if (tid < SLOTS) tc::mbar_init(tc::su32(full + tid), 1);
+  if (a.stream) kv::build_prefix<R>(a, prefix);
+  if (tid < S::SLOTS) tc::mbar_init(tc::su32(full + tid), 1);
   if (tid == 0) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncthreads();
-  // lane 0 of a warp: page i of the run into its slot (a hole: an empty slot)
-  auto issue = [&](int i, int id) {
-    const int slot = i % SLOTS;
-    const uint32_t bar = tc::su32(full + slot);
-    if (id >= a.n_pages) flag_status(a.status, kDevBounds);
-    const bool ok = id >= 0 && id < a.n_pages;
-    slot_ok[slot] = ok;
-    if (ok) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      tc::mbar_expect_tx(bar, REC);
-      tc::bulk_load(tc::su32(ring + slot * REC), a.pages + ((size_t)id * a.n_kv + h) * REC, REC, bar);
-    } else {
-      mbar_arrive(bar);
-    }
-  };
-  if (lane == 0)
-    for (int i = warp; i < cnt && i < SLOTS; i += kWarps) issue(i, bt[i]);
 
-  // queries: row r of the tile is token (r0 + r) / group, head (r0 + r) % group of the KV head's
-  for (int r = warp; r < R; r += kWarps) {
-    constexpr int E = DH / 32;
-    float v[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = 0.f;
-    if (r0 + r < r1) {
-      const int t = (r0 + r) / a.group, hh = (r0 + r) % a.group;
-      load_q(static_cast<const T*>(a.q) + ((long long)b * a.T + t) * a.qs + (long long)(h * a.group + hh) * DH + lane * E, E, a.vec, v);
-    }
-    float amax = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      amax = fmaxf(amax, fabsf(v[i]));
-      bad |= !(fabsf(v[i]) <= 3.402823466e38f);
-    }
-    amax = warp_max(amax);
-    bad = __any_sync(0xffffffffu, bad);
-    // 2^k takes the largest element into [2^14, 2^15)
-    int k = 0;
-    if (amax > 0.f && !bad) k = min(max(14 - (ilogbf(amax)), -100), 100);
-    const float f = bad ? 0.f : exp2f((float)k);
-    if (lane == 0) {
-      row_sc[r] = bad ? NAN : a.scale_log2 * exp2f((float)-k);
-      const long long last = p0 + min(r0 + r, r1 - 1) / a.group;
-      row_keys[r] = make_int2(a.window ? (int)min(max(last - a.window + 1, 0LL), cap) : 0, (int)min(max(last + 1, 0LL), cap));
-    }
-    const int mt = r / 16, up = (r % 16) >= 8, g = r % 8;
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const int d = lane * E + i, c = d / (DH / 4), st = (d % (DH / 4)) / 4, reg = (d % 4 >= 2 ? 2 : 0) + up;
-      const float x0 = bad ? 0.f : v[i] * f, x1 = bad ? 0.f : v[i + 1] * f;
-      const uint32_t hi = pack_f16(x0, x1);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(qf + (mt * STEPS + st) * 32 + g * 4 + c) + reg;
-      *dst = hi;
-      if constexpr (NP == 2) dst[MT * STEPS * 128] = pack_f16(x0 - f16_lo(hi), x1 - f16_hi(hi));
-    }
-  }
-  __syncthreads();
-
-  float m[MT][2], l[MT][2], o[MT][DH / 8][4];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    m[mt][0] = m[mt][1] = -INFINITY;
-    l[mt][0] = l[mt][1] = 0.f;
-#pragma unroll
-    for (int dt = 0; dt < DH / 8; ++dt) o[mt][dt][0] = o[mt][dt][1] = o[mt][dt][2] = o[mt][dt][3] = 0.f;
-  }
-  // pages wholly inside every row's range need no masks
-  const int full_end = (int)min(max(p0 + t_lo + 1, 0LL), cap);
-  const int full_beg = a.window ? (int)min(max(p0 + t_hi - a.window + 1, 0LL), cap) : 0;
-
-  bool got = true;
-  int i = warp;
-  for (; i < cnt; i += kWarps) {
-    const int slot = i % SLOTS;
-    int id_next = -1;
-    if (lane == 0 && i + SLOTS < cnt) id_next = bt[i + SLOTS];
-    got = __all_sync(0xffffffffu, tc::mbar_wait(tc::su32(full + slot), (uint32_t)(i / SLOTS) & 1u, a.status));
-    if (!got) break;
-    if (slot_ok[slot]) {
-      const uint8_t* rec = ring + slot * REC;
-      const int key0 = (pa + i) * kv::kPage;
-      if (key0 >= full_beg && key0 + kv::kPage <= full_end) {
-        half_page<T, DH, MT, false>(rec, 0, qf, row_sc, row_keys, key0, key_end, m, l, o);
-        half_page<T, DH, MT, false>(rec, 1, qf, row_sc, row_keys, key0 + 32, key_end, m, l, o);
+  kv::Pieces<R> walk(a, prefix);
+  kv::Piece pc;
+  bool any = false, got = true;
+  int n_issue = 0, n_take = 0;  // pages this warp has asked for and taken, over all pieces
+  while (walk.next(pc)) {
+    any = true;
+    const int b = pc.j / a.row_tiles, rt = pc.j % a.row_tiles, h = pc.h;
+    const kv::Tile t = kv::tile_of<R>(a, b, rt);
+    if (tid == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
+      flag_status(a.status, kDevBounds);
+    const int pa = t.pg0 + pc.u0, cnt = min(pc.u1, t.np) - pc.u0;
+    const int32_t* bt = a.bt + (size_t)b * a.max_pages + pa;
+    // lane 0 of a warp: its next page (a hole: an empty slot)
+    auto issue = [&](int id) {
+      const int slot = warp + kWarps * (n_issue % PER);
+      const uint32_t bar = tc::su32(full + slot);
+      if (id >= a.n_pages) flag_status(a.status, kDevBounds);
+      const bool ok = id >= 0 && id < a.n_pages;
+      slot_ok[slot] = ok;
+      if (ok) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc::mbar_expect_tx(bar, REC);
+        tc::bulk_load(tc::su32(ring + slot * REC), a.pages + ((size_t)id * a.n_kv + h) * REC, REC, bar);
       } else {
-        half_page<T, DH, MT, true>(rec, 0, qf, row_sc, row_keys, key0, key_end, m, l, o);
-        if (key0 + 32 < key_end) half_page<T, DH, MT, true>(rec, 1, qf, row_sc, row_keys, key0 + 32, key_end, m, l, o);
+        mbar_arrive(bar);
+      }
+    };
+    for (int i = warp; i < cnt && i < PER * kWarps; i += kWarps) {
+      if (lane == 0) issue(bt[i]);
+      ++n_issue;
+    }
+
+    // queries: row r of the tile is token (r0 + r) / group, head (r0 + r) % group of the KV head's
+    for (int r = warp; r < R; r += kWarps) {
+      constexpr int E = DH / 32;
+      float v[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = 0.f;
+      if (t.r0 + r < t.r1) {
+        const int tk = (t.r0 + r) / a.group, hh = (t.r0 + r) % a.group;
+        load_q(static_cast<const T*>(a.q) + ((long long)b * a.T + tk) * a.qs + (long long)(h * a.group + hh) * DH + lane * E, E, a.vec, v);
+      }
+      float amax = 0.f;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        amax = fmaxf(amax, fabsf(v[i]));
+        bad |= !(fabsf(v[i]) <= 3.402823466e38f);
+      }
+      amax = warp_max(amax);
+      bad = __any_sync(0xffffffffu, bad);
+      // 2^k takes the largest element into [2^14, 2^15)
+      int k = 0;
+      if (amax > 0.f && !bad) k = min(max(14 - (ilogbf(amax)), -100), 100);
+      const float f = bad ? 0.f : exp2f((float)k);
+      if (lane == 0) {
+        row_sc[r] = bad ? NAN : a.scale_log2 * exp2f((float)-k);
+        const long long last = t.p0 + min(t.r0 + r, t.r1 - 1) / a.group;
+        row_keys[r] = make_int2(a.window ? (int)min(max(last - a.window + 1, 0LL), t.cap) : 0, (int)min(max(last + 1, 0LL), t.cap));
+      }
+      const int mt = r / 16, up = (r % 16) >= 8, g = r % 8;
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const int d = lane * E + i, c = d / (DH / 4), st = (d % (DH / 4)) / 4, reg = (d % 4 >= 2 ? 2 : 0) + up;
+        const float x0 = bad ? 0.f : v[i] * f, x1 = bad ? 0.f : v[i + 1] * f;
+        const uint32_t hi = pack_f16(x0, x1);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(qf + (mt * STEPS + st) * 32 + g * 4 + c) + reg;
+        *dst = hi;
+        if constexpr (NP == 2) dst[MT * STEPS * 128] = pack_f16(x0 - f16_lo(hi), x1 - f16_hi(hi));
       }
     }
-    __syncwarp();
-    if (lane == 0 && i + SLOTS < cnt) issue(i + SLOTS, id_next);
-  }
-  if (!__syncthreads_and(got)) {  // a copy never landed: let the issued ones finish (bounded) and leave
-    if (!got && lane == 0)
-      for (int k = i; k < cnt && k < i + SLOTS; k += kWarps)
-        tc::mbar_wait(tc::su32(full + k % SLOTS), (uint32_t)(k / SLOTS) & 1u, a.status);
     __syncthreads();
-    return;
-  }
 
-  // the warps' rows joined: maxima, then outputs scaled to the common maximum, summed in warp order
+    float m[MT][2], l[MT][2], o[MT][DH / 8][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
-      l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
-      if ((lane & 3) == 0) sm_m[warp * R + mt * 16 + e * 8 + (lane >> 2)] = m[mt][e];
+      for (int dt = 0; dt < DH / 8; ++dt) o[mt][dt][0] = o[mt][dt][1] = o[mt][dt][2] = o[mt][dt][3] = 0.f;
     }
-  __syncthreads();
-  float* ob = reinterpret_cast<float*>(ring);
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = mt * 16 + e * 8 + (lane >> 2);
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * R + r]);
-      const float f = m[mt][e] == -INFINITY ? 0.f : tc::ex2_approx(m[mt][e] - M);
-      if ((lane & 3) == 0) sm_l[warp * R + r] = l[mt][e] * f;
-      float* dst = ob + (warp * R + r) * LDO + 2 * (lane & 3);
-#pragma unroll
-      for (int dt = 0; dt < DH / 8; ++dt)
-        *reinterpret_cast<float2*>(dst + dt * 8) = make_float2(o[mt][dt][2 * e] * f, o[mt][dt][2 * e + 1] * f);
+    // pages wholly inside every row's range need no masks
+    const int full_end = (int)min(max(t.p0 + t.t_lo + 1, 0LL), t.cap);
+    const int full_beg = a.window ? (int)min(max(t.p0 + t.t_hi - a.window + 1, 0LL), t.cap) : 0;
+
+    for (int i = warp; i < cnt; i += kWarps) {
+      const int slot = warp + kWarps * (n_take % PER);
+      const bool more = i + PER * kWarps < cnt;
+      int id_next = -1;
+      if (lane == 0 && more) id_next = bt[i + PER * kWarps];
+      // a copy that never lands: no further page is taken, the status says so, the barriers below are kept
+      got = got && __all_sync(0xffffffffu, tc::mbar_wait(tc::su32(full + slot), (uint32_t)(n_take / PER) & 1u, a.status));
+      ++n_take;
+      if (got && slot_ok[slot]) {
+        const uint8_t* rec = ring + slot * REC;
+        const int key0 = (pa + i) * kv::kPage;
+        if (key0 >= full_beg && key0 + kv::kPage <= full_end) {
+          half_page<T, DH, MT, false>(rec, 0, qf, row_sc, row_keys, key0, t.key_end, m, l, o);
+          half_page<T, DH, MT, false>(rec, 1, qf, row_sc, row_keys, key0 + 32, t.key_end, m, l, o);
+        } else {
+          half_page<T, DH, MT, true>(rec, 0, qf, row_sc, row_keys, key0, t.key_end, m, l, o);
+          if (key0 + 32 < t.key_end) half_page<T, DH, MT, true>(rec, 1, qf, row_sc, row_keys, key0 + 32, t.key_end, m, l, o);
+        }
+      }
+      __syncwarp();
+      if (more) {
+        if (lane == 0 && got) issue(id_next);
+        ++n_issue;
+      }
     }
-  __syncthreads();
-  const size_t seg = ((size_t)b * a.n_kv + h) * a.row_tiles + rt;
-  for (int u = tid; u < R * (DH / 4); u += 32 * kWarps) {
-    const int r = u / (DH / 4), d = (u % (DH / 4)) * 4;
-    if (r0 + r >= r1) break;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f, M = -INFINITY;
+
+    // the warps' rows joined: maxima, then outputs scaled to the common maximum, summed in warp order
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 v = *reinterpret_cast<const float4*>(ob + (w * R + r) * LDO + d);
-      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-      L += sm_l[w * R + r];
-      M = fmaxf(M, sm_m[w * R + r]);
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
+        l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
+        if ((lane & 3) == 0) sm_m[warp * R + mt * 16 + e * 8 + (lane >> 2)] = m[mt][e];
+      }
+    __syncthreads();
+    float* ob = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = mt * 16 + e * 8 + (lane >> 2);
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * R + r]);
+        const float f = m[mt][e] == -INFINITY ? 0.f : tc::ex2_approx(m[mt][e] - M);
+        if ((lane & 3) == 0) sm_l[warp * R + r] = l[mt][e] * f;
+        float* dst = ob + (warp * R + r) * LDO + 2 * (lane & 3);
+#pragma unroll
+        for (int dt = 0; dt < DH / 8; ++dt)
+          *reinterpret_cast<float2*>(dst + dt * 8) = make_float2(o[mt][dt][2 * e] * f, o[mt][dt][2 * e + 1] * f);
+      }
+    __syncthreads();
+    const bool whole = pc.u0 == 0 && pc.u1 == pc.nu;
+    for (int u = tid; u < R * (DH / 4); u += 32 * kWarps) {
+      const int r = u / (DH / 4), d = (u % (DH / 4)) * 4;
+      if (t.r0 + r >= t.r1) break;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f, M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(ob + (w * R + r) * LDO + d);
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        L += sm_l[w * R + r];
+        M = fmaxf(M, sm_m[w * R + r]);
+      }
+      if (whole) {
+        const int tk = (t.r0 + r) / a.group, hq = h * a.group + (t.r0 + r) % a.group;
+        const long long row = (long long)b * a.T + tk;
+        const float inv = L == 0.f ? 0.f : a.v_scale / L;
+        store4(static_cast<T*>(a.out) + row * a.os + (long long)hq * DH + d,
+               make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), a.vec);
+        if (a.lse && d == 0) a.lse[row * a.n_q + hq] = kv::lse_of(M, L, a.weight_exp);
+      } else {
+        const size_t pr = kv::part_row(pc, R) + r;
+        *reinterpret_cast<float4*>(a.part_o + pr * DH + d) = acc;
+        if (d == 0) a.part_ml[pr] = make_float2(M, L);
+      }
     }
-    if (a.nsplit == 1) {
-      const int t = (r0 + r) / a.group, hq = h * a.group + (r0 + r) % a.group;
-      const long long row = (long long)b * a.T + t;
-      const float inv = L == 0.f ? 0.f : a.v_scale / L;
-      store4(static_cast<T*>(a.out) + row * a.os + (long long)hq * DH + d,
-             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), a.vec);
-      if (a.lse && d == 0) a.lse[row * a.n_q + hq] = L == 0.f ? -INFINITY : (M - kWeightExp + log2f(L)) * 0.6931471805599453f;
-    } else {
-      const size_t pr = (seg * a.nsplit + split) * R + r;
-      *reinterpret_cast<float4*>(a.part_o + pr * DH + d) = acc;
-      if (d == 0) a.part_ml[pr] = make_float2(M, L);
-    }
+    // the ring is the copies' again
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
   }
+  if (!got && lane == 0)  // let the copies in flight end (bounded) before the memory is given back
+    for (int i = 0; i < PER && n_take + i < n_issue; ++i)
+      tc::mbar_wait(tc::su32(full + warp + kWarps * ((n_take + i) % PER)), (uint32_t)((n_take + i) / PER) & 1u, a.status);
+  if (a.stream && tid == 0) a.joins[blockIdx.x] = walk.join_of(any, pc);
 }
 
-// Joins the splits of a tile: one warp per row, in split order.
+// Joins the pieces of the segment that begins in CTA blockIdx.x's run and goes on after it: one warp per row, in order.
 template <typename T, int DH, int R>
-__global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvAttnArgs a) {
+__global__ void __launch_bounds__(256) kv_attention_join_kernel(const AttnArgs a) {
   pdl_trigger();
   pdl_wait();
+  const int2 jn = a.joins[blockIdx.x];
+  if (jn.y < 1) return;
   const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const size_t seg = blockIdx.x;
-  const int rt = (int)(seg % a.row_tiles), h = (int)(seg / a.row_tiles % a.n_kv), b = (int)(seg / a.row_tiles / a.n_kv);
+  const int h = jn.x % a.n_kv, j = jn.x / a.n_kv, b = j / a.row_tiles, rt = j % a.row_tiles;
   const int n = a.n_rows ? min(max(a.n_rows[b], 0), a.T) : a.T;
   if (rt * R + r >= n * a.group) return;
-  const size_t pr = seg * a.nsplit * R + r;
+  // piece k: slot 1 of this CTA, then slot 0 of those after it
+  auto row_of = [&](int k) { return ((size_t)(blockIdx.x + k) * 2 + (k == 0)) * R + r; };
   float M = -INFINITY;
-  for (int s = lane; s < a.nsplit; s += 32) M = fmaxf(M, a.part_ml[pr + (size_t)s * R].x);
+  for (int k = lane; k < jn.y; k += 32) M = fmaxf(M, a.part_ml[row_of(k)].x);
   M = warp_max(M);
   float L = 0.f, acc[DH / 32];
 #pragma unroll
   for (int i = 0; i < DH / 32; ++i) acc[i] = 0.f;
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float2 ml = a.part_ml[pr + (size_t)s * R];
-    const float f = ml.x == -INFINITY ? 0.f : tc::ex2_approx(ml.x - M);
-    L = fmaf(f, ml.y, L);
+  for (int k0 = 0; k0 < jn.y; k0 += 32) {
+    float w = 0.f, lw = 0.f;
+    if (k0 + lane < jn.y) {
+      const float2 ml = a.part_ml[row_of(k0 + lane)];
+      w = ml.x == -INFINITY ? 0.f : tc::ex2_approx(ml.x - M);
+      lw = w * ml.y;
+    }
+    L += warp_sum(lw);
+    const int kn = min(32, jn.y - k0);
+#pragma unroll 4
+    for (int k = 0; k < kn; ++k) {
+      const float f = __shfl_sync(0xffffffffu, w, k);
+      const float* o = a.part_o + row_of(k0 + k) * DH + lane;
 #pragma unroll
-    for (int i = 0; i < DH / 32; ++i) acc[i] = fmaf(f, a.part_o[(pr + (size_t)s * R) * DH + 32 * i + lane], acc[i]);
+      for (int i = 0; i < DH / 32; ++i) acc[i] = fmaf(f, o[32 * i], acc[i]);
+    }
   }
   const int t = (rt * R + r) / a.group, hq = h * a.group + (rt * R + r) % a.group;
   const long long row = (long long)b * a.T + t;
@@ -494,25 +498,23 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvAttnArgs
     else
       out[32 * i + lane] = __float2bfloat16_rn(acc[i] * inv);
   }
-  if (a.lse && lane == 0) a.lse[row * a.n_q + hq] = L == 0.f ? -INFINITY : (M - kWeightExp + log2f(L)) * 0.6931471805599453f;
+  if (a.lse && lane == 0) a.lse[row * a.n_q + hq] = kv::lse_of(M, L, a.weight_exp);
 }
 
-struct Plan {
-  int mt = 1, row_tiles = 1, nsplit = 1;
-  size_t segs = 0;
-  size_t bytes(int d_h) const { return nsplit == 1 ? 0 : segs * nsplit * 16 * mt * ((size_t)d_h * 4 + 8); }
-};
-
-Plan make_plan(const dlite_kv_attention_args& g) {
-  Plan p;
+kv::AttnPlan make_plan(const dlite_kv_attention_args& g) {
+  kv::AttnPlan p;
   const int rows = g.n_q / g.cache.n_kv * g.T;
+  p.tc = KV_TC && g.dtype == DLITE_BF16 && g.cache.d_h == 128;
   // 32-row tiles halve the conversions per row; float32 queries have twice the fragments and would spill
-  p.mt = rows <= 16 || g.dtype == DLITE_F32 ? 1 : 2;
-  p.row_tiles = (rows + 16 * p.mt - 1) / (16 * p.mt);
-  p.segs = (size_t)g.B * g.cache.n_kv * p.row_tiles;
-  // one CTA per SM: as many splits of a tile as fill the SMs, each with a page for every warp at least
-  const int sms = device_sms();
-  p.nsplit = (int)std::max<size_t>(1, std::min<size_t>(sms / p.segs, (g.cache.max_pages + kWarps - 1) / kWarps));
+  p.rows = rows <= 16 || g.dtype == DLITE_F32 ? 16 : 32;
+  p.row_tiles = (rows + p.rows - 1) / p.rows;
+  p.unit = p.tc ? 2 : 1;
+  p.min_quota = p.tc ? 4 : kWarps;  // a page for every warp
+  p.grid = device_sms();            // one CTA an SM: its shared memory is the ring
+  // segments that a CTA's least run holds whole are not cut
+  const int most = (g.cache.max_pages + p.unit - 1) / p.unit;
+  p.stream = most > p.min_quota && (long long)g.B * p.row_tiles <= kv::kMaxList;
+  if (!p.stream) p.grid = (int)std::min<long long>((long long)g.B * p.row_tiles * g.cache.n_kv, p.grid);
   return p;
 }
 
@@ -527,23 +529,35 @@ int check_attention(const dlite_kv_attention_args* g) {
   if (g->q_stride < cols || g->out_stride < cols || ((uintptr_t)g->q | (uintptr_t)g->out) % es || ((uintptr_t)g->lse & 3))
     return DLITE_ERR_INVALID_ARG;
   const long long rows = (long long)(g->n_q / c.n_kv) * g->T;
-  if (rows > (1 << 20) || c.n_kv * ((rows + 15) / 16) > 65535) return DLITE_ERR_UNSUPPORTED_SHAPE;
+  if (rows > (1 << 20) || (long long)c.n_pages * c.n_kv > 0x7fffffffLL || g->B * ((rows + 15) / 16) * c.n_kv > 0x7fffffffLL)
+    return DLITE_ERR_UNSUPPORTED_SHAPE;
   return DLITE_OK;
 }
 
+template <typename T, int DH, int R>
+cudaError_t join(const AttnArgs& a, const kv::AttnPlan& p, cudaStream_t s) {
+  if (!p.stream) return cudaSuccess;
+  return launch_pdl(kv_attention_join_kernel<T, DH, R>, dim3(p.grid, R / 8), dim3(256), 0, s, a);
+}
 template <typename T, int DH, int MT>
-cudaError_t launch(const KvAttnArgs& a, const Plan& p, int B, cudaStream_t s) {
+cudaError_t launch(const AttnArgs& a, const kv::AttnPlan& p, cudaStream_t s) {
   using S = Shape<T, DH, MT>;
   cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, DH, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kv_attention_kernel<T, DH, MT>, dim3(p.nsplit, a.n_kv * p.row_tiles, B), dim3(32 * kWarps), S::SMEM, s, a);
-  if (e != cudaSuccess || p.nsplit == 1) return e;
-  return launch_pdl(kv_attention_join_kernel<T, DH, S::R>, dim3((unsigned)p.segs, S::R / 8), dim3(256), 0, s, a);
+  e = launch_pdl(kv_attention_kernel<T, DH, MT>, dim3(p.grid), dim3(32 * kWarps), S::SMEM, s, a);
+  return e != cudaSuccess ? e : join<T, DH, S::R>(a, p, s);
 }
-cudaError_t launch(const KvAttnArgs& a, const Plan& p, int B, int d_h, int dtype, cudaStream_t s) {
-  if (dtype == DLITE_F32) return d_h == 128 ? launch<float, 128, 1>(a, p, B, s) : launch<float, 64, 1>(a, p, B, s);
-  if (d_h == 128) return p.mt == 1 ? launch<bf16, 128, 1>(a, p, B, s) : launch<bf16, 128, 2>(a, p, B, s);
-  return p.mt == 1 ? launch<bf16, 64, 1>(a, p, B, s) : launch<bf16, 64, 2>(a, p, B, s);
+cudaError_t launch(const AttnArgs& a, const kv::AttnPlan& p, int d_h, int dtype, cudaStream_t s) {
+#if KV_TC
+  if (p.tc) {
+    const cudaError_t e = kv::launch_attention_tc(a, p, s);
+    return e != cudaSuccess ? e : p.rows == 16 ? join<bf16, 128, 16>(a, p, s) : join<bf16, 128, 32>(a, p, s);
+  }
+#else
+  if (dtype == DLITE_BF16 && d_h == 128) return p.rows == 16 ? launch<bf16, 128, 1>(a, p, s) : launch<bf16, 128, 2>(a, p, s);
+#endif
+  if (dtype == DLITE_F32) return d_h == 128 ? launch<float, 128, 1>(a, p, s) : launch<float, 64, 1>(a, p, s);
+  return p.rows == 16 ? launch<bf16, 64, 1>(a, p, s) : launch<bf16, 64, 2>(a, p, s);
 }
 
 }  // namespace
@@ -558,21 +572,25 @@ extern "C" int dlite_kv_attention(const dlite_kv_attention_args* g, dlite_stream
   using namespace dlite;
   if (const int rc = check_attention(g)) return rc;
   const dlite_kv_cache& c = g->cache;
-  const Plan p = make_plan(*g);
+  const kv::AttnPlan p = make_plan(*g);
   const size_t need = p.bytes(c.d_h);
   if (need && (!g->workspace || g->workspace_bytes < need || ((uintptr_t)g->workspace & 15))) return DLITE_ERR_INVALID_ARG;
-  KvAttnArgs a = {};
+  AttnArgs a = {};
   a.pages = static_cast<const uint8_t*>(c.pages);
   a.bt = c.block_table;
   a.n_pages = c.n_pages;
   a.n_kv = c.n_kv;
   a.max_pages = c.max_pages;
+  a.B = g->B;
   a.T = g->T;
   a.n_q = g->n_q;
   a.group = g->n_q / c.n_kv;
   a.row_tiles = p.row_tiles;
   a.window = g->window;
-  a.nsplit = p.nsplit;
+  a.unit = p.unit;
+  a.min_quota = p.min_quota;
+  a.stream = p.stream;
+  a.weight_exp = p.tc ? kv::kTcWeightExp : kWeightExp;
   a.scale_log2 = (float)ldexp((double)g->scale * 1.4426950408889634, c.k_exp);
   a.v_scale = ldexpf(1.f, c.v_exp);
   a.q = g->q;
@@ -583,9 +601,10 @@ extern "C" int dlite_kv_attention(const dlite_kv_attention_args* g, dlite_stream
   a.pos = g->pos;
   a.n_rows = g->n_rows;
   a.part_o = static_cast<float*>(g->workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + p.segs * p.nsplit * 16 * p.mt * (size_t)c.d_h);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)p.grid * 2 * p.rows * c.d_h);
+  a.joins = reinterpret_cast<int2*>(a.part_ml + (size_t)p.grid * 2 * p.rows);
   const int V = g->dtype == DLITE_F32 ? 4 : 8;
   a.vec = !(((uintptr_t)g->q | (uintptr_t)g->out) & 15) && g->q_stride % V == 0 && g->out_stride % V == 0;
   a.status = g->status;
-  return launch_status(launch(a, p, g->B, c.d_h, g->dtype, (cudaStream_t)stream));
+  return launch_status(launch(a, p, c.d_h, g->dtype, (cudaStream_t)stream));
 }
