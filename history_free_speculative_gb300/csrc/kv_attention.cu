@@ -25,7 +25,7 @@
 #include <algorithm>
 
 #ifndef KV_TC
-#define KV_TC 0
+#define KV_TC 1
 #endif
 
 #include "kv_attention.cuh"
@@ -590,7 +590,7 @@ extern "C" int dlite_kv_attention(const dlite_kv_attention_args* g, dlite_stream
   a.unit = p.unit;
   a.min_quota = p.min_quota;
   a.stream = p.stream;
-  a.weight_exp = p.tc ? kv::kTcWeightExp : kWeightExp;
+  a.weight_exp = p.tc ? 0.f : kWeightExp;  // the tcgen05 kernel leaves its offset itself
   a.scale_log2 = (float)ldexp((double)g->scale * 1.4426950408889634, c.k_exp);
   a.v_scale = ldexpf(1.f, c.v_exp);
   a.q = g->q;

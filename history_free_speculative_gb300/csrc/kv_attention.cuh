@@ -179,7 +179,6 @@ struct AttnPlan {
   bool stream = false;
   size_t bytes(int d_h) const { return stream ? (size_t)grid * (2 * rows * ((size_t)d_h * 4 + 8) + 8) : 0; }
 };
-constexpr float kTcWeightExp = 10.f;  // of the tcgen05 kernel's weights
 cudaError_t launch_attention_tc(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
 }  // namespace kv

@@ -1,0 +1,662 @@
+// Attention over the paged 4-bit cache on the tcgen05 tensor cores: bf16 queries, heads of 128.
+//
+// A unit is a tile of 128 keys (two pages) of one KV head. The keys are the rows of the first product and the columns of a head
+// the rows of the second, so both cached operands are A operands, and those can come from tensor memory:
+//   S^T [128 keys x N rows] = K [128 x 128] Q^T,   O^T [128 columns x N rows] += V^T [128 x 128 keys] P^T.
+// A thread of the dequantising warps owns one lane of tensor memory: one key (its 64 bytes of codes, 8 scales) or one
+// column (its 64 bytes of codes along the tokens, the scales of 128 tokens). It turns its codes into f16 (e2m1 x e4m3 is exact)
+// and writes them with tcgen05.st, so the cache never passes through shared memory a second time. N = 16 or 32
+// query rows; Q^T and P^T are the B operands in shared memory.
+// Warps: 0-3 keys (and the value scales as f16, once for the 16 columns that share them), 4-7 values, 8-15 softmax and
+// output (thread = key, then column). Warp 0 also issues the copies, warp 1 the first product, warp 4 the second, each where its
+// own work next waits for that: 16 warps leave 128 registers a thread, which the softmax needs.
+// The softmax warps are two groups that take the tiles in turn, each with its own scores, weights, maxima, sums and O, joined at
+// a piece's end: one group's latencies pass under the other's tile (one group alone took 3,300 clocks a tile). A group keeps one
+// reference m per row, moved only when a score passes it by more than 2^4 (a vote of its 128 threads per tile); only then
+// are exact maxima formed and O, the sums rescaled. Weights are 2^(s - m + 10) <= 2^14, rounded to f16: weights down
+// to 2^-35 of the reference count, and the largest score is never below it. Queries are scaled by one power of two per
+// tile into f16's range: exact for bf16 elements down to 2^-32 of the tile's largest, and off by 2^-39 of that below.
+// The issuing warps stay converged and elect a lane: 17 clocks an MMA, 46 from a branch on the lane (the operands then
+// go from vector to uniform registers one by one).
+// mma.sync does both products of a 32-row tile in 8 clocks a key an SM (measured 2.0 per m16n8k16), above the 6.8 that the bytes take
+// at the copy rate of HBM, and needs its operands and outputs in registers: the mma.sync kernel ran at 19.
+#include <math.h>
+
+#include "kv_attention.cuh"
+#include "tc_gemm.h"
+
+namespace dlite {
+namespace kv {
+namespace {
+
+constexpr int DH = 128, REC = rec_bytes(DH), TILE = 2 * REC;
+constexpr int kStages = 9;
+constexpr int kThreads = 16 * 32;  // four warps a scheduler: 128 registers each
+constexpr int kAhead = kStages - 2;  // tiles the copies are ahead of the keys
+// a stage: key codes of both pages (rows of 64 B, 64-byte swizzle), value codes (rows of 32 B, 32-byte swizzle), scales
+constexpr int kV = 8192, kS = 16384;
+// tensor memory columns: K and V^T tiles twice, S^T twice, O^T
+constexpr int kTmK = 0, kTmV = 128, kTmS = 256, kTmCols = 512;
+constexpr float kTcWeightExp = 10.f;
+constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key
+
+template <int N>
+struct Smem {
+  static constexpr int Q = kStages * TILE;           // [2 halves][N rows][128 B], 128-byte swizzle
+  static constexpr int P = Q + N * 256;              // [2][128 keys][N rows] f16, rows of N contiguous
+  static constexpr int VS = P + 2 * 128 * N * 2;     // [2][8 blocks][128 tokens] f16: value scales
+  static constexpr int ROWS = VS + 2 * 2048;         // floats: offset [2][N], alpha [2][N], l [2][4][N], red [2][4][N], tile max
+  static constexpr int KEYS = ROWS + 20 * N * 4 + 64;  // int2: keys a row sees
+  static constexpr int OUT = KEYS + N * 8;           // int64: where a row's output and lse go
+  static constexpr int BARS = OUT + N * 16;
+  static constexpr int NBARS = 2 * kStages + 17;
+  static constexpr int OK = BARS + NBARS * 8;        // per stage: which of its pages came
+  static constexpr int TM = OK + kStages * 4;
+  static constexpr int PREFIX = TM + 8;
+  static constexpr int BYTES = PREFIX + (kMaxList + 1) * 4 + 1024;  // alignment of the swizzled stages
+  static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// N columns of this warp's 32 lanes; complete on return
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
+  uint32_t r[N / 16][16];
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) tc::tmem_ld16_nowait(addr + 16 * i, r[i]);
+  tc::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i / 16][i % 16]);
+}
+// 8 or 16 columns
+template <int M>
+__device__ __forceinline__ void tmem_ld_part(uint32_t addr, float (&v)[M]) {
+  if constexpr (M == 16) {
+    tmem_ld<16>(addr, v);
+  } else {
+    static_assert(M == 8, "rows of a group");
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) {
+    uint32_t r[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[16 * i + e]);
+    tmem_st16(addr + 16 * i, r);
+  }
+}
+// D (tensor memory) (+)= A (tensor memory) B (shared memory)
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+// f16 operands, fp32 accumulator; B with its rows contiguous along N where b_mn
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// P^T as B operand, N contiguous: 8 keys of N x 2 bytes form one swizzle atom, atoms follow each other along the keys
+template <int N>
+__device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
+  constexpr uint32_t atom = 8 * N * 2;
+  constexpr uint64_t swizzle = N == 32 ? 4 : 6;  // 64 or 32 bytes
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(atom >> 4) << 16) | ((uint64_t)(atom >> 4) << 32) | ((uint64_t)1 << 46) |
+         (swizzle << 61);
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(z)
+      : "memory");
+}
+// Whether q holds in any of the 128 threads of softmax group g (a barrier among them)
+__device__ __forceinline__ bool any_of_group(bool q, int g) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, r;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred r, %2, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)q), "r"(1 + g)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_barrier(int g) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + g) : "memory"); }
+__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attention_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
+  using S = Smem<N>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024 - (tc::su32(raw) & 1023)) & 1023);
+  const uint32_t sb = tc::su32(sm);
+  float* rows_f = reinterpret_cast<float*>(sm + S::ROWS);
+  auto row_off = [&](int g) { return rows_f + g * N; };              // 10 - m: a weight is 2^(score + offset)
+  auto row_alpha = [&](int g) { return rows_f + (2 + g) * N; };
+  auto row_l = [&](int g) { return rows_f + (4 + 4 * g) * N; };      // [warp][row]
+  auto row_red = [&](int g) { return rows_f + (12 + 4 * g) * N; };   // [warp][row]
+  float* q_max = rows_f + 20 * N;                                    // [8 warps]
+  int2* row_keys = reinterpret_cast<int2*>(sm + S::KEYS);
+  long long* row_out = reinterpret_cast<long long*>(sm + S::OUT);  // [row] of out, [N + row] of lse
+  int* stage_ok = reinterpret_cast<int*>(sm + S::OK);
+  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + S::TM);
+  int* prefix = reinterpret_cast<int*>(sm + S::PREFIX);
+  const uint32_t bars = sb + S::BARS;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+  auto bar = [&](int kind, int buf) { return bars + 8 * (2 * kStages + 2 * kind + buf); };
+  enum { kReady, kFree, vReady, vFree, sFull, sFree, pReady, cReady };   // each twice; then q_ready
+  const uint32_t q_ready = bars + 8 * (2 * kStages + 16);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  pdl_wait();  // no early trigger: the grid fills the SMs
+  if (a.stream) build_prefix<N>(a, prefix);
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(full(s), 1);
+      tc::mbar_init(empty(s), 8);  // a warp of keys or values each
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(kReady, i), 4);
+      tc::mbar_init(bar(kFree, i), 1);
+      tc::mbar_init(bar(vReady, i), 4);
+      tc::mbar_init(bar(vFree, i), 1);  // the second product is done: V tile, P tile and O
+      tc::mbar_init(bar(sFull, i), 1);
+      tc::mbar_init(bar(sFree, i), 4);
+      tc::mbar_init(bar(pReady, i), 4);
+      tc::mbar_init(bar(cReady, i), 4);  // value scales
+    }
+    tc::mbar_init(q_ready, 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tm_slot)), "r"(kTmCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = *tm_slot;
+  constexpr uint32_t tmO = kTmS + 2 * N;
+
+  Pieces<N> walk(a, prefix);
+  Piece pc;
+  bool any = false, ok = true;
+  int it = 0;  // tiles so far, over all pieces: buffer it & 1, stage it % kStages
+  // Wait until a buffer (or stage) has been filled for its `turn`-th use, the whole warp; false once a wait has run out.
+  auto wait_turn = [&](uint32_t b, int turn) {
+    return ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(b, (uint32_t)turn & 1u, a.status));
+  };
+  // ... until its use before the `turn`-th is over: nothing to wait for in the first
+  auto wait_left = [&](uint32_t b, int turn) { return turn == 0 ? ok : wait_turn(b, turn - 1); };
+
+  if (warp < 4) {  // ---------------------------------------------------------------- keys, value scales
+    const int page = warp >> 1, row = 32 * (warp & 1) + lane;  // key 32 warp + lane of the tile
+    const int blk = tid >> 4, tok = (tid & 15) * 8;            // scales of 8 tokens of a block of 16 columns
+    const bool one = elect_one();
+    // copies (warp 0): a walk of their own, kAhead tiles ahead
+    Pieces<N> copies(a, prefix);
+    Piece cp;
+    int c_it = 0, c_u = 0, c_np = 0, id0 = -1, id1 = -1;
+    const int32_t* c_bt = nullptr;
+    cp.u1 = 0;
+    auto page_of = [&](int i) { return i < c_np ? c_bt[i] : -1; };
+    auto copy_next = [&]() {
+      if (c_u >= cp.u1) {
+        if (!copies.next(cp)) return false;
+        const int b = cp.j / a.row_tiles;
+        const Tile t = tile_of<N>(a, b, cp.j % a.row_tiles);
+        c_bt = a.bt + (size_t)b * a.max_pages + t.pg0;
+        c_np = t.np;
+        c_u = cp.u0;
+        id0 = page_of(2 * c_u);
+        id1 = page_of(2 * c_u + 1);
+      }
+      const int st = c_it % kStages;
+      if (!wait_left(empty(st), c_it / kStages)) return false;
+      const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
+      if (one) {
+        if (id0 >= a.n_pages || id1 >= a.n_pages) flag_status(a.status, kDevBounds);
+        stage_ok[st] = came;
+        if (came) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          tc::mbar_expect_tx(full(st), (came == 3 ? 2 : 1) * REC);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            if (!(came >> p & 1)) continue;
+            const long long rec = (long long)(p ? id1 : id0) * a.n_kv + cp.h;
+            const uint32_t dst = sb + st * TILE;
+            tma_load_3d(dst + p * 4096, &mk, full(st), (int)rec);
+            tma_load_3d(dst + kV + p * 4096, &mv, full(st), (int)rec);
+            tc::bulk_load(dst + kS + p * 1024, a.pages + rec * REC + ks_off(DH), 1024, full(st));
+          }
+        } else {
+          tc::mbar_arrive(full(st));
+        }
+      }
+      __syncwarp();
+      ++c_it;
+      ++c_u;
+      id0 = c_u < cp.u1 ? page_of(2 * c_u) : -1;  // read a tile before they are used
+      id1 = c_u < cp.u1 ? page_of(2 * c_u + 1) : -1;
+      return true;
+    };
+    if (warp == 0)
+      for (int i = 0; i < kAhead && copy_next(); ++i) {
+      }
+    int pieces = 0;
+    while (walk.next(pc)) {
+      const Tile t = tile_of<N>(a, pc.j / a.row_tiles, pc.j % a.row_tiles);
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int st = it % kStages, buf = it & 1;
+        // the scales' buffer is the values' of tile it - 2
+        if (!wait_turn(full(st), it / kStages) || !wait_left(bar(kFree, buf), it >> 1) || !wait_left(bar(vReady, buf), it >> 1)) break;
+        tc::fence_after();
+        const uint8_t* stage = sm + st * TILE;
+        {
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + kS + (tok >> 6) * 1024 + 512 + blk * 64 + (tok & 63));
+          uint32_t s[4] = {fp8x2_to_f16x2((uint16_t)w.x), fp8x2_to_f16x2((uint16_t)(w.x >> 16)), fp8x2_to_f16x2((uint16_t)w.y),
+                           fp8x2_to_f16x2((uint16_t)(w.y >> 16))};
+          // keys past the end, or of a page that is not there, hold anything, a NaN scale too: their values are 0
+          const int came = stage_ok[st], left = t.key_end - (t.pg0 + 2 * u) * kPage;
+          if (came != 3 || left < 128) {
+            const int valid = (came >> (tok >> 6) & 1) ? left - tok : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = 2 * i + 1 < valid ? s[i] : 2 * i < valid ? s[i] & 0xffffu : 0u;
+          }
+          *reinterpret_cast<uint4*>(sm + S::VS + buf * 2048 + blk * 256 + tok * 2) = make_uint4(s[0], s[1], s[2], s[3]);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(cReady, buf));
+        const uint8_t* base = stage + page * 4096 + row * 64;
+        const uint2 sc = *reinterpret_cast<const uint2*>(stage + kS + page * 1024 + row * 8);
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[32];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint4 w = *reinterpret_cast<const uint4*>(base + (((2 * half + q) ^ ((row >> 1) & 3)) << 4));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t s2 = fp8x2_to_f16x2((uint16_t)((half ? sc.y : sc.x) >> (16 * q)));
+            const uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t s = i < 2 ? s0 : s1;
+              r[16 * q + 4 * i] = mul_f16x2(fp4x2_of<0>(ww[i]), s);
+              r[16 * q + 4 * i + 1] = mul_f16x2(fp4x2_of<1>(ww[i]), s);
+              r[16 * q + 4 * i + 2] = mul_f16x2(fp4x2_of<2>(ww[i]), s);
+              r[16 * q + 4 * i + 3] = mul_f16x2(fp4x2_of<3>(ww[i]), s);
+            }
+          }
+          tmem_st32(tm + ((uint32_t)(32 * warp) << 16) + kTmK + 64 * buf + 32 * half, r);
+        }
+        if (lane == 0) tc::mbar_arrive(empty(st));
+        __syncwarp();
+        tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(kReady, buf));
+        __syncwarp();
+        if (warp == 0) copy_next();
+        if (warp == 1) {  // the first product of this tile
+          if (u == pc.u0) wait_turn(q_ready, pieces++);
+          if (wait_turn(bar(kReady, buf), it >> 1) && wait_left(bar(sFree, buf), it >> 1)) {
+            tc::fence_after();
+            if (one) {
+              const uint64_t bd = tc::sw128_desc(sb + S::Q);
+              const uint32_t ka = tm + kTmK + 64 * buf, d = tm + kTmS + N * buf;
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                umma_ts(d, ka + 8 * ks, bd + (ks >> 2) * N * 8 + (ks & 3) * 2, idesc_f16(128, N, false), ks > 0);
+              tc::umma_commit(bar(kFree, buf));
+              tc::umma_commit(bar(sFull, buf));
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+  } else if (warp < 8) {  // ---------------------------------------------------------------- values
+    const int d = 32 * (warp - 4) + lane;
+    const bool one = elect_one();
+    // warp 4: the second product of tile i, the `first` of its group's in the piece
+    auto second = [&](int i, bool first) {
+      const int buf = i & 1;
+      if (!wait_turn(bar(vReady, buf), i >> 1) || !wait_turn(bar(pReady, buf), i >> 1)) return;
+      tc::fence_after();
+      if (one) {
+        const uint64_t bd = p_desc<N>(sb + S::P + buf * 128 * N * 2);
+        const uint32_t va = tm + kTmV + 64 * buf, o = tm + tmO + N * buf;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) umma_ts(o, va + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || !first);
+        tc::umma_commit(bar(vFree, buf));
+      }
+      __syncwarp();
+    };
+    while (walk.next(pc)) {
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int st = it % kStages, buf = it & 1;
+        if (!wait_turn(full(st), it / kStages) || !wait_turn(bar(cReady, buf), it >> 1) || !wait_left(bar(vFree, buf), it >> 1)) break;
+        tc::fence_after();
+#pragma unroll
+        for (int page = 0; page < 2; ++page) {
+          const uint8_t* base = sm + st * TILE + kV + page * 4096 + d * 32;
+          const uint8_t* sp = sm + S::VS + buf * 2048 + (d >> 4) * 256 + page * 128;
+          uint32_t r[32];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {  // 32 tokens
+            const uint4 w = *reinterpret_cast<const uint4*>(base + ((q ^ ((d >> 2) & 1)) << 4));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 s = *reinterpret_cast<const uint4*>(sp + 64 * q + 16 * i);
+              r[16 * q + 4 * i] = mul_f16x2(fp4x2_of<0>(ww[i]), s.x);
+              r[16 * q + 4 * i + 1] = mul_f16x2(fp4x2_of<1>(ww[i]), s.y);
+              r[16 * q + 4 * i + 2] = mul_f16x2(fp4x2_of<2>(ww[i]), s.z);
+              r[16 * q + 4 * i + 3] = mul_f16x2(fp4x2_of<3>(ww[i]), s.w);
+            }
+          }
+          tmem_st32(tm + ((uint32_t)(32 * (warp - 4)) << 16) + kTmV + 64 * buf + 32 * page, r);
+        }
+        if (lane == 0) tc::mbar_arrive(empty(st));
+        __syncwarp();
+        tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(vReady, buf));
+        __syncwarp();
+        if (warp == 4 && u > pc.u0) second(it - 1, u - 1 - pc.u0 < 2);
+      }
+      if (warp == 4) second(it - 1, pc.u1 - pc.u0 <= 2);  // the next piece's queries come after this piece's output
+    }
+  } else {  // ---------------------------------------------------------------- softmax and output
+    const int g = (warp - 8) >> 2, w = warp & 3;
+    const uint32_t lanes = (uint32_t)(32 * w) << 16, tm_o = tm + lanes + tmO + N * g;
+    uint64_t l[N / 2];  // this thread's keys' part of every row's sum, two rows together
+    while (walk.next(pc)) {
+      const int b = pc.j / a.row_tiles, rt = pc.j % a.row_tiles, h = pc.h;
+      const Tile t = tile_of<N>(a, b, rt);
+      const int rows = t.r1 - t.r0;
+      if (warp == 8 && lane == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
+        flag_status(a.status, kDevBounds);
+      // Q (all of the last piece's first products are done): rows warp - 8, + 8, ...
+      float v[N / 8][4], amax = 0.f;
+      bool bad[N / 8];
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i) {
+        const int r = warp - 8 + 8 * i;
+        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+        if (r < rows) {
+          const int tk = (t.r0 + r) / a.group, hq = h * a.group + (t.r0 + r) % a.group;
+          const long long row = (long long)b * a.T + tk, last = t.p0 + tk;
+          const bf16* q = static_cast<const bf16*>(a.q) + row * a.qs + (long long)hq * DH + 4 * lane;
+          if (a.vec) {
+            const uint2 x = *reinterpret_cast<const uint2*>(q);
+            v[i][0] = __uint_as_float(x.x << 16), v[i][1] = __uint_as_float(x.x & 0xffff0000u);
+            v[i][2] = __uint_as_float(x.y << 16), v[i][3] = __uint_as_float(x.y & 0xffff0000u);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][e] = to_f32(q[e]);
+          }
+          if (lane == 0) {
+            row_out[r] = row * a.os + (long long)hq * DH;
+            row_out[N + r] = row * a.n_q + hq;
+            row_keys[r] = make_int2(a.window ? (int)min(max(last - a.window + 1, 0LL), t.cap) : 0, (int)min(max(last + 1, 0LL), t.cap));
+          }
+        } else if (lane == 0) {
+          row_keys[r] = make_int2(0, 0);
+        }
+        bool q_bad = false;
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          m = fmaxf(m, fabsf(v[i][e]));
+          q_bad |= !(fabsf(v[i][e]) <= 3.402823466e38f);
+        }
+        bad[i] = __any_sync(0xffffffffu, q_bad);
+        if (!bad[i]) amax = fmaxf(amax, m);
+        if (lane == 0) row_off(0)[r] = row_off(1)[r] = bad[i] ? NAN : kTcWeightExp - kNoRef;
+      }
+      amax = warp_max_f32(amax);
+      if (lane == 0) q_max[warp - 8] = amax;
+      softmax_barrier();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, q_max[i]);
+      // 2^k takes the tile's largest element into [2^14, 2^15)
+      const int k = amax > 0.f ? min(max(14 - ilogbf(amax), -100), 100) : 0;
+      const float f = exp2f((float)k), sc = a.scale_log2 * exp2f((float)-k);
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i) {
+        const int r = warp - 8 + 8 * i;
+        uint2 x = make_uint2(pack_f16(v[i][0] * f, v[i][1] * f), pack_f16(v[i][2] * f, v[i][3] * f));
+        if (bad[i]) x = make_uint2(0u, 0u);
+        // columns 4 lane ..: half lane / 16, 16-byte chunk (lane % 16) / 2 of the row, swizzled by the row
+        *reinterpret_cast<uint2*>(sm + S::Q + (lane >> 4) * N * 128 + r * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * (lane & 1)) = x;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_ready);
+#pragma unroll
+      for (int r = 0; r < N / 2; ++r) l[r] = 0;
+      const uint64_t sc2 = pack2f(sc, sc);
+      // tiles wholly inside every row's range need no masks
+      const int full_end = (int)min(max(t.p0 + t.t_lo + 1, 0LL), t.cap);
+      const int full_beg = a.window ? (int)min(max(t.p0 + t.t_hi - a.window + 1, 0LL), t.cap) : 0;
+      // lanes 0 and 1: the ids of the next tile's pages (a stage's flags may be the next tile's by the time its scores come)
+      const int32_t* bt = a.bt + (size_t)b * a.max_pages + t.pg0;
+      auto id_of = [&](int u) { return lane < 2 && u < pc.u1 && 2 * u + lane < t.np ? bt[2 * u + lane] : -1; };
+      const int first = pc.u0 + ((it ^ g) & 1);  // this group's first tile of the piece
+      int id = id_of(first), last = -1;          // last: its last tile so far
+      for (int u = first; u < pc.u1; u += 2) {
+        const int i = it + u - pc.u0, turn = i >> 1;
+        wait_turn(bar(sFull, g), turn);
+        tc::fence_after();
+        const int key0 = (t.pg0 + 2 * u) * kPage, key = key0 + 32 * w + lane;
+        const int came = __ballot_sync(0xffffffffu, id >= 0 && id < a.n_pages) & 3;
+        id = id_of(u + 2);
+        const bool masked = came != 3 || key0 < full_beg || key0 + 128 > full_end, there = (came >> (w >> 1)) & 1;
+        uint64_t x[N / 2];
+        auto scores = [&]() {  // -inf where the row does not see this thread's key
+          float s[N];
+          if (ok) {
+            tmem_ld<N>(tm + lanes + kTmS + N * g, s);
+          } else {
+#pragma unroll
+            for (int r = 0; r < N; ++r) s[r] = 0.f;
+          }
+          if (masked) {
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+              const int2 see = row_keys[r];
+              if (!there || key < see.x || key >= see.y) s[r] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < N / 2; ++r) x[r] = pack2f(s[2 * r], s[2 * r + 1]);
+        };
+        auto exponents = [&]() {
+          float top = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < N / 2; r += 2) {
+            const ulonglong2 of = *reinterpret_cast<const ulonglong2*>(row_off(g) + 2 * r);
+            x[r] = fma2(x[r], sc2, of.x);
+            x[r + 1] = fma2(x[r + 1], sc2, of.y);
+            top = fmaxf(top, fmaxf(fmaxf(lo2f(x[r]), hi2f(x[r])), fmaxf(lo2f(x[r + 1]), hi2f(x[r + 1]))));
+          }
+          return top;
+        };
+        scores();
+        if (any_of_group(exponents() > kTcWeightExp + 4.f, g)) {
+          // new references: the exact maxima of the tile
+          scores();
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            const float mx = warp_max_f32(r & 1 ? hi2f(x[r / 2]) : lo2f(x[r / 2]));
+            if (lane == r) row_red(g)[w * N + r] = mx;
+          }
+          group_barrier(g);
+          if (w == 0 && lane < N) {
+            const float* red = row_red(g);
+            const float mx = fmaxf(fmaxf(red[lane], red[N + lane]), fmaxf(red[2 * N + lane], red[3 * N + lane]));
+            const float off0 = row_off(g)[lane], off1 = fminf(off0, kTcWeightExp - mx * sc);
+            row_alpha(g)[lane] = off1 < off0 ? tc::ex2_approx(off1 - off0) : 1.f;
+            if (off1 < off0) row_off(g)[lane] = off1;   // a NaN stays
+          }
+          group_barrier(g);
+          if (last >= 0 && wait_turn(bar(vFree, g), last >> 1)) {  // O holds the group's tiles before this one
+            tc::fence_after();
+            float o[N];
+            tmem_ld<N>(tm_o, o);
+#pragma unroll
+            for (int r = 0; r < N; ++r) o[r] *= row_alpha(g)[r];
+            tmem_store<N>(tm_o, o);
+            tmem_wait_st();
+          }
+#pragma unroll
+          for (int r = 0; r < N / 2; ++r) l[r] = mul2(l[r], *reinterpret_cast<const uint64_t*>(row_alpha(g) + 2 * r));
+          scores();
+          exponents();
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(sFree, g));
+#pragma unroll
+        for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
+        // P: this key's N weights side by side, once the group's last product has read the buffer
+        wait_left(bar(vFree, g), turn);
+        uint8_t* pp = sm + S::P + g * 128 * N * 2 + (32 * w + lane) * N * 2;
+#pragma unroll
+        for (int q = 0; q < N / 8; ++q) {
+          uint32_t p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = pack_f16(lo2f(x[4 * q + e]), hi2f(x[4 * q + e]));
+          const int sw = N == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+          *reinterpret_cast<uint4*>(pp + ((q ^ sw) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(pReady, g));
+#pragma unroll
+        for (int r = 0; r < N / 2; ++r) l[r] = add2(l[r], x[r]);
+        last = i;
+      }
+      any = true;
+      it += pc.u1 - pc.u0;
+      // the groups' rows joined; thread = column 32 w + lane, group g takes rows g N / 2 ..
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float sum = warp_sum(r & 1 ? hi2f(l[r / 2]) : lo2f(l[r / 2]));
+        if (lane == r) row_l(g)[w * N + r] = sum;
+      }
+      if (last >= 0) wait_turn(bar(vFree, g), last >> 1);
+      tc::fence_before();
+      softmax_barrier();
+      tc::fence_after();
+      const int np = pc.u1 - pc.u0, r_lo = g * (N / 2);
+      // whether a group had a tile: both from two tiles on, else the one whose turn the tile was
+      const bool has0 = np > 1 || ((it - np) & 1) == 0, has1 = np > 1 || ((it - np) & 1) == 1;
+      float L = 0.f, off = 0.f, f0 = 0.f, f1 = 0.f, inv = 0.f;  // of row `lane`
+      const bool whole = pc.u0 == 0 && pc.u1 == pc.nu;
+      if (lane < N) {
+        const float o0 = row_off(0)[lane], o1 = row_off(1)[lane];
+        off = fminf(o0, o1);
+        f0 = has0 ? (o0 == off ? 1.f : tc::ex2_approx(off - o0)) : 0.f;
+        f1 = has1 ? (o1 == off ? 1.f : tc::ex2_approx(off - o1)) : 0.f;
+        const float *l0 = row_l(0), *l1 = row_l(1);
+        L = f0 * (l0[lane] + l0[N + lane] + l0[2 * N + lane] + l0[3 * N + lane]) +
+            f1 * (l1[lane] + l1[N + lane] + l1[2 * N + lane] + l1[3 * N + lane]);
+        inv = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
+        if (w == 0 && lane >= r_lo && lane < min(rows, r_lo + N / 2) && ok) {
+          if (!whole)
+            a.part_ml[part_row(pc, N) + lane] = make_float2(-off, L);
+          else if (a.lse)
+            a.lse[row_out[N + lane]] = lse_of(-off, L, 0.f);
+        }
+      }
+      float o0[N / 2], o1[N / 2];
+#pragma unroll
+      for (int r = 0; r < N / 2; ++r) o0[r] = o1[r] = 0.f;
+      if (has0 && ok) tmem_ld_part<N / 2>(tm + lanes + tmO + r_lo, o0);
+      if (has1 && ok) tmem_ld_part<N / 2>(tm + lanes + tmO + N + r_lo, o1);
+      tc::fence_before();
+      const int d = 32 * w + lane;
+#pragma unroll
+      for (int r = 0; r < N / 2; ++r) {
+        const float e0 = __shfl_sync(0xffffffffu, f0 * inv, r_lo + r), e1 = __shfl_sync(0xffffffffu, f1 * inv, r_lo + r);
+        if (r_lo + r >= rows || !ok) continue;
+        const float v = fmaf(o0[r], e0, o1[r] * e1);
+        if (whole)
+          static_cast<bf16*>(a.out)[row_out[r_lo + r] + d] = __float2bfloat16_rn(v);
+        else
+          a.part_o[(part_row(pc, N) + r_lo + r) * DH + d] = v;
+      }
+      softmax_barrier();  // both O, row_l, row_off are the next piece's
+    }
+    if (a.stream && warp == 8 && lane == 0) a.joins[blockIdx.x] = walk.join_of(any, pc);
+  }
+  __syncwarp();
+  // every role is through; after a wait that ran out (status flagged) the copies and products in flight have had its time
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kTmCols) : "memory");
+}
+
+template <int N>
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int grid, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kv_attention_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N>::BYTES);
+  return e != cudaSuccess ? e : launch_pdl(kv_attention_tc_kernel<N>, dim3(grid), dim3(kThreads), Smem<N>::BYTES, s, mk, mv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tc(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+  CUtensorMap mk, mv;
+  const long long records = (long long)a.n_pages * a.n_kv;
+  if (!tc::make_record_map(&mk, a.pages, 64, 64, records, REC) || !tc::make_record_map(&mv, a.pages + v_off(DH), 32, 128, records, REC))
+    return cudaErrorInvalidValue;
+  return p.rows == 16 ? launch<16>(mk, mv, a, p.grid, s) : launch<32>(mk, mv, a, p.grid, s);
+}
+
+}  // namespace kv
+}  // namespace dlite
