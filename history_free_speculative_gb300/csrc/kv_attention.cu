@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const Attn
       int id_next = -1;
       if (lane == 0 && more) id_next = bt[i + PER * kWarps];
       // a copy that never lands: no further page is taken, the status says so, the barriers below are kept
-      got = got && __all_sync(0xffffffffu, tc::mbar_wait(tc::su32(full + slot), (uint32_t)(n_take / PER) & 1u, a.status));
+      got = got && __all_sync(0xffffffffu, tc::mbar_wait_hint(tc::su32(full + slot), (uint32_t)(n_take / PER) & 1u, a.status));
       ++n_take;
       if (got && slot_ok[slot]) {
         const uint8_t* rec = ring + slot * REC;

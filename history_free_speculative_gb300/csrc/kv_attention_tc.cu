@@ -8,19 +8,20 @@
 // and writes them with tcgen05.st, so the cache never passes through shared memory a second time. N = 16 or 32
 // query rows; Q^T and P^T are the B operands in shared memory.
 // Warps: 0-3 keys (and the value scales as f16, once for the 16 columns that share them), 4-7 values, 8-15 softmax and
-// output (thread = key, then column). Warp 0 also issues the copies, warp 1 the first product, warp 4 the second, each where its
-// own work next waits for that: 16 warps leave 128 registers a thread, which the softmax needs.
+// output (thread = key, then column), 16 copies, 17 and 18 the issue of the first and the second product.
 // The softmax warps are two groups that take the tiles in turn, each with its own scores, weights, maxima, sums and O, joined at
 // a piece's end: one group's latencies pass under the other's tile (one group alone took 3,300 clocks a tile). A group keeps one
-// reference m per row, moved only when a score passes it by more than 2^4 (a vote of its 128 threads per tile); only then
-// are exact maxima formed and O, the sums rescaled. Weights are 2^(s - m + 10) <= 2^14, rounded to f16: weights down
-// to 2^-35 of the reference count, and the largest score is never below it. Queries are scaled by one power of two per
+// reference m per row, moved only when a weight passes it by more than 2^8 (a vote of its 128 threads per tile); only then
+// are exact maxima formed and O, the sums rescaled. Weights are 2^(s - m + 6) <= 2^14, rounded to f16: weights down
+// to 2^-31 of the reference count, and the largest score is never below it. Queries are scaled by one power of two per
 // tile into f16's range: exact for bf16 elements down to 2^-32 of the tile's largest, and off by 2^-39 of that below.
 // The issuing warps stay converged and elect a lane: 17 clocks an MMA, 46 from a branch on the lane (the operands then
 // go from vector to uniform registers one by one).
 // mma.sync does both products of a 32-row tile in 8 clocks a key an SM (measured 2.0 per m16n8k16), above the 6.8 that the bytes take
 // at the copy rate of HBM, and needs its operands and outputs in registers: the mma.sync kernel ran at 19.
 #include <math.h>
+
+#include <type_traits>
 
 #include "kv_attention.cuh"
 #include "tc_gemm.h"
@@ -31,25 +32,25 @@ namespace {
 
 constexpr int DH = 128, REC = rec_bytes(DH), TILE = 2 * REC;
 constexpr int kStages = 9;
-constexpr int kThreads = 16 * 32;  // four warps a scheduler: 128 registers each
-constexpr int kAhead = kStages - 2;  // tiles the copies are ahead of the keys
+constexpr int kThreads = 19 * 32;
+constexpr int kScaleRing = 8;      // tiles of value scales: the keys' warps are never that far ahead of the values'
 // a stage: key codes of both pages (rows of 64 B, 64-byte swizzle), value codes (rows of 32 B, 32-byte swizzle), scales
 constexpr int kV = 8192, kS = 16384;
 // tensor memory columns: K and V^T tiles twice, S^T twice, O^T
 constexpr int kTmK = 0, kTmV = 128, kTmS = 256, kTmCols = 512;
-constexpr float kTcWeightExp = 10.f;
+constexpr float kTcWeightExp = 6.f;
 constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key
 
 template <int N>
 struct Smem {
   static constexpr int Q = kStages * TILE;           // [2 halves][N rows][128 B], 128-byte swizzle
   static constexpr int P = Q + N * 256;              // [2][128 keys][N rows] f16, rows of N contiguous
-  static constexpr int VS = P + 2 * 128 * N * 2;     // [2][8 blocks][128 tokens] f16: value scales
-  static constexpr int ROWS = VS + 2 * 2048;         // floats: offset [2][N], alpha [2][N], l [2][4][N], red [2][4][N], tile max
+  static constexpr int VS = P + 2 * 128 * N * 2;     // [ring][8 blocks][128 tokens] f16: value scales
+  static constexpr int ROWS = VS + kScaleRing * 2048;         // floats: offset [2][N], alpha [2][N], l [2][4][N], red [2][4][N], tile max
   static constexpr int KEYS = ROWS + 20 * N * 4 + 64;  // int2: keys a row sees
   static constexpr int OUT = KEYS + N * 8;           // int64: where a row's output and lse go
   static constexpr int BARS = OUT + N * 16;
-  static constexpr int NBARS = 2 * kStages + 17;
+  static constexpr int NBARS = 2 * kStages + 15 + kScaleRing;
   static constexpr int OK = BARS + NBARS * 8;        // per stage: which of its pages came
   static constexpr int TM = OK + kStages * 4;
   static constexpr int PREFIX = TM + 8;
@@ -161,6 +162,28 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Sums of N rows over a warp: the halves of the rows change sides step by step; lane i returns row i (N = 16: i / 2).
+template <int N>
+__device__ __forceinline__ float warp_row_sums(float (&v)[N], int lane) {
+  auto step = [&](auto cnt_c, int o) {
+    constexpr int cnt = decltype(cnt_c)::value;
+    const bool up = lane & o;
+#pragma unroll
+    for (int r = 0; r < cnt; ++r) {
+      const float give = up ? v[r] : v[r + cnt], keep = up ? v[r + cnt] : v[r];
+      v[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  };
+  step(std::integral_constant<int, N / 2>(), 16);
+  step(std::integral_constant<int, N / 4>(), 8);
+  step(std::integral_constant<int, N / 8>(), 4);
+  step(std::integral_constant<int, N / 16>(), 2);
+  if constexpr (N == 32) {
+    step(std::integral_constant<int, 1>(), 1);
+    return v[0];
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attention_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
@@ -169,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = raw + ((1024 - (tc::su32(raw) & 1023)) & 1023);
   const uint32_t sb = tc::su32(sm);
   float* rows_f = reinterpret_cast<float*>(sm + S::ROWS);
-  auto row_off = [&](int g) { return rows_f + g * N; };              // 10 - m: a weight is 2^(score + offset)
+  auto row_off = [&](int g) { return rows_f + g * N; };              // 6 - m: a weight is 2^(score + offset)
   auto row_alpha = [&](int g) { return rows_f + (2 + g) * N; };
   auto row_l = [&](int g) { return rows_f + (4 + 4 * g) * N; };      // [warp][row]
   auto row_red = [&](int g) { return rows_f + (12 + 4 * g) * N; };   // [warp][row]
@@ -183,8 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
   auto bar = [&](int kind, int buf) { return bars + 8 * (2 * kStages + 2 * kind + buf); };
-  enum { kReady, kFree, vReady, vFree, sFull, sFree, pReady, cReady };   // each twice; then q_ready
-  const uint32_t q_ready = bars + 8 * (2 * kStages + 16);
+  enum { kReady, kFree, vReady, vFree, sFull, sFree, pReady };   // each twice; then q_ready, and the ring of value scales
+  const uint32_t q_ready = bars + 8 * (2 * kStages + 14);
+  auto c_ready = [&](int i) { return bars + 8 * (2 * kStages + 15 + i % kScaleRing); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   pdl_wait();  // no early trigger: the grid fills the SMs
@@ -202,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(bar(sFull, i), 1);
       tc::mbar_init(bar(sFree, i), 4);
       tc::mbar_init(bar(pReady, i), 4);
-      tc::mbar_init(bar(cReady, i), 4);  // value scales
     }
+    for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(c_ready(i), 4);
     tc::mbar_init(q_ready, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -223,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int it = 0;  // tiles so far, over all pieces: buffer it & 1, stage it % kStages
   // Wait until a buffer (or stage) has been filled for its `turn`-th use, the whole warp; false once a wait has run out.
   auto wait_turn = [&](uint32_t b, int turn) {
-    return ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(b, (uint32_t)turn & 1u, a.status));
+    return ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_hint(b, (uint32_t)turn & 1u, a.status));
   };
   // ... until its use before the `turn`-th is over: nothing to wait for in the first
   auto wait_left = [&](uint32_t b, int turn) { return turn == 0 ? ok : wait_turn(b, turn - 1); };
@@ -231,64 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {  // ---------------------------------------------------------------- keys, value scales
     const int page = warp >> 1, row = 32 * (warp & 1) + lane;  // key 32 warp + lane of the tile
     const int blk = tid >> 4, tok = (tid & 15) * 8;            // scales of 8 tokens of a block of 16 columns
-    const bool one = elect_one();
-    // copies (warp 0): a walk of their own, kAhead tiles ahead
-    Pieces<N> copies(a, prefix);
-    Piece cp;
-    int c_it = 0, c_u = 0, c_np = 0, id0 = -1, id1 = -1;
-    const int32_t* c_bt = nullptr;
-    cp.u1 = 0;
-    auto page_of = [&](int i) { return i < c_np ? c_bt[i] : -1; };
-    auto copy_next = [&]() {
-      if (c_u >= cp.u1) {
-        if (!copies.next(cp)) return false;
-        const int b = cp.j / a.row_tiles;
-        const Tile t = tile_of<N>(a, b, cp.j % a.row_tiles);
-        c_bt = a.bt + (size_t)b * a.max_pages + t.pg0;
-        c_np = t.np;
-        c_u = cp.u0;
-        id0 = page_of(2 * c_u);
-        id1 = page_of(2 * c_u + 1);
-      }
-      const int st = c_it % kStages;
-      if (!wait_left(empty(st), c_it / kStages)) return false;
-      const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
-      if (one) {
-        if (id0 >= a.n_pages || id1 >= a.n_pages) flag_status(a.status, kDevBounds);
-        stage_ok[st] = came;
-        if (came) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          tc::mbar_expect_tx(full(st), (came == 3 ? 2 : 1) * REC);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            if (!(came >> p & 1)) continue;
-            const long long rec = (long long)(p ? id1 : id0) * a.n_kv + cp.h;
-            const uint32_t dst = sb + st * TILE;
-            tma_load_3d(dst + p * 4096, &mk, full(st), (int)rec);
-            tma_load_3d(dst + kV + p * 4096, &mv, full(st), (int)rec);
-            tc::bulk_load(dst + kS + p * 1024, a.pages + rec * REC + ks_off(DH), 1024, full(st));
-          }
-        } else {
-          tc::mbar_arrive(full(st));
-        }
-      }
-      __syncwarp();
-      ++c_it;
-      ++c_u;
-      id0 = c_u < cp.u1 ? page_of(2 * c_u) : -1;  // read a tile before they are used
-      id1 = c_u < cp.u1 ? page_of(2 * c_u + 1) : -1;
-      return true;
-    };
-    if (warp == 0)
-      for (int i = 0; i < kAhead && copy_next(); ++i) {
-      }
-    int pieces = 0;
     while (walk.next(pc)) {
       const Tile t = tile_of<N>(a, pc.j / a.row_tiles, pc.j % a.row_tiles);
       for (int u = pc.u0; u < pc.u1; ++u, ++it) {
         const int st = it % kStages, buf = it & 1;
-        // the scales' buffer is the values' of tile it - 2
-        if (!wait_turn(full(st), it / kStages) || !wait_left(bar(kFree, buf), it >> 1) || !wait_left(bar(vReady, buf), it >> 1)) break;
+        // The first product of tile it - 2 is done, so the scores of it - 4 had been read, the weights of it - 6 written, the second
+        // product of it - 8 been done: the ring's slot is free.
+        if (!wait_turn(full(st), it / kStages) || !wait_left(bar(kFree, buf), it >> 1)) break;
         tc::fence_after();
         const uint8_t* stage = sm + st * TILE;
         {
@@ -302,10 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[i] = 2 * i + 1 < valid ? s[i] : 2 * i < valid ? s[i] & 0xffffu : 0u;
           }
-          *reinterpret_cast<uint4*>(sm + S::VS + buf * 2048 + blk * 256 + tok * 2) = make_uint4(s[0], s[1], s[2], s[3]);
+          *reinterpret_cast<uint4*>(sm + S::VS + it % kScaleRing * 2048 + blk * 256 + tok * 2) = make_uint4(s[0], s[1], s[2], s[3]);
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(cReady, buf));
+        if (lane == 0) tc::mbar_arrive(c_ready(it));
         const uint8_t* base = stage + page * 4096 + row * 64;
         const uint2 sc = *reinterpret_cast<const uint2*>(stage + kS + page * 1024 + row * 8);
         __syncwarp();
@@ -335,52 +308,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(kReady, buf));
-        __syncwarp();
-        if (warp == 0) copy_next();
-        if (warp == 1) {  // the first product of this tile
-          if (u == pc.u0) wait_turn(q_ready, pieces++);
-          if (wait_turn(bar(kReady, buf), it >> 1) && wait_left(bar(sFree, buf), it >> 1)) {
-            tc::fence_after();
-            if (one) {
-              const uint64_t bd = tc::sw128_desc(sb + S::Q);
-              const uint32_t ka = tm + kTmK + 64 * buf, d = tm + kTmS + N * buf;
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                umma_ts(d, ka + 8 * ks, bd + (ks >> 2) * N * 8 + (ks & 3) * 2, idesc_f16(128, N, false), ks > 0);
-              tc::umma_commit(bar(kFree, buf));
-              tc::umma_commit(bar(sFull, buf));
-            }
-            __syncwarp();
-          }
-        }
       }
     }
   } else if (warp < 8) {  // ---------------------------------------------------------------- values
     const int d = 32 * (warp - 4) + lane;
-    const bool one = elect_one();
-    // warp 4: the second product of tile i, the `first` of its group's in the piece
-    auto second = [&](int i, bool first) {
-      const int buf = i & 1;
-      if (!wait_turn(bar(vReady, buf), i >> 1) || !wait_turn(bar(pReady, buf), i >> 1)) return;
-      tc::fence_after();
-      if (one) {
-        const uint64_t bd = p_desc<N>(sb + S::P + buf * 128 * N * 2);
-        const uint32_t va = tm + kTmV + 64 * buf, o = tm + tmO + N * buf;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) umma_ts(o, va + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || !first);
-        tc::umma_commit(bar(vFree, buf));
-      }
-      __syncwarp();
-    };
     while (walk.next(pc)) {
       for (int u = pc.u0; u < pc.u1; ++u, ++it) {
         const int st = it % kStages, buf = it & 1;
-        if (!wait_turn(full(st), it / kStages) || !wait_turn(bar(cReady, buf), it >> 1) || !wait_left(bar(vFree, buf), it >> 1)) break;
+        if (!wait_turn(full(st), it / kStages) || !wait_turn(c_ready(it), it / kScaleRing) || !wait_left(bar(vFree, buf), it >> 1)) break;
         tc::fence_after();
 #pragma unroll
         for (int page = 0; page < 2; ++page) {
           const uint8_t* base = sm + st * TILE + kV + page * 4096 + d * 32;
-          const uint8_t* sp = sm + S::VS + buf * 2048 + (d >> 4) * 256 + page * 128;
+          const uint8_t* sp = sm + S::VS + it % kScaleRing * 2048 + (d >> 4) * 256 + page * 128;
           uint32_t r[32];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {  // 32 tokens
@@ -403,12 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(vReady, buf));
-        __syncwarp();
-        if (warp == 4 && u > pc.u0) second(it - 1, u - 1 - pc.u0 < 2);
       }
-      if (warp == 4) second(it - 1, pc.u1 - pc.u0 <= 2);  // the next piece's queries come after this piece's output
     }
-  } else {  // ---------------------------------------------------------------- softmax and output
+  } else if (warp < 16) {  // ---------------------------------------------------------------- softmax and output
     const int g = (warp - 8) >> 2, w = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * w) << 16, tm_o = tm + lanes + tmO + N * g;
     uint64_t l[N / 2];  // this thread's keys' part of every row's sum, two rows together
@@ -422,13 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float v[N / 8][4], amax = 0.f;
       bool bad[N / 8];
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i) {
+      for (int i = 0; i < N / 8; ++i) {  // every row's load before the first use
         const int r = warp - 8 + 8 * i;
         v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
         if (r < rows) {
           const int tk = (t.r0 + r) / a.group, hq = h * a.group + (t.r0 + r) % a.group;
-          const long long row = (long long)b * a.T + tk, last = t.p0 + tk;
-          const bf16* q = static_cast<const bf16*>(a.q) + row * a.qs + (long long)hq * DH + 4 * lane;
+          const bf16* q = static_cast<const bf16*>(a.q) + ((long long)b * a.T + tk) * a.qs + (long long)hq * DH + 4 * lane;
           if (a.vec) {
             const uint2 x = *reinterpret_cast<const uint2*>(q);
             v[i][0] = __uint_as_float(x.x << 16), v[i][1] = __uint_as_float(x.x & 0xffff0000u);
@@ -437,14 +373,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[i][e] = to_f32(q[e]);
           }
-          if (lane == 0) {
-            row_out[r] = row * a.os + (long long)hq * DH;
-            row_out[N + r] = row * a.n_q + hq;
-            row_keys[r] = make_int2(a.window ? (int)min(max(last - a.window + 1, 0LL), t.cap) : 0, (int)min(max(last + 1, 0LL), t.cap));
-          }
-        } else if (lane == 0) {
-          row_keys[r] = make_int2(0, 0);
         }
+      }
+      if (warp == 8 && lane < N) {
+        const int r = t.r0 + lane, tk = r / a.group, hq = h * a.group + r % a.group;
+        const long long row = (long long)b * a.T + tk, seen = t.p0 + tk;
+        row_out[lane] = row * a.os + (long long)hq * DH;
+        row_out[N + lane] = row * a.n_q + hq;
+        row_keys[lane] = lane < rows ? make_int2(a.window ? (int)min(max(seen - a.window + 1, 0LL), t.cap) : 0, (int)min(max(seen + 1, 0LL), t.cap))
+                                     : make_int2(0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i) {
+        const int r = warp - 8 + 8 * i;
         bool q_bad = false;
         float m = 0.f;
 #pragma unroll
@@ -525,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return top;
         };
         scores();
-        if (any_of_group(exponents() > kTcWeightExp + 4.f, g)) {
+        if (any_of_group(exponents() > kTcWeightExp + 8.f, g)) {
           // new references: the exact maxima of the tile
           scores();
 #pragma unroll
@@ -542,17 +483,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (off1 < off0) row_off(g)[lane] = off1;   // a NaN stays
           }
           group_barrier(g);
-          if (last >= 0 && wait_turn(bar(vFree, g), last >> 1)) {  // O holds the group's tiles before this one
-            tc::fence_after();
-            float o[N];
-            tmem_ld<N>(tm_o, o);
+          if (last >= 0) {  // O holds the group's tiles before this one
+            if (wait_turn(bar(vFree, g), last >> 1)) {
+              tc::fence_after();
+#pragma unroll 1
+              for (int r = 0; r < N; r += 16) {
+                float o[16];
+                tmem_ld<16>(tm_o + r, o);
 #pragma unroll
-            for (int r = 0; r < N; ++r) o[r] *= row_alpha(g)[r];
-            tmem_store<N>(tm_o, o);
-            tmem_wait_st();
+                for (int e = 0; e < 16; ++e) o[e] *= row_alpha(g)[r + e];
+                tmem_store<16>(tm_o + r, o);
+              }
+              tmem_wait_st();
+            }
+#pragma unroll
+            for (int r = 0; r < N / 2; ++r) l[r] = mul2(l[r], *reinterpret_cast<const uint64_t*>(row_alpha(g) + 2 * r));
           }
-#pragma unroll
-          for (int r = 0; r < N / 2; ++r) l[r] = mul2(l[r], *reinterpret_cast<const uint64_t*>(row_alpha(g) + 2 * r));
           scores();
           exponents();
         }
@@ -583,10 +529,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       any = true;
       it += pc.u1 - pc.u0;
       // the groups' rows joined; thread = column 32 w + lane, group g takes rows g N / 2 ..
+      {
+        float v[N];
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        const float sum = warp_sum(r & 1 ? hi2f(l[r / 2]) : lo2f(l[r / 2]));
-        if (lane == r) row_l(g)[w * N + r] = sum;
+        for (int r = 0; r < N / 2; ++r) v[2 * r] = lo2f(l[r]), v[2 * r + 1] = hi2f(l[r]);
+        const float sum = warp_row_sums<N>(v, lane);
+        if (N == 32 || (lane & 1) == 0) row_l(g)[w * N + (N == 32 ? lane : lane >> 1)] = sum;
       }
       if (last >= 0) wait_turn(bar(vFree, g), last >> 1);
       tc::fence_before();
@@ -633,6 +581,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       softmax_barrier();  // both O, row_l, row_off are the next piece's
     }
     if (a.stream && warp == 8 && lane == 0) a.joins[blockIdx.x] = walk.join_of(any, pc);
+  } else if (warp == 16) {  // ---------------------------------------------------------------- copies
+    const bool one = elect_one();
+    while (walk.next(pc)) {
+      const int b = pc.j / a.row_tiles;
+      const Tile t = tile_of<N>(a, b, pc.j % a.row_tiles);
+      const int32_t* bt = a.bt + (size_t)b * a.max_pages + t.pg0;
+      auto page_of = [&](int i) { return i < t.np ? bt[i] : -1; };
+      int id0 = page_of(2 * pc.u0), id1 = page_of(2 * pc.u0 + 1);
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int st = it % kStages;
+        const int next0 = u + 1 < pc.u1 ? page_of(2 * u + 2) : -1, next1 = u + 1 < pc.u1 ? page_of(2 * u + 3) : -1;
+        if (!wait_left(empty(st), it / kStages)) break;
+        const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
+        if (one) {
+          if (id0 >= a.n_pages || id1 >= a.n_pages) flag_status(a.status, kDevBounds);
+          stage_ok[st] = came;
+          if (came) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc::mbar_expect_tx(full(st), (came == 3 ? 2 : 1) * REC);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              if (!(came >> p & 1)) continue;
+              const long long rec = (long long)(p ? id1 : id0) * a.n_kv + pc.h;
+              const uint32_t dst = sb + st * TILE;
+              tma_load_3d(dst + p * 4096, &mk, full(st), (int)rec);
+              tma_load_3d(dst + kV + p * 4096, &mv, full(st), (int)rec);
+              tc::bulk_load(dst + kS + p * 1024, a.pages + rec * REC + ks_off(DH), 1024, full(st));
+            }
+          } else {
+            tc::mbar_arrive(full(st));
+          }
+        }
+        __syncwarp();
+        id0 = next0;
+        id1 = next1;
+      }
+    }
+  } else if (warp == 17) {  // ---------------------------------------------------------------- first product
+    const bool one = elect_one();
+    int pieces = 0;
+    while (walk.next(pc)) {
+      if (!wait_turn(q_ready, pieces++)) break;
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int buf = it & 1;
+        if (!wait_turn(bar(kReady, buf), it >> 1) || !wait_left(bar(sFree, buf), it >> 1)) break;
+        tc::fence_after();
+        if (one) {
+          const uint64_t bd = tc::sw128_desc(sb + S::Q);
+          const uint32_t ka = tm + kTmK + 64 * buf, d = tm + kTmS + N * buf;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_ts(d, ka + 8 * ks, bd + (ks >> 2) * N * 8 + (ks & 3) * 2, idesc_f16(128, N, false), ks > 0);
+          tc::umma_commit(bar(kFree, buf));
+          tc::umma_commit(bar(sFull, buf));
+        }
+        __syncwarp();
+      }
+    }
+  } else {  // ---------------------------------------------------------------- second product
+    const bool one = elect_one();
+    while (walk.next(pc)) {
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int buf = it & 1;
+        if (!wait_turn(bar(vReady, buf), it >> 1) || !wait_turn(bar(pReady, buf), it >> 1)) break;
+        tc::fence_after();
+        if (one) {
+          const uint64_t bd = p_desc<N>(sb + S::P + buf * 128 * N * 2);
+          const uint32_t va = tm + kTmV + 64 * buf, o = tm + tmO + N * buf;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)  // a group's first tile of the piece starts its O
+            umma_ts(o, va + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || u - pc.u0 >= 2);
+          tc::umma_commit(bar(vFree, buf));
+        }
+        __syncwarp();
+      }
+    }
   }
   __syncwarp();
   // every role is through; after a wait that ran out (status flagged) the copies and products in flight have had its time

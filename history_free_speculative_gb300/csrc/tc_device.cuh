@@ -54,6 +54,28 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* st
     }
   }
 }
+// The same with a suspend hint: a waiting thread sleeps instead of polling, which leaves the issue slots to the
+// other warps of a kernel that has many kinds of them waiting for each other.
+__device__ __forceinline__ bool mbar_wait_hint(uint32_t bar, uint32_t parity, int* status) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok) return true;
+    const uint64_t t = gtimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kTimeoutNs) {
+      flag_status(status, kDevTimeout);
+      return false;
+    }
+  }
+}
 // Warp-wide bounded wait: every lane polls, lane 0's view decides, so the
 // result is uniform across the warp.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status,

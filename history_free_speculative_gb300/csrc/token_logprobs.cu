@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C, int
   if (chunks) {
     // the first stage alone: its maximum is every warp's first reference (later rescales are rare then), the
     // maxima of groups of threads give the first floor
-    ok = tc::mbar_wait(tc::su32(full), 0, a.status);
+    ok = tc::mbar_wait_hint(tc::su32(full), 0, a.status);
     float cm = -INFINITY;
     const int n = ok ? min(R::PIECES, v1 - v0) : 0;
     for (int q = tid; q < n; q += NT) {
@@ -418,10 +418,10 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C, int
   for (int c = 0; c < chunks; ++c) {
     // the stage of chunk c - 1 is refilled now: the other warps have had a chunk's time to leave it
     if (tid == 0 && c >= 1 && c - 1 + stages < chunks) {
-      ok &= tc::mbar_wait(tc::su32(empty + (stage ? stage : stages) - 1), stage ? phase : phase ^ 1u, a.status);
+      ok &= tc::mbar_wait_hint(tc::su32(empty + (stage ? stage : stages) - 1), stage ? phase : phase ^ 1u, a.status);
       if (ok) issue(c - 1 + stages, (stage ? stage : stages) - 1);
     }
-    ok = ok && tc::mbar_wait(tc::su32(full + stage), phase, a.status);
+    ok = ok && tc::mbar_wait_hint(tc::su32(full + stage), phase, a.status);
     // a copy never landed: the status says so, the row's outputs mean nothing; the barriers below are kept
     const int n = __all_sync(0xffffffffu, ok) ? min(R::PIECES, v1 - v0 - c * R::PIECES) : 0;
     const uint4* src = reinterpret_cast<const uint4*>(ring + stage * R::BYTES);
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C, int
   }
   if (tid == 0 && !ok)  // let the copies in flight end (bounded) before the memory is given back
     for (int i = 0; i < stages && i < chunks; ++i)
-      for (uint32_t ph = 0; ph < 2; ++ph) tc::mbar_wait(tc::su32(full + i), ph, a.status);
+      for (uint32_t ph = 0; ph < 2; ++ph) tc::mbar_wait_hint(tc::su32(full + i), ph, a.status);
   if (rank == C - 1 && tail + first < a.V) {
     const uint32_t v[1] = {__float_as_uint(tail + tid < a.V ? to_f32(x[tail + tid]) : -INFINITY)};
     take<float>(v, tail + tid, tail + tid < a.V, a.k, st, own, top);

@@ -6,8 +6,8 @@ sum |q k| scale (the accumulator may truncate), exp2 adds 2^-22, and the sums ov
 (n / 16 + 64) 2^-24. Each relative error of a weight moves the output by at most twice
 reach = sum p |v| / sum p (numerator and denominator); the result is rounded once (bf16: 2^-8 relative).
 Far weights add an absolute term: f16's smallest step is 2^-24 and the largest weight is kept as 2^14 (bf16 queries with heads of
-128: as at least 2^10, since a row's reference is passed by at most 2^4), so each is off by at most 2^-25 / 2^14 = 2^-39
-(2^-35) of the largest, which is at most their sum: `keys` of them move an output by at most keys 2^-39 (2^-35) max |v|, and no
+128: as at least 2^6, since a row's reference is passed by at most 2^8), so each is off by at most 2^-25 / 2^14 = 2^-39
+(2^-31) of the largest, which is at most their sum: `keys` of them move an output by at most keys 2^-39 (2^-31) max |v|, and no
 scale of these tests' caches is above 0.6875 (byte 0x33), no code above 6."""
 import math
 
@@ -37,7 +37,7 @@ def _cache(n_pages, H, d, B, max_pages, seed, k_exp=0, v_exp=0):
 
 
 def _tolerance(want, reach, eps, keys, d, dtype, v_exp=0):
-    far = keys * 2.0 ** (-35 if dtype == "bf16" and d == 128 else -39) * 6 * 0.6875 * 2.0 ** v_exp
+    far = keys * 2.0 ** (-31 if dtype == "bf16" and d == 128 else -39) * 6 * 0.6875 * 2.0 ** v_exp
     s = (d / 8 + 8) * 2.0 ** -23 * eps                       # nats
     w = (2.0 ** -11 if dtype == "bf16" else 2.0 ** -21) + 2.0 ** -22 + (keys / 16 + 64) * 2.0 ** -24 + s
     return (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(want) + 2 * w[..., None] * reach + far, 2 * w + 2.0 ** -22 * 20
