@@ -164,6 +164,15 @@ struct Pieces {
     return make_int2(p.j * a.n_kv + p.h, (int)(last / quota) - (int)blockIdx.x + 1);
   }
 };
+// The pieces of a CTA as a list in shared memory, a batch at a time: one thread walks, one thread a piece works out its
+// tile. (Walked by every role of a kernel itself, the divisions and loads were there five times over and sat in every change of pieces.)
+struct PieceTile {
+  Piece p;
+  Tile t;
+  int b, rt;
+  __device__ __forceinline__ bool whole() const { return p.u0 == 0 && p.u1 == p.nu; }
+};
+constexpr int kBatch = 32;
 // Row of the workspace of this CTA's piece p (not its whole segment)
 __device__ __forceinline__ size_t part_row(const Piece& p, int R) { return ((size_t)blockIdx.x * 2 + (p.u0 == 0)) * R; }
 

@@ -53,7 +53,8 @@ struct Smem {
   static constexpr int NBARS = 2 * kStages + 15 + kScaleRing;
   static constexpr int OK = BARS + NBARS * 8;        // per stage: which of its pages came
   static constexpr int TM = OK + kStages * 4;
-  static constexpr int PREFIX = TM + 8;
+  static constexpr int LIST = (TM + 8 + 15) / 16 * 16;   // PieceTile [kBatch], then their number
+  static constexpr int PREFIX = LIST + kBatch * (int)sizeof(PieceTile) + 8;
   static constexpr int BYTES = PREFIX + (kMaxList + 1) * 4 + 1024;  // alignment of the swizzled stages
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
 };
@@ -184,6 +185,29 @@ __device__ __forceinline__ float warp_row_sums(float (&v)[N], int lane) {
   }
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
+// A wait that did not end at once: sleep and look again, up to the limit. Then the status says so, and *gave_up ends this wait
+// and every later one of the CTA: the roles run to their ends on whatever the buffers hold.
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up, int* status) {
+  const uint64_t t0 = tc::gtimer();
+  while (!*gave_up) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok) return;
+    if (tc::gtimer() - t0 > tc::kTimeoutNs) {
+      flag_status(status, kDevTimeout);
+      *gave_up = 1;
+    }
+  }
+}
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volatile int* gave_up, int* status) {
+  if (!tc::mbar_try(bar, parity)) wait_slow(bar, parity, gave_up, status);
+  __syncwarp();
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attention_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
@@ -202,11 +226,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* stage_ok = reinterpret_cast<int*>(sm + S::OK);
   uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + S::TM);
   int* prefix = reinterpret_cast<int*>(sm + S::PREFIX);
+  PieceTile* list = reinterpret_cast<PieceTile*>(sm + S::LIST);
+  int* listed = reinterpret_cast<int*>(list + kBatch);
   const uint32_t bars = sb + S::BARS;
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
   auto bar = [&](int kind, int buf) { return bars + 8 * (2 * kStages + 2 * kind + buf); };
   enum { kReady, kFree, vReady, vFree, sFull, sFree, pReady };   // each twice; then q_ready, and the ring of value scales
+  volatile int* gave_up = reinterpret_cast<volatile int*>(sm + S::TM + 4);
   const uint32_t q_ready = bars + 8 * (2 * kStages + 14);
   auto c_ready = [&](int i) { return bars + 8 * (2 * kStages + 15 + i % kScaleRing); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -228,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(bar(pReady, i), 4);
     }
     for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(c_ready(i), 4);
+    *gave_up = 0;
     tc::mbar_init(q_ready, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -241,27 +269,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = *tm_slot;
   constexpr uint32_t tmO = kTmS + 2 * N;
 
-  Pieces<N> walk(a, prefix);
-  Piece pc;
-  bool any = false, ok = true;
+  Pieces<N> walk(a, prefix);  // thread 0's
   int it = 0;  // tiles so far, over all pieces: buffer it & 1, stage it % kStages
-  // Wait until a buffer (or stage) has been filled for its `turn`-th use, the whole warp; false once a wait has run out.
-  auto wait_turn = [&](uint32_t b, int turn) {
-    return ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_hint(b, (uint32_t)turn & 1u, a.status));
-  };
+  // Wait until a buffer (or stage) has been filled for its `turn`-th use.
+  auto wait_turn = [&](uint32_t b, int turn) { wait_phase(b, (uint32_t)turn & 1u, gave_up, a.status); };
   // ... until its use before the `turn`-th is over: nothing to wait for in the first
-  auto wait_left = [&](uint32_t b, int turn) { return turn == 0 ? ok : wait_turn(b, turn - 1); };
+  auto wait_left = [&](uint32_t b, int turn) {
+    if (turn) wait_turn(b, turn - 1);
+  };
 
+  int st = 0, st_turn = 0;  // stage of tile it, and how often the ring has been round
+  auto next_stage = [&]() {
+    if (++st == kStages) {
+      st = 0;
+      ++st_turn;
+    }
+  };
+  int l_pieces = 0;  // pieces whose queries the first product's warp has waited for
+  int2 join = make_int2(0, 0);
+#pragma unroll 1
+  while (true) {
+    if (tid == 0) {
+      int n = 0;
+      while (n < kBatch && walk.next(list[n].p)) ++n;
+      *listed = n;
+      if (n && a.stream) join = walk.join_of(true, list[n - 1].p);
+    }
+    __syncthreads();
+    const int batch = *listed;
+    if (tid < batch) {
+      PieceTile& x = list[tid];
+      x.b = x.p.j / a.row_tiles;
+      x.rt = x.p.j - x.b * a.row_tiles;
+      x.t = tile_of<N>(a, x.b, x.rt);
+    }
+    __syncthreads();
+    if (!batch) break;
   if (warp < 4) {  // ---------------------------------------------------------------- keys, value scales
     const int page = warp >> 1, row = 32 * (warp & 1) + lane;  // key 32 warp + lane of the tile
     const int blk = tid >> 4, tok = (tid & 15) * 8;            // scales of 8 tokens of a block of 16 columns
-    while (walk.next(pc)) {
-      const Tile t = tile_of<N>(a, pc.j / a.row_tiles, pc.j % a.row_tiles);
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int st = it % kStages, buf = it & 1;
+#pragma unroll 1
+    for (int k = 0; k < batch; ++k) {
+      const Piece pc = list[k].p;
+      const int key_end = list[k].t.key_end, pg0 = list[k].t.pg0;
+#pragma unroll 1
+      for (int u = pc.u0; u < pc.u1; ++u, ++it, next_stage()) {
+        const int buf = it & 1;
         // The first product of tile it - 2 is done, so the scores of it - 4 had been read, the weights of it - 6 written, the second
         // product of it - 8 been done: the ring's slot is free.
-        if (!wait_turn(full(st), it / kStages) || !wait_left(bar(kFree, buf), it >> 1)) break;
+        wait_turn(full(st), st_turn);
+        wait_left(bar(kFree, buf), it >> 1);
         tc::fence_after();
         const uint8_t* stage = sm + st * TILE;
         {
@@ -269,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s[4] = {fp8x2_to_f16x2((uint16_t)w.x), fp8x2_to_f16x2((uint16_t)(w.x >> 16)), fp8x2_to_f16x2((uint16_t)w.y),
                            fp8x2_to_f16x2((uint16_t)(w.y >> 16))};
           // keys past the end, or of a page that is not there, hold anything, a NaN scale too: their values are 0
-          const int came = stage_ok[st], left = t.key_end - (t.pg0 + 2 * u) * kPage;
+          const int came = stage_ok[st], left = key_end - (pg0 + 2 * u) * kPage;
           if (came != 3 || left < 128) {
             const int valid = (came >> (tok >> 6) & 1) ? left - tok : 0;
 #pragma unroll
@@ -312,10 +369,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 8) {  // ---------------------------------------------------------------- values
     const int d = 32 * (warp - 4) + lane;
-    while (walk.next(pc)) {
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int st = it % kStages, buf = it & 1;
-        if (!wait_turn(full(st), it / kStages) || !wait_turn(c_ready(it), it / kScaleRing) || !wait_left(bar(vFree, buf), it >> 1)) break;
+#pragma unroll 1
+    for (int k = 0; k < batch; ++k) {
+      const Piece pc = list[k].p;
+#pragma unroll 1
+      for (int u = pc.u0; u < pc.u1; ++u, ++it, next_stage()) {
+        const int buf = it & 1;
+        wait_turn(full(st), st_turn);
+        wait_turn(c_ready(it), it / kScaleRing);
+        wait_left(bar(vFree, buf), it >> 1);
         tc::fence_after();
 #pragma unroll
         for (int page = 0; page < 2; ++page) {
@@ -349,10 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = (warp - 8) >> 2, w = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * w) << 16, tm_o = tm + lanes + tmO + N * g;
     uint64_t l[N / 2];  // this thread's keys' part of every row's sum, two rows together
-    while (walk.next(pc)) {
-      const int b = pc.j / a.row_tiles, rt = pc.j % a.row_tiles, h = pc.h;
-      const Tile t = tile_of<N>(a, b, rt);
-      const int rows = t.r1 - t.r0;
+#pragma unroll 1
+    for (int k = 0; k < batch; ++k) {
+      const Piece pc = list[k].p;
+      const Tile t = list[k].t;
+      const int b = list[k].b, rt = list[k].rt, h = pc.h, rows = t.r1 - t.r0;
       if (warp == 8 && lane == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
         flag_status(a.status, kDevBounds);
       // Q (all of the last piece's first products are done): rows warp - 8, + 8, ...
@@ -403,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) amax = fmaxf(amax, q_max[i]);
       // 2^k takes the tile's largest element into [2^14, 2^15)
-      const int k = amax > 0.f ? min(max(14 - ilogbf(amax), -100), 100) : 0;
-      const float f = exp2f((float)k), sc = a.scale_log2 * exp2f((float)-k);
+      const int e2 = amax > 0.f ? min(max(14 - ilogbf(amax), -100), 100) : 0;
+      const float f = exp2f((float)e2), sc = a.scale_log2 * exp2f((float)-e2);
 #pragma unroll
       for (int i = 0; i < N / 8; ++i) {
         const int r = warp - 8 + 8 * i;
@@ -427,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto id_of = [&](int u) { return lane < 2 && u < pc.u1 && 2 * u + lane < t.np ? bt[2 * u + lane] : -1; };
       const int first = pc.u0 + ((it ^ g) & 1);  // this group's first tile of the piece
       int id = id_of(first), last = -1;          // last: its last tile so far
+#pragma unroll 1
       for (int u = first; u < pc.u1; u += 2) {
         const int i = it + u - pc.u0, turn = i >> 1;
         wait_turn(bar(sFull, g), turn);
@@ -438,12 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t x[N / 2];
         auto scores = [&]() {  // -inf where the row does not see this thread's key
           float s[N];
-          if (ok) {
-            tmem_ld<N>(tm + lanes + kTmS + N * g, s);
-          } else {
-#pragma unroll
-            for (int r = 0; r < N; ++r) s[r] = 0.f;
-          }
+          tmem_ld<N>(tm + lanes + kTmS + N * g, s);
           if (masked) {
 #pragma unroll
             for (int r = 0; r < N; ++r) {
@@ -484,18 +543,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           group_barrier(g);
           if (last >= 0) {  // O holds the group's tiles before this one
-            if (wait_turn(bar(vFree, g), last >> 1)) {
-              tc::fence_after();
+            wait_turn(bar(vFree, g), last >> 1);
+            tc::fence_after();
 #pragma unroll 1
-              for (int r = 0; r < N; r += 16) {
-                float o[16];
-                tmem_ld<16>(tm_o + r, o);
+            for (int r = 0; r < N; r += 16) {
+              float o[16];
+              tmem_ld<16>(tm_o + r, o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] *= row_alpha(g)[r + e];
-                tmem_store<16>(tm_o + r, o);
-              }
-              tmem_wait_st();
+              for (int e = 0; e < 16; ++e) o[e] *= row_alpha(g)[r + e];
+              tmem_store<16>(tm_o + r, o);
             }
+            tmem_wait_st();
 #pragma unroll
             for (int r = 0; r < N / 2; ++r) l[r] = mul2(l[r], *reinterpret_cast<const uint64_t*>(row_alpha(g) + 2 * r));
           }
@@ -526,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = 0; r < N / 2; ++r) l[r] = add2(l[r], x[r]);
         last = i;
       }
-      any = true;
       it += pc.u1 - pc.u0;
       // the groups' rows joined; thread = column 32 w + lane, group g takes rows g N / 2 ..
       {
@@ -554,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         L = f0 * (l0[lane] + l0[N + lane] + l0[2 * N + lane] + l0[3 * N + lane]) +
             f1 * (l1[lane] + l1[N + lane] + l1[2 * N + lane] + l1[3 * N + lane]);
         inv = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
-        if (w == 0 && lane >= r_lo && lane < min(rows, r_lo + N / 2) && ok) {
+        if (w == 0 && lane >= r_lo && lane < min(rows, r_lo + N / 2)) {
           if (!whole)
             a.part_ml[part_row(pc, N) + lane] = make_float2(-off, L);
           else if (a.lse)
@@ -564,14 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float o0[N / 2], o1[N / 2];
 #pragma unroll
       for (int r = 0; r < N / 2; ++r) o0[r] = o1[r] = 0.f;
-      if (has0 && ok) tmem_ld_part<N / 2>(tm + lanes + tmO + r_lo, o0);
-      if (has1 && ok) tmem_ld_part<N / 2>(tm + lanes + tmO + N + r_lo, o1);
+      if (has0) tmem_ld_part<N / 2>(tm + lanes + tmO + r_lo, o0);
+      if (has1) tmem_ld_part<N / 2>(tm + lanes + tmO + N + r_lo, o1);
       tc::fence_before();
       const int d = 32 * w + lane;
 #pragma unroll
       for (int r = 0; r < N / 2; ++r) {
         const float e0 = __shfl_sync(0xffffffffu, f0 * inv, r_lo + r), e1 = __shfl_sync(0xffffffffu, f1 * inv, r_lo + r);
-        if (r_lo + r >= rows || !ok) continue;
+        if (r_lo + r >= rows) continue;
         const float v = fmaf(o0[r], e0, o1[r] * e1);
         if (whole)
           static_cast<bf16*>(a.out)[row_out[r_lo + r] + d] = __float2bfloat16_rn(v);
@@ -580,19 +637,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       softmax_barrier();  // both O, row_l, row_off are the next piece's
     }
-    if (a.stream && warp == 8 && lane == 0) a.joins[blockIdx.x] = walk.join_of(any, pc);
   } else if (warp == 16) {  // ---------------------------------------------------------------- copies
     const bool one = elect_one();
-    while (walk.next(pc)) {
-      const int b = pc.j / a.row_tiles;
-      const Tile t = tile_of<N>(a, b, pc.j % a.row_tiles);
-      const int32_t* bt = a.bt + (size_t)b * a.max_pages + t.pg0;
+#pragma unroll 1
+    for (int k = 0; k < batch; ++k) {
+      const Piece pc = list[k].p;
+      const Tile t = list[k].t;
+      const int32_t* bt = a.bt + (size_t)list[k].b * a.max_pages + t.pg0;
       auto page_of = [&](int i) { return i < t.np ? bt[i] : -1; };
       int id0 = page_of(2 * pc.u0), id1 = page_of(2 * pc.u0 + 1);
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int st = it % kStages;
+#pragma unroll 1
+      for (int u = pc.u0; u < pc.u1; ++u, ++it, next_stage()) {
         const int next0 = u + 1 < pc.u1 ? page_of(2 * u + 2) : -1, next1 = u + 1 < pc.u1 ? page_of(2 * u + 3) : -1;
-        if (!wait_left(empty(st), it / kStages)) break;
+        wait_left(empty(st), st_turn);
         const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
         if (one) {
           if (id0 >= a.n_pages || id1 >= a.n_pages) flag_status(a.status, kDevBounds);
@@ -620,12 +677,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 17) {  // ---------------------------------------------------------------- first product
     const bool one = elect_one();
-    int pieces = 0;
-    while (walk.next(pc)) {
-      if (!wait_turn(q_ready, pieces++)) break;
+#pragma unroll 1
+    for (int k = 0; k < batch; ++k) {
+      const Piece pc = list[k].p;
+      wait_turn(q_ready, l_pieces++);
+#pragma unroll 1
       for (int u = pc.u0; u < pc.u1; ++u, ++it) {
         const int buf = it & 1;
-        if (!wait_turn(bar(kReady, buf), it >> 1) || !wait_left(bar(sFree, buf), it >> 1)) break;
+        wait_turn(bar(kReady, buf), it >> 1);
+        wait_left(bar(sFree, buf), it >> 1);
         tc::fence_after();
         if (one) {
           const uint64_t bd = tc::sw128_desc(sb + S::Q);
@@ -641,10 +701,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {  // ---------------------------------------------------------------- second product
     const bool one = elect_one();
-    while (walk.next(pc)) {
+#pragma unroll 1
+    for (int k = 0; k < batch; ++k) {
+      const Piece pc = list[k].p;
+#pragma unroll 1
       for (int u = pc.u0; u < pc.u1; ++u, ++it) {
         const int buf = it & 1;
-        if (!wait_turn(bar(vReady, buf), it >> 1) || !wait_turn(bar(pReady, buf), it >> 1)) break;
+        wait_turn(bar(vReady, buf), it >> 1);
+        wait_turn(bar(pReady, buf), it >> 1);
         tc::fence_after();
         if (one) {
           const uint64_t bd = p_desc<N>(sb + S::P + buf * 128 * N * 2);
@@ -659,6 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
+  __syncthreads();  // the list is the next batch's
+  }
+  if (tid == 0 && a.stream) a.joins[blockIdx.x] = join;
   // every role is through; after a wait that ran out (status flagged) the copies and products in flight have had its time
   tc::fence_before();
   __syncthreads();
