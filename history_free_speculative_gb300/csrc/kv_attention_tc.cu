@@ -6,12 +6,13 @@
 // A thread of the dequantising warps owns one lane of tensor memory: one key (its 64 bytes of codes, 8 scales) or one
 // column (its 64 bytes of codes along the tokens, the scales of 128 tokens). It turns its codes into f16 (e2m1 x e4m3 is exact)
 // and writes them with tcgen05.st, so the cache never passes through shared memory a second time. N = 16 or 32
-// query rows; Q^T and P^T are the B operands in shared memory.
+// query rows; Q^T and P^T are the B operands in shared memory. The sums of the weights are a third product with a tile of
+// ones, L [128 x N] += 1 P^T: the tensor pipe is idle four fifths of the time, and the 32 sums a thread would hold itself spilled.
 // Warps: 0-3 keys (and the value scales as f16, once for the 16 columns that share them), 4-7 values, 8-15 softmax and
 // output (thread = key, then column), 16 copies, 17 and 18 the issue of the first and the second product.
 // The softmax warps are two groups that take the tiles in turn, each with its own scores, weights, maxima, sums and O, joined at
 // a piece's end: one group's latencies pass under the other's tile (one group alone took 3,300 clocks a tile). A group keeps one
-// reference m per row, moved only when a weight passes it by more than 2^8 (a vote of its 128 threads per tile); only then
+// reference m per row, moved only when a weight passes it by more than 2^8 (a vote of its four warps per tile); only then
 // are exact maxima formed and O, the sums rescaled. Weights are 2^(s - m + 6) <= 2^14, rounded to f16: weights down
 // to 2^-31 of the reference count, and the largest score is never below it. Queries are scaled by one power of two per
 // tile into f16's range: exact for bf16 elements down to 2^-32 of the tile's largest, and off by 2^-39 of that below.
@@ -20,8 +21,6 @@
 // mma.sync does both products of a 32-row tile in 8 clocks a key an SM (measured 2.0 per m16n8k16), above the 6.8 that the bytes take
 // at the copy rate of HBM, and needs its operands and outputs in registers: the mma.sync kernel ran at 19.
 #include <math.h>
-
-#include <type_traits>
 
 #include "kv_attention.cuh"
 #include "tc_gemm.h"
@@ -33,11 +32,12 @@ namespace {
 constexpr int DH = 128, REC = rec_bytes(DH), TILE = 2 * REC;
 constexpr int kStages = 9;
 constexpr int kThreads = 19 * 32;
+constexpr int kFlagRing = 32;      // the copies are at most kStages + 4 tiles ahead of the softmax
 constexpr int kScaleRing = 8;      // tiles of value scales: the keys' warps are never that far ahead of the values'
 // a stage: key codes of both pages (rows of 64 B, 64-byte swizzle), value codes (rows of 32 B, 32-byte swizzle), scales
 constexpr int kV = 8192, kS = 16384;
-// tensor memory columns: K and V^T tiles twice, S^T twice, O^T
-constexpr int kTmK = 0, kTmV = 128, kTmS = 256, kTmCols = 512;
+// tensor memory columns: K and V^T tiles twice; then S^T, O^T and L twice each; a tile of ones
+constexpr int kTmK = 0, kTmV = 128, kTmS = 256, kTmOnes = 448, kTmCols = 512;
 constexpr float kTcWeightExp = 6.f;
 constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key
 
@@ -50,10 +50,10 @@ struct Smem {
   static constexpr int KEYS = ROWS + 20 * N * 4 + 64;  // int2: keys a row sees
   static constexpr int OUT = KEYS + N * 8;           // int64: where a row's output and lse go
   static constexpr int BARS = OUT + N * 16;
-  static constexpr int NBARS = 2 * kStages + 15 + kScaleRing;
-  static constexpr int OK = BARS + NBARS * 8;        // per stage: which of its pages came
-  static constexpr int TM = OK + kStages * 4;
-  static constexpr int LIST = (TM + 8 + 15) / 16 * 16;   // PieceTile [kBatch], then their number
+  static constexpr int NBARS = 2 * kStages + 17 + kScaleRing;
+  static constexpr int OK = BARS + NBARS * 8;        // [kFlagRing]: which of a tile's pages came
+  static constexpr int TM = OK + kFlagRing * 4;
+  static constexpr int LIST = (TM + 16 + 15) / 16 * 16;   // PieceTile [kBatch], then their number
   static constexpr int PREFIX = LIST + kBatch * (int)sizeof(PieceTile) + 8;
   static constexpr int BYTES = PREFIX + (kMaxList + 1) * 4 + 1024;  // alignment of the swizzled stages
   static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
@@ -145,16 +145,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(z)
       : "memory");
 }
-// Whether q holds in any of the 128 threads of softmax group g (a barrier among them)
-__device__ __forceinline__ bool any_of_group(bool q, int g) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, r;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred r, %2, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)q), "r"(1 + g)
-      : "memory");
-  return r != 0;
-}
 __device__ __forceinline__ void group_barrier(int g) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 __device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
 __device__ __forceinline__ bool elect_one() {
@@ -163,28 +153,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Sums of N rows over a warp: the halves of the rows change sides step by step; lane i returns row i (N = 16: i / 2).
-template <int N>
-__device__ __forceinline__ float warp_row_sums(float (&v)[N], int lane) {
-  auto step = [&](auto cnt_c, int o) {
-    constexpr int cnt = decltype(cnt_c)::value;
-    const bool up = lane & o;
-#pragma unroll
-    for (int r = 0; r < cnt; ++r) {
-      const float give = up ? v[r] : v[r + cnt], keep = up ? v[r + cnt] : v[r];
-      v[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
-  };
-  step(std::integral_constant<int, N / 2>(), 16);
-  step(std::integral_constant<int, N / 4>(), 8);
-  step(std::integral_constant<int, N / 8>(), 4);
-  step(std::integral_constant<int, N / 16>(), 2);
-  if constexpr (N == 32) {
-    step(std::integral_constant<int, 1>(), 1);
-    return v[0];
-  }
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
-}
 // A wait that did not end at once: sleep and look again, up to the limit. Then the status says so, and *gave_up ends this wait
 // and every later one of the CTA: the roles run to their ends on whatever the buffers hold.
 __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up, int* status) {
@@ -234,7 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int kind, int buf) { return bars + 8 * (2 * kStages + 2 * kind + buf); };
   enum { kReady, kFree, vReady, vFree, sFull, sFree, pReady };   // each twice; then q_ready, and the ring of value scales
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + S::TM + 4);
+  volatile int* move_ref = gave_up + 1;   // [group]: a weight of the tile passes its reference by too much
   const uint32_t q_ready = bars + 8 * (2 * kStages + 14);
+  auto voted = [&](int g) { return bars + 8 * (2 * kStages + 15 + kScaleRing + g); };
   auto c_ready = [&](int i) { return bars + 8 * (2 * kStages + 15 + i % kScaleRing); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -255,6 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(bar(pReady, i), 4);
     }
     for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(c_ready(i), 4);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(voted(i), 4);
+      move_ref[i] = 0;
+    }
     *gave_up = 0;
     tc::mbar_init(q_ready, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -267,7 +241,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tm = *tm_slot;
-  constexpr uint32_t tmO = kTmS + 2 * N;
+  if (warp < 4) {  // read after the next barrier
+    uint32_t ones[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) ones[i] = 0x3C003C00u;
+    tmem_st32(tm + ((uint32_t)(32 * warp) << 16) + kTmOnes, ones);
+    tmem_st32(tm + ((uint32_t)(32 * warp) << 16) + kTmOnes + 32, ones);
+    tmem_wait_st();
+    tc::fence_before();
+  }
+  constexpr uint32_t tmO = kTmS + 2 * N, tmL = kTmS + 4 * N;
+  static_assert(tmL + 2 * N <= kTmOnes, "tensor memory");
 
   Pieces<N> walk(a, prefix);  // thread 0's
   int it = 0;  // tiles so far, over all pieces: buffer it & 1, stage it % kStages
@@ -326,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s[4] = {fp8x2_to_f16x2((uint16_t)w.x), fp8x2_to_f16x2((uint16_t)(w.x >> 16)), fp8x2_to_f16x2((uint16_t)w.y),
                            fp8x2_to_f16x2((uint16_t)(w.y >> 16))};
           // keys past the end, or of a page that is not there, hold anything, a NaN scale too: their values are 0
-          const int came = stage_ok[st], left = key_end - (pg0 + 2 * u) * kPage;
+          const int came = stage_ok[it % kFlagRing], left = key_end - (pg0 + 2 * u) * kPage;
           if (came != 3 || left < 128) {
             const int valid = (came >> (tok >> 6) & 1) ? left - tok : 0;
 #pragma unroll
@@ -375,8 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int u = pc.u0; u < pc.u1; ++u, ++it, next_stage()) {
         const int buf = it & 1;
-        wait_turn(full(st), st_turn);
-        wait_turn(c_ready(it), it / kScaleRing);
+        wait_turn(c_ready(it), it / kScaleRing);  // the keys' warps have waited for the stage
         wait_left(bar(vFree, buf), it >> 1);
         tc::fence_after();
 #pragma unroll
@@ -409,8 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 16) {  // ---------------------------------------------------------------- softmax and output
     const int g = (warp - 8) >> 2, w = warp & 3;
-    const uint32_t lanes = (uint32_t)(32 * w) << 16, tm_o = tm + lanes + tmO + N * g;
-    uint64_t l[N / 2];  // this thread's keys' part of every row's sum, two rows together
+    const uint32_t lanes = (uint32_t)(32 * w) << 16;
 #pragma unroll 1
     for (int k = 0; k < batch; ++k) {
       const Piece pc = list[k].p;
@@ -479,25 +461,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(q_ready);
-#pragma unroll
-      for (int r = 0; r < N / 2; ++r) l[r] = 0;
       const uint64_t sc2 = pack2f(sc, sc);
       // tiles wholly inside every row's range need no masks
       const int full_end = (int)min(max(t.p0 + t.t_lo + 1, 0LL), t.cap);
       const int full_beg = a.window ? (int)min(max(t.p0 + t.t_hi - a.window + 1, 0LL), t.cap) : 0;
-      // lanes 0 and 1: the ids of the next tile's pages (a stage's flags may be the next tile's by the time its scores come)
-      const int32_t* bt = a.bt + (size_t)b * a.max_pages + t.pg0;
-      auto id_of = [&](int u) { return lane < 2 && u < pc.u1 && 2 * u + lane < t.np ? bt[2 * u + lane] : -1; };
       const int first = pc.u0 + ((it ^ g) & 1);  // this group's first tile of the piece
-      int id = id_of(first), last = -1;          // last: its last tile so far
+      int last = -1;                             // its last tile so far
 #pragma unroll 1
       for (int u = first; u < pc.u1; u += 2) {
         const int i = it + u - pc.u0, turn = i >> 1;
         wait_turn(bar(sFull, g), turn);
         tc::fence_after();
         const int key0 = (t.pg0 + 2 * u) * kPage, key = key0 + 32 * w + lane;
-        const int came = __ballot_sync(0xffffffffu, id >= 0 && id < a.n_pages) & 3;
-        id = id_of(u + 2);
+        wait_turn(c_ready(i), i / kScaleRing);  // long over: for the flags' sake
+        const int came = stage_ok[i % kFlagRing];
         const bool masked = came != 3 || key0 < full_beg || key0 + 128 > full_end, there = (came >> (w >> 1)) & 1;
         uint64_t x[N / 2];
         auto scores = [&]() {  // -inf where the row does not see this thread's key
@@ -525,7 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           return top;
         };
         scores();
-        if (any_of_group(exponents() > kTcWeightExp + 8.f, g)) {
+        if (exponents() > kTcWeightExp + 8.f) move_ref[g] = 1;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(voted(g));
+#pragma unroll
+        for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
+        wait_turn(voted(g), turn);
+        if (move_ref[g]) {
           // new references: the exact maxima of the tile
           scores();
 #pragma unroll
@@ -540,31 +523,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float off0 = row_off(g)[lane], off1 = fminf(off0, kTcWeightExp - mx * sc);
             row_alpha(g)[lane] = off1 < off0 ? tc::ex2_approx(off1 - off0) : 1.f;
             if (off1 < off0) row_off(g)[lane] = off1;   // a NaN stays
+            if (lane == 0) move_ref[g] = 0;
           }
           group_barrier(g);
-          if (last >= 0) {  // O holds the group's tiles before this one
+          if (last >= 0) {  // O and L hold the group's tiles before this one
             wait_turn(bar(vFree, g), last >> 1);
             tc::fence_after();
 #pragma unroll 1
-            for (int r = 0; r < N; r += 16) {
+            for (int r = 0; r < 2 * N; r += 16) {
+              const uint32_t at = tm + lanes + (r < N ? tmO + N * g + r : tmL + N * g + r - N);
               float o[16];
-              tmem_ld<16>(tm_o + r, o);
+              tmem_ld<16>(at, o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= row_alpha(g)[r + e];
-              tmem_store<16>(tm_o + r, o);
+              for (int e = 0; e < 16; ++e) o[e] *= row_alpha(g)[r % N + e];
+              tmem_store<16>(at, o);
             }
             tmem_wait_st();
-#pragma unroll
-            for (int r = 0; r < N / 2; ++r) l[r] = mul2(l[r], *reinterpret_cast<const uint64_t*>(row_alpha(g) + 2 * r));
           }
           scores();
           exponents();
+#pragma unroll
+          for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
         }
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(sFree, g));
-#pragma unroll
-        for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
         // P: this key's N weights side by side, once the group's last product has read the buffer
         wait_left(bar(vFree, g), turn);
         uint8_t* pp = sm + S::P + g * 128 * N * 2 + (32 * w + lane) * N * 2;
@@ -580,20 +563,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(pReady, g));
-#pragma unroll
-        for (int r = 0; r < N / 2; ++r) l[r] = add2(l[r], x[r]);
         last = i;
       }
       it += pc.u1 - pc.u0;
       // the groups' rows joined; thread = column 32 w + lane, group g takes rows g N / 2 ..
-      {
-        float v[N];
+      if (last >= 0) {
+        wait_turn(bar(vFree, g), last >> 1);
+        tc::fence_after();
+        if (w == 0) {  // every lane of L has the sums
+          float sum[N];
+          tmem_ld<N>(tm + lanes + tmL + N * g, sum);
+          if (lane == 0)
 #pragma unroll
-        for (int r = 0; r < N / 2; ++r) v[2 * r] = lo2f(l[r]), v[2 * r + 1] = hi2f(l[r]);
-        const float sum = warp_row_sums<N>(v, lane);
-        if (N == 32 || (lane & 1) == 0) row_l(g)[w * N + (N == 32 ? lane : lane >> 1)] = sum;
+            for (int r = 0; r < N; ++r) row_l(g)[r] = sum[r];
+        }
       }
-      if (last >= 0) wait_turn(bar(vFree, g), last >> 1);
       tc::fence_before();
       softmax_barrier();
       tc::fence_after();
@@ -608,8 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f0 = has0 ? (o0 == off ? 1.f : tc::ex2_approx(off - o0)) : 0.f;
         f1 = has1 ? (o1 == off ? 1.f : tc::ex2_approx(off - o1)) : 0.f;
         const float *l0 = row_l(0), *l1 = row_l(1);
-        L = f0 * (l0[lane] + l0[N + lane] + l0[2 * N + lane] + l0[3 * N + lane]) +
-            f1 * (l1[lane] + l1[N + lane] + l1[2 * N + lane] + l1[3 * N + lane]);
+        L = (has0 ? f0 * l0[lane] : 0.f) + (has1 ? f1 * l1[lane] : 0.f);
         inv = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
         if (w == 0 && lane >= r_lo && lane < min(rows, r_lo + N / 2)) {
           if (!whole)
@@ -653,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
         if (one) {
           if (id0 >= a.n_pages || id1 >= a.n_pages) flag_status(a.status, kDevBounds);
-          stage_ok[st] = came;
+          stage_ok[it % kFlagRing] = came;
           if (came) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc::mbar_expect_tx(full(st), (came == 3 ? 2 : 1) * REC);
@@ -716,6 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // a group's first tile of the piece starts its O
             umma_ts(o, va + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || u - pc.u0 >= 2);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_ts(tm + tmL + N * buf, tm + kTmOnes + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || u - pc.u0 >= 2);
           tc::umma_commit(bar(vFree, buf));
         }
         __syncwarp();
