@@ -8,8 +8,8 @@
 // and writes them with tcgen05.st, so the cache never passes through shared memory a second time. N = 16 or 32
 // query rows; Q^T and P^T are the B operands in shared memory. The sums of the weights are a third product with a tile of
 // ones, L [128 x N] += 1 P^T: the tensor pipe is idle four fifths of the time, and the 32 sums a thread would hold itself spilled.
-// Warps: 0-3 keys (and the value scales as f16, once for the 16 columns that share them), 4-7 values, 8-15 softmax and
-// output (thread = key, then column), 16 copies, 17 and 18 the issue of the first and the second product.
+// Warps: 0-3 keys, 4-7 values, 8-15 softmax and output (thread = key, then column), 16 value scales to f16, 17 and 18 the issue
+// of the first and the second product, 19 copies: five warps a scheduler.
 // The softmax warps are two groups that take the tiles in turn, each with its own scores, weights, maxima, sums and O, joined at
 // a piece's end: one group's latencies pass under the other's tile (one group alone took 3,300 clocks a tile). A group keeps one
 // reference m per row, moved only when a weight passes it by more than 2^8 (a vote of its four warps per tile); only then
@@ -30,10 +30,11 @@ namespace kv {
 namespace {
 
 constexpr int DH = 128, REC = rec_bytes(DH), TILE = 2 * REC;
-constexpr int kStages = 9;
-constexpr int kThreads = 19 * 32;
-constexpr int kFlagRing = 32;      // the copies are at most kStages + 4 tiles ahead of the softmax
-constexpr int kScaleRing = 8;      // tiles of value scales: the keys' warps are never that far ahead of the values'
+constexpr int kStages = 8;
+constexpr int kThreads = 20 * 32;
+// A tile's flags and the barrier of its value scales, which the softmax looks at last: the copies and scales of tile i + 16 take
+// the stage of i + 8, whose values take the buffer of i + 6, whose second product comes after the softmax of i + 6 and so of i.
+constexpr int kRing = 2 * kStages;
 // a stage: key codes of both pages (rows of 64 B, 64-byte swizzle), value codes (rows of 32 B, 32-byte swizzle), scales
 constexpr int kV = 8192, kS = 16384;
 // tensor memory columns: K and V^T tiles twice; then S^T, O^T and L twice each; a tile of ones
@@ -45,14 +46,14 @@ template <int N>
 struct Smem {
   static constexpr int Q = kStages * TILE;           // [2 halves][N rows][128 B], 128-byte swizzle
   static constexpr int P = Q + N * 256;              // [2][128 keys][N rows] f16, rows of N contiguous
-  static constexpr int VS = P + 2 * 128 * N * 2;     // [ring][8 blocks][128 tokens] f16: value scales
-  static constexpr int ROWS = VS + kScaleRing * 2048;         // floats: offset [2][N], alpha [2][N], l [2][4][N], red [2][4][N], tile max
+  static constexpr int VS = P + 2 * 128 * N * 2;     // [stage][8 blocks][128 tokens] f16: value scales
+  static constexpr int ROWS = VS + kStages * 2048;         // floats: offset [2][N], alpha [2][N], l [2][4][N], red [2][4][N], tile max
   static constexpr int KEYS = ROWS + 20 * N * 4 + 64;  // int2: keys a row sees
   static constexpr int OUT = KEYS + N * 8;           // int64: where a row's output and lse go
   static constexpr int BARS = OUT + N * 16;
-  static constexpr int NBARS = 2 * kStages + 17 + kScaleRing;
-  static constexpr int OK = BARS + NBARS * 8;        // [kFlagRing]: which of a tile's pages came
-  static constexpr int TM = OK + kFlagRing * 4;
+  static constexpr int NBARS = 2 * kStages + 17 + kRing;
+  static constexpr int OK = BARS + NBARS * 8;        // [kRing]: which of a tile's pages came
+  static constexpr int TM = OK + kRing * 4;
   static constexpr int LIST = (TM + 16 + 15) / 16 * 16;   // PieceTile [kBatch], then their number
   static constexpr int PREFIX = LIST + kBatch * (int)sizeof(PieceTile) + 8;
   static constexpr int BYTES = PREFIX + (kMaxList + 1) * 4 + 1024;  // alignment of the swizzled stages
@@ -200,12 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
   auto bar = [&](int kind, int buf) { return bars + 8 * (2 * kStages + 2 * kind + buf); };
-  enum { kReady, kFree, vReady, vFree, sFull, sFree, pReady };   // each twice; then q_ready, and the ring of value scales
+  enum { kReady, kFree, vReady, vFree, sFull, sFree, pReady };   // each twice; then q_ready, voted twice, a tile's value scales
   volatile int* gave_up = reinterpret_cast<volatile int*>(sm + S::TM + 4);
   volatile int* move_ref = gave_up + 1;   // [group]: a weight of the tile passes its reference by too much
   const uint32_t q_ready = bars + 8 * (2 * kStages + 14);
-  auto voted = [&](int g) { return bars + 8 * (2 * kStages + 15 + kScaleRing + g); };
-  auto c_ready = [&](int i) { return bars + 8 * (2 * kStages + 15 + i % kScaleRing); };
+  auto voted = [&](int g) { return bars + 8 * (2 * kStages + 15 + g); };
+  auto c_ready = [&](int i) { return bars + 8 * (2 * kStages + 17 + i % kRing); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   pdl_wait();  // no early trigger: the grid fills the SMs
@@ -215,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(full(s), 1);
       tc::mbar_init(empty(s), 8);  // a warp of keys or values each
     }
+    for (int i = 0; i < kRing; ++i) tc::mbar_init(c_ready(i), 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(kReady, i), 4);
       tc::mbar_init(bar(kFree, i), 1);
@@ -224,7 +226,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(bar(sFree, i), 4);
       tc::mbar_init(bar(pReady, i), 4);
     }
-    for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(c_ready(i), 4);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(voted(i), 4);
       move_ref[i] = 0;
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(tmL + 2 * N <= kTmOnes, "tensor memory");
 
   Pieces<N> walk(a, prefix);  // thread 0's
-  int it = 0;  // tiles so far, over all pieces: buffer it & 1, stage it % kStages
+  int it = 0;  // tiles so far, over all pieces: buffer it & 1, stage it % kStages of turn it / kStages
   // Wait until a buffer (or stage) has been filled for its `turn`-th use.
   auto wait_turn = [&](uint32_t b, int turn) { wait_phase(b, (uint32_t)turn & 1u, gave_up, a.status); };
   // ... until its use before the `turn`-th is over: nothing to wait for in the first
@@ -262,13 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (turn) wait_turn(b, turn - 1);
   };
 
-  int st = 0, st_turn = 0;  // stage of tile it, and how often the ring has been round
-  auto next_stage = [&]() {
-    if (++st == kStages) {
-      st = 0;
-      ++st_turn;
-    }
-  };
   int l_pieces = 0;  // pieces whose queries the first product's warp has waited for
   int2 join = make_int2(0, 0);
 #pragma unroll 1
@@ -289,40 +283,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (!batch) break;
-  if (warp < 4) {  // ---------------------------------------------------------------- keys, value scales
+  if (warp < 4) {  // ---------------------------------------------------------------- keys
     const int page = warp >> 1, row = 32 * (warp & 1) + lane;  // key 32 warp + lane of the tile
-    const int blk = tid >> 4, tok = (tid & 15) * 8;            // scales of 8 tokens of a block of 16 columns
 #pragma unroll 1
     for (int k = 0; k < batch; ++k) {
       const Piece pc = list[k].p;
-      const int key_end = list[k].t.key_end, pg0 = list[k].t.pg0;
 #pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it, next_stage()) {
-        const int buf = it & 1;
-        // The first product of tile it - 2 is done, so the scores of it - 4 had been read, the weights of it - 6 written, the second
-        // product of it - 8 been done: the ring's slot is free.
-        wait_turn(full(st), st_turn);
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int buf = it & 1, st = it % kStages;
+        wait_turn(full(st), it / kStages);
         wait_left(bar(kFree, buf), it >> 1);
         tc::fence_after();
         const uint8_t* stage = sm + st * TILE;
-        {
-          const uint2 w = *reinterpret_cast<const uint2*>(stage + kS + (tok >> 6) * 1024 + 512 + blk * 64 + (tok & 63));
-          uint32_t s[4] = {fp8x2_to_f16x2((uint16_t)w.x), fp8x2_to_f16x2((uint16_t)(w.x >> 16)), fp8x2_to_f16x2((uint16_t)w.y),
-                           fp8x2_to_f16x2((uint16_t)(w.y >> 16))};
-          // keys past the end, or of a page that is not there, hold anything, a NaN scale too: their values are 0
-          const int came = stage_ok[it % kFlagRing], left = key_end - (pg0 + 2 * u) * kPage;
-          if (came != 3 || left < 128) {
-            const int valid = (came >> (tok >> 6) & 1) ? left - tok : 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = 2 * i + 1 < valid ? s[i] : 2 * i < valid ? s[i] & 0xffffu : 0u;
-          }
-          *reinterpret_cast<uint4*>(sm + S::VS + it % kScaleRing * 2048 + blk * 256 + tok * 2) = make_uint4(s[0], s[1], s[2], s[3]);
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(c_ready(it));
         const uint8_t* base = stage + page * 4096 + row * 64;
         const uint2 sc = *reinterpret_cast<const uint2*>(stage + kS + page * 1024 + row * 8);
-        __syncwarp();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t r[32];
@@ -357,15 +331,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < batch; ++k) {
       const Piece pc = list[k].p;
 #pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it, next_stage()) {
-        const int buf = it & 1;
-        wait_turn(c_ready(it), it / kScaleRing);  // the keys' warps have waited for the stage
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int buf = it & 1, st = it % kStages;
+        wait_turn(c_ready(it), it / kRing);  // and the stage with them
         wait_left(bar(vFree, buf), it >> 1);
         tc::fence_after();
 #pragma unroll
         for (int page = 0; page < 2; ++page) {
           const uint8_t* base = sm + st * TILE + kV + page * 4096 + d * 32;
-          const uint8_t* sp = sm + S::VS + it % kScaleRing * 2048 + (d >> 4) * 256 + page * 128;
+          const uint8_t* sp = sm + S::VS + st * 2048 + (d >> 4) * 256 + page * 128;
           uint32_t r[32];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {  // 32 tokens
@@ -401,23 +375,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == 8 && lane == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
         flag_status(a.status, kDevBounds);
       // Q (all of the last piece's first products are done): rows warp - 8, + 8, ...
+      uint2 raw_q[N / 8];
       float v[N / 8][4], amax = 0.f;
       bool bad[N / 8];
 #pragma unroll
       for (int i = 0; i < N / 8; ++i) {  // every row's load before the first use
-        const int r = warp - 8 + 8 * i;
-        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-        if (r < rows) {
-          const int tk = (t.r0 + r) / a.group, hq = h * a.group + (t.r0 + r) % a.group;
-          const bf16* q = static_cast<const bf16*>(a.q) + ((long long)b * a.T + tk) * a.qs + (long long)hq * DH + 4 * lane;
-          if (a.vec) {
-            const uint2 x = *reinterpret_cast<const uint2*>(q);
-            v[i][0] = __uint_as_float(x.x << 16), v[i][1] = __uint_as_float(x.x & 0xffff0000u);
-            v[i][2] = __uint_as_float(x.y << 16), v[i][3] = __uint_as_float(x.y & 0xffff0000u);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][e] = to_f32(q[e]);
-          }
+        const int r = min(warp - 8 + 8 * i, rows - 1);
+        const int tk = (t.r0 + r) / a.group, hq = h * a.group + (t.r0 + r) % a.group;
+        const bf16* q = static_cast<const bf16*>(a.q) + ((long long)b * a.T + tk) * a.qs + (long long)hq * DH + 4 * lane;
+        if (a.vec) {
+          raw_q[i] = *reinterpret_cast<const uint2*>(q);
+        } else {
+          const unsigned short* q16 = reinterpret_cast<const unsigned short*>(q);
+          raw_q[i] = make_uint2(q16[0] | (uint32_t)q16[1] << 16, q16[2] | (uint32_t)q16[3] << 16);
         }
       }
       if (warp == 8 && lane < N) {
@@ -431,6 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < N / 8; ++i) {
         const int r = warp - 8 + 8 * i;
+        const uint2 x = r < rows ? raw_q[i] : make_uint2(0u, 0u);
+        v[i][0] = __uint_as_float(x.x << 16), v[i][1] = __uint_as_float(x.x & 0xffff0000u);
+        v[i][2] = __uint_as_float(x.y << 16), v[i][3] = __uint_as_float(x.y & 0xffff0000u);
         bool q_bad = false;
         float m = 0.f;
 #pragma unroll
@@ -473,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_turn(bar(sFull, g), turn);
         tc::fence_after();
         const int key0 = (t.pg0 + 2 * u) * kPage, key = key0 + 32 * w + lane;
-        wait_turn(c_ready(i), i / kScaleRing);  // long over: for the flags' sake
-        const int came = stage_ok[i % kFlagRing];
+        wait_turn(c_ready(i), i / kRing);  // long over: for the flags' sake
+        const int came = stage_ok[i % kRing];
         const bool masked = came != 3 || key0 < full_beg || key0 + 128 > full_end, there = (came >> (w >> 1)) & 1;
         uint64_t x[N / 2];
         auto scores = [&]() {  // -inf where the row does not see this thread's key
@@ -620,7 +593,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       softmax_barrier();  // both O, row_l, row_off are the next piece's
     }
-  } else if (warp == 16) {  // ---------------------------------------------------------------- copies
+  } else if (warp == 16) {  // ---------------------------------------------------------------- value scales
+    // as f16, once for the 16 columns that share them: lane = block of 16 columns lane / 4, 32 tokens
+    const int blk = lane >> 2, tok = (lane & 3) * 32;
+#pragma unroll 1
+    for (int k = 0; k < batch; ++k) {
+      const Piece pc = list[k].p;
+      const int key_end = list[k].t.key_end, pg0 = list[k].t.pg0;
+#pragma unroll 1
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int st = it % kStages;
+        wait_turn(full(st), it / kStages);
+        // keys past the end, or of a page that is not there, hold anything, a NaN scale too: their values are 0
+        const int came = stage_ok[it % kRing], left = key_end - (pg0 + 2 * u) * kPage;
+        const int valid = came == 3 && left >= 128 ? 32 : (came >> (tok >> 6) & 1) ? left - tok : 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint4 w = *reinterpret_cast<const uint4*>(sm + st * TILE + kS + (tok >> 6) * 1024 + 512 + blk * 64 + (tok & 63) + 16 * q);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          uint32_t s[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            s[i] = fp8x2_to_f16x2((uint16_t)(ww[i / 2] >> (16 * (i & 1))));
+            const int at = 16 * q + 2 * i;
+            if (valid < 32) s[i] = at + 1 < valid ? s[i] : at < valid ? s[i] & 0xffffu : 0u;
+          }
+          uint4* to = reinterpret_cast<uint4*>(sm + S::VS + st * 2048 + blk * 256 + tok * 2 + 32 * q);
+          to[0] = make_uint4(s[0], s[1], s[2], s[3]);
+          to[1] = make_uint4(s[4], s[5], s[6], s[7]);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(c_ready(it));
+      }
+    }
+  } else if (warp == 19) {  // ---------------------------------------------------------------- copies
     const bool one = elect_one();
 #pragma unroll 1
     for (int k = 0; k < batch; ++k) {
@@ -630,13 +636,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto page_of = [&](int i) { return i < t.np ? bt[i] : -1; };
       int id0 = page_of(2 * pc.u0), id1 = page_of(2 * pc.u0 + 1);
 #pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it, next_stage()) {
+      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+        const int st = it % kStages;
         const int next0 = u + 1 < pc.u1 ? page_of(2 * u + 2) : -1, next1 = u + 1 < pc.u1 ? page_of(2 * u + 3) : -1;
-        wait_left(empty(st), st_turn);
+        wait_left(empty(st), it / kStages);
         const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
         if (one) {
           if (id0 >= a.n_pages || id1 >= a.n_pages) flag_status(a.status, kDevBounds);
-          stage_ok[it % kFlagRing] = came;
+          stage_ok[it % kRing] = came;
           if (came) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc::mbar_expect_tx(full(st), (came == 3 ? 2 : 1) * REC);
