@@ -1,14 +1,13 @@
 // Append to and read from the paged 4-bit cache of the target side.
 //
-// Append: one CTA per (page a request's new rows touch, KV head, request). Its
-// items are (token, 16 columns) for keys and for values: one thread loads 16
-// columns (and, for rotated keys, their partners), rotates, quantises and has the
-// scale byte and eight code bytes of that token. Keys go straight out (8 bytes
-// of a token's row). Value codes are transposed through shared memory, because
-// a byte holds two neighbouring tokens of a column: a page that is filled whole
+// Append: one CTA per (page a request's new rows touch, KV head, request). An
+// item is two blocks of 16 columns: of a key, a block and the block of its rotation
+// partners, so that a column is loaded and a table entry read once; of the values, a
+// block of two neighbouring tokens, whose codes share bytes. Keys go straight out (8 bytes
+// of a token's row). Value codes are transposed through shared memory: a page that is filled whole
 // leaves as 16-byte stores, else each byte is one thread's, and a byte whose
-// other token is old is read and merged. Bound: HBM for prompts (values in, 9/16
-// byte out); launch latency and two dependent loads (position, page id) for a token.
+// other token is old is read and merged. Bound: instructions for prompts; launch latency and two
+// dependent loads (position, page id) for a token.
 //
 // Read: the CTA fetches its record with one bulk copy (9 KB at d_h 128) and decodes the
 // rows asked for out of shared memory.
@@ -32,6 +31,7 @@ struct AppendArgs {
   const int64_t* pos;
   const int32_t* n_rows;
   const float2* table;  // null: no rotation
+  int pairs;            // blocks of 16 columns whose partners fill a block too (16-byte access, halves): 0 or rot / 32
   int* status;
 };
 
@@ -112,7 +112,7 @@ __device__ __forceinline__ bool page_span(const int64_t* pos, const int32_t* n_r
 template <typename T, int DH, bool VEC>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   constexpr int NB = DH / 16;
-  __shared__ __align__(16) uint8_t vc[DH][kv::kPage];  // value codes, one byte each
+  __shared__ __align__(16) uint8_t vc[DH * 32];  // the page's value codes, as they go out
   pdl_trigger();
   pdl_wait();
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, nthr = blockDim.x;
@@ -125,66 +125,90 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
     return;
   }
   uint8_t* rec = a.pages + ((size_t)id * a.n_kv + h) * kv::rec_bytes(DH);
-  const int nt = sp.hi - sp.lo, items = nt * NB;
+  const int nt = sp.hi - sp.lo, b0 = sp.lo >> 1, nb = ((sp.hi + 1) >> 1) - b0;  // tokens; bytes (pairs of tokens) of a column
+  const int k_items = nt * (NB / 2), items = k_items + nb * NB;
   bool bad = false;
-  for (int u = tid; u < 2 * items; u += nthr) {
-    float v[16];
-    uint2 codes;
-    uint32_t scale;
-    if (u < items) {  // keys: the blocks of a token side by side
-      const int i = u / NB, j = u % NB;
+  for (int u = tid; u < items; u += nthr) {
+    float v[2][16];
+    uint2 codes[2];
+    uint32_t scale[2];
+    if (u < k_items) {  // a token's key, two blocks of 16 columns
+      const int i = u / (NB / 2), q = u % (NB / 2), tok = sp.lo + i;
+      const bool pair = q < a.pairs;  // the blocks are each other's partners
+      const int j0 = pair ? q : 2 * q, j1 = pair ? q + a.pairs : 2 * q + 1;
       const T* row = static_cast<const T*>(a.k) + ((long long)b * a.T + sp.t0 + i) * a.ks + (long long)h * DH;
       const float2* tab = nullptr;
       if (a.table) {
-        long long p = sp.page * 64 + sp.lo + i;
+        long long p = sp.page * 64 + tok;
         if (p >= a.n_pos) {
           p = a.n_pos - 1;
           flag_status(a.status, kDevBounds);
         }
         tab = a.table + p * a.half;
       }
-      rotated8<T, VEC>(row, 16 * j, a.half, a.inter, tab, v);
-      rotated8<T, VEC>(row, 16 * j + 8, a.half, a.inter, tab, v + 8);
-      bad |= kv::quantise16(v, a.k_inv, codes, scale);
-      const int tok = sp.lo + i;
-      *reinterpret_cast<uint2*>(rec + tok * (DH / 2) + 8 * j) = codes;
-      rec[kv::ks_off(DH) + tok * NB + j] = (uint8_t)scale;
-    } else {  // values: the tokens of a block side by side
-      const int j = (u - items) / nt, i = (u - items) - j * nt, tok = sp.lo + i;
-      const T* row = static_cast<const T*>(a.v) + ((long long)b * a.T + sp.t0 + i) * a.vs + (long long)h * DH + 16 * j;
-      load8<T, VEC>(row, v);
-      load8<T, VEC>(row + 8, v + 8);
-      bad |= kv::quantise16(v, a.v_inv, codes, scale);
-      rec[kv::vs_off(DH) + j * 64 + tok] = (uint8_t)scale;
+      if (VEC && pair) {
+        load8<T, VEC>(row + 16 * j0, v[0]);
+        load8<T, VEC>(row + 16 * j0 + 8, v[0] + 8);
+        load8<T, VEC>(row + 16 * j1, v[1]);
+        load8<T, VEC>(row + 16 * j1 + 8, v[1] + 8);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) vc[16 * j + e][tok] = (uint8_t)(((e < 8 ? codes.x : codes.y) >> ((e & 7) * 4)) & 15u);
+        for (int e = 0; e < 16; e += 2) {
+          const float4 cs = *reinterpret_cast<const float4*>(tab + 16 * j0 + e);
+          rope_pair(v[0][e], v[1][e], make_float2(cs.x, cs.y), v[0][e], v[1][e]);
+          rope_pair(v[0][e + 1], v[1][e + 1], make_float2(cs.z, cs.w), v[0][e + 1], v[1][e + 1]);
+        }
+      } else {
+        rotated8<T, VEC>(row, 16 * j0, a.half, a.inter, tab, v[0]);
+        rotated8<T, VEC>(row, 16 * j0 + 8, a.half, a.inter, tab, v[0] + 8);
+        rotated8<T, VEC>(row, 16 * j1, a.half, a.inter, tab, v[1]);
+        rotated8<T, VEC>(row, 16 * j1 + 8, a.half, a.inter, tab, v[1] + 8);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = x ? j1 : j0;
+        bad |= kv::quantise16(v[x], a.k_inv, codes[x], scale[x]);
+        *reinterpret_cast<uint2*>(rec + tok * (DH / 2) + 8 * j) = codes[x];
+        rec[kv::ks_off(DH) + tok * NB + j] = (uint8_t)scale[x];
+      }
+    } else {  // a block of 16 value columns, two tokens: the pairs of a block side by side
+      const int j = (u - k_items) / nb, by = b0 + (u - k_items) - j * nb;
+      const int i0 = 2 * by - sp.lo;  // -1: the even token is not new
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (i0 + x >= 0 && i0 + x < nt) {
+          const T* row = static_cast<const T*>(a.v) + ((long long)b * a.T + sp.t0 + i0 + x) * a.vs + (long long)h * DH + 16 * j;
+          load8<T, VEC>(row, v[x]);
+          load8<T, VEC>(row + 8, v[x] + 8);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[x][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        bad |= kv::quantise16(v[x], a.v_inv, codes[x], scale[x]);
+        if (i0 + x >= 0 && i0 + x < nt) rec[kv::vs_off(DH) + j * 64 + 2 * by + x] = (uint8_t)scale[x];
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {  // nibbles of 8 columns of both tokens -> a byte a column
+        const uint32_t c0 = w ? codes[0].y : codes[0].x, c1 = w ? codes[1].y : codes[1].x;
+        const uint32_t even = (c0 & 0x0f0f0f0fu) | ((c1 & 0x0f0f0f0fu) << 4), uneven = ((c0 >> 4) & 0x0f0f0f0fu) | (c1 & 0xf0f0f0f0u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vc[(16 * j + 8 * w + e) * 32 + by] = (uint8_t)((e & 1 ? uneven : even) >> (4 * (e & ~1)));
+      }
     }
   }
   if (bad) flag_status(a.status, kDevNonfinite);
   __syncthreads();
   uint8_t* vd = rec + kv::v_off(DH);
   if (nt == 64) {
-    for (int u = tid; u < DH * 2; u += nthr) {  // 32 tokens of a column
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(&vc[u >> 1][(u & 1) * 32]);
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // four code bytes c0 c1 c2 c3 -> c0 | c1 << 4, c2 | c3 << 4
-        const uint32_t x0 = src[2 * q] | (src[2 * q] >> 4), x1 = src[2 * q + 1] | (src[2 * q + 1] >> 4);
-        w[q] = __byte_perm(x0, x1, 0x6420);
-      }
-      *reinterpret_cast<uint4*>(vd + u * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    for (int u = tid; u < DH * 2; u += nthr) reinterpret_cast<uint4*>(vd)[u] = reinterpret_cast<const uint4*>(vc)[u];
   } else {
-    const int b0 = sp.lo >> 1, nb = ((sp.hi + 1) >> 1) - b0;
     for (int u = tid; u < DH * nb; u += nthr) {
-      const int d = u / nb, by = b0 + (u - d * nb), t = 2 * by;
-      uint8_t* dst = vd + d * 32 + by;
-      const bool n0 = t >= sp.lo, n1 = t + 1 < sp.hi;  // which of the byte's tokens are new
-      uint32_t w = n0 && n1 ? 0u : *dst;
-      if (n0) w = (w & 0xf0u) | vc[d][t];
-      if (n1) w = (w & 0x0fu) | ((uint32_t)vc[d][t + 1] << 4);
-      *dst = (uint8_t)w;
+      const int d = u / nb, by = b0 + (u - d * nb), at = d * 32 + by;
+      // the byte's old token, if it has one, stays
+      const uint32_t old = 2 * by < sp.lo ? 0x0fu : 2 * by + 1 >= sp.hi ? 0xf0u : 0u;
+      vd[at] = (uint8_t)(old ? (vd[at] & old) | (vc[at] & ~old) : vc[at]);
     }
   }
 }
@@ -329,6 +353,7 @@ extern "C" int dlite_kv_append(const dlite_kv_append_args* g, dlite_stream_t str
   const int V = 16 / es;
   const bool vec = !(((uintptr_t)g->k | (uintptr_t)g->v) & 15) && g->k_stride % V == 0 && g->v_stride % V == 0 &&
                    (!g->table || g->rot % (a.inter ? 8 : 16) == 0);
+  a.pairs = vec && g->table && !a.inter && g->rot % 32 == 0 && (uintptr_t)g->table % 16 == 0 ? g->rot / 32 : 0;
   void (*fn)(AppendArgs);
   if (g->dtype == DLITE_F32)
     fn = c.d_h == 128 ? (vec ? kv_append_kernel<float, 128, true> : kv_append_kernel<float, 128, false>)

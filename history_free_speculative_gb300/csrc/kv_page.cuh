@@ -52,11 +52,16 @@ __device__ __forceinline__ float fp8_to_f32(uint32_t byte) {
   const uint32_t h = fp8x2_to_f16x2((uint16_t)byte);
   return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
 }
-// Nearest e2m1 codes of (lo, hi), ties to even, saturating: one byte.
-__device__ __forceinline__ uint32_t f32x2_to_fp4(float lo, float hi) {
+// Nearest e2m1 codes of 8 numbers, ties to even, saturating: nibble e is v[e]'s.
+__device__ __forceinline__ uint32_t f32x8_to_fp4(const float (&v)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, t, t, t};\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
-  return r & 0xffu;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -66,26 +71,45 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 // Codes (nibble e of the pair lo, hi: column e) and scale byte of 16 columns.
 // v is overwritten. Returns whether a value was NaN or infinite.
+//
+// A code is the nearest to the fp32 quotient v / s. It is had without 16 divisions: with r the rounded 1 / s and q = v r, one
+// correction q + (v - q s) r, whose residual is exact (s has four significant bits), is v / s to 2^-46 before its rounding. The
+// borders t between codes (1/4, 3/4 .. 5) are fp32 numbers and so are the t s: at v = t s the sum rounds to t, the tie that the
+// quotient is, and the next fp32 number after t s is more than half a step of t away from t after the division (2^-23 / m
+// of t, m < 2 the significand of t s, against 2^-24 over that of t), so both fall on the same side. Overflow: v / s is below 7 unless s is
+// the largest scale, 448. The sign is v's: a zero keeps it.
 __device__ __forceinline__ bool quantise16(float (&v)[16], float inv_exp, uint2& codes, uint32_t& scale) {
-  float amax = 0.f;
-  bool bad = false;
+  float amax = 0.f, odd = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     v[i] *= inv_exp;
-    const float m = fabsf(v[i]);
-    if (m <= 3.402823466e38f)
-      amax = fmaxf(amax, m);
-    else
-      bad = true;
-    if (v[i] != v[i]) v[i] = 0.f;
+    amax = fmaxf(amax, fabsf(v[i]));
+    odd = fmaf(v[i], 0.f, odd);  // a NaN once a value is not finite
+  }
+  const bool bad = odd != 0.f;
+  if (bad) {
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (fabsf(v[i]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(v[i]));
+    const float far = fminf(2.f * amax, 3.402823466e38f);  // over 6 s, and its quotient is finite
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(fabsf(v[i]) <= 3.402823466e38f)) v[i] = v[i] != v[i] ? 0.f : copysignf(far, v[i]);
   }
   scale = f32_to_fp8(fminf(__fdiv_rn(amax, 6.f), 448.f));
   const float s = fp8_to_f32(scale);
-  uint32_t w[2] = {0u, 0u};
-  if (s > 0.f) {
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2)
-      w[i >> 3] |= f32x2_to_fp4(__fdiv_rn(v[i], s), __fdiv_rn(v[i + 1], s)) << ((i & 7) * 4);
+  for (int i = 0; i < 2; ++i) {
+    float q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = v[8 * i + e], q0 = x * r;
+      q[e] = copysignf(fmaf(fmaf(-q0, s, x), r, q0), x);
+    }
+    w[i] = s > 0.f ? f32x8_to_fp4(q) : 0u;
   }
   codes = make_uint2(w[0], w[1]);
   return bad;
