@@ -1,6 +1,6 @@
 // Append to and read from the paged 4-bit cache of the target side.
 //
-// Append: one CTA per (page a request's new rows touch, KV head, request). An
+// Append: one CTA per (page a request's new rows touch, KV head, keys or values, request). An
 // item is two blocks of 16 columns: of a key, a block and the block of its rotation
 // partners, so that a column is loaded and a table entry read once; of the values, a
 // block of two neighbouring tokens, whose codes share bytes. Keys go straight out (8 bytes
@@ -110,12 +110,13 @@ __device__ __forceinline__ bool page_span(const int64_t* pos, const int32_t* n_r
 }
 
 template <typename T, int DH, bool VEC>
-__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(AppendArgs a) {
   constexpr int NB = DH / 16;
-  __shared__ __align__(16) uint8_t vc[DH * 32];  // the page's value codes, as they go out
+  constexpr int BLK = 16 * 32 + 16;  // bytes of a block of columns; + 16: blocks start in banks of their own
+  __shared__ __align__(16) uint8_t vc[NB * BLK];  // the page's value codes, as they go out
   pdl_trigger();
   pdl_wait();
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, nthr = blockDim.x;
+  const int h = blockIdx.y >> 1, b = blockIdx.z, tid = threadIdx.x, nthr = blockDim.x;
   Span sp;
   if (!page_span(a.pos, a.n_rows, a.T, b, blockIdx.x, sp)) return;
   int id = -1;
@@ -126,13 +127,12 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   }
   uint8_t* rec = a.pages + ((size_t)id * a.n_kv + h) * kv::rec_bytes(DH);
   const int nt = sp.hi - sp.lo, b0 = sp.lo >> 1, nb = ((sp.hi + 1) >> 1) - b0;  // tokens; bytes (pairs of tokens) of a column
-  const int k_items = nt * (NB / 2), items = k_items + nb * NB;
   bool bad = false;
-  for (int u = tid; u < items; u += nthr) {
-    float v[2][16];
-    uint2 codes[2];
-    uint32_t scale[2];
-    if (u < k_items) {  // a token's key, two blocks of 16 columns
+  float v[2][16];
+  uint2 codes[2];
+  uint32_t scale[2];
+  if (blockIdx.y & 1) {  // a token's key, two blocks of 16 columns
+    for (int u = tid; u < nt * (NB / 2); u += nthr) {
       const int i = u / (NB / 2), q = u % (NB / 2), tok = sp.lo + i;
       const bool pair = q < a.pairs;  // the blocks are each other's partners
       const int j0 = pair ? q : 2 * q, j1 = pair ? q + a.pairs : 2 * q + 1;
@@ -170,45 +170,50 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
         *reinterpret_cast<uint2*>(rec + tok * (DH / 2) + 8 * j) = codes[x];
         rec[kv::ks_off(DH) + tok * NB + j] = (uint8_t)scale[x];
       }
-    } else {  // a block of 16 value columns, two tokens: the pairs of a block side by side
-      const int j = (u - k_items) / nb, by = b0 + (u - k_items) - j * nb;
-      const int i0 = 2 * by - sp.lo;  // -1: the even token is not new
+    }
+    if (bad) flag_status(a.status, kDevNonfinite);
+    return;
+  }
+  for (int u = tid; u < nb * NB; u += nthr) {  // a block of 16 value columns, two tokens
+    const int j = u % NB, by = b0 + u / NB;
+    const int i0 = 2 * by - sp.lo;  // -1: the even token is not new
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (i0 + x >= 0 && i0 + x < nt) {
-          const T* row = static_cast<const T*>(a.v) + ((long long)b * a.T + sp.t0 + i0 + x) * a.vs + (long long)h * DH + 16 * j;
-          load8<T, VEC>(row, v[x]);
-          load8<T, VEC>(row + 8, v[x] + 8);
-        } else {
+    for (int x = 0; x < 2; ++x) {
+      if (i0 + x >= 0 && i0 + x < nt) {
+        const T* row = static_cast<const T*>(a.v) + ((long long)b * a.T + sp.t0 + i0 + x) * a.vs + (long long)h * DH + 16 * j;
+        load8<T, VEC>(row, v[x]);
+        load8<T, VEC>(row + 8, v[x] + 8);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[x][e] = 0.f;
-        }
+        for (int e = 0; e < 16; ++e) v[x][e] = 0.f;
       }
+    }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        bad |= kv::quantise16(v[x], a.v_inv, codes[x], scale[x]);
-        if (i0 + x >= 0 && i0 + x < nt) rec[kv::vs_off(DH) + j * 64 + 2 * by + x] = (uint8_t)scale[x];
-      }
+    for (int x = 0; x < 2; ++x) {
+      bad |= kv::quantise16(v[x], a.v_inv, codes[x], scale[x]);
+      if (i0 + x >= 0 && i0 + x < nt) rec[kv::vs_off(DH) + j * 64 + 2 * by + x] = (uint8_t)scale[x];
+    }
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {  // nibbles of 8 columns of both tokens -> a byte a column
-        const uint32_t c0 = w ? codes[0].y : codes[0].x, c1 = w ? codes[1].y : codes[1].x;
-        const uint32_t even = (c0 & 0x0f0f0f0fu) | ((c1 & 0x0f0f0f0fu) << 4), uneven = ((c0 >> 4) & 0x0f0f0f0fu) | (c1 & 0xf0f0f0f0u);
+    for (int w = 0; w < 2; ++w) {  // nibbles of 8 columns of both tokens -> a byte a column
+      const uint32_t c0 = w ? codes[0].y : codes[0].x, c1 = w ? codes[1].y : codes[1].x;
+      const uint32_t even = (c0 & 0x0f0f0f0fu) | ((c1 & 0x0f0f0f0fu) << 4), uneven = ((c0 >> 4) & 0x0f0f0f0fu) | (c1 & 0xf0f0f0f0u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vc[(16 * j + 8 * w + e) * 32 + by] = (uint8_t)((e & 1 ? uneven : even) >> (4 * (e & ~1)));
-      }
+      for (int e = 0; e < 8; ++e) vc[j * BLK + (8 * w + e) * 32 + by] = (uint8_t)((e & 1 ? uneven : even) >> (4 * (e & ~1)));
     }
   }
   if (bad) flag_status(a.status, kDevNonfinite);
   __syncthreads();
   uint8_t* vd = rec + kv::v_off(DH);
   if (nt == 64) {
-    for (int u = tid; u < DH * 2; u += nthr) reinterpret_cast<uint4*>(vd)[u] = reinterpret_cast<const uint4*>(vc)[u];
+    for (int u = tid; u < DH * 2; u += nthr)
+      reinterpret_cast<uint4*>(vd)[u] = *reinterpret_cast<const uint4*>(vc + (u >> 5) * BLK + (u & 31) * 16);
   } else {
     for (int u = tid; u < DH * nb; u += nthr) {
       const int d = u / nb, by = b0 + (u - d * nb), at = d * 32 + by;
+      const uint8_t code = vc[(d >> 4) * BLK + (d & 15) * 32 + by];
       // the byte's old token, if it has one, stays
       const uint32_t old = 2 * by < sp.lo ? 0x0fu : 2 * by + 1 >= sp.hi ? 0xf0u : 0u;
-      vd[at] = (uint8_t)(old ? (vd[at] & old) | (vc[at] & ~old) : vc[at]);
+      vd[at] = (uint8_t)(old ? (vd[at] & old) | (code & ~old) : code);
     }
   }
 }
@@ -361,7 +366,7 @@ extern "C" int dlite_kv_append(const dlite_kv_append_args* g, dlite_stream_t str
   else
     fn = c.d_h == 128 ? (vec ? kv_append_kernel<bf16, 128, true> : kv_append_kernel<bf16, 128, false>)
                       : (vec ? kv_append_kernel<bf16, 64, true> : kv_append_kernel<bf16, 64, false>);
-  return launch_status(launch_pdl(fn, dim3(touched_pages(g->T), c.n_kv, g->B), dim3(cta_threads(g->T, c.d_h)), 0,
+  return launch_status(launch_pdl(fn, dim3(touched_pages(g->T), 2 * c.n_kv, g->B), dim3(cta_threads(g->T, c.d_h)), 0,
                                   (cudaStream_t)stream, a));
 }
 

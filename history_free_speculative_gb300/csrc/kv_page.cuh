@@ -121,7 +121,7 @@ inline int check_cache(const dlite_kv_cache& c, int B, int T, const int64_t* pos
   if (((uintptr_t)c.pages & 15) || ((uintptr_t)c.block_table & 3) || ((uintptr_t)pos & 7)) return DLITE_ERR_INVALID_ARG;
   if (B < 1 || T < 1 || c.n_pages < 1 || c.n_kv < 1 || c.max_pages < 1) return DLITE_ERR_INVALID_ARG;
   if (c.k_exp < -64 || c.k_exp > 64 || c.v_exp < -64 || c.v_exp > 64) return DLITE_ERR_INVALID_ARG;
-  if ((c.d_h != 64 && c.d_h != 128) || c.n_kv > 65535 || B > 65535 || c.max_pages >= (1 << 25) || T >= (1 << 30))
+  if ((c.d_h != 64 && c.d_h != 128) || c.n_kv > 32767 || B > 65535 || c.max_pages >= (1 << 25) || T >= (1 << 30))
     return DLITE_ERR_UNSUPPORTED_SHAPE;
   return DLITE_OK;
 }
