@@ -3,7 +3,8 @@
 //
 // A segment is one tile of query rows of one (request, KV head); its pages are counted in units (UP pages). Stream form:
 // the units of all segments, in order, are cut into equal runs of `quota` units, one per CTA, whatever the lengths of
-// the requests; a CTA walks the pieces of segments in its run. A piece that is its whole
+// the requests; a CTA walks the pieces of segments in its run. Every
+// segment begins with `change` units without pages, which stand for the time that a change of pieces takes. A piece that is its whole
 // segment writes the output; other pieces leave (max, sum, unnormalised output) in the workspace, at most two a CTA, and the
 // join kernel adds them up in order. Every CTA works the cut out for itself from pos and n_rows, so that lengths stay on the device.
 // Whole form (segments that are short by the table's width, or too many for the list of prefix sums): CTAs take whole
@@ -26,6 +27,7 @@ struct AttnArgs {
   int row_tiles;        // of a KV head's group x T rows
   int unit;             // pages of a unit
   int min_quota;        // units a CTA takes at least (stream form)
+  int change;           // what a change of pieces costs a CTA, in units
   int stream;           // 1: stream form
   float scale_log2;     // scale log2(e) 2^k_exp
   float v_scale;        // 2^v_exp
@@ -76,12 +78,14 @@ struct Piece {
   int u0, u1, nu;  // units [u0, u1) of the segment's nu
 };
 
-// prefix [row tiles + 1]: units of the row tiles before (of one KV head). All threads of the CTA; ends with a barrier.
+// prefix [row tiles + 1]: units of the row tiles before (of one KV head), with those of the changes. All threads of the CTA; ends with a barrier.
 template <int R>
 __device__ __forceinline__ void build_prefix(const AttnArgs& a, int* prefix) {
   const int J = a.B * a.row_tiles;
-  for (int j = threadIdx.x; j < J; j += blockDim.x)
-    prefix[j + 1] = units_of(tile_of<R>(a, j / a.row_tiles, j % a.row_tiles), a.unit);
+  for (int j = threadIdx.x; j < J; j += blockDim.x) {
+    const int units = units_of(tile_of<R>(a, j / a.row_tiles, j % a.row_tiles), a.unit);
+    prefix[j + 1] = units ? units + a.change : 0;
+  }
   if (threadIdx.x == 0) prefix[0] = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -108,19 +112,20 @@ struct Pieces {
   const AttnArgs& a;
   const int* prefix;
   int J;
-  long long u, end, quota;
+  uint32_t u, end, quota;  // the host takes the stream form where all units are below 2^31
   int j;
   __device__ __forceinline__ Pieces(const AttnArgs& args, const int* pre) : a(args), prefix(pre) {
     J = a.B * a.row_tiles;
+    j = 0;
     if (a.stream) {
-      const long long U = (long long)prefix[J] * a.n_kv;
-      quota = max((U + gridDim.x - 1) / (long long)gridDim.x, (long long)a.min_quota);
+      const uint32_t U = (uint32_t)prefix[J] * a.n_kv;
+      quota = max((U + gridDim.x - 1) / gridDim.x, (uint32_t)a.min_quota);
       u = min(quota * blockIdx.x, U);
       end = min(u + quota, U);
       int lo = 0, hi = J;  // last j with prefix[j] n_kv <= u
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((long long)prefix[mid] * a.n_kv <= u)
+        if ((uint32_t)prefix[mid] * a.n_kv <= u)
           lo = mid;
         else
           hi = mid;
@@ -128,21 +133,24 @@ struct Pieces {
       j = lo;
     } else {
       u = blockIdx.x;
-      end = (long long)J * a.n_kv;
+      end = (uint32_t)J * a.n_kv;
     }
   }
   __device__ __forceinline__ bool next(Piece& p) {
     if (a.stream) {
-      if (u >= end) return false;
-      while ((long long)prefix[j + 1] * a.n_kv <= u) ++j;
-      const long long rem = u - (long long)prefix[j] * a.n_kv;
-      p.j = j;
-      p.nu = prefix[j + 1] - prefix[j];
-      p.h = (int)(rem / p.nu);
-      p.u0 = (int)(rem - (long long)p.h * p.nu);
-      p.u1 = (int)min((long long)p.nu, p.u0 + (end - u));
-      u += p.u1 - p.u0;
-      return true;
+      while (u < end) {
+        while ((uint32_t)prefix[j + 1] * a.n_kv <= u) ++j;
+        const uint32_t rem = u - (uint32_t)prefix[j] * a.n_kv, all = prefix[j + 1] - prefix[j];
+        p.j = j;
+        p.nu = (int)all - a.change;
+        p.h = (int)(rem / all);
+        const int v0 = (int)(rem - p.h * all), v1 = (int)min(all, v0 + (end - u));
+        u += v1 - v0;
+        p.u0 = max(v0 - a.change, 0);
+        p.u1 = v1 - a.change;
+        if (p.u1 > p.u0) return true;  // else the run ends before the segment's first page
+      }
+      return false;
     }
     for (; u < end; u += gridDim.x) {
       p.j = (int)(u / a.n_kv);
@@ -160,7 +168,7 @@ struct Pieces {
   // What the join kernel has to know of this CTA: p is its last piece (if any).
   __device__ __forceinline__ int2 join_of(bool any, const Piece& p) const {
     if (!any || p.u0 || p.u1 == p.nu) return make_int2(0, 0);
-    const long long last = (long long)prefix[p.j] * a.n_kv + (long long)(p.h + 1) * p.nu - 1;
+    const uint32_t last = (uint32_t)prefix[p.j] * a.n_kv + (uint32_t)(p.h + 1) * (p.nu + a.change) - 1;
     return make_int2(p.j * a.n_kv + p.h, (int)(last / quota) - (int)blockIdx.x + 1);
   }
 };
@@ -184,7 +192,7 @@ __device__ __forceinline__ float lse_of(float M, float L, float weight_exp) {
 struct AttnPlan {
   int rows = 16;    // of a tile
   bool tc = false;  // the tcgen05 kernel
-  int row_tiles = 1, unit = 1, min_quota = 8, grid = 1;
+  int row_tiles = 1, unit = 1, min_quota = 8, change = 0, grid = 1;
   bool stream = false;
   size_t bytes(int d_h) const { return stream ? (size_t)grid * (2 * rows * ((size_t)d_h * 4 + 8) + 8) : 0; }
 };

@@ -35,8 +35,11 @@ constexpr int kThreads = 20 * 32;
 // A tile's flags and the barrier of its value scales, which the softmax looks at last: the copies and scales of tile i + 16 take
 // the stage of i + 8, whose values take the buffer of i + 6, whose second product comes after the softmax of i + 6 and so of i.
 constexpr int kRing = 2 * kStages;
-// a stage: key codes of both pages (rows of 64 B, 64-byte swizzle), value codes (rows of 32 B, 32-byte swizzle), scales
-constexpr int kV = 8192, kS = 16384;
+// A stage holds both pages' records as they are, one copy each, as rows of 128 bytes under a 128-byte swizzle.
+constexpr int kRow = 128, kRecRows = REC / kRow;
+static_assert(REC % 1024 == 0 && kRecRows <= 256, "rows of a copy");
+// 16-byte chunk c of a record
+__device__ __forceinline__ int chunk(int c) { return c / 8 * kRow + (((c ^ (c >> 3)) & 7) << 4); }
 // tensor memory columns: K and V^T tiles twice; then S^T, O^T and L twice each; a tile of ones
 constexpr int kTmK = 0, kTmV = 128, kTmS = 256, kTmOnes = 448, kTmCols = 512;
 constexpr float kTcWeightExp = 6.f;
@@ -179,7 +182,7 @@ __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volati
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv_attention_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
+    kv_attention_tc_kernel(const __grid_constant__ CUtensorMap map, const AttnArgs a) {
   using S = Smem<N>;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (tc::su32(raw) & 1023)) & 1023);
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto c_ready = [&](int i) { return bars + 8 * (2 * kStages + 17 + i % kRing); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  pdl_wait();  // no early trigger: the grid fills the SMs
+  pdl_wait();
   if (a.stream) build_prefix<N>(a, prefix);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -295,14 +298,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_left(bar(kFree, buf), it >> 1);
         tc::fence_after();
         const uint8_t* stage = sm + st * TILE;
-        const uint8_t* base = stage + page * 4096 + row * 64;
-        const uint2 sc = *reinterpret_cast<const uint2*>(stage + kS + page * 1024 + row * 8);
+        const uint8_t* rec = stage + page * REC;
+        const uint2 sc = *reinterpret_cast<const uint2*>(rec + chunk(ks_off(DH) / 16 + (row >> 1)) + 8 * (row & 1));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t r[32];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const uint4 w = *reinterpret_cast<const uint4*>(base + (((2 * half + q) ^ ((row >> 1) & 3)) << 4));
+            const uint4 w = *reinterpret_cast<const uint4*>(rec + chunk(4 * row + 2 * half + q));
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
             const uint32_t s2 = fp8x2_to_f16x2((uint16_t)((half ? sc.y : sc.x) >> (16 * q)));
             const uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
@@ -338,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after();
 #pragma unroll
         for (int page = 0; page < 2; ++page) {
-          const uint8_t* base = sm + st * TILE + kV + page * 4096 + d * 32;
+          const uint8_t* rec = sm + st * TILE + page * REC;
           const uint8_t* sp = sm + S::VS + st * 2048 + (d >> 4) * 256 + page * 128;
           uint32_t r[32];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {  // 32 tokens
-            const uint4 w = *reinterpret_cast<const uint4*>(base + ((q ^ ((d >> 2) & 1)) << 4));
+            const uint4 w = *reinterpret_cast<const uint4*>(rec + chunk(v_off(DH) / 16 + 2 * d + q));
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -367,22 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 16) {  // ---------------------------------------------------------------- softmax and output
     const int g = (warp - 8) >> 2, w = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * w) << 16;
-#pragma unroll 1
-    for (int k = 0; k < batch; ++k) {
-      const Piece pc = list[k].p;
-      const Tile t = list[k].t;
-      const int b = list[k].b, rt = list[k].rt, h = pc.h, rows = t.r1 - t.r0;
-      if (warp == 8 && lane == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
-        flag_status(a.status, kDevBounds);
-      // Q (all of the last piece's first products are done): rows warp - 8, + 8, ...
-      uint2 raw_q[N / 8];
-      float v[N / 8][4], amax = 0.f;
-      bool bad[N / 8];
+    uint2 raw_q[N / 8];
+    auto load_q = [&](int k) {  // rows warp - 8, + 8, ... of a piece: every load before the first use
+      const Tile& t = list[k].t;
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i) {  // every row's load before the first use
-        const int r = min(warp - 8 + 8 * i, rows - 1);
-        const int tk = (t.r0 + r) / a.group, hq = h * a.group + (t.r0 + r) % a.group;
-        const bf16* q = static_cast<const bf16*>(a.q) + ((long long)b * a.T + tk) * a.qs + (long long)hq * DH + 4 * lane;
+      for (int i = 0; i < N / 8; ++i) {
+        const int r = t.r0 + min(warp - 8 + 8 * i, t.r1 - t.r0 - 1), tk = r / a.group, hq = list[k].p.h * a.group + r - tk * a.group;
+        const bf16* q = static_cast<const bf16*>(a.q) + ((long long)list[k].b * a.T + tk) * a.qs + (long long)hq * DH + 4 * lane;
         if (a.vec) {
           raw_q[i] = *reinterpret_cast<const uint2*>(q);
         } else {
@@ -390,6 +384,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           raw_q[i] = make_uint2(q16[0] | (uint32_t)q16[1] << 16, q16[2] | (uint32_t)q16[3] << 16);
         }
       }
+    };
+    load_q(0);
+#pragma unroll 1
+    for (int k = 0; k < batch; ++k) {
+      const Piece pc = list[k].p;
+      const Tile t = list[k].t;
+      const int b = list[k].b, rt = list[k].rt, h = pc.h, rows = t.r1 - t.r0;
+      if (warp == 8 && lane == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
+        flag_status(a.status, kDevBounds);
+      // Q: all of the last piece's first products are done
+      float v[N / 8][4], amax = 0.f;
+      bool bad[N / 8];
       if (warp == 8 && lane < N) {
         const int r = t.r0 + lane, tk = r / a.group, hq = h * a.group + r % a.group;
         const long long row = (long long)b * a.T + tk, seen = t.p0 + tk;
@@ -475,15 +481,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           return top;
         };
         scores();
-        if (exponents() > kTcWeightExp + 8.f) move_ref[g] = 1;
+        const bool first_tile = last < 0;  // its references are new in any case
+        if (!first_tile && exponents() > kTcWeightExp + 8.f) move_ref[g] = 1;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(voted(g));
+        if (!first_tile) {
 #pragma unroll
-        for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
-        wait_turn(voted(g), turn);
-        if (move_ref[g]) {
-          // new references: the exact maxima of the tile
-          scores();
+          for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
+          wait_turn(voted(g), turn);
+        }
+        if (first_tile || move_ref[g]) {
+          if (!first_tile) scores();
+          // the exact maxima of the tile
 #pragma unroll
           for (int r = 0; r < N; ++r) {
             const float mx = warp_max_f32(r & 1 ? hi2f(x[r / 2]) : lo2f(x[r / 2]));
@@ -513,7 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
           }
-          scores();
           exponents();
 #pragma unroll
           for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
@@ -539,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         last = i;
       }
       it += pc.u1 - pc.u0;
+      if (k + 1 < batch) load_q(k + 1);
       // the groups' rows joined; thread = column 32 w + lane, group g takes rows g N / 2 ..
       if (last >= 0) {
         wait_turn(bar(vFree, g), last >> 1);
@@ -609,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int valid = came == 3 && left >= 128 ? 32 : (came >> (tok >> 6) & 1) ? left - tok : 0;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sm + st * TILE + kS + (tok >> 6) * 1024 + 512 + blk * 64 + (tok & 63) + 16 * q);
+          const uint4 w = *reinterpret_cast<const uint4*>(sm + st * TILE + (tok >> 6) * REC + chunk(vs_off(DH) / 16 + 4 * blk + ((tok & 63) >> 4) + q));
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
           uint32_t s[8];
 #pragma unroll
@@ -633,12 +642,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece pc = list[k].p;
       const Tile t = list[k].t;
       const int32_t* bt = a.bt + (size_t)list[k].b * a.max_pages + t.pg0;
-      auto page_of = [&](int i) { return i < t.np ? bt[i] : -1; };
-      int id0 = page_of(2 * pc.u0), id1 = page_of(2 * pc.u0 + 1);
+      // 32 page ids at a time, the next 32 on their way: with one tile's ids loaded ahead, a load's latency was every tile's
+      const int pages = min(t.np, 2 * pc.u1);
+      auto page_of = [&](int i) { return i < pages ? bt[i] : -1; };
+      int ids = page_of(2 * pc.u0 + lane), next_ids = page_of(2 * pc.u0 + 32 + lane);
 #pragma unroll 1
       for (int u = pc.u0; u < pc.u1; ++u, ++it) {
         const int st = it % kStages;
-        const int next0 = u + 1 < pc.u1 ? page_of(2 * u + 2) : -1, next1 = u + 1 < pc.u1 ? page_of(2 * u + 3) : -1;
+        const int at = (2 * (u - pc.u0)) & 31;
+        if (at == 0 && u > pc.u0) {
+          ids = next_ids;
+          next_ids = page_of(2 * u + 32 + lane);
+        }
+        const int id0 = __shfl_sync(0xffffffffu, ids, at), id1 = __shfl_sync(0xffffffffu, ids, at + 1);
         wait_left(empty(st), it / kStages);
         const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
         if (one) {
@@ -651,18 +667,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int p = 0; p < 2; ++p) {
               if (!(came >> p & 1)) continue;
               const long long rec = (long long)(p ? id1 : id0) * a.n_kv + pc.h;
-              const uint32_t dst = sb + st * TILE;
-              tma_load_3d(dst + p * 4096, &mk, full(st), (int)rec);
-              tma_load_3d(dst + kV + p * 4096, &mv, full(st), (int)rec);
-              tc::bulk_load(dst + kS + p * 1024, a.pages + rec * REC + ks_off(DH), 1024, full(st));
+              tma_load_3d(sb + st * TILE + p * REC, &map, full(st), (int)rec);
             }
           } else {
             tc::mbar_arrive(full(st));
           }
         }
         __syncwarp();
-        id0 = next0;
-        id1 = next1;
       }
     }
   } else if (warp == 17) {  // ---------------------------------------------------------------- first product
@@ -719,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();  // the list is the next batch's
   }
   if (tid == 0 && a.stream) a.joins[blockIdx.x] = join;
+  pdl_trigger();  // late: the grid fills the SMs
   // every role is through; after a wait that ran out (status flagged) the copies and products in flight have had its time
   tc::fence_before();
   __syncthreads();
@@ -727,19 +739,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int N>
-cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& map, const AttnArgs& a, int grid, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kv_attention_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N>::BYTES);
-  return e != cudaSuccess ? e : launch_pdl(kv_attention_tc_kernel<N>, dim3(grid), dim3(kThreads), Smem<N>::BYTES, s, mk, mv, a);
+  return e != cudaSuccess ? e : launch_pdl(kv_attention_tc_kernel<N>, dim3(grid), dim3(kThreads), Smem<N>::BYTES, s, map, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_tc(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-  CUtensorMap mk, mv;
+  CUtensorMap map;
   const long long records = (long long)a.n_pages * a.n_kv;
-  if (!tc::make_record_map(&mk, a.pages, 64, 64, records, REC) || !tc::make_record_map(&mv, a.pages + v_off(DH), 32, 128, records, REC))
-    return cudaErrorInvalidValue;
-  return p.rows == 16 ? launch<16>(mk, mv, a, p.grid, s) : launch<32>(mk, mv, a, p.grid, s);
+  if (!tc::make_record_map(&map, a.pages, kRow, kRecRows, records, REC)) return cudaErrorInvalidValue;
+  return p.rows == 16 ? launch<16>(map, a, p.grid, s) : launch<32>(map, a, p.grid, s);
 }
 
 }  // namespace kv
