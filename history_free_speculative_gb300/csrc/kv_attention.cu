@@ -25,10 +25,6 @@
 #include <algorithm>
 #include <type_traits>
 
-#ifndef KV_TC
-#define KV_TC 1
-#endif
-
 #include "kv_attention.cuh"
 
 namespace dlite {
@@ -465,8 +461,9 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const AttnArgs a
   if (rt * R + r >= n * a.group) return;
   // piece k: slot 1 of this CTA, then slot 0 of those after it
   auto row_of = [&](int k) { return ((size_t)(blockIdx.x + k) * 2 + (k == 0)) * R + r; };
-  float M = -INFINITY;
-  for (int k = lane; k < jn.y; k += 32) M = fmaxf(M, a.part_ml[row_of(k)].x);
+  const float2 first = lane < jn.y ? a.part_ml[row_of(lane)] : make_float2(-INFINITY, 0.f);
+  float M = first.x;
+  for (int k = lane + 32; k < jn.y; k += 32) M = fmaxf(M, a.part_ml[row_of(k)].x);
   M = warp_max(M);
   constexpr int C = DH / 32;  // columns C lane ..
   using Part = typename std::conditional<C == 4, float4, float2>::type;
@@ -476,7 +473,7 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const AttnArgs a
   for (int k0 = 0; k0 < jn.y; k0 += 32) {
     float w = 0.f, lw = 0.f;
     if (k0 + lane < jn.y) {
-      const float2 ml = a.part_ml[row_of(k0 + lane)];
+      const float2 ml = k0 ? a.part_ml[row_of(k0 + lane)] : first;
       w = ml.x == -INFINITY ? 0.f : tc::ex2_approx(ml.x - M);
       lw = w * ml.y;
     }
@@ -510,7 +507,7 @@ constexpr int kTcChange = 8;
 kv::AttnPlan make_plan(const dlite_kv_attention_args& g) {
   kv::AttnPlan p;
   const int rows = g.n_q / g.cache.n_kv * g.T;
-  p.tc = KV_TC && g.dtype == DLITE_BF16 && g.cache.d_h == 128;
+  p.tc = g.dtype == DLITE_BF16 && g.cache.d_h == 128;
   // 32-row tiles halve the conversions per row; float32 queries have twice the fragments and would spill
   p.rows = rows <= 16 || g.dtype == DLITE_F32 ? 16 : 32;
   p.row_tiles = (rows + p.rows - 1) / p.rows;
@@ -556,14 +553,10 @@ cudaError_t launch(const AttnArgs& a, const kv::AttnPlan& p, cudaStream_t s) {
   return e != cudaSuccess ? e : join<T, DH, S::R>(a, p, s);
 }
 cudaError_t launch(const AttnArgs& a, const kv::AttnPlan& p, int d_h, int dtype, cudaStream_t s) {
-#if KV_TC
   if (p.tc) {
     const cudaError_t e = kv::launch_attention_tc(a, p, s);
     return e != cudaSuccess ? e : p.rows == 16 ? join<bf16, 128, 16>(a, p, s) : join<bf16, 128, 32>(a, p, s);
   }
-#else
-  if (dtype == DLITE_BF16 && d_h == 128) return p.rows == 16 ? launch<bf16, 128, 1>(a, p, s) : launch<bf16, 128, 2>(a, p, s);
-#endif
   if (dtype == DLITE_F32) return d_h == 128 ? launch<float, 128, 1>(a, p, s) : launch<float, 64, 1>(a, p, s);
   return p.rows == 16 ? launch<bf16, 64, 1>(a, p, s) : launch<bf16, 64, 2>(a, p, s);
 }

@@ -212,8 +212,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto c_ready = [&](int i) { return bars + 8 * (2 * kStages + 17 + i % kRing); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  pdl_wait();
-  if (a.stream) build_prefix<N>(a, prefix);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(full(s), 1);
@@ -236,11 +234,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     *gave_up = 0;
     tc::mbar_init(q_ready, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tm_slot)), "r"(kTmCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  pdl_wait();  // what is above reads nothing that the stream writes
+  if (a.stream) build_prefix<N>(a, prefix);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
