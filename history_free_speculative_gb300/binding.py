@@ -473,6 +473,8 @@ def kv_attention(q, pages, block_table, pos, scale=None, window=0, n_rows=None, 
     if need:
         if workspace is None:
             workspace = _new(s, (need,), torch.uint8)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace: contiguous uint8 expected")
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib.dlite_kv_attention(ctypes.byref(a), ptr), "dlite_kv_attention")
     return out, lse

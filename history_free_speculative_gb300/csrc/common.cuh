@@ -102,6 +102,12 @@ __device__ __forceinline__ void pdl_trigger() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A request's first position, from the caller. Positions of 2^40 and beyond lie outside every table and cache; clamped
+// there, sums with them stay far from the ends of 64 bits.
+__device__ __forceinline__ long long first_position(const int64_t* pos, int b) {
+  return min(max((long long)pos[b], -(1LL << 40)), 1LL << 40);
+}
+
 // ---------------------------------------------------------------- packed fp32 pairs
 __device__ __forceinline__ uint64_t pack2f(float lo, float hi) {
   return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);

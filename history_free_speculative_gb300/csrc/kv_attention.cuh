@@ -56,7 +56,7 @@ template <int R>
 __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int b, int rt) {
   Tile t;
   const int n = a.n_rows ? min(max(a.n_rows[b], 0), a.T) : a.T;
-  t.p0 = a.pos[b];
+  t.p0 = first_position(a.pos, b);
   t.cap = (long long)a.max_pages * kPage;
   t.r0 = rt * R;
   t.r1 = min(t.r0 + R, n * a.group);

@@ -236,11 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
   }
+  pdl_wait();  // what is above reads nothing that the stream writes and takes nothing that the kernel before may still need
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tm_slot)), "r"(kTmCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  pdl_wait();  // what is above reads nothing that the stream writes
   if (a.stream) build_prefix<N>(a, prefix);
   tc::fence_before();
   __syncthreads();

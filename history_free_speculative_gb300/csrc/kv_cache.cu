@@ -98,7 +98,7 @@ struct Span {
   int lo, hi, t0;
 };
 __device__ __forceinline__ bool page_span(const int64_t* pos, const int32_t* n_rows, int T, int b, int page_i, Span& s) {
-  const long long p0 = pos[b];
+  const long long p0 = first_position(pos, b);
   const int n = n_rows ? min(max(n_rows[b], 0), T) : T;
   s.page = (p0 >> 6) + page_i;
   const long long first = max(p0, s.page * 64), last = min(p0 + n, s.page * 64 + 64);

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   const long long tok = blockIdx.x;
   const int b = (int)(blockIdx.x / (unsigned)a.T), t = (int)(blockIdx.x - (unsigned)b * (unsigned)a.T);
   if (a.n_rows && t >= a.n_rows[b]) return;
-  long long p = a.pos[b] + t;
+  long long p = first_position(a.pos, b) + t;
   if (p < 0 || p >= a.n_pos) {
     if (threadIdx.x == 0) flag_status(a.status, kDevBounds);
     p = p < 0 ? 0 : a.n_pos - 1;

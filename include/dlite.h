@@ -488,7 +488,8 @@ typedef struct {
  * arithmetic of dlite_rope without its last rounding to dtype; NULL: keys are
  * stored as they come (already rotated). Any T: a decoded token, a
  * verification block, a prompt. No other row of the cache changes. Two requests
- * of a call must not append into the same page (a shared page is copied first). A row at a
+ * of a call must not append into the same page (a shared page is copied first), nor one
+ * request into a page that its table names twice. A row at a
  * position outside [0, 64 max_pages) or in a page whose id is outside [0, n_pages)
  * is not stored and flags DLITE_DEV_BOUNDS; so does a position the table does not
  * hold (taken to its nearest end, as dlite_rope does). */
