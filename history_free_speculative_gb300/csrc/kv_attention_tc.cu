@@ -6,21 +6,31 @@
 // A thread of the dequantising warps owns one lane of tensor memory: one key (its 64 bytes of codes, 8 scales) or one
 // column (its 64 bytes of codes along the tokens, the scales of 128 tokens). It turns its codes into f16 (e2m1 x e4m3 is exact)
 // and writes them with tcgen05.st, so the cache never passes through shared memory a second time. N = 16 or 32
-// query rows; Q^T and P^T are the B operands in shared memory. The sums of the weights are a third product with a tile of
-// ones, L [128 x N] += 1 P^T: the tensor pipe is idle four fifths of the time, and the 32 sums a thread would hold itself spilled.
+// query rows; Q^T and P^T are the B operands in shared memory.
 // Warps: 0-3 keys, 4-7 values, 8-15 softmax and output (thread = key, then column), 16 value scales to f16, 17 and 18 the issue
 // of the first and the second product, 19 copies: five warps a scheduler.
 // The softmax warps are two groups that take the tiles in turn, each with its own scores, weights, maxima, sums and O, joined at
 // a piece's end: one group's latencies pass under the other's tile (one group alone took 3,300 clocks a tile). A group keeps one
 // reference m per row, moved only when a weight passes it by more than 2^8 (a vote of its four warps per tile); only then
 // are exact maxima formed and O, the sums rescaled. Weights are 2^(s - m + 6) <= 2^14, rounded to f16: weights down
-// to 2^-31 of the reference count, and the largest score is never below it. Queries are scaled by one power of two per
+// to 2^-31 of the reference count, and the largest score is never below it. The sums are of the weights before that rounding, in
+// fp32, a thread's own in tensor memory: 32 more registers spilled (67 us for the 52 below), and a product of the rounded weights
+// with ones was 3 us faster but its lse off by more than 10^-6. Queries are scaled by one power of two per
 // tile into f16's range: exact for bf16 elements down to 2^-32 of the tile's largest, and off by 2^-39 of that below.
 // The issuing warps stay converged and elect a lane: 17 clocks an MMA, 46 from a branch on the lane (the operands then
 // go from vector to uniform registers one by one).
+// Bound: issue slots. A tile of 128 keys takes 1,050 clocks at N = 16 and 1,200 at N = 32 (820 warp instructions a
+// scheduler, more than half of them conversions of codes); its 18 KB take 795 at the copy rate of HBM. Twice the
+// dequantising warps (28 in all, registers shared out again with setmaxnreg) changed nothing, nor did 9 or 10 stages for 8. Around the
+// tiles: 6 us up to the first weights (lengths, list of pieces, first records, first maxima), 1.5 us at the end, 6 us the
+// join with its launch; a change of pieces costs a CTA 8 tiles.
+// Measured (32 query heads, 8 KV heads, with the join): one request of 118,000 keys 41 us for one token, 52 us for eight; eight requests
+// of 8,192 keys, one token each, 22 us; 32 requests of up to 40,960 keys, up to eight tokens each, 209 us (53% of the copy rate).
 // mma.sync does both products of a 32-row tile in 8 clocks a key an SM (measured 2.0 per m16n8k16), above the 6.8 that the bytes take
 // at the copy rate of HBM, and needs its operands and outputs in registers: the mma.sync kernel ran at 19.
 #include <math.h>
+
+#include <type_traits>
 
 #include "kv_attention.cuh"
 #include "tc_gemm.h"
@@ -40,8 +50,8 @@ constexpr int kRow = 128, kRecRows = REC / kRow;
 static_assert(REC % 1024 == 0 && kRecRows <= 256, "rows of a copy");
 // 16-byte chunk c of a record
 __device__ __forceinline__ int chunk(int c) { return c / 8 * kRow + (((c ^ (c >> 3)) & 7) << 4); }
-// tensor memory columns: K and V^T tiles twice; then S^T, O^T and L twice each; a tile of ones
-constexpr int kTmK = 0, kTmV = 128, kTmS = 256, kTmOnes = 448, kTmCols = 512;
+// tensor memory columns: K and V^T tiles twice; then S^T, O^T and the threads' sums twice each
+constexpr int kTmK = 0, kTmV = 128, kTmS = 256, kTmCols = 512;
 constexpr float kTcWeightExp = 6.f;
 constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key
 
@@ -50,7 +60,7 @@ struct Smem {
   static constexpr int Q = kStages * TILE;           // [2 halves][N rows][128 B], 128-byte swizzle
   static constexpr int P = Q + N * 256;              // [2][128 keys][N rows] f16, rows of N contiguous
   static constexpr int VS = P + 2 * 128 * N * 2;     // [stage][8 blocks][128 tokens] f16: value scales
-  static constexpr int ROWS = VS + kStages * 2048;         // floats: offset [2][N], alpha [2][N], l [2][4][N], red [2][4][N], tile max
+  static constexpr int ROWS = VS + kStages * 2048;         // floats: offset [2][N], alpha [2][N], l [2][N], red [2][4][N], tile max
   static constexpr int KEYS = ROWS + 20 * N * 4 + 64;  // int2: keys a row sees
   static constexpr int OUT = KEYS + N * 8;           // int64: where a row's output and lse go
   static constexpr int BARS = OUT + N * 16;
@@ -157,6 +167,28 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Sums of N rows over a warp: the halves of the rows change sides step by step; lane i returns row i (N = 16: i / 2).
+template <int N>
+__device__ __forceinline__ float warp_row_sums(float (&v)[N], int lane) {
+  auto step = [&](auto cnt_c, int o) {
+    constexpr int cnt = decltype(cnt_c)::value;
+    const bool up = lane & o;
+#pragma unroll
+    for (int r = 0; r < cnt; ++r) {
+      const float give = up ? v[r] : v[r + cnt], keep = up ? v[r + cnt] : v[r];
+      v[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  };
+  step(std::integral_constant<int, N / 2>(), 16);
+  step(std::integral_constant<int, N / 4>(), 8);
+  step(std::integral_constant<int, N / 8>(), 4);
+  step(std::integral_constant<int, N / 16>(), 2);
+  if constexpr (N == 32) {
+    step(std::integral_constant<int, 1>(), 1);
+    return v[0];
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
 // A wait that did not end at once: sleep and look again, up to the limit. Then the status says so, and *gave_up ends this wait
 // and every later one of the CTA: the roles run to their ends on whatever the buffers hold.
 __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up, int* status) {
@@ -246,17 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tm = *tm_slot;
-  if (warp < 4) {  // read after the next barrier
-    uint32_t ones[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) ones[i] = 0x3C003C00u;
-    tmem_st32(tm + ((uint32_t)(32 * warp) << 16) + kTmOnes, ones);
-    tmem_st32(tm + ((uint32_t)(32 * warp) << 16) + kTmOnes + 32, ones);
-    tmem_wait_st();
-    tc::fence_before();
-  }
   constexpr uint32_t tmO = kTmS + 2 * N, tmL = kTmS + 4 * N;
-  static_assert(tmL + 2 * N <= kTmOnes, "tensor memory");
+  static_assert(tmL + 2 * N <= kTmCols, "tensor memory");
 
   Pieces<N> walk(a, prefix);  // thread 0's
   int it = 0;  // tiles so far, over all pieces: buffer it & 1, stage it % kStages of turn it / kStages
@@ -545,6 +568,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(pReady, g));
+        // this thread's keys' part of every row's sum, from the weights before their rounding
+#pragma unroll
+        for (int r = 0; r < N; r += 16) {
+          const uint32_t at = tm + lanes + tmL + N * g + r;
+          float sum[16];
+          if (!first_tile) {
+            tmem_ld<16>(at, sum);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint64_t two = add2(pack2f(sum[2 * e], sum[2 * e + 1]), x[r / 2 + e]);
+            sum[2 * e] = lo2f(two), sum[2 * e + 1] = hi2f(two);
+          }
+          tmem_store<16>(at, sum);
+        }
+        tmem_wait_st();
         last = i;
       }
       it += pc.u1 - pc.u0;
@@ -553,13 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (last >= 0) {
         wait_turn(bar(vFree, g), last >> 1);
         tc::fence_after();
-        if (w == 0) {  // every lane of L has the sums
-          float sum[N];
-          tmem_ld<N>(tm + lanes + tmL + N * g, sum);
-          if (lane == 0)
-#pragma unroll
-            for (int r = 0; r < N; ++r) row_l(g)[r] = sum[r];
-        }
+        float v[N];
+        tmem_ld<N>(tm + lanes + tmL + N * g, v);
+        const float sum = warp_row_sums<N>(v, lane);
+        if (N == 32 || (lane & 1) == 0) row_l(g)[w * N + (N == 32 ? lane : lane >> 1)] = sum;
       }
       tc::fence_before();
       softmax_barrier();
@@ -575,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         f0 = has0 ? (o0 == off ? 1.f : tc::ex2_approx(off - o0)) : 0.f;
         f1 = has1 ? (o1 == off ? 1.f : tc::ex2_approx(off - o1)) : 0.f;
         const float *l0 = row_l(0), *l1 = row_l(1);
-        L = (has0 ? f0 * l0[lane] : 0.f) + (has1 ? f1 * l1[lane] : 0.f);
+        L = (has0 ? f0 * (l0[lane] + l0[N + lane] + l0[2 * N + lane] + l0[3 * N + lane]) : 0.f) +
+            (has1 ? f1 * (l1[lane] + l1[N + lane] + l1[2 * N + lane] + l1[3 * N + lane]) : 0.f);
         inv = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
         if (w == 0 && lane >= r_lo && lane < min(rows, r_lo + N / 2)) {
           if (!whole)
@@ -718,9 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // a group's first tile of the piece starts its O
             umma_ts(o, va + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || u - pc.u0 >= 2);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_ts(tm + tmL + N * buf, tm + kTmOnes + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || u - pc.u0 >= 2);
           tc::umma_commit(bar(vFree, buf));
         }
         __syncwarp();
