@@ -14,7 +14,7 @@
 // reference m per row, moved only when a weight passes it by more than 2^8 (a vote of its four warps per tile); only then
 // are exact maxima formed and O, the sums rescaled. Weights are 2^(s - m + 6) <= 2^14, rounded to f16: weights down
 // to 2^-31 of the reference count, and the largest score is never below it. The sums are of the weights before that rounding, in
-// fp32, a thread's own in tensor memory: 32 more registers spilled (67 us for the 52 below), and a product of the rounded weights
+// fp32, a thread's own in tensor memory: 32 more registers spilled (67 us, then, for 52), and a product of the rounded weights
 // with ones was 3 us faster but its lse off by more than 10^-6. Queries are scaled by one power of two per
 // tile into f16's range: exact for bf16 elements down to 2^-32 of the tile's largest, and off by 2^-39 of that below.
 // The issuing warps stay converged and elect a lane: 17 clocks an MMA, 46 from a branch on the lane (the operands then
@@ -22,10 +22,10 @@
 // Bound: issue slots. A tile of 128 keys takes 1,050 clocks at N = 16 and 1,200 at N = 32 (820 warp instructions a
 // scheduler, more than half of them conversions of codes); its 18 KB take 795 at the copy rate of HBM. Twice the
 // dequantising warps (28 in all, registers shared out again with setmaxnreg) changed nothing, nor did 9 or 10 stages for 8. Around the
-// tiles: 6 us up to the first weights (lengths, list of pieces, first records, first maxima), 1.5 us at the end, 6 us the
+// tiles: 6 us up to the first weights (lengths, list of pieces, first records, first maxima), 1.5 us at the end, 4 us the
 // join with its launch; a change of pieces costs a CTA 8 tiles.
-// Measured (32 query heads, 8 KV heads, with the join): one request of 118,000 keys 41 us for one token, 52 us for eight; eight requests
-// of 8,192 keys, one token each, 22 us; 32 requests of up to 40,960 keys, up to eight tokens each, 209 us (53% of the copy rate).
+// Measured (32 query heads, 8 KV heads, with the join): one request of 118,000 keys 40 us for one token, 50 us for eight; eight requests
+// of 8,192 keys, one token each, 21 us; 32 requests of up to 40,960 keys, up to eight tokens each, 209 us (53% of the copy rate).
 // mma.sync does both products of a 32-row tile in 8 clocks a key an SM (measured 2.0 per m16n8k16), above the 6.8 that the bytes take
 // at the copy rate of HBM, and needs its operands and outputs in registers: the mma.sync kernel ran at 19.
 #include <math.h>
