@@ -11,7 +11,8 @@
 // dependent loads (position, page id) for a token (5.4 us).
 //
 // Read: the CTA fetches its record with one bulk copy (9 KB at d_h 128) and decodes the
-// rows asked for out of shared memory (the 8,192 tokens: 12 us, 3.6 TB/s).
+// rows asked for out of shared memory; two tokens' values share bytes and are decoded together (the 8,192 tokens: 11 us,
+// 3.9 TB/s).
 #include <algorithm>
 
 #include "kv_page.cuh"
@@ -249,6 +250,17 @@ __device__ __forceinline__ void store16(T* p, const float (&v)[16], bool vec) {
   }
 }
 
+// The values of 8 codes (nibble e of w)
+__device__ __forceinline__ void decode8(uint32_t w, float s, float* v) {
+  const uint32_t p[4] = {kv::fp4x2_of<0>(w), kv::fp4x2_of<1>(w), kv::fp4x2_of<2>(w), kv::fp4x2_of<3>(w)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+    v[2 * i] = f.x * s;
+    v[2 * i + 1] = f.y * s;
+  }
+}
+
 template <typename T, int DH>
 __global__ void __launch_bounds__(256) kv_read_kernel(ReadArgs a, bool vec) {
   constexpr int NB = DH / 16;
@@ -278,38 +290,37 @@ __global__ void __launch_bounds__(256) kv_read_kernel(ReadArgs a, bool vec) {
     __syncthreads();
     return;
   }
-  const int nt = sp.hi - sp.lo, items = nt * NB;
-  for (int u = tid; u < 2 * items; u += nthr) {
+  const int nt = sp.hi - sp.lo, b0 = sp.lo >> 1, nb = ((sp.hi + 1) >> 1) - b0;  // tokens; bytes (pairs of tokens) of a column
+  const long long row0 = (long long)b * a.T + sp.t0 - sp.lo, c0 = (long long)h * DH;
+  const int k_items = nt * NB;
+  for (int u = tid; u < k_items + nb * NB; u += nthr) {
     float v[16];
-    uint32_t by[8];
-    float s;
-    const bool key = u < items;
-    int i, j;
-    if (key) {
-      i = u / NB, j = u % NB;
-      const int tok = sp.lo + i;
+    if (u < k_items) {  // 16 key columns of a token
+      const int tok = sp.lo + u / NB, j = u % NB;
       const uint2 w = *reinterpret_cast<const uint2*>(rec + tok * (DH / 2) + 8 * j);
+      const float s = kv::fp8_to_f32(rec[kv::ks_off(DH) + tok * NB + j]) * a.k_scale;
+      decode8(w.x, s, v);
+      decode8(w.y, s, v + 8);
+      store16(static_cast<T*>(a.k) + (row0 + tok) * a.ks + c0 + 16 * j, v, vec);
+    } else {  // 16 value columns of two tokens, which share bytes: the pairs of a block side by side
+      const int j = (u - k_items) / nb, by = b0 + (u - k_items) - j * nb;
+      uint32_t w[2][2] = {{0u, 0u}, {0u, 0u}};  // [token][8 columns]
 #pragma unroll
-      for (int e = 0; e < 8; ++e) by[e] = ((e < 4 ? w.x : w.y) >> ((e & 3) * 8)) & 0xffu;
-      s = kv::fp8_to_f32(rec[kv::ks_off(DH) + tok * NB + j]) * a.k_scale;
-    } else {
-      j = (u - items) / nt, i = (u - items) - j * nt;
-      const int tok = sp.lo + i, sh = (tok & 1) * 4;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint8_t* col = rec + kv::v_off(DH) + (16 * j + 2 * e) * 32 + (tok >> 1);
-        by[e] = ((col[0] >> sh) & 15u) | (((col[32] >> sh) & 15u) << 4);
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t x = rec[kv::v_off(DH) + (16 * j + e) * 32 + by];
+        w[0][e >> 3] |= (x & 15u) << (4 * (e & 7));
+        w[1][e >> 3] |= (x >> 4) << (4 * (e & 7));
       }
-      s = kv::fp8_to_f32(rec[kv::vs_off(DH) + j * 64 + tok]) * a.v_scale;
-    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t p = kv::fp4x2_to_f16x2(by[e]);
-      v[2 * e] = __half2float(__ushort_as_half((unsigned short)(p & 0xffffu))) * s;
-      v[2 * e + 1] = __half2float(__ushort_as_half((unsigned short)(p >> 16))) * s;
+      for (int i = 0; i < 2; ++i) {
+        const int tok = 2 * by + i;
+        if (tok < sp.lo || tok >= sp.hi) continue;
+        const float s = kv::fp8_to_f32(rec[kv::vs_off(DH) + j * 64 + tok]) * a.v_scale;
+        decode8(w[i][0], s, v);
+        decode8(w[i][1], s, v + 8);
+        store16(static_cast<T*>(a.v) + (row0 + tok) * a.vs + c0 + 16 * j, v, vec);
+      }
     }
-    const long long r = (long long)b * a.T + sp.t0 + i, c = (long long)h * DH + 16 * j;
-    store16(key ? static_cast<T*>(a.k) + r * a.ks + c : static_cast<T*>(a.v) + r * a.vs + c, v, vec);
   }
 }
 

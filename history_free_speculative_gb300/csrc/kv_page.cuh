@@ -16,14 +16,9 @@ __host__ __device__ constexpr int v_off(int d_h) { return 32 * d_h; }
 __host__ __device__ constexpr int ks_off(int d_h) { return 64 * d_h; }
 __host__ __device__ constexpr int vs_off(int d_h) { return 68 * d_h; }
 
-// Two e2m1 codes (byte: low nibble first) / two e4m3 numbers as an f16 pair. Both are
+// Two e2m1 codes (a byte, low nibble first) / two e4m3 numbers as an f16 pair. Both are
 // exact, and so is the product of a code and a scale (2 + 4 significant bits, 2^-10..2688).
-__device__ __forceinline__ uint32_t fp4x2_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(byte));
-  return r;
-}
-// byte B of a word
+// byte B of a word of codes
 template <int B>
 __device__ __forceinline__ uint32_t fp4x2_of(uint32_t w) {
   uint32_t r;
