@@ -514,8 +514,10 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const AttnArgs a
   if (a.lse && lane == 0) a.lse[row * a.n_q + hq] = kv::lse_of(M, L, a.weight_exp);
 }
 
-// A change of pieces of the tcgen05 kernel, in its tiles of 128 keys: 9,000 to 12,000 clocks against 1,100 a tile.
-constexpr int kTcChange = 8;
+// A change of pieces in units: of the tcgen05 kernel in tiles of 128 keys (9,000 to 12,000 clocks against 1,100 a tile), of the other in
+// pages (118,000 keys, 8 float32 tokens 101 us at 0, 97 at 8, 93.5 at 16, 94.5 at 24; 8 requests of 8,192 keys 31.4, 26.2, 25.5, 25.9;
+// heads of 64, 32 ragged requests 207, 190, 180, 177).
+constexpr int kTcChange = 8, kChange = 16;
 
 kv::AttnPlan make_plan(const dlite_kv_attention_args& g) {
   kv::AttnPlan p;
@@ -525,13 +527,14 @@ kv::AttnPlan make_plan(const dlite_kv_attention_args& g) {
   p.rows = rows <= 16 || g.dtype == DLITE_F32 ? 16 : 32;
   p.row_tiles = (rows + p.rows - 1) / p.rows;
   p.unit = p.tc ? 2 : 1;
-  p.change = p.tc ? kTcChange : 0;
-  p.min_quota = p.tc ? 4 + kTcChange : kWarps;  // a page for every warp
+  p.change = p.tc ? kTcChange : kChange;
+  // two tiles (4,000 keys, 8 tokens: 14.4 us; 19.4 with twelve; 1,000 keys: 12.8, 15.2 with four), a page for every warp
+  p.min_quota = p.tc ? 2 : kWarps;
   p.grid = device_sms();            // one CTA an SM: its shared memory is the ring
   // segments that a CTA's least run holds whole are not cut
   const int most = (g.cache.max_pages + p.unit - 1) / p.unit;
   const long long tiles = (long long)g.B * p.row_tiles;
-  p.stream = most + p.change > p.min_quota && tiles <= kv::kMaxList && tiles * (most + p.change) * g.cache.n_kv < (1LL << 31);
+  p.stream = most > p.min_quota && tiles <= kv::kMaxList && tiles * (most + p.change) * g.cache.n_kv < (1LL << 31);
   if (!p.stream) p.grid = (int)std::min<long long>((long long)g.B * p.row_tiles * g.cache.n_kv, p.grid);
   return p;
 }

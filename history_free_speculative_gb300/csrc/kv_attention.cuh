@@ -141,14 +141,16 @@ struct Pieces {
       while (u < end) {
         while ((uint32_t)prefix[j + 1] * a.n_kv <= u) ++j;
         const uint32_t rem = u - (uint32_t)prefix[j] * a.n_kv, all = prefix[j + 1] - prefix[j];
-        p.j = j;
-        p.nu = (int)all - a.change;
-        p.h = (int)(rem / all);
-        const int v0 = (int)(rem - p.h * all), v1 = (int)min(all, v0 + (end - u));
+        const int h = (int)(rem / all);
+        const int v0 = (int)(rem - h * all), v1 = (int)min(all, v0 + (end - u));
         u += v1 - v0;
+        if (v1 <= a.change) continue;  // the run ends before the segment's first page; p stays the last piece
+        p.j = j;
+        p.h = h;
+        p.nu = (int)all - a.change;
         p.u0 = max(v0 - a.change, 0);
         p.u1 = v1 - a.change;
-        if (p.u1 > p.u0) return true;  // else the run ends before the segment's first page
+        return true;
       }
       return false;
     }
