@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const AttnArgs a
   if (a.lse && lane == 0) a.lse[row * a.n_q + hq] = kv::lse_of(M, L, a.weight_exp);
 }
 
-// A change of pieces in units: of the tcgen05 kernel in tiles of 128 keys (9,000 to 12,000 clocks against 1,100 a tile), of the other in
+// A change of pieces in units: of the tcgen05 kernel in tiles of 128 keys (9,000 to 12,000 clocks against 1,090 to 1,370 a tile), of the other in
 // pages (118,000 keys, 8 float32 tokens 101 us at 0, 97 at 8, 93.5 at 16, 94.5 at 24; 8 requests of 8,192 keys 31.4, 26.2, 25.5, 25.9;
 // heads of 64, 32 ragged requests 207, 190, 180, 177).
 constexpr int kTcChange = 8, kChange = 16;

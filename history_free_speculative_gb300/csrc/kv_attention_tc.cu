@@ -19,7 +19,7 @@
 // tile into f16's range: exact for bf16 elements down to 2^-32 of the tile's largest, and off by 2^-39 of that below.
 // The issuing warps stay converged and elect a lane: 17 clocks an MMA, 46 from a branch on the lane (the operands then
 // go from vector to uniform registers one by one).
-// Bound: issue slots. A tile of 128 keys takes 1,050 clocks at N = 16 and 1,200 at N = 32 (820 warp instructions a
+// Bound: issue slots. A tile of 128 keys takes 1,090 clocks at N = 16 and 1,370 at N = 32 (from the slope between 118,000 and 236,000 keys; 820 warp instructions a
 // scheduler, more than half of them conversions of codes); its 18 KB take 795 at the copy rate of HBM. Twice the
 // dequantising warps (28 in all, registers shared out again with setmaxnreg) changed nothing, nor did 9 or 10 stages for 8. Around the
 // tiles: 6 us up to the first weights (lengths, list of pieces, first records, first maxima), 1.5 us at the end, 4 us the
