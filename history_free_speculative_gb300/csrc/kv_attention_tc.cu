@@ -452,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 8; ++i) amax = fmaxf(amax, q_max[i]);
       // 2^k takes the tile's largest element into [2^14, 2^15)
       const int e2 = amax > 0.f ? min(max(14 - ilogbf(amax), -100), 100) : 0;
-      const float f = exp2f((float)e2), sc = a.scale_log2 * exp2f((float)-e2);
+      // the factor of the scores stays above 0: below 2^-126 all weights are 1 to float32's precision, and a masked -inf stays -inf
+      const float f = exp2f((float)e2), sc = fmaxf(a.scale_log2 * exp2f((float)-e2), 1.17549435e-38f);
 #pragma unroll
       for (int i = 0; i < N / 8; ++i) {
         const int r = warp - 8 + 8 * i;
