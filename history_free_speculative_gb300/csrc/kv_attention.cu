@@ -9,7 +9,7 @@
 //
 // Codes become f16 operands exactly: e2m1 x e4m3 has 6 significant bits between 2^-10 and 2688. Queries are scaled by a power
 // of two per row (largest element in [2^14, 2^15)), so a bf16 query is exact in f16 too; a float32 query
-// takes two planes (hi + lo, 22 bits). Softmax weights are held as 2^(s - m + 14) so that f16 keeps
+// takes two planes (hi + lo, 22 bits). Softmax weights are held as 2^(s - m + 14), in powers of two, so that f16 keeps
 // weights down to 2^-38 of the largest; they are rounded to f16 (2^-12 relative, below the bf16 output's 2^-9),
 // for float32 outputs as hi + lo. Scores, maxima, sums and outputs are fp32.
 // Measured: one float32 token over 500 keys, 4 query and 2 KV heads of 64, 6.8 us with the join; bound by two launches and a
@@ -33,9 +33,9 @@ namespace dlite {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr float kWeightExp = 14.f;  // weights are kept as 2^(s - m + 14)
 
 using kv::AttnArgs;
+using kv::kWeightExp;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -171,7 +171,7 @@ __device__ __forceinline__ void half_page(const uint8_t* rec, int hf, const uint
         }
       }
   }
-  // online softmax; weights 2^(s - m + 14)
+  // online softmax; weights 2^((s - m) sc + 14), m the largest raw score
   uint32_t p[NP][MT][2][4];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -186,10 +186,11 @@ __device__ __forceinline__ void half_page(const uint8_t* rec, int hf, const uint
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
     const float sc[2] = {row_sc[mt * 16 + g], row_sc[mt * 16 + 8 + g]};
-    const float n0 = fmaxf(m[mt][0], x0 * sc[0]), n1 = fmaxf(m[mt][1], x1 * sc[1]);
+    const float n0 = fmaxf(m[mt][0], x0), n1 = fmaxf(m[mt][1], x1);
     if (n0 != m[mt][0] || n1 != m[mt][1]) {
-      const float al0 = n0 == m[mt][0] ? 1.f : tc::ex2_approx(m[mt][0] - n0);
-      const float al1 = n1 == m[mt][1] ? 1.f : tc::ex2_approx(m[mt][1] - n1);
+      // no key before (m = -inf): nothing to rescale
+      const float al0 = n0 == m[mt][0] || m[mt][0] == -INFINITY ? 1.f : tc::ex2_approx((m[mt][0] - n0) * sc[0]);
+      const float al1 = n1 == m[mt][1] || m[mt][1] == -INFINITY ? 1.f : tc::ex2_approx((m[mt][1] - n1) * sc[1]);
       l[mt][0] *= al0;
       l[mt][1] *= al1;
 #pragma unroll
@@ -203,13 +204,13 @@ __device__ __forceinline__ void half_page(const uint8_t* rec, int hf, const uint
       m[mt][1] = n1;
     }
     // a row with no key yet (m = -inf): every weight is 0
-    const float b0 = n0 == -INFINITY ? 0.f : kWeightExp - n0, b1 = n1 == -INFINITY ? 0.f : kWeightExp - n1;
+    const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       float w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        w[e] = tc::ex2_approx(fmaf(s[mt][nt][e], sc[e >> 1], e < 2 ? b0 : b1));
+        w[e] = tc::ex2_approx(fmaf(s[mt][nt][e] - (e < 2 ? r0 : r1), sc[e >> 1], kWeightExp));
         if constexpr (MASKED) w[e] = s[mt][nt][e] == -INFINITY ? 0.f : w[e];
       }
       l[mt][0] += w[0] + w[1];
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const Attn
       for (int e = 0; e < 2; ++e) {
         l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
         l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
+        m[mt][e] *= m[mt][e] == -INFINITY ? 1.f : row_sc[mt * 16 + e * 8 + (lane >> 2)];   // a power of two from here on
         if ((lane & 3) == 0) sm_m[warp * R + mt * 16 + e * 8 + (lane >> 2)] = m[mt][e];
       }
     __syncthreads();
@@ -608,7 +610,7 @@ extern "C" int dlite_kv_attention(const dlite_kv_attention_args* g, dlite_stream
   a.min_quota = p.min_quota;
   a.change = p.change;
   a.stream = p.stream;
-  a.weight_exp = p.tc ? 0.f : kWeightExp;  // the tcgen05 kernel leaves its offset itself
+  a.weight_exp = p.tc ? kv::kTcWeightExp : kWeightExp;
   a.scale_log2 = (float)ldexp((double)g->scale * 1.4426950408889634, c.k_exp);
   a.v_scale = ldexpf(1.f, c.v_exp);
   a.q = g->q;

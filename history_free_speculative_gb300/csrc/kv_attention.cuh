@@ -19,6 +19,11 @@ namespace kv {
 
 constexpr int kMaxList = 2048;  // row tiles of all requests in the stream form
 
+// Weights are kept as 2^((s - ref) factor + exp): s a raw score (the products' sum), ref the row's reference, a raw score too, factor what
+// takes raw scores to powers of two. The difference comes before the factor: with the reference as a power of two, its rounding
+// (half a step of the score) moved the largest weight itself, and scores of 2^26 and more passed f16's range.
+constexpr float kWeightExp = 14.f, kTcWeightExp = 6.f;
+
 struct AttnArgs {
   const uint8_t* pages;
   const int32_t* bt;
@@ -187,7 +192,7 @@ constexpr int kBatch = 32;
 __device__ __forceinline__ size_t part_row(const Piece& p, int R) { return ((size_t)blockIdx.x * 2 + (p.u0 == 0)) * R; }
 
 __device__ __forceinline__ float lse_of(float M, float L, float weight_exp) {
-  return L == 0.f ? -INFINITY : (M - weight_exp + log2f(L)) * 0.6931471805599453f;
+  return L == 0.f ? -INFINITY : (M + (log2f(L) - weight_exp)) * 0.6931471805599453f;
 }
 
 // Host side

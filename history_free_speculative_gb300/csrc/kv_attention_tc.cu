@@ -11,8 +11,8 @@
 // of the first and the second product, 19 copies: five warps a scheduler.
 // The softmax warps are two groups that take the tiles in turn, each with its own scores, weights, maxima, sums and O, joined at
 // a piece's end: one group's latencies pass under the other's tile (one group alone took 3,300 clocks a tile). A group keeps one
-// reference m per row, moved only when a weight passes it by more than 2^8 (a vote of its four warps per tile); only then
-// are exact maxima formed and O, the sums rescaled. Weights are 2^(s - m + 6) <= 2^14, rounded to f16: weights down
+// reference m per row, a raw score, moved only when a weight passes it by more than 2^8 (a vote of its four warps per tile); only then
+// are exact maxima formed and O, the sums rescaled. Weights are 2^((s - m) factor + 6) <= 2^14, rounded to f16: weights down
 // to 2^-31 of the reference count, and the largest score is never below it. The sums are of the weights before that rounding, in
 // fp32, a thread's own in tensor memory: 32 more registers spilled (67 us, then, for 52), and a product of the rounded weights
 // with ones was 3 us faster but its lse off by more than 10^-6. Queries are scaled by one power of two per
@@ -52,15 +52,14 @@ static_assert(REC % 1024 == 0 && kRecRows <= 256, "rows of a copy");
 __device__ __forceinline__ int chunk(int c) { return c / 8 * kRow + (((c ^ (c >> 3)) & 7) << 4); }
 // tensor memory columns: K and V^T tiles twice; then S^T, O^T and the threads' sums twice each
 constexpr int kTmK = 0, kTmV = 128, kTmS = 256, kTmCols = 512;
-constexpr float kTcWeightExp = 6.f;
-constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key
+constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key: raw scores are below 2^36
 
 template <int N>
 struct Smem {
   static constexpr int Q = kStages * TILE;           // [2 halves][N rows][128 B], 128-byte swizzle
   static constexpr int P = Q + N * 256;              // [2][128 keys][N rows] f16, rows of N contiguous
   static constexpr int VS = P + 2 * 128 * N * 2;     // [stage][8 blocks][128 tokens] f16: value scales
-  static constexpr int ROWS = VS + kStages * 2048;         // floats: offset [2][N], alpha [2][N], l [2][N], red [2][4][N], tile max
+  static constexpr int ROWS = VS + kStages * 2048;         // floats: reference [2][N], alpha [2][N], l [2][N], red [2][4][N], tile max
   static constexpr int KEYS = ROWS + 20 * N * 4 + 64;  // int2: keys a row sees
   static constexpr int OUT = KEYS + N * 8;           // int64: where a row's output and lse go
   static constexpr int BARS = OUT + N * 16;
@@ -220,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = raw + ((1024 - (tc::su32(raw) & 1023)) & 1023);
   const uint32_t sb = tc::su32(sm);
   float* rows_f = reinterpret_cast<float*>(sm + S::ROWS);
-  auto row_off = [&](int g) { return rows_f + g * N; };              // 6 - m: a weight is 2^(score + offset)
+  auto row_ref = [&](int g) { return rows_f + g * N; };              // references, raw scores
   auto row_alpha = [&](int g) { return rows_f + (2 + g) * N; };
   auto row_l = [&](int g) { return rows_f + (4 + 4 * g) * N; };      // [warp][row]
   auto row_red = [&](int g) { return rows_f + (12 + 4 * g) * N; };   // [warp][row]
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bad[i] = __any_sync(0xffffffffu, q_bad);
         if (!bad[i]) amax = fmaxf(amax, m);
-        if (lane == 0) row_off(0)[r] = row_off(1)[r] = bad[i] ? NAN : kTcWeightExp - kNoRef;
+        if (lane == 0) row_ref(0)[r] = row_ref(1)[r] = bad[i] ? NAN : kNoRef;
       }
       amax = warp_max_f32(amax);
       if (lane == 0) q_max[warp - 8] = amax;
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(q_ready);
-      const uint64_t sc2 = pack2f(sc, sc);
+      const uint64_t sc2 = pack2f(sc, sc), we2 = pack2f(kTcWeightExp, kTcWeightExp);
       // tiles wholly inside every row's range need no masks
       const int full_end = (int)min(max(t.p0 + t.t_lo + 1, 0LL), t.cap);
       const int full_beg = a.window ? (int)min(max(t.p0 + t.t_hi - a.window + 1, 0LL), t.cap) : 0;
@@ -498,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float top = -INFINITY;
 #pragma unroll
           for (int r = 0; r < N / 2; r += 2) {
-            const ulonglong2 of = *reinterpret_cast<const ulonglong2*>(row_off(g) + 2 * r);
-            x[r] = fma2(x[r], sc2, of.x);
-            x[r + 1] = fma2(x[r + 1], sc2, of.y);
+            const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(row_ref(g) + 2 * r);
+            x[r] = fma2(sub2(x[r], ref.x), sc2, we2);
+            x[r + 1] = fma2(sub2(x[r + 1], ref.y), sc2, we2);
             top = fmaxf(top, fmaxf(fmaxf(lo2f(x[r]), hi2f(x[r])), fmaxf(lo2f(x[r + 1]), hi2f(x[r + 1]))));
           }
           return top;
@@ -527,9 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (w == 0 && lane < N) {
             const float* red = row_red(g);
             const float mx = fmaxf(fmaxf(red[lane], red[N + lane]), fmaxf(red[2 * N + lane], red[3 * N + lane]));
-            const float off0 = row_off(g)[lane], off1 = fminf(off0, kTcWeightExp - mx * sc);
-            row_alpha(g)[lane] = off1 < off0 ? tc::ex2_approx(off1 - off0) : 1.f;
-            if (off1 < off0) row_off(g)[lane] = off1;   // a NaN stays
+            const float ref = row_ref(g)[lane];
+            row_alpha(g)[lane] = mx > ref ? tc::ex2_approx((ref - mx) * sc) : 1.f;
+            if (mx > ref) row_ref(g)[lane] = mx;   // a NaN stays
             if (lane == 0) move_ref[g] = 0;
           }
           group_barrier(g);
@@ -607,22 +606,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int np = pc.u1 - pc.u0, r_lo = g * (N / 2);
       // whether a group had a tile: both from two tiles on, else the one whose turn the tile was
       const bool has0 = np > 1 || ((it - np) & 1) == 0, has1 = np > 1 || ((it - np) & 1) == 1;
-      float L = 0.f, off = 0.f, f0 = 0.f, f1 = 0.f, inv = 0.f;  // of row `lane`
+      float L = 0.f, M = 0.f, f0 = 0.f, f1 = 0.f, inv = 0.f;  // of row `lane`
       const bool whole = pc.u0 == 0 && pc.u1 == pc.nu;
       if (lane < N) {
-        const float o0 = row_off(0)[lane], o1 = row_off(1)[lane];
-        off = fminf(o0, o1);
-        f0 = has0 ? (o0 == off ? 1.f : tc::ex2_approx(off - o0)) : 0.f;
-        f1 = has1 ? (o1 == off ? 1.f : tc::ex2_approx(off - o1)) : 0.f;
+        const float r0 = row_ref(0)[lane], r1 = row_ref(1)[lane], ref = fmaxf(r0, r1);
+        M = ref * sc;
+        f0 = has0 ? (r0 == ref ? 1.f : tc::ex2_approx((r0 - ref) * sc)) : 0.f;
+        f1 = has1 ? (r1 == ref ? 1.f : tc::ex2_approx((r1 - ref) * sc)) : 0.f;
         const float *l0 = row_l(0), *l1 = row_l(1);
         L = (has0 ? f0 * (l0[lane] + l0[N + lane] + l0[2 * N + lane] + l0[3 * N + lane]) : 0.f) +
             (has1 ? f1 * (l1[lane] + l1[N + lane] + l1[2 * N + lane] + l1[3 * N + lane]) : 0.f);
         inv = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
         if (w == 0 && lane >= r_lo && lane < min(rows, r_lo + N / 2)) {
           if (!whole)
-            a.part_ml[part_row(pc, N) + lane] = make_float2(-off, L);
+            a.part_ml[part_row(pc, N) + lane] = make_float2(M, L);
           else if (a.lse)
-            a.lse[row_out[N + lane]] = lse_of(-off, L, 0.f);
+            a.lse[row_out[N + lane]] = lse_of(M, L, kTcWeightExp);
         }
       }
       float o0[N / 2], o1[N / 2];
@@ -642,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           a.part_o[(part_row(pc, N) + r_lo + r) * DH + d] = v;
       }
-      softmax_barrier();  // both O, row_l, row_off are the next piece's
+      softmax_barrier();  // both O, row_l, row_ref are the next piece's
     }
   } else if (warp == 16) {  // ---------------------------------------------------------------- value scales
     // as f16, once for the 16 columns that share them: lane = block of 16 columns lane / 4, 32 tokens

@@ -30,3 +30,44 @@ def test_factors_of_the_scores_at_the_ends_of_float32(dtype, d, size, scale, k_e
     pages, bt = _cache(5, 1, d, 1, 5, 45)
     q = (torch.randn(1, 2, 4, d, generator=_gen(46)) * size).to(DT[dtype])
     _check(q, pages, bt, 270, scale, dtype, k_exp)
+
+
+@pytest.mark.parametrize("T", [1, 8])
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_scores_below_minus_10_to_the_30(dtype, d, T):
+    """Keys of 2 and then of 1 in every column, queries of -2^100: scores of -2 d 2^100 and -d 2^100, exact in any order. The keys of
+    1 share the weight alike; before the first of them a row has the others'."""
+    nq = 4
+    pages, _ = _cache(5, 1, d, 1, 5, 47)
+    pages[..., :32 * d] = 0x22            # codes of 1
+    pages[..., 64 * d:68 * d] = 0x38      # scales of 1
+    pages[:3, :, 64 * d:68 * d] = 0x40    # of 2
+    bt = torch.arange(5, dtype=torch.int32)[None]
+    q = torch.full((1, T, nq, d), -2.0 ** 100).to(DT[dtype])
+    for pos in (100, 300):
+        first, n, key = (0, pos, -2.0) if pos < 192 else (192, pos, -1.0)
+        out, lse = binding.kv_attention(q.to(DEV), pages.to(DEV), bt.to(DEV), torch.tensor([pos], device=DEV), scale=1.0, lse=True)
+        v = np.concatenate([TO.read_record(pages.numpy()[p, 0], 0, 0)[1] for p in range(5)])
+        want = np.stack([v[first:n + t + 1].mean(0) for t in range(T)])[None, :, None].repeat(nq, 2)
+        reach = np.stack([np.abs(v[first:n + t + 1]).mean(0) for t in range(T)])[None, :, None].repeat(nq, 2)
+        tol, _ = _tolerance(want, reach, np.zeros((1, T, nq)), pos + T, d, dtype)
+        _within(out, want, tol)
+        wl = np.full((1, T, nq), key * d * 2.0 ** 100)
+        _within(lse, wl, 2.0 ** -21 * np.abs(wl))
+
+
+@pytest.mark.parametrize("pos", [300, 4000])       # one piece, and pieces of several CTAs
+@pytest.mark.parametrize("scale", [1.1 * 2.0 ** 18, 1.1 * 2.0 ** 40, 1.1 * 2.0 ** 100])
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_scores_far_above_their_rounding(dtype, d, scale, pos):
+    """Sharp rows, as with a scale that makes attention take the best key alone. q . k are multiples of a half below 2^13, exact in
+    float32, so a row's weights are those of its largest keys, equal among equals."""
+    T, nq, mp = 8, 4, pos // 64 + 2
+    pages, bt = _cache(mp, 1, d, 1, mp, 48)
+    pages[..., 64 * d:68 * d] = 0x38      # key scales of 1
+    q = torch.randint(-3, 4, (1, T, nq, d), generator=_gen(49)).to(DT[dtype])
+    want, wl, reach, eps = TO.attention(q.float().numpy(), pages.numpy(), bt.numpy(), [pos], scale)
+    out, lse = binding.kv_attention(q.to(DEV), pages.to(DEV), bt.to(DEV), torch.tensor([pos], device=DEV), scale=scale, lse=True)
+    tol, _ = _tolerance(want, reach, np.zeros_like(eps), pos + T, d, dtype)
+    _within(out, want, tol)
+    _within(lse, wl, 2.0 ** -21 * np.abs(wl))
