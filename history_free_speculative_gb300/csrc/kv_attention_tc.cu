@@ -15,8 +15,9 @@
 // are exact maxima formed and O, the sums rescaled. Weights are 2^((s - m) factor + 6) <= 2^14, rounded to f16: weights down
 // to 2^-31 of the reference count, and the largest score is never below it. The sums are of the weights before that rounding, in
 // fp32, a thread's own in tensor memory: 32 more registers spilled (67 us, then, for 52), and a product of the rounded weights
-// with ones was 3 us faster but its lse off by more than 10^-6. Queries are scaled by one power of two per
-// tile into f16's range: exact for bf16 elements down to 2^-32 of the tile's largest, and off by 2^-39 of that below.
+// with ones was 3 us faster but its lse off by more than 10^-6. Queries are scaled by a power of two per
+// row into f16's range: exact for bf16 elements down to 2^-32 of the row's largest, and off by 2^-39 of that below. (One power of two
+// per tile saves the loads of the factors, 4% of the ragged batch, but a row beside much larger ones lost its bits; both, by a branch per tile: no faster.)
 // The issuing warps stay converged and elect a lane: 17 clocks an MMA, 46 from a branch on the lane (the operands then
 // go from vector to uniform registers one by one).
 // Bound: issue slots. A tile of 128 keys takes 1,090 clocks at N = 16 and 1,370 at N = 32 (from the slope between 118,000 and 236,000 keys; 820 warp instructions a
@@ -59,8 +60,8 @@ struct Smem {
   static constexpr int Q = kStages * TILE;           // [2 halves][N rows][128 B], 128-byte swizzle
   static constexpr int P = Q + N * 256;              // [2][128 keys][N rows] f16, rows of N contiguous
   static constexpr int VS = P + 2 * 128 * N * 2;     // [stage][8 blocks][128 tokens] f16: value scales
-  static constexpr int ROWS = VS + kStages * 2048;         // floats: reference [2][N], alpha [2][N], l [2][N], red [2][4][N], tile max
-  static constexpr int KEYS = ROWS + 20 * N * 4 + 64;  // int2: keys a row sees
+  static constexpr int ROWS = VS + kStages * 2048;         // floats: reference [2][N], alpha [2][N], l [2][N], red [2][4][N], factor [N]
+  static constexpr int KEYS = ROWS + 21 * N * 4;  // int2: keys a row sees
   static constexpr int OUT = KEYS + N * 8;           // int64: where a row's output and lse go
   static constexpr int BARS = OUT + N * 16;
   static constexpr int NBARS = 2 * kStages + 17 + kRing;
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto row_alpha = [&](int g) { return rows_f + (2 + g) * N; };
   auto row_l = [&](int g) { return rows_f + (4 + 4 * g) * N; };      // [warp][row]
   auto row_red = [&](int g) { return rows_f + (12 + 4 * g) * N; };   // [warp][row]
-  float* q_max = rows_f + 20 * N;                                    // [8 warps]
+  float* row_sc = rows_f + 20 * N;                                   // factors of the raw scores
   int2* row_keys = reinterpret_cast<int2*>(sm + S::KEYS);
   long long* row_out = reinterpret_cast<long long*>(sm + S::OUT);  // [row] of out, [N + row] of lse
   int* stage_ok = reinterpret_cast<int*>(sm + S::OK);
@@ -417,8 +418,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == 8 && lane == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
         flag_status(a.status, kDevBounds);
       // Q: all of the last piece's first products are done
-      float v[N / 8][4], amax = 0.f;
-      bool bad[N / 8];
       if (warp == 8 && lane < N) {
         const int r = t.r0 + lane, tk = r / a.group, hq = h * a.group + r % a.group;
         const long long row = (long long)b * a.T + tk, seen = t.p0 + tk;
@@ -430,41 +429,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < N / 8; ++i) {
         const int r = warp - 8 + 8 * i;
-        const uint2 x = r < rows ? raw_q[i] : make_uint2(0u, 0u);
-        v[i][0] = __uint_as_float(x.x << 16), v[i][1] = __uint_as_float(x.x & 0xffff0000u);
-        v[i][2] = __uint_as_float(x.y << 16), v[i][3] = __uint_as_float(x.y & 0xffff0000u);
+        uint2 x = r < rows ? raw_q[i] : make_uint2(0u, 0u);
+        const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                            __uint_as_float(x.y & 0xffff0000u)};
         bool q_bad = false;
-        float m = 0.f;
+        float amax = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          m = fmaxf(m, fabsf(v[i][e]));
-          q_bad |= !(fabsf(v[i][e]) <= 3.402823466e38f);
+          amax = fmaxf(amax, fabsf(v[e]));
+          q_bad |= !(fabsf(v[e]) <= 3.402823466e38f);
         }
-        bad[i] = __any_sync(0xffffffffu, q_bad);
-        if (!bad[i]) amax = fmaxf(amax, m);
-        if (lane == 0) row_ref(0)[r] = row_ref(1)[r] = bad[i] ? NAN : kNoRef;
-      }
-      amax = warp_max_f32(amax);
-      if (lane == 0) q_max[warp - 8] = amax;
-      softmax_barrier();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, q_max[i]);
-      // 2^k takes the tile's largest element into [2^14, 2^15)
-      const int e2 = amax > 0.f ? min(max(14 - ilogbf(amax), -100), 100) : 0;
-      // the factor of the scores stays above 0: below 2^-126 all weights are 1 to float32's precision, and a masked -inf stays -inf
-      const float f = exp2f((float)e2), sc = fmaxf(a.scale_log2 * exp2f((float)-e2), 1.17549435e-38f);
-#pragma unroll
-      for (int i = 0; i < N / 8; ++i) {
-        const int r = warp - 8 + 8 * i;
-        uint2 x = make_uint2(pack_f16(v[i][0] * f, v[i][1] * f), pack_f16(v[i][2] * f, v[i][3] * f));
-        if (bad[i]) x = make_uint2(0u, 0u);
+        const bool bad = __any_sync(0xffffffffu, q_bad);
+        amax = warp_max_f32(amax);
+        // 2^k takes the row's largest element into [2^14, 2^15)
+        const int e2 = amax > 0.f && !bad ? min(max(14 - ilogbf(amax), -100), 100) : 0;
+        const float f = exp2f((float)e2);
+        x = bad ? make_uint2(0u, 0u) : make_uint2(pack_f16(v[0] * f, v[1] * f), pack_f16(v[2] * f, v[3] * f));
         // columns 4 lane ..: half lane / 16, 16-byte chunk (lane % 16) / 2 of the row, swizzled by the row
         *reinterpret_cast<uint2*>(sm + S::Q + (lane >> 4) * N * 128 + r * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * (lane & 1)) = x;
+        if (lane == 0) {
+          row_ref(0)[r] = row_ref(1)[r] = bad ? NAN : kNoRef;
+          // above 0: below 2^-126 all weights are 1 to float32's precision, and a masked -inf stays -inf
+          row_sc[r] = fmaxf(a.scale_log2 * exp2f((float)-e2), 1.17549435e-38f);
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(q_ready);
-      const uint64_t sc2 = pack2f(sc, sc), we2 = pack2f(kTcWeightExp, kTcWeightExp);
+      softmax_barrier();
+      const uint64_t we2 = pack2f(kTcWeightExp, kTcWeightExp);
       // tiles wholly inside every row's range need no masks
       const int full_end = (int)min(max(t.p0 + t.t_lo + 1, 0LL), t.cap);
       const int full_beg = a.window ? (int)min(max(t.p0 + t.t_hi - a.window + 1, 0LL), t.cap) : 0;
@@ -498,8 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < N / 2; r += 2) {
             const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(row_ref(g) + 2 * r);
-            x[r] = fma2(sub2(x[r], ref.x), sc2, we2);
-            x[r + 1] = fma2(sub2(x[r + 1], ref.y), sc2, we2);
+            const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(row_sc + 2 * r);
+            x[r] = fma2(sub2(x[r], ref.x), sc.x, we2);
+            x[r + 1] = fma2(sub2(x[r + 1], ref.y), sc.y, we2);
             top = fmaxf(top, fmaxf(fmaxf(lo2f(x[r]), hi2f(x[r])), fmaxf(lo2f(x[r + 1]), hi2f(x[r + 1]))));
           }
           return top;
@@ -527,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* red = row_red(g);
             const float mx = fmaxf(fmaxf(red[lane], red[N + lane]), fmaxf(red[2 * N + lane], red[3 * N + lane]));
             const float ref = row_ref(g)[lane];
-            row_alpha(g)[lane] = mx > ref ? tc::ex2_approx((ref - mx) * sc) : 1.f;
+            row_alpha(g)[lane] = mx > ref ? tc::ex2_approx((ref - mx) * row_sc[lane]) : 1.f;
             if (mx > ref) row_ref(g)[lane] = mx;   // a NaN stays
             if (lane == 0) move_ref[g] = 0;
           }
@@ -609,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float L = 0.f, M = 0.f, f0 = 0.f, f1 = 0.f, inv = 0.f;  // of row `lane`
       const bool whole = pc.u0 == 0 && pc.u1 == pc.nu;
       if (lane < N) {
-        const float r0 = row_ref(0)[lane], r1 = row_ref(1)[lane], ref = fmaxf(r0, r1);
+        const float r0 = row_ref(0)[lane], r1 = row_ref(1)[lane], ref = fmaxf(r0, r1), sc = row_sc[lane];
         M = ref * sc;
         f0 = has0 ? (r0 == ref ? 1.f : tc::ex2_approx((r0 - ref) * sc)) : 0.f;
         f1 = has1 ? (r1 == ref ? 1.f : tc::ex2_approx((r1 - ref) * sc)) : 0.f;

@@ -71,3 +71,18 @@ def test_scores_far_above_their_rounding(dtype, d, scale, pos):
     tol, _ = _tolerance(want, reach, np.zeros_like(eps), pos + T, d, dtype)
     _within(out, want, tol)
     _within(lse, wl, 2.0 ** -21 * np.abs(wl))
+
+
+@pytest.mark.parametrize("near", [False, True])
+@pytest.mark.parametrize("T", [1, 8])
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_rows_of_different_sizes_in_one_tile(dtype, d, T, near):
+    """A row's result does not depend on the rows beside it: rows of 1, 2^40 and 2^-40 (near: 2^4 and 2^-4), each with scores of order one at
+    one of the scales (the others: a row of nearly equal weights, or one key alone, whose tolerance is wide)."""
+    nq = 8
+    pages, bt = _cache(6, 1, d, 1, 6, 41)
+    size = torch.tensor([0, 4, -4, 0, -3, 0, 4, -4, 0, 3, 0] if near else [0, 40, -40, 0, -33, 0, 40, -40, 0, 33, 0])
+    size = size.repeat((T * nq + 10) // 11)[:T * nq].view(1, T, nq, 1)
+    q = (torch.randn(1, T, nq, d, generator=_gen(42)) * torch.exp2(size.float())).to(DT[dtype])
+    for e in (0, 4, -4) if near else (0, 40, -40):
+        _check(q, pages, bt, 300, d ** -0.5 * 2.0 ** -e, dtype)
