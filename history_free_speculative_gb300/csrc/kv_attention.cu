@@ -328,12 +328,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const Attn
       }
       amax = warp_max(amax);
       bad = __any_sync(0xffffffffu, bad);
-      // 2^k takes the largest element into [2^14, 2^15)
-      int k = 0;
-      if (amax > 0.f && !bad) k = min(max(14 - (ilogbf(amax)), -100), 100);
-      const float f = bad ? 0.f : exp2f((float)k);
+      const kv::RowScale rs = kv::row_scale(a, bad ? 0.f : amax);
       if (lane == 0) {
-        row_sc[r] = bad ? NAN : a.scale_log2 * exp2f((float)-k);
+        row_sc[r] = bad ? NAN : rs.factor;
         const long long last = t.p0 + min(t.r0 + r, t.r1 - 1) / a.group;
         row_keys[r] = make_int2(a.window ? (int)min(max(last - a.window + 1, 0LL), t.cap) : 0, (int)min(max(last + 1, 0LL), t.cap));
       }
@@ -341,7 +338,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const Attn
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
         const int d = lane * E + i, c = d / (DH / 4), st = (d % (DH / 4)) / 4, reg = (d % 4 >= 2 ? 2 : 0) + up;
-        const float x0 = bad ? 0.f : v[i] * f, x1 = bad ? 0.f : v[i + 1] * f;
+        const float x0 = bad ? 0.f : v[i] * rs.f0 * rs.f1, x1 = bad ? 0.f : v[i + 1] * rs.f0 * rs.f1;
         const uint32_t hi = pack_f16(x0, x1);
         uint32_t* dst = reinterpret_cast<uint32_t*>(qf + (mt * STEPS + st) * 32 + g * 4 + c) + reg;
         *dst = hi;
@@ -611,7 +608,8 @@ extern "C" int dlite_kv_attention(const dlite_kv_attention_args* g, dlite_stream
   a.change = p.change;
   a.stream = p.stream;
   a.weight_exp = p.tc ? kv::kTcWeightExp : kWeightExp;
-  a.scale_log2 = (float)ldexp((double)g->scale * 1.4426950408889634, c.k_exp);
+  a.scale_mant = (float)frexp((double)g->scale * 1.4426950408889634, &a.scale_exp);
+  a.scale_exp += c.k_exp;
   a.v_scale = ldexpf(1.f, c.v_exp);
   a.q = g->q;
   a.qs = g->q_stride;

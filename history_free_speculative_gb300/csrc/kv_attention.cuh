@@ -34,7 +34,8 @@ struct AttnArgs {
   int min_quota;        // units a CTA takes at least (stream form)
   int change;           // what a change of pieces costs a CTA, in units
   int stream;           // 1: stream form
-  float scale_log2;     // scale log2(e) 2^k_exp
+  float scale_mant;     // scale log2(e) 2^k_exp = scale_mant 2^scale_exp, scale_mant in [1/2, 1)
+  int scale_exp;
   float v_scale;        // 2^v_exp
   float weight_exp;     // weights are kept as 2^(s - m + weight_exp)
   const void* q;
@@ -50,6 +51,19 @@ struct AttnArgs {
   int vec;          // q and out rows on 16 bytes
   int* status;
 };
+
+// How a query row becomes f16: multiplied by f0 f1 = 2^e2, which takes its largest element into [2^14, 2^15) (two factors, since e2 goes from -113
+// to 163), and factor, which takes the row's raw scores to powers of two. The factor's exponent is worked out before its value: scale, k_exp
+// and e2 may each pass float32's range where their sum does not. Below 2^-126 all weights are 1 to float32's precision; it
+// stays above 0 so that a masked -inf stays -inf. Above 2^127 all but scores near 0 are past float32.
+struct RowScale {
+  float f0, f1, factor;
+};
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }  // -126 <= k <= 127
+__device__ __forceinline__ RowScale row_scale(const AttnArgs& a, float amax) {  // amax finite
+  const int e2 = amax > 0.f ? 14 - ilogbf(amax) : 0, h = e2 >> 1;
+  return {pow2(h), pow2(e2 - h), a.scale_mant * pow2(min(max(a.scale_exp - e2, -125), 127))};
+}
 
 // One tile of rows of a request: rows [r0, r1) (row r is token r / group, head r % group), keys [key_beg, key_end) that some
 // row may see, the pages they lie in.

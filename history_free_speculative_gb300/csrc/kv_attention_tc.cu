@@ -441,16 +441,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool bad = __any_sync(0xffffffffu, q_bad);
         amax = warp_max_f32(amax);
-        // 2^k takes the row's largest element into [2^14, 2^15)
-        const int e2 = amax > 0.f && !bad ? min(max(14 - ilogbf(amax), -100), 100) : 0;
-        const float f = exp2f((float)e2);
-        x = bad ? make_uint2(0u, 0u) : make_uint2(pack_f16(v[0] * f, v[1] * f), pack_f16(v[2] * f, v[3] * f));
+        const RowScale rs = row_scale(a, bad ? 0.f : amax);
+        auto f16x2 = [&](float lo, float hi) { return pack_f16(lo * rs.f0 * rs.f1, hi * rs.f0 * rs.f1); };
+        x = bad ? make_uint2(0u, 0u) : make_uint2(f16x2(v[0], v[1]), f16x2(v[2], v[3]));
         // columns 4 lane ..: half lane / 16, 16-byte chunk (lane % 16) / 2 of the row, swizzled by the row
         *reinterpret_cast<uint2*>(sm + S::Q + (lane >> 4) * N * 128 + r * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * (lane & 1)) = x;
         if (lane == 0) {
           row_ref(0)[r] = row_ref(1)[r] = bad ? NAN : kNoRef;
-          // above 0: below 2^-126 all weights are 1 to float32's precision, and a masked -inf stays -inf
-          row_sc[r] = fmaxf(a.scale_log2 * exp2f((float)-e2), 1.17549435e-38f);
+          row_sc[r] = rs.factor;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -534,7 +534,9 @@ int dlite_kv_read(const dlite_kv_read_args *args, dlite_stream_t stream);
  * keys (positions pos[b] .. pos[b] + T - 1) are appended before this call, and a
  * negative page id is a hole (an evicted page). Then
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  lse = ln sum_j p_j,
- * with float32 scores, statistics and sums. A row that sees no key gets zeros and
+ * with float32 scores, statistics and sums, for queries and scales of any size whose scores are
+ * float32 numbers. (A query's elements are held to 2^-39 of the largest of their head, float32 ones
+ * to 2^-23 of themselves as well.) A row that sees no key gets zeros and
  * lse = -inf; a row whose query holds a NaN or infinity gets NaN. An id >= n_pages or a block
  * past the cache's end flags DLITE_DEV_BOUNDS. Rows of other requests and of
  * tokens not yet appended never reach a result, whatever their bytes hold.

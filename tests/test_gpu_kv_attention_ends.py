@@ -23,10 +23,11 @@ def _check(q, pages, bt, pos, scale, dtype, k_exp=0):
     return out, lse
 
 
-@pytest.mark.parametrize("size,scale,k_exp", [(1.0, 1e-42, 0), (2.0 ** -87, 0.125, -46)])
+@pytest.mark.parametrize("size,scale,k_exp", [(1.0, 1e-42, 0), (2.0 ** -87, 0.125, -46), (2.0 ** -130, 2.0 ** 64, 64)])
 @pytest.mark.parametrize("dtype,d", KINDS)
 def test_factors_of_the_scores_at_the_ends_of_float32(dtype, d, size, scale, k_exp):
-    """scale 2^k_exp and the queries' own factor, whose product is below what float32 holds: nearly equal weights."""
+    """scale 2^k_exp and the queries' own factor, whose product is below or one of which is above what float32 holds: nearly
+    equal weights, and scores of order one."""
     pages, bt = _cache(5, 1, d, 1, 5, 45)
     q = (torch.randn(1, 2, 4, d, generator=_gen(46)) * size).to(DT[dtype])
     _check(q, pages, bt, 270, scale, dtype, k_exp)
@@ -86,3 +87,12 @@ def test_rows_of_different_sizes_in_one_tile(dtype, d, T, near):
     q = (torch.randn(1, T, nq, d, generator=_gen(42)) * torch.exp2(size.float())).to(DT[dtype])
     for e in (0, 4, -4) if near else (0, 40, -40):
         _check(q, pages, bt, 300, d ** -0.5 * 2.0 ** -e, dtype)
+
+
+@pytest.mark.parametrize("size,scale", [(2.0 ** 125, 2.0 ** -128), (2.0 ** 116, 2.0 ** -119), (2.0 ** -125, 2.0 ** 122)])
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_queries_at_the_ends_of_float32(dtype, d, size, scale):
+    pages, bt = _cache(5, 1, d, 1, 5, 43)
+    q = (torch.randn(1, 2, 4, d, generator=_gen(44)) * size).to(DT[dtype])
+    assert bool(torch.isfinite(q).all()) and bool((q != 0).any(-1).all())
+    _check(q, pages, bt, 270, scale, dtype)
