@@ -37,6 +37,8 @@ namespace {
 constexpr int kGroups = 64;  // groups of threads behind the floor
 constexpr int kList = 512;   // listed places, and listed elements, at most
 constexpr int kMaxCluster = 8;
+constexpr int kStatic = 13 * 1024;                     // the kernel's own shared memory is below this
+constexpr int kMaxDynamic = 227 * 1024 - kStatic;
 
 struct LpArgs {
   int V, n_top;
@@ -605,14 +607,14 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
   // Residency: as many CTAs an SM as the rows come to (at most 5), no more: with room for more the rows are spread unevenly
   // (456 rows, three an SM, took as long as 608). What shared memory that leaves holds stages.
   const int res = (int)std::min(5LL, std::max(1LL, ((long long)C * g->rows + device_sms() - 1) / device_sms()));
-  const int budget = 228 * 1024 / res - 1024 - 13 * 1024;  // the kernel's own shared memory is below 13 KB
+  const int budget = 228 * 1024 / res - 1024 - kStatic;
   const int stage_bytes = wide ? Ring<512>::BYTES : Ring<256>::BYTES;
   const int stages = std::min(budget / stage_bytes, (int)Ring<256>::MAX_STAGES);
   const int smem = budget / 1024 * 1024;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C * g->rows);
   cfg.blockDim = dim3(wide ? 512 : 256);
-  cfg.dynamicSmemBytes = (size_t)std::min(smem, 227 * 1024 - 13 * 1024);
+  cfg.dynamicSmemBytes = (size_t)std::min(smem, kMaxDynamic);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -623,7 +625,8 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  // always the same: the attribute is the process's, and another thread may launch between the two calls
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, fn, a, C, stages);
   return launch_status(e);
 }
