@@ -22,7 +22,8 @@
 // reaches the floor have all their elements read again, each warp keeps its best 32 and these are merged.
 // (512 bf16 rows of 151,936, n_top 20: reading all elements of the owning threads again costs 12 to 20 us of 55, listing single
 // elements as they pass 28.)
-// Bound: issue slots for many rows (the 512: 47 us, half of the copy rate of HBM; 2,048 of them 167 us, 56%), a dependent chain of
+// Bound: for many rows the slots of the SMs whose last row runs alone (512 rows, 3.4 an SM, take 47 us, half of the copy rate of HBM; 608, four an
+// SM, 48 us; 2,048 138 us, 68%, with two stages a CTA, 167 us with one) and their issue slots, 60% used; a dependent chain of
 // loads, cluster joins and places for a few (8 f32 rows: 11 us).
 #include <math.h>
 
@@ -37,8 +38,6 @@ namespace {
 constexpr int kGroups = 64;  // groups of threads behind the floor
 constexpr int kList = 512;   // listed places, and listed elements, at most
 constexpr int kMaxCluster = 8;
-constexpr int kStatic = 13 * 1024;                     // the kernel's own shared memory is below this
-constexpr int kMaxDynamic = 227 * 1024 - kStatic;
 
 struct LpArgs {
   int V, n_top;
@@ -303,26 +302,46 @@ __device__ __forceinline__ void st_cluster_u64(uint64_t* local, uint32_t rank, u
 template <int NT>
 struct Ring {
   static constexpr int PIECES = 4 * NT, BYTES = PIECES * 16, MAX_STAGES = 8;
-  static constexpr int smem(int stages) { return stages * BYTES; }
 };
+
+// The kernel's shared memory but for the ring
+template <int NT>
+struct Shared {
+  uint64_t full[Ring<NT>::MAX_STAGES], empty[Ring<NT>::MAX_STAGES];
+  uint64_t list[kList], cand[kList];  // places, and elements, that reach the floor
+  uint64_t result[32];                // this CTA's alternatives
+  // of rank 0: what the CTAs of the cluster send
+  uint64_t gather_key[kMaxCluster * 32];
+  Stat gather_stat[kMaxCluster];
+  Stat stats[NT / 32];
+  float group_max[kGroups];
+  uint16_t owner[NT];
+  int n_owner, n_list, n_cand;
+  float s_floor, s_ref;
+};
+constexpr int kSmSmem = 228 * 1024, kCtaSmem = 227 * 1024;  // of an SM, of which a resident CTA takes 1 KB for itself; at most of a CTA
+constexpr int kMostCtas = 5;                                // an SM
+// Dynamic shared memory of a CTA when `res` are to be resident
+template <int NT>
+constexpr int dynamic_smem(int res) {
+  constexpr int own = (int)(sizeof(Shared<NT>) + 127) / 128 * 128;
+  const int left = kSmSmem / res - 1024 - own, most = kCtaSmem - own;
+  return (left < most ? left : most) / 1024 * 1024;
+}
+static_assert(dynamic_smem<256>(kMostCtas) >= 2 * Ring<256>::BYTES, "copies are under way while a stage is read");
 
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT) token_logprobs_kernel(LpArgs a, int C, int stages) {
   using R = Ring<NT>;
   constexpr int E = 16 / sizeof(T), NW = NT / 32, GS = NT / kGroups;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(8) uint64_t full[R::MAX_STAGES], empty[R::MAX_STAGES];
   static_assert(kList >= NT, "the merges' lists share the list's memory");
-  __shared__ uint64_t list[kList], cand[kList];  // places, and elements, that reach the floor
-  __shared__ float group_max[kGroups];
-  __shared__ uint64_t result[32];        // this CTA's alternatives
-  __shared__ Stat stats[NW];
-  // of rank 0: what the CTAs of the cluster send
-  __shared__ uint64_t gather_key[kMaxCluster * 32];
-  __shared__ __align__(16) Stat gather_stat[kMaxCluster];
-  __shared__ uint16_t owner[NT];
-  __shared__ int n_owner, n_list, n_cand;
-  __shared__ float s_floor, s_ref;
+  __shared__ __align__(16) Shared<NT> sh;
+  auto& full = sh.full; auto& empty = sh.empty; auto& list = sh.list; auto& cand = sh.cand; auto& result = sh.result;
+  auto& gather_key = sh.gather_key; auto& gather_stat = sh.gather_stat; auto& stats = sh.stats;
+  auto& group_max = sh.group_max; auto& owner = sh.owner;
+  int &n_owner = sh.n_owner, &n_list = sh.n_list, &n_cand = sh.n_cand;
+  float &s_floor = sh.s_floor, &s_ref = sh.s_ref;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -606,15 +625,13 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
                                                        : (wide ? token_logprobs_kernel<bf16, 512> : token_logprobs_kernel<bf16, 256>);
   // Residency: as many CTAs an SM as the rows come to (at most 5), no more: with room for more the rows are spread unevenly
   // (456 rows, three an SM, took as long as 608). What shared memory that leaves holds stages.
-  const int res = (int)std::min(5LL, std::max(1LL, ((long long)C * g->rows + device_sms() - 1) / device_sms()));
-  const int budget = 228 * 1024 / res - 1024 - kStatic;
-  const int stage_bytes = wide ? Ring<512>::BYTES : Ring<256>::BYTES;
-  const int stages = std::min(budget / stage_bytes, (int)Ring<256>::MAX_STAGES);
-  const int smem = budget / 1024 * 1024;
+  const int res = (int)std::min<long long>(kMostCtas, std::max(1LL, ((long long)C * g->rows + device_sms() - 1) / device_sms()));
+  const int smem = wide ? dynamic_smem<512>(res) : dynamic_smem<256>(res);
+  const int stages = std::min(smem / (wide ? Ring<512>::BYTES : Ring<256>::BYTES), (int)Ring<256>::MAX_STAGES);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C * g->rows);
   cfg.blockDim = dim3(wide ? 512 : 256);
-  cfg.dynamicSmemBytes = (size_t)std::min(smem, kMaxDynamic);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -626,7 +643,8 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 2 : 1;
   // always the same: the attribute is the process's, and another thread may launch between the two calls
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       wide ? dynamic_smem<512>(1) : dynamic_smem<256>(1));
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, fn, a, C, stages);
   return launch_status(e);
 }
