@@ -294,6 +294,13 @@ def _dtype(t, what):
     return code
 
 
+def _int(v, what):
+    """v, if a C int holds it (ctypes would keep its low 32 bits)."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{what}: {v} is outside 32 bits")
+    return v
+
+
 def _here(stream, *tensors):
     """(pointer, stream or None) of the stream to launch on: None for the current one. Every tensor
     has to be on the current CUDA device."""
@@ -325,6 +332,7 @@ def _row_stride(t, what):
     if t.dim() != 4:
         raise ValueError(f"{what}: [B, T, heads, d_h] expected, got {list(t.shape)}")
     B, T, H, d = t.shape
+    _int(max(t.shape), what)
     sb, st, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (H > 1 and sh != d):
         raise ValueError(f"{what}: the heads of a row have to be dense")
@@ -352,10 +360,11 @@ def rope_table(n_pos, rot, theta=1e6, scaling="plain", factor=1.0, orig_len=0.0,
     lib = load()
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling: one of {sorted(ROPE_SCALINGS)} expected")
+    n_pos, rot = _int(int(n_pos), "n_pos"), _int(int(rot), "rot")
     ptr, s = _here(stream)
-    table = _new(s, (max(int(n_pos), 0), max(int(rot), 0) // 2, 2), torch.float32)
-    cfg = RopeConfig(int(rot), ROPE_SCALINGS[scaling], theta, factor, orig_len, beta_fast, beta_slow, attn_factor)
-    _check(lib.dlite_rope_table(ctypes.byref(cfg), int(n_pos), table.data_ptr() or None, ptr), "dlite_rope_table")
+    table = _new(s, (max(n_pos, 0), max(rot, 0) // 2, 2), torch.float32)
+    cfg = RopeConfig(rot, ROPE_SCALINGS[scaling], theta, factor, orig_len, beta_fast, beta_slow, attn_factor)
+    _check(lib.dlite_rope_table(ctypes.byref(cfg), n_pos, table.data_ptr() or None, ptr), "dlite_rope_table")
     return table
 
 
@@ -365,7 +374,7 @@ def _table(table, layout):
         raise ValueError(f"layout: one of {sorted(ROPE_LAYOUTS)} expected")
     if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
         raise ValueError("table: contiguous float32 [n_pos, rot / 2, 2] expected")
-    return 2 * table.shape[1], ROPE_LAYOUTS[layout], table.shape[0]
+    return _int(2 * table.shape[1], "table"), ROPE_LAYOUTS[layout], _int(table.shape[0], "table")
 
 
 def rope(x, pos, table, layout="half", n_rows=None, out=None, status=None, stream=None):
@@ -403,7 +412,8 @@ def _kv_desc(pages, block_table, B, k_exp, v_exp):
     if block_table.dim() != 2:
         raise ValueError("block_table: int32 [B, max_pages] expected")
     bt = _vec(block_table, torch.int32, (B, block_table.shape[1]), "block_table")
-    return KvCacheDesc(pages.data_ptr(), bt, n_pages, n_kv, rec // 72, block_table.shape[1], k_exp, v_exp)
+    return KvCacheDesc(pages.data_ptr(), bt, _int(n_pages, "pages"), _int(n_kv, "pages"), _int(rec // 72, "pages"),
+                       _int(block_table.shape[1], "block_table"), _int(k_exp, "k_exp"), _int(v_exp, "v_exp"))
 
 
 def kv_append(pages, block_table, k, v, pos, table=None, layout="half", n_rows=None, k_exp=0, v_exp=0, status=None, stream=None):
@@ -433,7 +443,7 @@ def kv_read(pages, block_table, pos, T, n_rows=None, k_exp=0, v_exp=0, dtype=tor
         raise ValueError("k_out and v_out: both or neither expected")
     B = block_table.shape[0]
     desc = _kv_desc(pages, block_table, B, k_exp, v_exp)
-    shape = (B, T, desc.n_kv, desc.d_h)
+    shape = (B, _int(T, "T"), desc.n_kv, desc.d_h)
     if k_out is None:
         k_out, v_out = (_new(s, shape, dtype, zero=True) for _ in range(2))
     elif tuple(k_out.shape) != shape or tuple(v_out.shape) != shape or v_out.dtype != k_out.dtype:
@@ -465,7 +475,7 @@ def kv_attention(q, pages, block_table, pos, scale=None, window=0, n_rows=None, 
         raise ValueError("out: q's shape and type expected")
     if lse is True:
         lse = _new(s, (B, T, H), torch.float32, zero=n_rows is not None)
-    a = KvAttentionArgs(desc, B, T, H, _dtype(q, "q"), window, d ** -0.5 if scale is None else scale, q.data_ptr(), qs,
+    a = KvAttentionArgs(desc, B, T, H, _dtype(q, "q"), _int(window, "window"), d ** -0.5 if scale is None else scale, q.data_ptr(), qs,
                         out.data_ptr(), _row_stride(out, "out"), _vec(lse, torch.float32, (B, T, H), "lse"),
                         _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"), None, 0,
                         _vec(status, torch.int32, (1,), "status"))
@@ -482,6 +492,8 @@ def kv_attention(q, pages, block_table, pos, scale=None, window=0, n_rows=None, 
 
 def kv_attention_workspace(B, T, n_q, n_kv, d_h, max_pages, dtype=torch.bfloat16):
     """Bytes of workspace a kv_attention call of these sizes needs on the current device (0: none)."""
+    for n, what in ((B, "B"), (T, "T"), (n_q, "n_q"), (n_kv, "n_kv"), (d_h, "d_h"), (max_pages, "max_pages")):
+        _int(n, what)
     a = KvAttentionArgs(KvCacheDesc(16, 16, 1, n_kv, d_h, max_pages, 0, 0), B, T, n_q, _DTYPES[dtype], 0, 1.0, 16, n_q * d_h,
                         16, n_q * d_h, None, 16, None, None, 0, None)
     return load().dlite_kv_attention_workspace(ctypes.byref(a))
@@ -509,7 +521,7 @@ def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entro
             elif st != span:
                 raise ValueError("logits: rows have to be evenly spaced")
             span = st * n
-    n_top = int(n_top)
+    n_top = _int(int(n_top), "n_top")
     at = lead + (max(n_top, 0),)
     outs = []
     for name, t, shape, dt in (("logprob", logprob, lead, torch.float32), ("entropy", entropy, lead, torch.float32),
@@ -519,7 +531,7 @@ def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entro
         else:
             _vec(t, dt, shape, name)
         outs.append(t)
-    a = LogprobsArgs(rows, V, n_top, _dtype(logits, "logits"), temperature, logits.data_ptr(), stride,
+    a = LogprobsArgs(_int(rows, "logits"), _int(V, "logits"), n_top, _dtype(logits, "logits"), temperature, logits.data_ptr(), stride,
                      _vec(tokens, torch.int32, lead, "tokens"), *(t.data_ptr() for t in outs), _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_token_logprobs(ctypes.byref(a), ptr), "dlite_token_logprobs")
     return dict(logprob=outs[0], entropy=outs[1], top_ids=outs[2], top_logprobs=outs[3])
