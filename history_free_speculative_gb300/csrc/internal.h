@@ -26,6 +26,12 @@ inline int device_sms() {
   return n;
 }
 
+// Whether every pointer (NULL among them) is aligned to 4 bytes
+template <typename... P>
+inline bool aligned4(const P*... p) {
+  return ((0 | ... | (uintptr_t)p) & 3) == 0;
+}
+
 // Status code of a launch; an error is kept for dlite_last_cuda_error (api.cu).
 int launch_status(cudaError_t e);
 

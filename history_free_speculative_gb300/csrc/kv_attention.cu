@@ -541,7 +541,7 @@ kv::AttnPlan make_plan(const dlite_kv_attention_args& g) {
 int check_attention(const dlite_kv_attention_args* g) {
   if (!g || !g->q || !g->out) return DLITE_ERR_INVALID_ARG;
   const dlite_kv_cache& c = g->cache;
-  if (const int rc = kv::check_cache(c, g->B, g->T, g->pos)) return rc;
+  if (const int rc = kv::check_cache(c, g->B, g->T, g->pos, g->n_rows, g->status)) return rc;
   if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
   if (g->n_q < 1 || g->n_q % c.n_kv || g->window < 0 || !(g->scale > 0.f) || isinf(g->scale)) return DLITE_ERR_INVALID_ARG;
   const int es = g->dtype == DLITE_F32 ? 4 : 2;

@@ -336,7 +336,7 @@ extern "C" int dlite_kv_append(const dlite_kv_append_args* g, dlite_stream_t str
   using namespace dlite;
   if (!g || !g->k || !g->v) return DLITE_ERR_INVALID_ARG;
   const dlite_kv_cache& c = g->cache;
-  if (const int rc = kv::check_cache(c, g->B, g->T, g->pos)) return rc;
+  if (const int rc = kv::check_cache(c, g->B, g->T, g->pos, g->n_rows, g->status)) return rc;
   if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
   const int es = g->dtype == DLITE_F32 ? 4 : 2;
   const long long cols = (long long)c.n_kv * c.d_h;
@@ -386,7 +386,7 @@ extern "C" int dlite_kv_read(const dlite_kv_read_args* g, dlite_stream_t stream)
   using namespace dlite;
   if (!g || !g->k_out || !g->v_out) return DLITE_ERR_INVALID_ARG;
   const dlite_kv_cache& c = g->cache;
-  if (const int rc = kv::check_cache(c, g->B, g->T, g->pos)) return rc;
+  if (const int rc = kv::check_cache(c, g->B, g->T, g->pos, g->n_rows, g->status)) return rc;
   if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
   const int es = g->dtype == DLITE_F32 ? 4 : 2, V = 16 / es;
   const long long cols = (long long)c.n_kv * c.d_h;

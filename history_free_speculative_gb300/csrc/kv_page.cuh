@@ -111,9 +111,9 @@ __device__ __forceinline__ bool quantise16(float (&v)[16], float inv_exp, uint2&
 }
 
 // Host checks shared by the cache's calls.
-inline int check_cache(const dlite_kv_cache& c, int B, int T, const int64_t* pos) {
+inline int check_cache(const dlite_kv_cache& c, int B, int T, const int64_t* pos, const int32_t* n_rows, const int* status) {
   if (!c.pages || !c.block_table || !pos) return DLITE_ERR_INVALID_ARG;
-  if (((uintptr_t)c.pages & 15) || ((uintptr_t)c.block_table & 3) || ((uintptr_t)pos & 7)) return DLITE_ERR_INVALID_ARG;
+  if (((uintptr_t)c.pages & 15) || ((uintptr_t)pos & 7) || !aligned4(c.block_table, n_rows, status)) return DLITE_ERR_INVALID_ARG;
   if (B < 1 || T < 1 || c.n_pages < 1 || c.n_kv < 1 || c.max_pages < 1) return DLITE_ERR_INVALID_ARG;
   if (c.k_exp < -64 || c.k_exp > 64 || c.v_exp < -64 || c.v_exp > 64) return DLITE_ERR_INVALID_ARG;
   if ((c.d_h != 64 && c.d_h != 128) || c.n_kv > 32767 || B > 65535 || c.max_pages >= (1 << 25) || T >= (1 << 30))

@@ -197,7 +197,9 @@ extern "C" int dlite_rope(const dlite_rope_args* g, dlite_stream_t stream) {
   if (g->x_stride < cols || g->out_stride < cols) return DLITE_ERR_INVALID_ARG;
   if (g->out == g->x && g->out_stride != g->x_stride) return DLITE_ERR_INVALID_ARG;
   const int es = g->dtype == DLITE_F32 ? 4 : 2, V = 16 / es;
-  if (((uintptr_t)g->x | (uintptr_t)g->out) % es || (uintptr_t)g->pos % 8 || (uintptr_t)g->table % 8) return DLITE_ERR_INVALID_ARG;
+  if (((uintptr_t)g->x | (uintptr_t)g->out) % es || (uintptr_t)g->pos % 8 || (uintptr_t)g->table % 8 ||
+      !dlite::aligned4(g->n_rows, g->status))
+    return DLITE_ERR_INVALID_ARG;
   const bool inter = g->layout == DLITE_ROPE_INTERLEAVED;
   // 16-byte accesses need every item to start on 16 bytes: rows, heads, the rotated part and (half layout) its half
   const bool vec = !(((uintptr_t)g->x | (uintptr_t)g->out) & 15) && g->x_stride % V == 0 && g->out_stride % V == 0 &&

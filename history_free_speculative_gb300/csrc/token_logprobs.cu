@@ -599,7 +599,9 @@ extern "C" int dlite_token_logprobs(const dlite_logprobs_args* g, dlite_stream_t
   if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
   if (!(g->temperature > 0.f) || isinf(g->temperature)) return DLITE_ERR_INVALID_ARG;
   if (g->n_top && (!g->top_ids || !g->top_logprobs)) return DLITE_ERR_INVALID_ARG;
-  if ((uintptr_t)g->logits % (g->dtype == DLITE_F32 ? 4 : 2)) return DLITE_ERR_INVALID_ARG;
+  if ((uintptr_t)g->logits % (g->dtype == DLITE_F32 ? 4 : 2) ||
+      !aligned4(g->tokens, g->logprob, g->entropy, g->top_ids, g->top_logprobs, g->status))
+    return DLITE_ERR_INVALID_ARG;
   if (g->n_top > DLITE_MAX_TOP || g->rows > (1 << 27) || g->V > (1 << 30)) return DLITE_ERR_UNSUPPORTED_SHAPE;
   LpArgs a = {};
   a.V = g->V;
