@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const Attn
           *reinterpret_cast<float2*>(dst + dt * 8) = make_float2(o[mt][dt][2 * e] * f, o[mt][dt][2 * e + 1] * f);
       }
     __syncthreads();
-    const bool whole = pc.u0 == 0 && pc.u1 == pc.nu;
+    const bool whole = pc.whole();
     for (int u = tid; u < R * (DH / 4); u += 32 * kWarps) {
       const int r = u / (DH / 4), d = (u % (DH / 4)) * 4;
       if (t.r0 + r >= t.r1) break;

@@ -95,6 +95,7 @@ __device__ __forceinline__ int units_of(const Tile& t, int unit) {
 struct Piece {
   int j, h;        // row tile of all requests (b row_tiles + rt), KV head
   int u0, u1, nu;  // units [u0, u1) of the segment's nu
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == nu; }
 };
 
 // prefix [row tiles + 1]: units of the row tiles before (of one KV head), with those of the changes. All threads of the CTA; ends with a barrier.
@@ -188,7 +189,7 @@ struct Pieces {
   }
   // What the join kernel has to know of this CTA: p is its last piece (if any).
   __device__ __forceinline__ int2 join_of(bool any, const Piece& p) const {
-    if (!any || p.u0 || p.u1 == p.nu) return make_int2(0, 0);
+    if (!any || p.u0 || p.whole()) return make_int2(0, 0);
     const uint32_t last = (uint32_t)prefix[p.j] * a.n_kv + (uint32_t)(p.h + 1) * (p.nu + a.change) - 1;
     return make_int2(p.j * a.n_kv + p.h, (int)(last / quota) - (int)blockIdx.x + 1);
   }
@@ -199,7 +200,6 @@ struct PieceTile {
   Piece p;
   Tile t;
   int b, rt;
-  __device__ __forceinline__ bool whole() const { return p.u0 == 0 && p.u1 == p.nu; }
 };
 constexpr int kBatch = 32;
 // Row of the workspace of this CTA's piece p (not its whole segment)

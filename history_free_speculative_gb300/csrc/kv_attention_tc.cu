@@ -310,454 +310,454 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (!batch) break;
-  if (warp < 4) {  // ---------------------------------------------------------------- keys
-    const int page = warp >> 1, row = 32 * (warp & 1) + lane;  // key 32 warp + lane of the tile
+    if (warp < 4) {  // ---------------------------------------------------------------- keys
+      const int page = warp >> 1, row = 32 * (warp & 1) + lane;  // key 32 warp + lane of the tile
 #pragma unroll 1
-    for (int k = 0; k < batch; ++k) {
-      const Piece pc = list[k].p;
+      for (int k = 0; k < batch; ++k) {
+        const Piece pc = list[k].p;
 #pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int buf = it & 1, st = it % kStages;
-        wait_turn(full(st), it / kStages);
-        wait_left(bar(kFree, buf), it >> 1);
-        tc::fence_after();
-        const uint8_t* stage = sm + st * TILE;
-        const uint8_t* rec = stage + page * REC;
-        const uint2 sc = *reinterpret_cast<const uint2*>(rec + chunk(ks_off(DH) / 16 + (row >> 1)) + 8 * (row & 1));
+        for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+          const int buf = it & 1, st = it % kStages;
+          wait_turn(full(st), it / kStages);
+          wait_left(bar(kFree, buf), it >> 1);
+          tc::fence_after();
+          const uint8_t* stage = sm + st * TILE;
+          const uint8_t* rec = stage + page * REC;
+          const uint2 sc = *reinterpret_cast<const uint2*>(rec + chunk(ks_off(DH) / 16 + (row >> 1)) + 8 * (row & 1));
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[32];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t r[32];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint4 w = *reinterpret_cast<const uint4*>(rec + chunk(4 * row + 2 * half + q));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            const uint32_t s2 = fp8x2_to_f16x2((uint16_t)((half ? sc.y : sc.x) >> (16 * q)));
-            const uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
+            for (int q = 0; q < 2; ++q) {
+              const uint4 w = *reinterpret_cast<const uint4*>(rec + chunk(4 * row + 2 * half + q));
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+              const uint32_t s2 = fp8x2_to_f16x2((uint16_t)((half ? sc.y : sc.x) >> (16 * q)));
+              const uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t s = i < 2 ? s0 : s1;
-              r[16 * q + 4 * i] = mul_f16x2(fp4x2_of<0>(ww[i]), s);
-              r[16 * q + 4 * i + 1] = mul_f16x2(fp4x2_of<1>(ww[i]), s);
-              r[16 * q + 4 * i + 2] = mul_f16x2(fp4x2_of<2>(ww[i]), s);
-              r[16 * q + 4 * i + 3] = mul_f16x2(fp4x2_of<3>(ww[i]), s);
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t s = i < 2 ? s0 : s1;
+                r[16 * q + 4 * i] = mul_f16x2(fp4x2_of<0>(ww[i]), s);
+                r[16 * q + 4 * i + 1] = mul_f16x2(fp4x2_of<1>(ww[i]), s);
+                r[16 * q + 4 * i + 2] = mul_f16x2(fp4x2_of<2>(ww[i]), s);
+                r[16 * q + 4 * i + 3] = mul_f16x2(fp4x2_of<3>(ww[i]), s);
+              }
             }
+            tmem_st32(tm + ((uint32_t)(32 * warp) << 16) + kTmK + 64 * buf + 32 * half, r);
           }
-          tmem_st32(tm + ((uint32_t)(32 * warp) << 16) + kTmK + 64 * buf + 32 * half, r);
+          if (lane == 0) tc::mbar_arrive(empty(st));
+          __syncwarp();
+          tmem_wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(kReady, buf));
         }
-        if (lane == 0) tc::mbar_arrive(empty(st));
-        __syncwarp();
-        tmem_wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(kReady, buf));
       }
-    }
-  } else if (warp < 8) {  // ---------------------------------------------------------------- values
-    const int d = 32 * (warp - 4) + lane;
+    } else if (warp < 8) {  // ---------------------------------------------------------------- values
+      const int d = 32 * (warp - 4) + lane;
 #pragma unroll 1
-    for (int k = 0; k < batch; ++k) {
-      const Piece pc = list[k].p;
+      for (int k = 0; k < batch; ++k) {
+        const Piece pc = list[k].p;
 #pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int buf = it & 1, st = it % kStages;
-        wait_turn(c_ready(it), it / kRing);  // and the stage with them
-        wait_left(bar(vFree, buf), it >> 1);
-        tc::fence_after();
+        for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+          const int buf = it & 1, st = it % kStages;
+          wait_turn(c_ready(it), it / kRing);  // and the stage with them
+          wait_left(bar(vFree, buf), it >> 1);
+          tc::fence_after();
 #pragma unroll
-        for (int page = 0; page < 2; ++page) {
-          const uint8_t* rec = sm + st * TILE + page * REC;
-          const uint8_t* sp = sm + S::VS + st * 2048 + (d >> 4) * 256 + page * 128;
-          uint32_t r[32];
+          for (int page = 0; page < 2; ++page) {
+            const uint8_t* rec = sm + st * TILE + page * REC;
+            const uint8_t* sp = sm + S::VS + st * 2048 + (d >> 4) * 256 + page * 128;
+            uint32_t r[32];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {  // 32 tokens
-            const uint4 w = *reinterpret_cast<const uint4*>(rec + chunk(v_off(DH) / 16 + 2 * d + q));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            for (int q = 0; q < 2; ++q) {  // 32 tokens
+              const uint4 w = *reinterpret_cast<const uint4*>(rec + chunk(v_off(DH) / 16 + 2 * d + q));
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 s = *reinterpret_cast<const uint4*>(sp + 64 * q + 16 * i);
-              r[16 * q + 4 * i] = mul_f16x2(fp4x2_of<0>(ww[i]), s.x);
-              r[16 * q + 4 * i + 1] = mul_f16x2(fp4x2_of<1>(ww[i]), s.y);
-              r[16 * q + 4 * i + 2] = mul_f16x2(fp4x2_of<2>(ww[i]), s.z);
-              r[16 * q + 4 * i + 3] = mul_f16x2(fp4x2_of<3>(ww[i]), s.w);
+              for (int i = 0; i < 4; ++i) {
+                const uint4 s = *reinterpret_cast<const uint4*>(sp + 64 * q + 16 * i);
+                r[16 * q + 4 * i] = mul_f16x2(fp4x2_of<0>(ww[i]), s.x);
+                r[16 * q + 4 * i + 1] = mul_f16x2(fp4x2_of<1>(ww[i]), s.y);
+                r[16 * q + 4 * i + 2] = mul_f16x2(fp4x2_of<2>(ww[i]), s.z);
+                r[16 * q + 4 * i + 3] = mul_f16x2(fp4x2_of<3>(ww[i]), s.w);
+              }
             }
+            tmem_st32(tm + ((uint32_t)(32 * (warp - 4)) << 16) + kTmV + 64 * buf + 32 * page, r);
           }
-          tmem_st32(tm + ((uint32_t)(32 * (warp - 4)) << 16) + kTmV + 64 * buf + 32 * page, r);
+          if (lane == 0) tc::mbar_arrive(empty(st));
+          __syncwarp();
+          tmem_wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(vReady, buf));
         }
-        if (lane == 0) tc::mbar_arrive(empty(st));
-        __syncwarp();
-        tmem_wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(vReady, buf));
       }
-    }
-  } else if (warp < 16) {  // ---------------------------------------------------------------- softmax and output
-    const int g = (warp - 8) >> 2, w = warp & 3;
-    const uint32_t lanes = (uint32_t)(32 * w) << 16;
-    uint2 raw_q[N / 8];
-    auto load_q = [&](int k) {  // rows warp - 8, + 8, ... of a piece: every load before the first use
-      const Tile& t = list[k].t;
+    } else if (warp < 16) {  // ---------------------------------------------------------------- softmax and output
+      const int g = (warp - 8) >> 2, w = warp & 3;
+      const uint32_t lanes = (uint32_t)(32 * w) << 16;
+      uint2 raw_q[N / 8];
+      auto load_q = [&](int k) {  // rows warp - 8, + 8, ... of a piece: every load before the first use
+        const Tile& t = list[k].t;
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i) {
-        const int r = t.r0 + min(warp - 8 + 8 * i, t.r1 - t.r0 - 1), tk = r / a.group, hq = list[k].p.h * a.group + r - tk * a.group;
-        const bf16* q = static_cast<const bf16*>(a.q) + ((long long)list[k].b * a.T + tk) * a.qs + (long long)hq * DH + 4 * lane;
-        if (a.vec) {
-          raw_q[i] = *reinterpret_cast<const uint2*>(q);
-        } else {
-          const unsigned short* q16 = reinterpret_cast<const unsigned short*>(q);
-          raw_q[i] = make_uint2(q16[0] | (uint32_t)q16[1] << 16, q16[2] | (uint32_t)q16[3] << 16);
+        for (int i = 0; i < N / 8; ++i) {
+          const int r = t.r0 + min(warp - 8 + 8 * i, t.r1 - t.r0 - 1), tk = r / a.group, hq = list[k].p.h * a.group + r - tk * a.group;
+          const bf16* q = static_cast<const bf16*>(a.q) + ((long long)list[k].b * a.T + tk) * a.qs + (long long)hq * DH + 4 * lane;
+          if (a.vec) {
+            raw_q[i] = *reinterpret_cast<const uint2*>(q);
+          } else {
+            const unsigned short* q16 = reinterpret_cast<const unsigned short*>(q);
+            raw_q[i] = make_uint2(q16[0] | (uint32_t)q16[1] << 16, q16[2] | (uint32_t)q16[3] << 16);
+          }
         }
-      }
-    };
-    load_q(0);
+      };
+      load_q(0);
 #pragma unroll 1
-    for (int k = 0; k < batch; ++k) {
-      const Piece pc = list[k].p;
-      const Tile t = list[k].t;
-      const int b = list[k].b, rt = list[k].rt, h = pc.h, rows = t.r1 - t.r0;
-      if (warp == 8 && lane == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
-        flag_status(a.status, kDevBounds);
-      // Q: all of the last piece's first products are done
-      if (warp == 8 && lane < N) {
-        const int r = t.r0 + lane, tk = r / a.group, hq = h * a.group + r % a.group;
-        const long long row = (long long)b * a.T + tk, seen = t.p0 + tk;
-        row_out[lane] = row * a.os + (long long)hq * DH;
-        row_out[N + lane] = row * a.n_q + hq;
-        row_keys[lane] = lane < rows ? make_int2(a.window ? (int)min(max(seen - a.window + 1, 0LL), t.cap) : 0, (int)min(max(seen + 1, 0LL), t.cap))
-                                     : make_int2(0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < N / 8; ++i) {
-        const int r = warp - 8 + 8 * i;
-        uint2 x = r < rows ? raw_q[i] : make_uint2(0u, 0u);
-        const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                            __uint_as_float(x.y & 0xffff0000u)};
-        bool q_bad = false;
-        float amax = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          amax = fmaxf(amax, fabsf(v[e]));
-          q_bad |= !(fabsf(v[e]) <= 3.402823466e38f);
+      for (int k = 0; k < batch; ++k) {
+        const Piece pc = list[k].p;
+        const Tile t = list[k].t;
+        const int b = list[k].b, rt = list[k].rt, h = pc.h, rows = t.r1 - t.r0;
+        if (warp == 8 && lane == 0 && rt == 0 && pc.u0 == 0 && (t.p0 < 0 || t.p0 + (a.n_rows ? min(a.n_rows[b], a.T) : a.T) > t.cap))
+          flag_status(a.status, kDevBounds);
+        // Q: all of the last piece's first products are done
+        if (warp == 8 && lane < N) {
+          const int r = t.r0 + lane, tk = r / a.group, hq = h * a.group + r % a.group;
+          const long long row = (long long)b * a.T + tk, seen = t.p0 + tk;
+          row_out[lane] = row * a.os + (long long)hq * DH;
+          row_out[N + lane] = row * a.n_q + hq;
+          row_keys[lane] = lane < rows ? make_int2(a.window ? (int)min(max(seen - a.window + 1, 0LL), t.cap) : 0, (int)min(max(seen + 1, 0LL), t.cap))
+                                       : make_int2(0, 0);
         }
-        const bool bad = __any_sync(0xffffffffu, q_bad);
-        amax = warp_max_f32(amax);
-        const RowScale rs = row_scale(a, bad ? 0.f : amax);
-        auto f16x2 = [&](float lo, float hi) { return pack_f16(lo * rs.f0 * rs.f1, hi * rs.f0 * rs.f1); };
-        x = bad ? make_uint2(0u, 0u) : make_uint2(f16x2(v[0], v[1]), f16x2(v[2], v[3]));
-        // columns 4 lane ..: half lane / 16, 16-byte chunk (lane % 16) / 2 of the row, swizzled by the row
-        *reinterpret_cast<uint2*>(sm + S::Q + (lane >> 4) * N * 128 + r * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * (lane & 1)) = x;
-        if (lane == 0) {
-          row_ref(0)[r] = row_ref(1)[r] = bad ? NAN : kNoRef;
-          row_sc[r] = rs.factor;
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(q_ready);
-      softmax_barrier();
-      const uint64_t we2 = pack2f(kTcWeightExp, kTcWeightExp);
-      // tiles wholly inside every row's range need no masks
-      const int full_end = (int)min(max(t.p0 + t.t_lo + 1, 0LL), t.cap);
-      const int full_beg = a.window ? (int)min(max(t.p0 + t.t_hi - a.window + 1, 0LL), t.cap) : 0;
-      const int first = pc.u0 + ((it ^ g) & 1);  // this group's first tile of the piece
-      int last = -1;                             // its last tile so far
-#pragma unroll 1
-      for (int u = first; u < pc.u1; u += 2) {
-        const int i = it + u - pc.u0, turn = i >> 1;
-        wait_turn(bar(sFull, g), turn);
-        tc::fence_after();
-        const int key0 = (t.pg0 + 2 * u) * kPage, key = key0 + 32 * w + lane;
-        wait_turn(c_ready(i), i / kRing);  // long over: for the flags' sake
-        const int came = stage_ok[i % kRing];
-        const bool masked = came != 3 || key0 < full_beg || key0 + 128 > full_end, there = (came >> (w >> 1)) & 1;
-        uint64_t x[N / 2];
-        auto scores = [&]() {  // -inf where the row does not see this thread's key
-          float s[N];
-          tmem_ld<N>(tm + lanes + kTmS + N * g, s);
-          if (masked) {
 #pragma unroll
-            for (int r = 0; r < N; ++r) {
-              const int2 see = row_keys[r];
-              if (!there || key < see.x || key >= see.y) s[r] = -INFINITY;
-            }
+        for (int i = 0; i < N / 8; ++i) {
+          const int r = warp - 8 + 8 * i;
+          uint2 x = r < rows ? raw_q[i] : make_uint2(0u, 0u);
+          const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                              __uint_as_float(x.y & 0xffff0000u)};
+          bool q_bad = false;
+          float amax = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            amax = fmaxf(amax, fabsf(v[e]));
+            q_bad |= !(fabsf(v[e]) <= 3.402823466e38f);
           }
-#pragma unroll
-          for (int r = 0; r < N / 2; ++r) x[r] = pack2f(s[2 * r], s[2 * r + 1]);
-        };
-        auto exponents = [&]() {
-          float top = -INFINITY;
-#pragma unroll
-          for (int r = 0; r < N / 2; r += 2) {
-            const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(row_ref(g) + 2 * r);
-            const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(row_sc + 2 * r);
-            x[r] = fma2(sub2(x[r], ref.x), sc.x, we2);
-            x[r + 1] = fma2(sub2(x[r + 1], ref.y), sc.y, we2);
-            top = fmaxf(top, fmaxf(fmaxf(lo2f(x[r]), hi2f(x[r])), fmaxf(lo2f(x[r + 1]), hi2f(x[r + 1]))));
+          const bool bad = __any_sync(0xffffffffu, q_bad);
+          amax = warp_max_f32(amax);
+          const RowScale rs = row_scale(a, bad ? 0.f : amax);
+          auto f16x2 = [&](float lo, float hi) { return pack_f16(lo * rs.f0 * rs.f1, hi * rs.f0 * rs.f1); };
+          x = bad ? make_uint2(0u, 0u) : make_uint2(f16x2(v[0], v[1]), f16x2(v[2], v[3]));
+          // columns 4 lane ..: half lane / 16, 16-byte chunk (lane % 16) / 2 of the row, swizzled by the row
+          *reinterpret_cast<uint2*>(sm + S::Q + (lane >> 4) * N * 128 + r * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * (lane & 1)) = x;
+          if (lane == 0) {
+            row_ref(0)[r] = row_ref(1)[r] = bad ? NAN : kNoRef;
+            row_sc[r] = rs.factor;
           }
-          return top;
-        };
-        scores();
-        const bool first_tile = last < 0;  // its references are new in any case
-        if (!first_tile && exponents() > kTcWeightExp + 8.f) move_ref[g] = 1;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(voted(g));
-        if (!first_tile) {
-#pragma unroll
-          for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
-          wait_turn(voted(g), turn);
-        }
-        if (first_tile || move_ref[g]) {
-          if (!first_tile) scores();
-          // the exact maxima of the tile
-#pragma unroll
-          for (int r = 0; r < N; ++r) {
-            const float mx = warp_max_f32(r & 1 ? hi2f(x[r / 2]) : lo2f(x[r / 2]));
-            if (lane == r) row_red(g)[w * N + r] = mx;
-          }
-          group_barrier(g);
-          if (w == 0 && lane < N) {
-            const float* red = row_red(g);
-            const float mx = fmaxf(fmaxf(red[lane], red[N + lane]), fmaxf(red[2 * N + lane], red[3 * N + lane]));
-            const float ref = row_ref(g)[lane];
-            row_alpha(g)[lane] = mx > ref ? tc::ex2_approx((ref - mx) * row_sc[lane]) : 1.f;
-            if (mx > ref) row_ref(g)[lane] = mx;   // a NaN stays
-            if (lane == 0) move_ref[g] = 0;
-          }
-          group_barrier(g);
-          if (last >= 0) {  // O and L hold the group's tiles before this one
-            wait_turn(bar(vFree, g), last >> 1);
-            tc::fence_after();
-#pragma unroll 1
-            for (int r = 0; r < 2 * N; r += 16) {
-              const uint32_t at = tm + lanes + (r < N ? tmO + N * g + r : tmL + N * g + r - N);
-              float o[16];
-              tmem_ld<16>(at, o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= row_alpha(g)[r % N + e];
-              tmem_store<16>(at, o);
-            }
-            tmem_wait_st();
-          }
-          exponents();
-#pragma unroll
-          for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
-        }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(sFree, g));
-        // P: this key's N weights side by side, once the group's last product has read the buffer
-        wait_left(bar(vFree, g), turn);
-        uint8_t* pp = sm + S::P + g * 128 * N * 2 + (32 * w + lane) * N * 2;
-#pragma unroll
-        for (int q = 0; q < N / 8; ++q) {
-          uint32_t p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = pack_f16(lo2f(x[4 * q + e]), hi2f(x[4 * q + e]));
-          const int sw = N == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1;
-          *reinterpret_cast<uint4*>(pp + ((q ^ sw) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(pReady, g));
-        // this thread's keys' part of every row's sum, from the weights before their rounding
-#pragma unroll
-        for (int r = 0; r < N; r += 16) {
-          const uint32_t at = tm + lanes + tmL + N * g + r;
-          float sum[16];
-          if (!first_tile) {
-            tmem_ld<16>(at, sum);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sum[e] = 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint64_t two = add2(pack2f(sum[2 * e], sum[2 * e + 1]), x[r / 2 + e]);
-            sum[2 * e] = lo2f(two), sum[2 * e + 1] = hi2f(two);
-          }
-          tmem_store<16>(at, sum);
-        }
-        tmem_wait_st();
-        last = i;
-      }
-      it += pc.u1 - pc.u0;
-      if (k + 1 < batch) load_q(k + 1);
-      // the groups' rows joined; thread = column 32 w + lane, group g takes rows g N / 2 ..
-      if (last >= 0) {
-        wait_turn(bar(vFree, g), last >> 1);
-        tc::fence_after();
-        float v[N];
-        tmem_ld<N>(tm + lanes + tmL + N * g, v);
-        const float sum = warp_row_sums<N>(v, lane);
-        if (N == 32 || (lane & 1) == 0) row_l(g)[w * N + (N == 32 ? lane : lane >> 1)] = sum;
-      }
-      tc::fence_before();
-      softmax_barrier();
-      tc::fence_after();
-      const int np = pc.u1 - pc.u0, r_lo = g * (N / 2);
-      // whether a group had a tile: both from two tiles on, else the one whose turn the tile was
-      const bool has0 = np > 1 || ((it - np) & 1) == 0, has1 = np > 1 || ((it - np) & 1) == 1;
-      float L = 0.f, M = 0.f, f0 = 0.f, f1 = 0.f, inv = 0.f;  // of row `lane`
-      const bool whole = pc.u0 == 0 && pc.u1 == pc.nu;
-      if (lane < N) {
-        const float r0 = row_ref(0)[lane], r1 = row_ref(1)[lane], ref = fmaxf(r0, r1), sc = row_sc[lane];
-        M = ref * sc;
-        f0 = has0 ? (r0 == ref ? 1.f : tc::ex2_approx((r0 - ref) * sc)) : 0.f;
-        f1 = has1 ? (r1 == ref ? 1.f : tc::ex2_approx((r1 - ref) * sc)) : 0.f;
-        const float *l0 = row_l(0), *l1 = row_l(1);
-        L = (has0 ? f0 * (l0[lane] + l0[N + lane] + l0[2 * N + lane] + l0[3 * N + lane]) : 0.f) +
-            (has1 ? f1 * (l1[lane] + l1[N + lane] + l1[2 * N + lane] + l1[3 * N + lane]) : 0.f);
-        inv = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
-        if (w == 0 && lane >= r_lo && lane < min(rows, r_lo + N / 2)) {
-          if (!whole)
-            a.part_ml[part_row(pc, N) + lane] = make_float2(M, L);
-          else if (a.lse)
-            a.lse[row_out[N + lane]] = lse_of(M, L, kTcWeightExp);
-        }
-      }
-      float o0[N / 2], o1[N / 2];
-#pragma unroll
-      for (int r = 0; r < N / 2; ++r) o0[r] = o1[r] = 0.f;
-      if (has0) tmem_ld_part<N / 2>(tm + lanes + tmO + r_lo, o0);
-      if (has1) tmem_ld_part<N / 2>(tm + lanes + tmO + N + r_lo, o1);
-      tc::fence_before();
-      const int d = 32 * w + lane;
-#pragma unroll
-      for (int r = 0; r < N / 2; ++r) {
-        const float e0 = __shfl_sync(0xffffffffu, f0 * inv, r_lo + r), e1 = __shfl_sync(0xffffffffu, f1 * inv, r_lo + r);
-        if (r_lo + r >= rows) continue;
-        const float v = fmaf(o0[r], e0, o1[r] * e1);
-        if (whole)
-          static_cast<bf16*>(a.out)[row_out[r_lo + r] + d] = __float2bfloat16_rn(v);
-        else
-          a.part_o[(part_row(pc, N) + r_lo + r) * DH + d] = v;
-      }
-      softmax_barrier();  // both O, row_l, row_ref are the next piece's
-    }
-  } else if (warp == 16) {  // ---------------------------------------------------------------- value scales
-    // as f16, once for the 16 columns that share them: lane = block of 16 columns lane / 4, 32 tokens
-    const int blk = lane >> 2, tok = (lane & 3) * 32;
+        if (lane == 0) tc::mbar_arrive(q_ready);
+        softmax_barrier();
+        const uint64_t we2 = pack2f(kTcWeightExp, kTcWeightExp);
+        // tiles wholly inside every row's range need no masks
+        const int full_end = (int)min(max(t.p0 + t.t_lo + 1, 0LL), t.cap);
+        const int full_beg = a.window ? (int)min(max(t.p0 + t.t_hi - a.window + 1, 0LL), t.cap) : 0;
+        const int first = pc.u0 + ((it ^ g) & 1);  // this group's first tile of the piece
+        int last = -1;                             // its last tile so far
 #pragma unroll 1
-    for (int k = 0; k < batch; ++k) {
-      const Piece pc = list[k].p;
-      const int key_end = list[k].t.key_end, pg0 = list[k].t.pg0;
-#pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int st = it % kStages;
-        wait_turn(full(st), it / kStages);
-        // keys past the end, or of a page that is not there, hold anything, a NaN scale too: their values are 0
-        const int came = stage_ok[it % kRing], left = key_end - (pg0 + 2 * u) * kPage;
-        const int valid = came == 3 && left >= 128 ? 32 : (came >> (tok >> 6) & 1) ? left - tok : 0;
+        for (int u = first; u < pc.u1; u += 2) {
+          const int i = it + u - pc.u0, turn = i >> 1;
+          wait_turn(bar(sFull, g), turn);
+          tc::fence_after();
+          const int key0 = (t.pg0 + 2 * u) * kPage, key = key0 + 32 * w + lane;
+          wait_turn(c_ready(i), i / kRing);  // long over: for the flags' sake
+          const int came = stage_ok[i % kRing];
+          const bool masked = came != 3 || key0 < full_beg || key0 + 128 > full_end, there = (came >> (w >> 1)) & 1;
+          uint64_t x[N / 2];
+          auto scores = [&]() {  // -inf where the row does not see this thread's key
+            float s[N];
+            tmem_ld<N>(tm + lanes + kTmS + N * g, s);
+            if (masked) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sm + st * TILE + (tok >> 6) * REC + chunk(vs_off(DH) / 16 + 4 * blk + ((tok & 63) >> 4) + q));
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-          uint32_t s[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s[i] = fp8x2_to_f16x2((uint16_t)(ww[i / 2] >> (16 * (i & 1))));
-            const int at = 16 * q + 2 * i;
-            if (valid < 32) s[i] = at + 1 < valid ? s[i] : at < valid ? s[i] & 0xffffu : 0u;
-          }
-          uint4* to = reinterpret_cast<uint4*>(sm + S::VS + st * 2048 + blk * 256 + tok * 2 + 32 * q);
-          to[0] = make_uint4(s[0], s[1], s[2], s[3]);
-          to[1] = make_uint4(s[4], s[5], s[6], s[7]);
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(c_ready(it));
-      }
-    }
-  } else if (warp == 19) {  // ---------------------------------------------------------------- copies
-    const bool one = elect_one();
-#pragma unroll 1
-    for (int k = 0; k < batch; ++k) {
-      const Piece pc = list[k].p;
-      const Tile t = list[k].t;
-      const int32_t* bt = a.bt + (size_t)list[k].b * a.max_pages + t.pg0;
-      // 32 page ids at a time, the next 32 on their way: with one tile's ids loaded ahead, a load's latency was every tile's
-      const int pages = min(t.np, 2 * pc.u1);
-      auto page_of = [&](int i) { return i < pages ? bt[i] : -1; };
-      int ids = page_of(2 * pc.u0 + lane), next_ids = page_of(2 * pc.u0 + 32 + lane);
-#pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int st = it % kStages;
-        const int at = (2 * (u - pc.u0)) & 31;
-        if (at == 0 && u > pc.u0) {
-          ids = next_ids;
-          next_ids = page_of(2 * u + 32 + lane);
-        }
-        const int id0 = __shfl_sync(0xffffffffu, ids, at), id1 = __shfl_sync(0xffffffffu, ids, at + 1);
-        wait_left(empty(st), it / kStages);
-        const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
-        if (one) {
-          if (id0 >= a.n_pages || id1 >= a.n_pages) flag_status(a.status, kDevBounds);
-          stage_ok[it % kRing] = came;
-          if (came) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            tc::mbar_expect_tx(full(st), (came == 3 ? 2 : 1) * REC);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              if (!(came >> p & 1)) continue;
-              const long long rec = (long long)(p ? id1 : id0) * a.n_kv + pc.h;
-              tma_load_3d(sb + st * TILE + p * REC, &map, full(st), (int)rec);
+              for (int r = 0; r < N; ++r) {
+                const int2 see = row_keys[r];
+                if (!there || key < see.x || key >= see.y) s[r] = -INFINITY;
+              }
             }
-          } else {
-            tc::mbar_arrive(full(st));
+#pragma unroll
+            for (int r = 0; r < N / 2; ++r) x[r] = pack2f(s[2 * r], s[2 * r + 1]);
+          };
+          auto exponents = [&]() {
+            float top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < N / 2; r += 2) {
+              const ulonglong2 ref = *reinterpret_cast<const ulonglong2*>(row_ref(g) + 2 * r);
+              const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(row_sc + 2 * r);
+              x[r] = fma2(sub2(x[r], ref.x), sc.x, we2);
+              x[r + 1] = fma2(sub2(x[r + 1], ref.y), sc.y, we2);
+              top = fmaxf(top, fmaxf(fmaxf(lo2f(x[r]), hi2f(x[r])), fmaxf(lo2f(x[r + 1]), hi2f(x[r + 1]))));
+            }
+            return top;
+          };
+          scores();
+          const bool first_tile = last < 0;  // its references are new in any case
+          if (!first_tile && exponents() > kTcWeightExp + 8.f) move_ref[g] = 1;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(voted(g));
+          if (!first_tile) {
+#pragma unroll
+            for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
+            wait_turn(voted(g), turn);
+          }
+          if (first_tile || move_ref[g]) {
+            if (!first_tile) scores();
+            // the exact maxima of the tile
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+              const float mx = warp_max_f32(r & 1 ? hi2f(x[r / 2]) : lo2f(x[r / 2]));
+              if (lane == r) row_red(g)[w * N + r] = mx;
+            }
+            group_barrier(g);
+            if (w == 0 && lane < N) {
+              const float* red = row_red(g);
+              const float mx = fmaxf(fmaxf(red[lane], red[N + lane]), fmaxf(red[2 * N + lane], red[3 * N + lane]));
+              const float ref = row_ref(g)[lane];
+              row_alpha(g)[lane] = mx > ref ? tc::ex2_approx((ref - mx) * row_sc[lane]) : 1.f;
+              if (mx > ref) row_ref(g)[lane] = mx;   // a NaN stays
+              if (lane == 0) move_ref[g] = 0;
+            }
+            group_barrier(g);
+            if (last >= 0) {  // O and L hold the group's tiles before this one
+              wait_turn(bar(vFree, g), last >> 1);
+              tc::fence_after();
+#pragma unroll 1
+              for (int r = 0; r < 2 * N; r += 16) {
+                const uint32_t at = tm + lanes + (r < N ? tmO + N * g + r : tmL + N * g + r - N);
+                float o[16];
+                tmem_ld<16>(at, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] *= row_alpha(g)[r % N + e];
+                tmem_store<16>(at, o);
+              }
+              tmem_wait_st();
+            }
+            exponents();
+#pragma unroll
+            for (int r = 0; r < N / 2; ++r) x[r] = pack2f(tc::ex2_approx(lo2f(x[r])), tc::ex2_approx(hi2f(x[r])));
+          }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(sFree, g));
+          // P: this key's N weights side by side, once the group's last product has read the buffer
+          wait_left(bar(vFree, g), turn);
+          uint8_t* pp = sm + S::P + g * 128 * N * 2 + (32 * w + lane) * N * 2;
+#pragma unroll
+          for (int q = 0; q < N / 8; ++q) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = pack_f16(lo2f(x[4 * q + e]), hi2f(x[4 * q + e]));
+            const int sw = N == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+            *reinterpret_cast<uint4*>(pp + ((q ^ sw) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(pReady, g));
+          // this thread's keys' part of every row's sum, from the weights before their rounding
+#pragma unroll
+          for (int r = 0; r < N; r += 16) {
+            const uint32_t at = tm + lanes + tmL + N * g + r;
+            float sum[16];
+            if (!first_tile) {
+              tmem_ld<16>(at, sum);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint64_t two = add2(pack2f(sum[2 * e], sum[2 * e + 1]), x[r / 2 + e]);
+              sum[2 * e] = lo2f(two), sum[2 * e + 1] = hi2f(two);
+            }
+            tmem_store<16>(at, sum);
+          }
+          tmem_wait_st();
+          last = i;
+        }
+        it += pc.u1 - pc.u0;
+        if (k + 1 < batch) load_q(k + 1);
+        // the groups' rows joined; thread = column 32 w + lane, group g takes rows g N / 2 ..
+        if (last >= 0) {
+          wait_turn(bar(vFree, g), last >> 1);
+          tc::fence_after();
+          float v[N];
+          tmem_ld<N>(tm + lanes + tmL + N * g, v);
+          const float sum = warp_row_sums<N>(v, lane);
+          if (N == 32 || (lane & 1) == 0) row_l(g)[w * N + (N == 32 ? lane : lane >> 1)] = sum;
+        }
+        tc::fence_before();
+        softmax_barrier();
+        tc::fence_after();
+        const int np = pc.u1 - pc.u0, r_lo = g * (N / 2);
+        // whether a group had a tile: both from two tiles on, else the one whose turn the tile was
+        const bool has0 = np > 1 || ((it - np) & 1) == 0, has1 = np > 1 || ((it - np) & 1) == 1;
+        float L = 0.f, M = 0.f, f0 = 0.f, f1 = 0.f, inv = 0.f;  // of row `lane`
+        const bool whole = pc.whole();
+        if (lane < N) {
+          const float r0 = row_ref(0)[lane], r1 = row_ref(1)[lane], ref = fmaxf(r0, r1), sc = row_sc[lane];
+          M = ref * sc;
+          f0 = has0 ? (r0 == ref ? 1.f : tc::ex2_approx((r0 - ref) * sc)) : 0.f;
+          f1 = has1 ? (r1 == ref ? 1.f : tc::ex2_approx((r1 - ref) * sc)) : 0.f;
+          const float *l0 = row_l(0), *l1 = row_l(1);
+          L = (has0 ? f0 * (l0[lane] + l0[N + lane] + l0[2 * N + lane] + l0[3 * N + lane]) : 0.f) +
+              (has1 ? f1 * (l1[lane] + l1[N + lane] + l1[2 * N + lane] + l1[3 * N + lane]) : 0.f);
+          inv = whole ? (L == 0.f ? 0.f : a.v_scale / L) : 1.f;
+          if (w == 0 && lane >= r_lo && lane < min(rows, r_lo + N / 2)) {
+            if (!whole)
+              a.part_ml[part_row(pc, N) + lane] = make_float2(M, L);
+            else if (a.lse)
+              a.lse[row_out[N + lane]] = lse_of(M, L, kTcWeightExp);
           }
         }
-        __syncwarp();
-      }
-    }
-  } else if (warp == 17) {  // ---------------------------------------------------------------- first product
-    const bool one = elect_one();
-#pragma unroll 1
-    for (int k = 0; k < batch; ++k) {
-      const Piece pc = list[k].p;
-      wait_turn(q_ready, l_pieces++);
-#pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int buf = it & 1;
-        wait_turn(bar(kReady, buf), it >> 1);
-        wait_left(bar(sFree, buf), it >> 1);
-        tc::fence_after();
-        if (one) {
-          const uint64_t bd = tc::sw128_desc(sb + S::Q);
-          const uint32_t ka = tm + kTmK + 64 * buf, d = tm + kTmS + N * buf;
+        float o0[N / 2], o1[N / 2];
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_ts(d, ka + 8 * ks, bd + (ks >> 2) * N * 8 + (ks & 3) * 2, idesc_f16(128, N, false), ks > 0);
-          tc::umma_commit(bar(kFree, buf));
-          tc::umma_commit(bar(sFull, buf));
-        }
-        __syncwarp();
-      }
-    }
-  } else {  // ---------------------------------------------------------------- second product
-    const bool one = elect_one();
-#pragma unroll 1
-    for (int k = 0; k < batch; ++k) {
-      const Piece pc = list[k].p;
-#pragma unroll 1
-      for (int u = pc.u0; u < pc.u1; ++u, ++it) {
-        const int buf = it & 1;
-        wait_turn(bar(vReady, buf), it >> 1);
-        wait_turn(bar(pReady, buf), it >> 1);
-        tc::fence_after();
-        if (one) {
-          const uint64_t bd = p_desc<N>(sb + S::P + buf * 128 * N * 2);
-          const uint32_t va = tm + kTmV + 64 * buf, o = tm + tmO + N * buf;
+        for (int r = 0; r < N / 2; ++r) o0[r] = o1[r] = 0.f;
+        if (has0) tmem_ld_part<N / 2>(tm + lanes + tmO + r_lo, o0);
+        if (has1) tmem_ld_part<N / 2>(tm + lanes + tmO + N + r_lo, o1);
+        tc::fence_before();
+        const int d = 32 * w + lane;
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)  // a group's first tile of the piece starts its O
-            umma_ts(o, va + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || u - pc.u0 >= 2);
-          tc::umma_commit(bar(vFree, buf));
+        for (int r = 0; r < N / 2; ++r) {
+          const float e0 = __shfl_sync(0xffffffffu, f0 * inv, r_lo + r), e1 = __shfl_sync(0xffffffffu, f1 * inv, r_lo + r);
+          if (r_lo + r >= rows) continue;
+          const float v = fmaf(o0[r], e0, o1[r] * e1);
+          if (whole)
+            static_cast<bf16*>(a.out)[row_out[r_lo + r] + d] = __float2bfloat16_rn(v);
+          else
+            a.part_o[(part_row(pc, N) + r_lo + r) * DH + d] = v;
         }
-        __syncwarp();
+        softmax_barrier();  // both O, row_l, row_ref are the next piece's
+      }
+    } else if (warp == 16) {  // ---------------------------------------------------------------- value scales
+      // as f16, once for the 16 columns that share them: lane = block of 16 columns lane / 4, 32 tokens
+      const int blk = lane >> 2, tok = (lane & 3) * 32;
+#pragma unroll 1
+      for (int k = 0; k < batch; ++k) {
+        const Piece pc = list[k].p;
+        const int key_end = list[k].t.key_end, pg0 = list[k].t.pg0;
+#pragma unroll 1
+        for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+          const int st = it % kStages;
+          wait_turn(full(st), it / kStages);
+          // keys past the end, or of a page that is not there, hold anything, a NaN scale too: their values are 0
+          const int came = stage_ok[it % kRing], left = key_end - (pg0 + 2 * u) * kPage;
+          const int valid = came == 3 && left >= 128 ? 32 : (came >> (tok >> 6) & 1) ? left - tok : 0;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint4 w = *reinterpret_cast<const uint4*>(sm + st * TILE + (tok >> 6) * REC + chunk(vs_off(DH) / 16 + 4 * blk + ((tok & 63) >> 4) + q));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint32_t s[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              s[i] = fp8x2_to_f16x2((uint16_t)(ww[i / 2] >> (16 * (i & 1))));
+              const int at = 16 * q + 2 * i;
+              if (valid < 32) s[i] = at + 1 < valid ? s[i] : at < valid ? s[i] & 0xffffu : 0u;
+            }
+            uint4* to = reinterpret_cast<uint4*>(sm + S::VS + st * 2048 + blk * 256 + tok * 2 + 32 * q);
+            to[0] = make_uint4(s[0], s[1], s[2], s[3]);
+            to[1] = make_uint4(s[4], s[5], s[6], s[7]);
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(c_ready(it));
+        }
+      }
+    } else if (warp == 19) {  // ---------------------------------------------------------------- copies
+      const bool one = elect_one();
+#pragma unroll 1
+      for (int k = 0; k < batch; ++k) {
+        const Piece pc = list[k].p;
+        const Tile t = list[k].t;
+        const int32_t* bt = a.bt + (size_t)list[k].b * a.max_pages + t.pg0;
+        // 32 page ids at a time, the next 32 on their way: with one tile's ids loaded ahead, a load's latency was every tile's
+        const int pages = min(t.np, 2 * pc.u1);
+        auto page_of = [&](int i) { return i < pages ? bt[i] : -1; };
+        int ids = page_of(2 * pc.u0 + lane), next_ids = page_of(2 * pc.u0 + 32 + lane);
+#pragma unroll 1
+        for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+          const int st = it % kStages;
+          const int at = (2 * (u - pc.u0)) & 31;
+          if (at == 0 && u > pc.u0) {
+            ids = next_ids;
+            next_ids = page_of(2 * u + 32 + lane);
+          }
+          const int id0 = __shfl_sync(0xffffffffu, ids, at), id1 = __shfl_sync(0xffffffffu, ids, at + 1);
+          wait_left(empty(st), it / kStages);
+          const int came = (id0 >= 0 && id0 < a.n_pages ? 1 : 0) | (id1 >= 0 && id1 < a.n_pages ? 2 : 0);
+          if (one) {
+            if (id0 >= a.n_pages || id1 >= a.n_pages) flag_status(a.status, kDevBounds);
+            stage_ok[it % kRing] = came;
+            if (came) {
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              tc::mbar_expect_tx(full(st), (came == 3 ? 2 : 1) * REC);
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                if (!(came >> p & 1)) continue;
+                const long long rec = (long long)(p ? id1 : id0) * a.n_kv + pc.h;
+                tma_load_3d(sb + st * TILE + p * REC, &map, full(st), (int)rec);
+              }
+            } else {
+              tc::mbar_arrive(full(st));
+            }
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp == 17) {  // ---------------------------------------------------------------- first product
+      const bool one = elect_one();
+#pragma unroll 1
+      for (int k = 0; k < batch; ++k) {
+        const Piece pc = list[k].p;
+        wait_turn(q_ready, l_pieces++);
+#pragma unroll 1
+        for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+          const int buf = it & 1;
+          wait_turn(bar(kReady, buf), it >> 1);
+          wait_left(bar(sFree, buf), it >> 1);
+          tc::fence_after();
+          if (one) {
+            const uint64_t bd = tc::sw128_desc(sb + S::Q);
+            const uint32_t ka = tm + kTmK + 64 * buf, d = tm + kTmS + N * buf;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_ts(d, ka + 8 * ks, bd + (ks >> 2) * N * 8 + (ks & 3) * 2, idesc_f16(128, N, false), ks > 0);
+            tc::umma_commit(bar(kFree, buf));
+            tc::umma_commit(bar(sFull, buf));
+          }
+          __syncwarp();
+        }
+      }
+    } else {  // ---------------------------------------------------------------- second product
+      const bool one = elect_one();
+#pragma unroll 1
+      for (int k = 0; k < batch; ++k) {
+        const Piece pc = list[k].p;
+#pragma unroll 1
+        for (int u = pc.u0; u < pc.u1; ++u, ++it) {
+          const int buf = it & 1;
+          wait_turn(bar(vReady, buf), it >> 1);
+          wait_turn(bar(pReady, buf), it >> 1);
+          tc::fence_after();
+          if (one) {
+            const uint64_t bd = p_desc<N>(sb + S::P + buf * 128 * N * 2);
+            const uint32_t va = tm + kTmV + 64 * buf, o = tm + tmO + N * buf;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)  // a group's first tile of the piece starts its O
+              umma_ts(o, va + 8 * ks, bd + ks * N * 2, idesc_f16(128, N, true), ks > 0 || u - pc.u0 >= 2);
+            tc::umma_commit(bar(vFree, buf));
+          }
+          __syncwarp();
+        }
       }
     }
-  }
-  __syncwarp();
-  __syncthreads();  // the list is the next batch's
+    __syncwarp();
+    __syncthreads();  // the list is the next batch's
   }
   if (tid == 0 && a.stream) a.joins[blockIdx.x] = join;
   pdl_trigger();  // late: the grid fills the SMs
@@ -779,7 +779,7 @@ cudaError_t launch(const CUtensorMap& map, const AttnArgs& a, int grid, cudaStre
 cudaError_t launch_attention_tc(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   CUtensorMap map;
   const long long records = (long long)a.n_pages * a.n_kv;
-  if (!tc::make_record_map(&map, a.pages, kRow, kRecRows, records, REC)) return cudaErrorInvalidValue;
+  if (!tc::make_record_map(&map, a.pages, kRecRows, records)) return cudaErrorInvalidValue;
   return p.rows == 16 ? launch<16>(map, a, p.grid, s) : launch<32>(map, a, p.grid, s);
 }
 

@@ -427,17 +427,15 @@ bool make_out_map(CUtensorMap* m, const void* base, int S, int rows, int outs) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_record_map(CUtensorMap* m, const void* base, int row_bytes, int rows, long long records, long long record_bytes) {
+bool make_record_map(CUtensorMap* m, const void* base, int rows, long long records) {
   EncodeTiledFn fn = encoder();
-  if (!fn || !base || ((uintptr_t)base & 15) || rows < 1 || rows > 256 || records < 1 || record_bytes % 16) return false;
-  const CUtensorMapSwizzle sw = row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                : row_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_NONE;
-  cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)rows, (cuuint64_t)records};
-  cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)record_bytes};
-  cuuint32_t box[3] = {(cuuint32_t)row_bytes, (cuuint32_t)rows, 1};
+  if (!fn || !base || ((uintptr_t)base & 15) || rows < 1 || rows > 256 || records < 1) return false;
+  cuuint64_t dims[3] = {128, (cuuint64_t)rows, (cuuint64_t)records};
+  cuuint64_t strides[2] = {128, (cuuint64_t)rows * 128};
+  cuuint32_t box[3] = {128, (cuuint32_t)rows, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -63,9 +63,9 @@ struct TcParams {
 bool make_map(CUtensorMap* m, const void* base, int rows, int K, int box_rows);
 // Tensor map of a bf16 weight in the tiled layout (rows a multiple of 64), box = one
 // k block of box_rows (a multiple of 64) rows.
-// Rows of row_bytes (16, 32, 64 or 128, which is the swizzle too) of records: coordinates (0, row, record), boxes of a whole record's rows.
-bool make_record_map(CUtensorMap* m, const void* base, int row_bytes, int rows, long long records, long long record_bytes);
 bool make_map_tiled(CUtensorMap* m, const void* base, int rows, int K, int box_rows);
+// Tensor map of dense byte records of `rows` rows of 128 bytes, box = one record under the 128-byte swizzle: coordinates (0, 0, record).
+bool make_record_map(CUtensorMap* m, const void* base, int rows, long long records);
 // Tensor map of fp32 split-K partials part[S][rows][outs] for 32-row x 32-column
 // bulk stores (128-byte swizzle): rows and columns past the extents are not written.
 bool make_out_map(CUtensorMap* m, const void* base, int S, int rows, int outs);
