@@ -294,11 +294,18 @@ def _dtype(t, what):
     return code
 
 
+_LEAST, _MOST = -(1 << 31), (1 << 31) - 1      # what a C int holds; of other numbers ctypes would keep the low 32 bits
+
+
 def _int(v, what):
-    """v, if a C int holds it (ctypes would keep its low 32 bits)."""
-    if not -(1 << 31) <= v < 1 << 31:
+    if not _LEAST <= v <= _MOST:
         raise ValueError(f"{what}: {v} is outside 32 bits")
     return v
+
+
+def _sizes(what, *n):
+    """Refuses sizes of a tensor that C ints do not hold (called where one of them does not)."""
+    raise ValueError(f"{what}: sizes {list(n)} are outside 32 bits")
 
 
 def _here(stream, *tensors):
@@ -332,7 +339,8 @@ def _row_stride(t, what):
     if t.dim() != 4:
         raise ValueError(f"{what}: [B, T, heads, d_h] expected, got {list(t.shape)}")
     B, T, H, d = t.shape
-    _int(max(t.shape), what)
+    if (B | T | H | d) >> 31:
+        _sizes(what, B, T, H, d)
     sb, st, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (H > 1 and sh != d):
         raise ValueError(f"{what}: the heads of a row have to be dense")
@@ -374,7 +382,10 @@ def _table(table, layout):
         raise ValueError(f"layout: one of {sorted(ROPE_LAYOUTS)} expected")
     if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
         raise ValueError("table: contiguous float32 [n_pos, rot / 2, 2] expected")
-    return _int(2 * table.shape[1], "table"), ROPE_LAYOUTS[layout], _int(table.shape[0], "table")
+    n_pos, half, _ = table.shape
+    if (n_pos | 2 * half) >> 31:
+        _sizes("table", n_pos, 2 * half)
+    return 2 * half, ROPE_LAYOUTS[layout], n_pos
 
 
 def rope(x, pos, table, layout="half", n_rows=None, out=None, status=None, stream=None):
@@ -411,9 +422,13 @@ def _kv_desc(pages, block_table, B, k_exp, v_exp):
         raise ValueError("pages: records of 72 d_h bytes expected")
     if block_table.dim() != 2:
         raise ValueError("block_table: int32 [B, max_pages] expected")
-    bt = _vec(block_table, torch.int32, (B, block_table.shape[1]), "block_table")
-    return KvCacheDesc(pages.data_ptr(), bt, _int(n_pages, "pages"), _int(n_kv, "pages"), _int(rec // 72, "pages"),
-                       _int(block_table.shape[1], "block_table"), _int(k_exp, "k_exp"), _int(v_exp, "v_exp"))
+    max_pages = block_table.shape[1]
+    bt = _vec(block_table, torch.int32, (B, max_pages), "block_table")
+    if (n_pages | n_kv | rec | max_pages) >> 31:
+        _sizes("pages, block_table", n_pages, n_kv, rec, max_pages)
+    if not (_LEAST <= k_exp <= _MOST and _LEAST <= v_exp <= _MOST):
+        _int(k_exp, "k_exp"), _int(v_exp, "v_exp")
+    return KvCacheDesc(pages.data_ptr(), bt, n_pages, n_kv, rec // 72, max_pages, k_exp, v_exp)
 
 
 def kv_append(pages, block_table, k, v, pos, table=None, layout="half", n_rows=None, k_exp=0, v_exp=0, status=None, stream=None):
@@ -443,7 +458,9 @@ def kv_read(pages, block_table, pos, T, n_rows=None, k_exp=0, v_exp=0, dtype=tor
         raise ValueError("k_out and v_out: both or neither expected")
     B = block_table.shape[0]
     desc = _kv_desc(pages, block_table, B, k_exp, v_exp)
-    shape = (B, _int(T, "T"), desc.n_kv, desc.d_h)
+    if not _LEAST <= T <= _MOST:
+        _int(T, "T")
+    shape = (B, T, desc.n_kv, desc.d_h)
     if k_out is None:
         k_out, v_out = (_new(s, shape, dtype, zero=True) for _ in range(2))
     elif tuple(k_out.shape) != shape or tuple(v_out.shape) != shape or v_out.dtype != k_out.dtype:
@@ -475,7 +492,9 @@ def kv_attention(q, pages, block_table, pos, scale=None, window=0, n_rows=None, 
         raise ValueError("out: q's shape and type expected")
     if lse is True:
         lse = _new(s, (B, T, H), torch.float32, zero=n_rows is not None)
-    a = KvAttentionArgs(desc, B, T, H, _dtype(q, "q"), _int(window, "window"), d ** -0.5 if scale is None else scale, q.data_ptr(), qs,
+    if not _LEAST <= window <= _MOST:
+        _int(window, "window")
+    a = KvAttentionArgs(desc, B, T, H, _dtype(q, "q"), window, d ** -0.5 if scale is None else scale, q.data_ptr(), qs,
                         out.data_ptr(), _row_stride(out, "out"), _vec(lse, torch.float32, (B, T, H), "lse"),
                         _vec(pos, torch.int64, (B,), "pos"), _vec(n_rows, torch.int32, (B,), "n_rows"), None, 0,
                         _vec(status, torch.int32, (1,), "status"))
@@ -521,7 +540,11 @@ def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entro
             elif st != span:
                 raise ValueError("logits: rows have to be evenly spaced")
             span = st * n
-    n_top = _int(int(n_top), "n_top")
+    n_top = int(n_top)
+    if not _LEAST <= n_top <= _MOST:
+        _int(n_top, "n_top")
+    if (rows | V) >> 31:
+        _sizes("logits", rows, V)
     at = lead + (max(n_top, 0),)
     outs = []
     for name, t, shape, dt in (("logprob", logprob, lead, torch.float32), ("entropy", entropy, lead, torch.float32),
@@ -531,7 +554,7 @@ def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entro
         else:
             _vec(t, dt, shape, name)
         outs.append(t)
-    a = LogprobsArgs(_int(rows, "logits"), _int(V, "logits"), n_top, _dtype(logits, "logits"), temperature, logits.data_ptr(), stride,
+    a = LogprobsArgs(rows, V, n_top, _dtype(logits, "logits"), temperature, logits.data_ptr(), stride,
                      _vec(tokens, torch.int32, lead, "tokens"), *(t.data_ptr() for t in outs), _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_token_logprobs(ctypes.byref(a), ptr), "dlite_token_logprobs")
     return dict(logprob=outs[0], entropy=outs[1], top_ids=outs[2], top_logprobs=outs[3])
