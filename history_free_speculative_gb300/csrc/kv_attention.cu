@@ -12,8 +12,10 @@
 // takes two planes (hi + lo, 22 bits). Softmax weights are held as 2^(s - m + 14), in powers of two, so that f16 keeps
 // weights down to 2^-38 of the largest; they are rounded to f16 (2^-12 relative, below the bf16 output's 2^-9),
 // for float32 outputs as hi + lo. Scores, maxima, sums and outputs are fp32.
-// Measured: one float32 token over 500 keys, 4 query and 2 KV heads of 64, 6.8 us with the join; bound by two launches and a
-// chain of dependent loads (position, page ids, records). Float32 long contexts: the products, twice the planes.
+// Measured: one float32 token over 500 keys, 4 query and 2 KV heads of 64, 7.0 us with the join; bound by two launches and a
+// chain of dependent loads (position, page ids, records). 118,000 keys, 32 query and 8 KV heads, eight tokens: float32 heads of 128 107 us (floor
+// 20), float32 heads of 64 62 us, bf16 heads of 64 45 us (floor 10): the products, twice
+// as many for float32.
 //
 // Both products run on mma.sync m16n8k16 straight from the packed bytes: within a product's inner dimension any order
 // serves if both operands share it, so each lane takes the codes it can load in one piece.
@@ -524,9 +526,9 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const AttnArgs a
   if (a.lse && lane == 0) a.lse[row * a.n_q + hq] = kv::lse_of(M, L, a.weight_exp);
 }
 
-// A change of pieces in units: of the tcgen05 kernel in tiles of 128 keys (9,000 to 12,000 clocks against 1,090 to 1,370 a tile), of the other in
-// pages (118,000 keys, 8 float32 tokens 101 us at 0, 97 at 8, 93.5 at 16, 94.5 at 24; 8 requests of 8,192 keys 31.4, 26.2, 25.5, 25.9;
-// heads of 64, 32 ragged requests 207, 190, 180, 177).
+// A change of pieces in units: of the tcgen05 kernel in tiles of 128 keys (9,000 to 12,000 clocks against 1,100 to 1,460 a tile; 32 ragged
+// requests 238 us at 4, 224 at 8, 225 at 12; 8 of 8,192 keys 20.5, 20.6, 21.3), of the other in pages (118,000 keys, 8 float32 tokens 113 us at 0,
+// 108 at 8, 107 at 16, 108 at 24; 8 requests of 8,192 keys 34.1, 28.5, 28.0, 28.3; bf16 heads of 64, 32 ragged requests 208, 192, 183, 179).
 constexpr int kTcChange = 8, kChange = 16;
 
 kv::AttnPlan make_plan(const dlite_kv_attention_args& g) {
@@ -538,7 +540,7 @@ kv::AttnPlan make_plan(const dlite_kv_attention_args& g) {
   p.row_tiles = (rows + p.rows - 1) / p.rows;
   p.unit = p.tc ? 2 : 1;
   p.change = p.tc ? kTcChange : kChange;
-  // two tiles (4,000 keys, 8 tokens: 14.4 us; 19.4 with twelve; 1,000 keys: 12.8, 15.2 with four), a page for every warp
+  // two tiles (4,000 keys, 8 tokens: 15.0 us; 20.5 with twelve; 1,000 keys: 13.3, 15.6 with four), a page for every warp
   p.min_quota = p.tc ? 2 : kWarps;
   p.grid = device_sms();            // one CTA an SM: its shared memory is the ring
   // segments that a CTA's least run holds whole are not cut

@@ -20,13 +20,15 @@
 // per tile saves the loads of the factors, 4% of the ragged batch, but a row beside much larger ones lost its bits; both, by a branch per tile: no faster.)
 // The issuing warps stay converged and elect a lane: 17 clocks an MMA, 46 from a branch on the lane (the operands then
 // go from vector to uniform registers one by one).
-// Bound: issue slots. A tile of 128 keys takes 1,090 clocks at N = 16 and 1,370 at N = 32 (from the slope between 118,000 and 236,000 keys; 820 warp instructions a
-// scheduler, more than half of them conversions of codes); its 18 KB take 795 at the copy rate of HBM. Twice the
-// dequantising warps (28 in all, registers shared out again with setmaxnreg) changed nothing, nor did 9 or 10 stages for 8. Around the
+// Bound: the chain of a softmax group's tile (scores out of tensor memory, vote, exponentials, weights to shared memory, sums), of which two groups
+// in turn hide half. A tile of 128 keys takes 1,100 clocks at N = 16 and 1,460 at N = 32 (from the slope between 118,000 and 236,000 keys);
+// its 18 KB take 795 at the copy rate of HBM, its warp instructions at most 820 and 1,040 of a scheduler's slots (75% and 70%; 256 of them
+// convert codes), the tensor pipe is active for 13%. Twice the dequantising warps (28 in all, registers shared out again with setmaxnreg)
+// changed nothing, nor did 9 or 10 stages for 8. Around the
 // tiles: 6 us up to the first weights (lengths, list of pieces, first records, first maxima), 1.5 us at the end, 4 us the
 // join with its launch; a change of pieces costs a CTA 8 tiles.
-// Measured (32 query heads, 8 KV heads, with the join): one request of 118,000 keys 40 us for one token, 50 us for eight; eight requests
-// of 8,192 keys, one token each, 21 us; 32 requests of up to 40,960 keys, up to eight tokens each, 209 us (53% of the copy rate).
+// Measured (32 query heads, 8 KV heads, with the join): one request of 118,000 keys 40 us for one token, 54 us for eight; eight requests
+// of 8,192 keys, one token each, 21 us; 32 requests of up to 40,960 keys, up to eight tokens each, 224 us (49% of the copy rate).
 // mma.sync does both products of a 32-row tile in 8 clocks a key an SM (measured 2.0 per m16n8k16), above the 6.8 that the bytes take
 // at the copy rate of HBM, and needs its operands and outputs in registers: the mma.sync kernel ran at 19.
 #include <math.h>

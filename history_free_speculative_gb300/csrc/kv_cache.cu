@@ -6,13 +6,14 @@
 // block of two neighbouring tokens, whose codes share bytes. Keys go straight out (8 bytes
 // of a token's row). Value codes are transposed through shared memory: a page that is filled whole
 // leaves as 16-byte stores, else each byte is one thread's, and a byte whose
-// other token is old is read and merged. Bound: instructions for prompts (8,192 bf16 tokens of 8 heads of 128, rotated: 23 us,
-// 1.9 TB/s; 39 us with a division per value and a block per thread); launch latency and two
-// dependent loads (position, page id) for a token (5.4 us).
+// other token is old is read and merged. Bound: for prompts a CTA's loads, which nothing covers since it loads,
+// computes and stores once (53% of the issue slots, 42% of the warps active, loads the first stall): 8,192 bf16 tokens of 8 heads of 128,
+// rotated, 22 us, 2.1 TB/s (35 us with a division per value and a block per thread); launch latency and two
+// dependent loads (position, page id) for a token (2.8 us).
 //
 // Read: the CTA fetches its record with one bulk copy (9 KB at d_h 128) and decodes the
-// rows asked for out of shared memory; two tokens' values share bytes and are decoded together (the 8,192 tokens: 11 us,
-// 3.9 TB/s).
+// rows asked for out of shared memory; two tokens' values share bytes and are decoded together (the 8,192 tokens: 12 us,
+// 3.5 TB/s, a byte at a time out of shared memory; one 2.2 us).
 #include <algorithm>
 
 #include "kv_page.cuh"

@@ -574,7 +574,8 @@ int dlite_kv_attention(const dlite_kv_attention_args *args, dlite_stream_t strea
  *   top_ids, top_logprobs [rows, n_top]   the n_top largest logits in descending order, the lower
  *                               id first among equals (-0 = +0)
  * logprob and entropy may be NULL. A logit of -inf is an impossible token (ln p = -inf, no
- * part in the entropy); a row of -inf alone gives ln p = -inf and entropy 0. A row with a
+ * part in the entropy), and so is one that lies further below its row's largest than float32
+ * reaches; a row of -inf alone gives ln p = -inf and entropy 0. A row with a
  * NaN or +inf gives NaN; its alternatives rank NaN as -inf. Sums are float32. */
 #define DLITE_MAX_TOP 32
 typedef struct {
