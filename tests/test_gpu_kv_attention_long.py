@@ -127,3 +127,24 @@ def test_prompts_in_whole_segments(dtype, d):
             tol, ltol = _tolerance(want, reach, eps, T + 100, d, dtype)
             _within(out[b:b + 1], want, tol)
             _within(lse[b:b + 1], wl, ltol)
+
+
+@pytest.mark.parametrize("dtype,d", KINDS + [("bf16", 128)])
+def test_prompts_in_a_cut(dtype, d):
+    """Two prompts behind cached rows whose causal tiles are cut among the CTAs, one of them padded."""
+    B, T, nq, nkv, mp = 2, 1500, 8, 2, 36
+    pages, _ = _cache(60, nkv, d, 1, 1, 58)
+    g = _gen(59)
+    bt = torch.randint(0, 60, (B, mp), generator=g).to(torch.int32).to(DEV)
+    pos, n_rows = torch.tensor([777, 30], device=DEV), [T, 1111]
+    q = torch.randn(B, T, nq, d, generator=g).to(DT[dtype]).to(DEV)
+    pages = pages.to(DEV)
+    assert binding.kv_attention_workspace(B, T, nq, nkv, d, mp, DT[dtype]) > 0
+    for window in (0, 300):
+        out, lse = binding.kv_attention(q, pages, bt, pos, window=window, n_rows=torch.tensor(n_rows, dtype=torch.int32, device=DEV), lse=True)
+        want, wl, reach, eps = _plain(q, pages, bt, pos, window)
+        tol, ltol = _tolerance(want, reach, eps, 64 * mp, d, dtype)
+        for b, n in enumerate(n_rows):
+            _within(out[b, :n], want[b, :n], tol[b, :n])
+            _within(lse[b, :n], wl[b, :n], ltol[b, :n])
+            assert not out[b, n:].any() and not lse[b, n:].any()
