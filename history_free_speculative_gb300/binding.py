@@ -119,6 +119,39 @@ class LogprobsArgs(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("tokens", "logprob", "entropy", "top_ids", "top_logprobs", "status")]
 
 
+class Fp8QuantiseArgs(ctypes.Structure):
+    """dlite_fp8_quantise_args."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "K", "dtype")] + \
+               [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("total", ctypes.c_void_p), ("total_stride", ctypes.c_int64), ("gain", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("codes", ctypes.c_void_p), ("codes_stride", ctypes.c_int64), ("scale", ctypes.c_void_p), ("n_rows", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class Fp8WeightArgs(ctypes.Structure):
+    """dlite_fp8_weight_args."""
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "K", "dtype")] + \
+               [("w", ctypes.c_void_p), ("w_stride", ctypes.c_int64), ("codes", ctypes.c_void_p), ("codes_stride", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class Fp8LinearArgs(ctypes.Structure):
+    """dlite_fp8_linear_args."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "K", "N", "dtype")] + \
+               [("codes", ctypes.c_void_p), ("codes_stride", ctypes.c_int64), ("scale", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("w_stride", ctypes.c_int64), ("w_scale", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("n_rows", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class Fp8GatedArgs(ctypes.Structure):
+    """dlite_fp8_gated_args."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "K", "F")] + \
+               [("codes", ctypes.c_void_p), ("codes_stride", ctypes.c_int64), ("scale", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("gate_scale", ctypes.c_void_p), ("up", ctypes.c_void_p), ("up_stride", ctypes.c_int64),
+                ("up_scale", ctypes.c_void_p), ("out_codes", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("out_scale", ctypes.c_void_p),
+                ("n_rows", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
 class Taps(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("z", "x", "b", "hs")]
 
@@ -156,6 +189,10 @@ _SIGS = {
     "dlite_kv_attention_workspace": (ctypes.c_size_t, [ctypes.POINTER(KvAttentionArgs)]),
     "dlite_kv_attention": (_I, [ctypes.POINTER(KvAttentionArgs), _P]),
     "dlite_token_logprobs": (_I, [ctypes.POINTER(LogprobsArgs), _P]),
+    "dlite_fp8_quantise": (_I, [ctypes.POINTER(Fp8QuantiseArgs), _P]),
+    "dlite_fp8_weight": (_I, [ctypes.POINTER(Fp8WeightArgs), _P]),
+    "dlite_fp8_linear": (_I, [ctypes.POINTER(Fp8LinearArgs), _P]),
+    "dlite_fp8_gated": (_I, [ctypes.POINTER(Fp8GatedArgs), _P]),
     "dlite_selftest_wait": (_I, [_P, _U64, _P, _P]),
     "dlite_device_status": (_I, [_P, _I, ctypes.POINTER(_I), _P]),
     "dlite_status_string": (ctypes.c_char_p, [_I]),
@@ -558,6 +595,155 @@ def token_logprobs(logits, tokens, temperature=1.0, n_top=0, logprob=None, entro
                      _vec(tokens, torch.int32, lead, "tokens"), *(t.data_ptr() for t in outs), _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_token_logprobs(ctypes.byref(a), ptr), "dlite_token_logprobs")
     return dict(logprob=outs[0], entropy=outs[1], top_ids=outs[2], top_logprobs=outs[3])
+
+
+# ---------------------------------------------------------------- products with 8-bit weights
+
+FP8_BLOCK = 128
+_E4M3 = torch.float8_e4m3fn
+
+
+def _rows_of(t, what):
+    """(B, T, C, elements between the rows) of [B, T, C]: dense columns, evenly spaced rows."""
+    if t.dim() != 3:
+        raise ValueError(f"{what}: [B, T, columns] expected, got {list(t.shape)}")
+    B, T, C = t.shape
+    if (B | T | C) >> 31:
+        _sizes(what, B, T, C)
+    if t.is_contiguous():
+        return B, T, C, C
+    sb, st, sc = t.stride()
+    if C > 1 and sc != 1:
+        raise ValueError(f"{what}: the columns of a row have to be dense")
+    row = st if T > 1 else (sb if B > 1 else C)
+    if T > 1 and B > 1 and sb != T * st:
+        raise ValueError(f"{what}: rows (b, t) have to be evenly spaced")
+    if row < C:
+        raise ValueError(f"{what}: rows overlap")
+    return B, T, C, row
+
+
+def _like(t, other, what):
+    """Row stride of t, which has to be of the shape and type of `other`."""
+    if t.shape != other.shape or t.dtype != other.dtype:
+        raise ValueError(f"{what}: {other.dtype} {list(other.shape)} expected, got {t.dtype} {list(t.shape)}")
+    return _rows_of(t, what)[3]
+
+
+def _codes_of(t, what):
+    """(B, T, C, bytes between the rows) of e4m3 codes [B, T, C]; one row's may be anything."""
+    if t.dtype != _E4M3:
+        raise ValueError(f"{what}: float8_e4m3fn expected, got {t.dtype}")
+    B, T, C, row = _rows_of(t, what)
+    return B, T, C, row if B * T > 1 else -(-C // 16) * 16
+
+
+def _weight_of(w, scale, K, what):
+    """(N, pointer, bytes between the rows, pointer of the scales) of codes [N, K] and their scales."""
+    if w.dtype != _E4M3 or w.dim() != 2 or w.shape[1] != K or (K > 1 and w.stride(1) != 1):
+        raise ValueError(f"{what}: float8_e4m3fn [N, {K}] with dense rows expected, got {w.dtype} {list(w.shape)}")
+    N = w.shape[0]
+    if N >> 31:
+        _sizes(what, N, K)
+    row = w.stride(0) if N > 1 else -(-K // 16) * 16
+    return N, w.data_ptr(), row, _vec(scale, torch.float32, (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)), what + "_scale")
+
+
+def _new_codes(stream, B, T, C):
+    pitch = -(-C // 16) * 16
+    t = _new(stream, (B, T, pitch), _E4M3)
+    return t if pitch == C else t[:, :, :C]
+
+
+def fp8_quantise(x, gain=None, eps=1e-6, residual=None, total=None, n_rows=None, codes=None, scale=None, status=None, stream=None):
+    """x [B, T, K] as 8-bit codes (float8_e4m3fn [B, T, K]) and scales (float32 [B, T, ceil(K / 128)]), one per 128 columns
+    (dlite_fp8_quantise). With residual: total = x + residual is stored (total None: in residual's place) and takes x's place; with
+    gain [K] it is normed by its root mean square. Rows t >= n_rows[b] are left as they were (in new outputs: anything).
+    Returns (codes, scale)."""
+    lib = load()
+    ptr, s = _here(stream, x, gain, residual, total, n_rows, codes, scale, status)
+    B, T, K, xs = _rows_of(x, "x")
+    if residual is None:
+        if total is not None:
+            raise ValueError("total: goes with a residual")
+        rs = ts = 0
+    else:
+        total = residual if total is None else total
+        rs, ts = _like(residual, x, "residual"), _like(total, x, "total")
+    if codes is None:
+        codes = _new_codes(s, B, T, K)
+    elif codes.shape != x.shape:
+        raise ValueError(f"codes: {list(x.shape)} expected, got {list(codes.shape)}")
+    if scale is None:
+        scale = _new(s, (B, T, -(-K // FP8_BLOCK)), torch.float32)
+    a = Fp8QuantiseArgs(B, T, K, _dtype(x, "x"), x.data_ptr(), xs, None if residual is None else residual.data_ptr(), rs,
+                        None if residual is None else total.data_ptr(), ts, _vec(gain, x.dtype, (K,), "gain"), eps, codes.data_ptr(),
+                        _codes_of(codes, "codes")[3], _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale"),
+                        _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_fp8_quantise(ctypes.byref(a), ptr), "dlite_fp8_quantise")
+    return codes, scale
+
+
+def fp8_weight(w, status=None, stream=None):
+    """A weight [N, K] as 8-bit codes (float8_e4m3fn [N, K], rows on 16 bytes) and float32 scales of its 128 x 128 blocks
+    (dlite_fp8_weight): once, where a model is loaded. Returns (codes, scale)."""
+    lib = load()
+    ptr, s = _here(stream, w, status)
+    if w.dim() != 2 or (w.shape[1] > 1 and w.stride(1) != 1):
+        raise ValueError(f"w: [N, K] with dense rows expected, got {list(w.shape)}")
+    N, K = w.shape
+    if (N | K) >> 31:
+        _sizes("w", N, K)
+    codes = _new_codes(s, 1, N, K)[0]
+    scale = _new(s, (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)), torch.float32)
+    a = Fp8WeightArgs(N, K, _dtype(w, "w"), w.data_ptr(), w.stride(0) if N > 1 else K, codes.data_ptr(), -(-K // 16) * 16, scale.data_ptr(),
+                      _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_fp8_weight(ctypes.byref(a), ptr), "dlite_fp8_weight")
+    return codes, scale
+
+
+def fp8_linear(codes, scale, w, w_scale, dtype=torch.bfloat16, n_rows=None, out=None, status=None, stream=None):
+    """x w^T [B, T, N] of rows in 8 bits (codes [B, T, K] and scale, fp8_quantise's or fp8_gated's) and a weight in 8 bits
+    (codes [N, K], float32 scales of 128 x 128 blocks), summed in float32 (dlite_fp8_linear). Rows t >= n_rows[b] of out are
+    left as they were (zeros in a new one). Returns out."""
+    lib = load()
+    ptr, s = _here(stream, codes, scale, w, w_scale, n_rows, out, status)
+    B, T, K, cs = _codes_of(codes, "codes")
+    N, wp, ws, wsp = _weight_of(w, w_scale, K, "w")
+    if out is None:
+        out = _new(s, (B, T, N), dtype, zero=n_rows is not None)
+    elif tuple(out.shape) != (B, T, N):
+        raise ValueError(f"out: {[B, T, N]} expected, got {list(out.shape)}")
+    a = Fp8LinearArgs(B, T, K, N, _dtype(out, "out"), codes.data_ptr(), cs, _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale"),
+                      wp, ws, wsp, out.data_ptr(), _rows_of(out, "out")[3], _vec(n_rows, torch.int32, (B,), "n_rows"),
+                      _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_fp8_linear(ctypes.byref(a), ptr), "dlite_fp8_linear")
+    return out
+
+
+def fp8_gated(codes, scale, gate, gate_scale, up, up_scale, n_rows=None, out=None, out_scale=None, status=None, stream=None):
+    """silu(x gate^T) (x up^T) of rows in 8 bits and two weights in 8 bits, in one kernel, as 8-bit rows again
+    (dlite_fp8_gated): what fp8_linear takes for the down projection. Returns (codes [B, T, F], scale [B, T, ceil(F / 128)]); rows
+    t >= n_rows[b] are left as they were (in new outputs: anything)."""
+    lib = load()
+    ptr, s = _here(stream, codes, scale, gate, gate_scale, up, up_scale, n_rows, out, out_scale, status)
+    B, T, K, cs = _codes_of(codes, "codes")
+    N, gp, gs, gsp = _weight_of(gate, gate_scale, K, "gate")
+    n, pp, ps, psp = _weight_of(up, up_scale, K, "up")
+    if n != N:
+        raise ValueError(f"up: the gate's {N} rows expected, got {n}")
+    if out is None:
+        out = _new_codes(s, B, T, N)
+    elif tuple(out.shape) != (B, T, N):
+        raise ValueError(f"out: {[B, T, N]} expected, got {list(out.shape)}")
+    at = (B, T, -(-N // FP8_BLOCK))
+    if out_scale is None:
+        out_scale = _new(s, at, torch.float32)
+    a = Fp8GatedArgs(B, T, K, N, codes.data_ptr(), cs, _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale"), gp, gs, gsp, pp, ps, psp,
+                     out.data_ptr(), _codes_of(out, "out")[3], _vec(out_scale, torch.float32, at, "out_scale"),
+                     _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
+    _check(lib.dlite_fp8_gated(ctypes.byref(a), ptr), "dlite_fp8_gated")
+    return out, out_scale
 
 
 def config_struct(cfg, B_max):

@@ -1,0 +1,83 @@
+// Shared parts of the 8-bit products: the block format, arguments, tensor maps' boxes.
+//
+// Activations: e4m3 codes and one scale per (row, 128 columns), the least 2^e (e >= -126) with max |x| <= 448 2^e. A power of two makes
+// the code one rounding of an exact product, whatever computes it, and costs e4m3 no precision: its steps are relative down to 2^-6.
+// Weights: e4m3 codes and a float32 scale per 128 x 128 elements.
+#pragma once
+
+#include <cuda.h>
+
+#include "internal.h"
+
+namespace dlite {
+namespace fp8 {
+
+constexpr int kBlock = DLITE_FP8_BLOCK;
+static_assert(kBlock == 128, "a k block is one 128-byte swizzled row of the operand tiles");
+
+__host__ __device__ constexpr int blocks_of(int n) { return n / kBlock + (n % kBlock != 0); }
+
+// Exponent of a block's scale: amax = m 2^k, 448 = 1.75 2^8, so that e = k - 8, or k - 7 where the significand is above 1.75 (the
+// addition carries into the exponent there).
+__device__ __forceinline__ int block_exponent(float amax) {
+  return max((int)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 135, -126);
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
+
+// Codes of four numbers (first lowest): nearest, ties to even. NaN becomes NaN.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+// The largest finite |v| of N numbers; what is not finite becomes NaN (the format holds no infinity) and sets `bad`.
+template <int N>
+__device__ __forceinline__ float finite_max(float (&v)[N], bool& bad) {
+  float amax = 0.f, odd = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    amax = fmaxf(amax, fabsf(v[i]));
+    odd = fmaf(v[i], 0.f, odd);  // NaN once a number is not finite
+  }
+  if (odd != 0.f) {
+    bad = true;
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (fabsf(v[i]) <= 3.402823466e38f)
+        amax = fmaxf(amax, fabsf(v[i]));
+      else
+        v[i] = __uint_as_float(0x7fffffffu);
+    }
+  }
+  return amax;
+}
+
+// A row's place among the requests' blocks: row (b, t) is valid iff t < n_rows[b].
+__device__ __forceinline__ bool valid_row(const int32_t* n_rows, int T, int row) {
+  return !n_rows || row % T < n_rows[row / T];
+}
+
+struct ProductArgs {
+  int rows, T;            // rows = B T
+  int K, kblocks;
+  int N;                  // outputs (gated: columns of the activation)
+  const int32_t* n_rows;
+  const float* xs;        // [rows][kblocks]
+  const float* ws[2];     // [N / 128][kblocks]; gated: gate, up
+  void* out;              // linear
+  long long os;
+  uint8_t* codes;         // gated
+  long long cs;
+  float* scale;           // [rows][N / 128]
+  int vec;                // linear: rows of out on 16 bytes
+  int* status;
+};
+
+// Map of byte rows [rows, K] of `stride` bytes for boxes of box_rows x 128 bytes under the 128-byte swizzle; columns and rows
+// past the matrix read as 0.
+bool make_map(CUtensorMap* m, const void* base, long long rows, int K, long long stride, int box_rows);
+
+}  // namespace fp8
+}  // namespace dlite

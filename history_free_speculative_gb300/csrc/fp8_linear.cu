@@ -1,0 +1,416 @@
+// Products of 8-bit rows and 8-bit weights with a scale per block, and the gated form whose activation leaves in 8 bits again.
+//
+//   linear: out[r, n] = sum_b xs[r, b] ws[n / 128, b] sum_{k in block b} x[r, k] w[n, k]
+//   gated:  g, u the same sums over two weights, a = silu(g) u, stored as codes with a scale per (row, 128 columns)
+//
+// This kernel serves few rows. A CTA computes 128 rows x 128 weight rows over a run of k blocks. Per k block four
+// tcgen05.mma kind::f8f6f4 (K = 32) write an accumulator of their own in tensor memory, two in turn; the epilogue warps (lane = row) multiply it by
+// the block's scales and add it to sums in registers, in float32, while the next block's products run. The k blocks of a tile are
+// dealt to `splits` CTAs of one cluster, whose sums meet in shared memory: every CTA reads all parts of the rows
+// that are its own, in order, so results are the same run to run.
+// Gated: a tile has 64 gate rows and the 64 up rows of the same columns; two CTAs of a cluster make up the 128 columns
+// that share a scale.
+// Bound: the weights' bytes.
+#include <algorithm>
+
+#include "fp8.cuh"
+#include "tc_device.cuh"
+
+namespace dlite {
+namespace {
+
+using fp8::kBlock;
+using fp8::ProductArgs;
+
+constexpr int kThreads = 192;              // copy warp, MMA warp, four epilogue warps
+constexpr uint32_t kWTile = 128 * 128;     // a k block of the weights' 128 rows
+constexpr uint32_t kCols = 256;            // tensor memory: two accumulators of 128 columns
+constexpr int kPitch = 132;                // floats of a staged row (16-byte stores of a warp's lanes fall on different banks)
+constexpr size_t kSmem = 112 * 1024;       // two CTAs an SM
+
+// Instruction descriptor, kind::f8f6f4: float32 sums, e4m3 on both sides, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+struct SmallPlan {
+  int box;     // rows of an activation tile's copy
+  int splits;  // of the k blocks
+  int stages;
+  uint32_t a_bytes;
+};
+
+template <bool GATED, typename OUT>
+__global__ void __launch_bounds__(kThreads, 2)
+    fp8_small_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw0,
+                     const __grid_constant__ CUtensorMap mw1, const ProductArgs p, const SmallPlan pl) {
+  // Shared memory: [barriers | pad to 1 KB] [stage 0] ..; stage = [activation tile][weight tile]. The sums of the rows are staged over the stages.
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = (uint64_t*)base;
+  const uint32_t full0 = tc::su32(bars), empty0 = tc::su32(bars + pl.stages), accf0 = tc::su32(bars + 2 * pl.stages);
+  const uint32_t acce0 = accf0 + 16, done = accf0 + 32;
+  uint32_t* tmem_holder = (uint32_t*)(bars + 2 * pl.stages + 5);
+  uint8_t* smem = base + 1024;
+  const uint32_t stage_bytes = pl.a_bytes + kWTile;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int halves = GATED ? 2 : 1, cl = halves * pl.splits;
+  const int rank = blockIdx.x % cl, half = GATED ? rank & 1 : 0, z = GATED ? rank >> 1 : rank;
+  const int tile = blockIdx.x / cl;                              // 128 columns of the result
+  const int row0 = blockIdx.y * 128, rows = min(128, p.rows - row0);
+  const int kb0 = (int)((long long)z * p.kblocks / pl.splits), kn = (int)((long long)(z + 1) * p.kblocks / pl.splits) - kb0;
+  const int quads = (rows + 31) / 32;                            // epilogue warps with rows
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < pl.stages; ++s) {
+      tc::mbar_init(full0 + 8 * s, 1);
+      tc::mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(accf0 + 8 * b, 1);
+      tc::mbar_init(acce0 + 8 * b, quads);
+    }
+    tc::mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tmem_holder)), "r"(kCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_trigger();
+  pdl_wait();
+  tc::fence_before();
+  // a tile without a valid row (padding of a ragged batch) is left out by the whole cluster
+  const bool live = __syncthreads_or((int)threadIdx.x < rows && fp8::valid_row(p.n_rows, p.T, row0 + threadIdx.x));
+  tc::fence_after();
+  const uint32_t tmem = *tmem_holder;
+  float* staged = (float*)smem;
+
+  if (live && warp == 0) {  // ---------------- copies
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int j = 0; j < kn && ok; ++j) {
+        if (j >= pl.stages) ok = tc::mbar_wait_hint(empty0 + 8 * s, ph ^ 1u, p.status);
+        if (!ok) break;
+        const uint32_t st = tc::su32(smem + (size_t)s * stage_bytes), bar = full0 + 8 * s;
+        const int k = (kb0 + j) * kBlock;
+        tc::mbar_expect_tx(bar, (uint32_t)pl.box * 128 + kWTile);
+        if (GATED) {
+          tc::tma_load_2d(st + pl.a_bytes, &mw0, bar, k, tile * 128 + half * 64);
+          tc::tma_load_2d(st + pl.a_bytes + kWTile / 2, &mw1, bar, k, tile * 128 + half * 64);
+        } else {
+          tc::tma_load_2d(st + pl.a_bytes, &mw0, bar, k, tile * 128);
+        }
+        tc::tma_load_2d(st, &mx, bar, k, row0);
+        if (++s == pl.stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      // no copy is in flight past this role, whoever gave up
+      const int last = kn < pl.stages ? kn : pl.stages;
+      if (!ok)
+        for (int i = 0; i < last; ++i) {
+          if (s == 0) {
+            s = pl.stages;
+            ph ^= 1u;
+          }
+          --s;
+          tc::mbar_wait_hint(full0 + 8 * s, ph, p.status);
+        }
+    }
+    __syncwarp();
+  } else if (live && warp == 1) {  // ---------------- products
+    constexpr uint32_t idesc = idesc_e4m3(128, 128);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int j = 0; j < kn && ok; ++j) {
+      const int b = j & 1;
+      if (j >= 2) ok = tc::mbar_wait_warp(acce0 + 8 * b, (uint32_t)((j >> 1) - 1) & 1u, p.status);
+      ok = ok && tc::mbar_wait_warp(full0 + 8 * s, ph, p.status);
+      if (!ok) break;
+      tc::fence_after();
+      if (lane == 0) {
+        const uint64_t a0 = tc::sw128_desc(tc::su32(smem + (size_t)s * stage_bytes)), b0 = a0 + (pl.a_bytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + 128 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
+        tc::umma_commit(empty0 + 8 * s);
+        tc::umma_commit(accf0 + 8 * b);
+      }
+      __syncwarp();
+      if (++s == pl.stages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    // every product issued has finished before the stages and the tensor memory go
+    if (lane == 0) tc::umma_commit(done);
+    __syncwarp();
+    tc::mbar_wait_warp(done, 0, p.status);
+  } else if (live && (warp & 3) < quads) {  // ---------------- sums: lane = row
+    const int q = warp & 3, r = q * 32 + lane;
+    const float* xs = p.xs + (long long)(row0 + min(r, rows - 1)) * p.kblocks + kb0;
+    const float* w0 = p.ws[0] + (long long)tile * p.kblocks + kb0;
+    const float* w1 = GATED ? p.ws[1] + (long long)tile * p.kblocks + kb0 : w0;
+    uint64_t acc[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) acc[i] = 0;
+    float x_next = xs[0], w0_next = w0[0], w1_next = w1[0];
+    bool ok = true;
+    for (int j = 0; j < kn; ++j) {
+      const int b = j & 1;
+      const float s0 = x_next * w0_next, s1 = GATED ? x_next * w1_next : s0;
+      if (j + 1 < kn) {
+        x_next = xs[j + 1];
+        w0_next = w0[j + 1];
+        if (GATED) w1_next = w1[j + 1];
+      }
+      ok = tc::mbar_wait_warp(accf0 + 8 * b, (uint32_t)(j >> 1) & 1u, p.status);
+      if (!ok) break;
+      tc::fence_after();
+      const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + 128 * b;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t v[16];
+        tc::tmem_ld16_nowait(t0 + 16 * c, v);
+        tc::tmem_wait_ld();
+        const float sc = c < 4 ? s0 : s1;
+        const uint64_t sc2 = pack2f(sc, sc);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          acc[8 * c + i] = fma2(pack2f(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2, acc[8 * c + i]);
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(acce0 + 8 * b);
+    }
+    // the last accumulator is there, so every product has read its stage: their memory takes the sums
+    if (ok && r < rows) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        *reinterpret_cast<float4*>(staged + r * kPitch + 4 * i) =
+            make_float4(lo2f(acc[2 * i]), hi2f(acc[2 * i]), lo2f(acc[2 * i + 1]), hi2f(acc[2 * i + 1]));
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (cl > 1) tc::cluster_sync_all();
+  if (warp == 1) {
+    tc::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+  }
+  if (live) {  // ---------------- the rows of the tile, dealt to the cluster's warps
+    const uint32_t mine = tc::su32(staged);
+    auto part = [&](int rk, int r, int c) { return ld_cluster4(tc::map_to_rank(mine, rk) + (uint32_t)(r * kPitch + c) * 4); };
+    for (int r = rank + cl * warp; r < rows; r += cl * (kThreads / 32)) {
+      const int row = row0 + r;
+      if (!fp8::valid_row(p.n_rows, p.T, row)) continue;
+      if constexpr (GATED) {
+        const int hf = lane >> 4, c = (lane & 15) * 4, n = tile * 128 + hf * 64 + c;
+        float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+        for (int i = 0; i < pl.splits; ++i) {
+          const float4 a = part(2 * i + hf, r, c), b = part(2 * i + hf, r, 64 + c);
+          g.x += a.x, g.y += a.y, g.z += a.z, g.w += a.w;
+          u.x += b.x, u.y += b.y, u.z += b.z, u.w += b.w;
+        }
+        float v[4] = {g.x / (1.f + expf(-g.x)) * u.x, g.y / (1.f + expf(-g.y)) * u.y, g.z / (1.f + expf(-g.z)) * u.z,
+                      g.w / (1.f + expf(-g.w)) * u.w};
+        bool bad = false;
+        const float amax = warp_max(fp8::finite_max(v, bad));   // columns past N are 0
+        const int e = fp8::block_exponent(amax);
+        const float inv = fp8::exp2i(-e);
+        const uint32_t w = fp8::codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+        uint8_t* dst = p.codes + (long long)row * p.cs + n;
+        if (n + 4 <= p.N)
+          *reinterpret_cast<uint32_t*>(dst) = w;
+        else
+          for (int i = 0; i < p.N - n; ++i) dst[i] = (uint8_t)(w >> (8 * i));
+        if (lane == 0) p.scale[(long long)row * fp8::blocks_of(p.N) + tile] = fp8::exp2i(e);
+        if (bad) flag_status(p.status, kDevNonfinite);
+      } else {
+        const int n = tile * 128 + lane * 4;
+        float4 o = part(0, r, lane * 4);
+        for (int i = 1; i < pl.splits; ++i) {
+          const float4 a = part(i, r, lane * 4);
+          o.x += a.x, o.y += a.y, o.z += a.z, o.w += a.w;
+        }
+        OUT* dst = static_cast<OUT*>(p.out) + (long long)row * p.os + n;
+        const float v[4] = {o.x, o.y, o.z, o.w};
+        OUT e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(OUT) == 2)
+            e[i] = __float2bfloat16_rn(v[i]);
+          else
+            e[i] = v[i];
+        }
+        if (p.vec && n + 4 <= p.N) {
+          if constexpr (sizeof(OUT) == 2)
+            *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(e);
+          else
+            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(e);
+        } else {
+          for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) dst[i] = e[i];
+        }
+      }
+    }
+  }
+  if (cl > 1) tc::cluster_sync_all();  // no CTA's sums go while another reads them
+}
+
+// ---------------------------------------------------------------- host side
+
+SmallPlan small_plan(const ProductArgs& p, bool gated) {
+  SmallPlan pl;
+  pl.box = p.rows >= 128 ? 128 : (p.rows + 7) / 8 * 8;
+  pl.a_bytes = (uint32_t)(pl.box * 128);
+  pl.stages = std::min<int>(16, (int)((kSmem - 2048) / (pl.a_bytes + kWTile)));
+  const int halves = gated ? 2 : 1;
+  const long long ctas = (long long)fp8::blocks_of(p.N) * halves * ((p.rows + 127) / 128);
+  pl.splits = 1;
+  while (pl.splits * 2 * halves <= 8 && pl.splits * 2 <= p.kblocks && ctas * pl.splits * 2 <= 2LL * device_sms()) pl.splits *= 2;
+  return pl;
+}
+
+template <bool GATED, typename OUT>
+cudaError_t launch_small(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, const SmallPlan& pl,
+                         cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(fp8_small_kernel<GATED, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  const int cl = (GATED ? 2 : 1) * pl.splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(fp8::blocks_of(p.N) * cl, (p.rows + 127) / 128);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, fp8_small_kernel<GATED, OUT>, x, w0, w1, p, pl);
+}
+
+template <bool GATED, typename OUT>
+int product(const ProductArgs& p, const void* x, long long x_stride, const void* w0, long long w0_stride, const void* w1, long long w1_stride,
+            cudaStream_t s) {
+  const SmallPlan pl = small_plan(p, GATED);
+  CUtensorMap mx, m0, m1;
+  const int wbox = GATED ? 64 : 128;
+  if (!fp8::make_map(&mx, x, p.rows, p.K, x_stride, pl.box) || !fp8::make_map(&m0, w0, p.N, p.K, w0_stride, wbox) ||
+      !fp8::make_map(&m1, w1, p.N, p.K, w1_stride, wbox))
+    return launch_status(cudaErrorInvalidValue);
+  return launch_status(launch_small<GATED, OUT>(mx, m0, m1, p, pl, s));
+}
+
+}  // namespace
+
+namespace fp8 {
+
+bool make_map(CUtensorMap* m, const void* base, long long rows, int K, long long stride, int box_rows) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? (Encode)f : (Encode) nullptr;
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
+  const cuuint32_t box[2] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace fp8
+}  // namespace dlite
+
+namespace {
+
+// What both products check of their operands.
+int check_product(int B, int T, int K, int N, const void* codes, int64_t codes_stride, const float* scale, const int32_t* n_rows, const int* status) {
+  if (!codes || !scale || B < 1 || T < 1 || K < 1 || N < 1) return DLITE_ERR_INVALID_ARG;
+  if (((uintptr_t)codes & 15) || codes_stride < K || codes_stride % 16 || !dlite::aligned4(scale, n_rows, status)) return DLITE_ERR_INVALID_ARG;
+  if ((long long)B * T > DLITE_FP8_MAX_ROWS || K > DLITE_FP8_MAX_K || N > DLITE_FP8_MAX_N || codes_stride >= (1LL << 40)) return DLITE_ERR_UNSUPPORTED_SHAPE;
+  return DLITE_OK;
+}
+int check_weight(const void* w, int64_t stride, const float* scale, int K) {
+  if (!w || !scale || ((uintptr_t)w & 15) || stride < K || stride % 16 || ((uintptr_t)scale & 3)) return DLITE_ERR_INVALID_ARG;
+  return stride >= (1LL << 40) ? DLITE_ERR_UNSUPPORTED_SHAPE : DLITE_OK;
+}
+
+}  // namespace
+
+extern "C" int dlite_fp8_linear(const dlite_fp8_linear_args* g, dlite_stream_t stream) {
+  using namespace dlite;
+  if (!g) return DLITE_ERR_INVALID_ARG;
+  if (const int rc = check_product(g->B, g->T, g->K, g->N, g->codes, g->codes_stride, g->scale, g->n_rows, g->status)) return rc;
+  if (const int rc = check_weight(g->w, g->w_stride, g->w_scale, g->K)) return rc;
+  if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
+  const int es = g->dtype == DLITE_F32 ? 4 : 2;
+  if (!g->out || (uintptr_t)g->out % es || g->out_stride < g->N) return DLITE_ERR_INVALID_ARG;
+  ProductArgs p = {};
+  p.rows = g->B * g->T;
+  p.T = g->T;
+  p.K = g->K;
+  p.kblocks = fp8::blocks_of(g->K);
+  p.N = g->N;
+  p.n_rows = g->n_rows;
+  p.xs = g->scale;
+  p.ws[0] = p.ws[1] = g->w_scale;
+  p.out = g->out;
+  p.os = g->out_stride;
+  p.vec = !((uintptr_t)g->out & 15) && g->out_stride % (16 / es) == 0;
+  p.status = g->status;
+  const cudaStream_t s = (cudaStream_t)stream;
+  return g->dtype == DLITE_F32 ? product<false, float>(p, g->codes, g->codes_stride, g->w, g->w_stride, g->w, g->w_stride, s)
+                               : product<false, bf16>(p, g->codes, g->codes_stride, g->w, g->w_stride, g->w, g->w_stride, s);
+}
+
+extern "C" int dlite_fp8_gated(const dlite_fp8_gated_args* g, dlite_stream_t stream) {
+  using namespace dlite;
+  if (!g) return DLITE_ERR_INVALID_ARG;
+  if (const int rc = check_product(g->B, g->T, g->K, g->F, g->codes, g->codes_stride, g->scale, g->n_rows, g->status)) return rc;
+  if (const int rc = check_weight(g->gate, g->gate_stride, g->gate_scale, g->K)) return rc;
+  if (const int rc = check_weight(g->up, g->up_stride, g->up_scale, g->K)) return rc;
+  if (!g->out_codes || ((uintptr_t)g->out_codes & 15) || g->out_stride < g->F || g->out_stride % 16 || !g->out_scale || ((uintptr_t)g->out_scale & 3))
+    return DLITE_ERR_INVALID_ARG;
+  ProductArgs p = {};
+  p.rows = g->B * g->T;
+  p.T = g->T;
+  p.K = g->K;
+  p.kblocks = fp8::blocks_of(g->K);
+  p.N = g->F;
+  p.n_rows = g->n_rows;
+  p.xs = g->scale;
+  p.ws[0] = g->gate_scale;
+  p.ws[1] = g->up_scale;
+  p.codes = g->out_codes;
+  p.cs = g->out_stride;
+  p.scale = g->out_scale;
+  p.status = g->status;
+  return product<true, float>(p, g->codes, g->codes_stride, g->gate, g->gate_stride, g->up, g->up_stride, (cudaStream_t)stream);
+}

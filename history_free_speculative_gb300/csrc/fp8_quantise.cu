@@ -1,0 +1,262 @@
+// Activations and weights into 8 bits with a scale per block.
+//
+// Rows: optionally total = x + residual (rounded to the stream's type and stored), then y = total / sqrt(mean total^2 + eps) gain, then the
+// codes of y. A thread holds eight neighbouring columns, so 16 neighbouring threads hold a block and its maximum is four shuffles.
+// With a norm a CTA takes a whole row (the sum of squares is over the row); without one the
+// row's pieces go to CTAs of their own.
+#include <algorithm>
+
+#include "fp8.cuh"
+
+namespace dlite {
+namespace {
+
+using fp8::kBlock;
+
+struct QuantiseArgs {
+  int rows, T, K, kblocks;
+  const void* x;
+  long long xs;
+  const void* res;
+  long long rs;
+  void* total;
+  long long ts;
+  const void* gain;
+  float eps;
+  uint8_t* codes;
+  long long cs;
+  float* scale;
+  const int32_t* n_rows;
+  int* status;
+};
+
+constexpr int kPer = 8;  // columns of a thread
+
+// Columns [c, c + 8) of a row, zeros past K
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* row, int c, int K, float (&v)[kPer]) {
+  if (VEC) {  // K is a multiple of 8 here
+    if (c < K) {
+      uint4 w[sizeof(T) / 2];
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(row + c)[i];
+      const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = to_f32(e[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = c + i < K ? to_f32(row[c + i]) : 0.f;
+  }
+}
+__device__ __forceinline__ float rounded(float v, float*) { return v; }
+__device__ __forceinline__ float rounded(float v, bf16*) { return round_bf16(v); }
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* row, int c, int K, const float (&v)[kPer]) {
+  T e[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if constexpr (sizeof(T) == 2)
+      e[i] = __float2bfloat16_rn(v[i]);
+    else
+      e[i] = v[i];
+  }
+  if (VEC) {
+    if (c < K)
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + c)[i] = reinterpret_cast<const uint4*>(e)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (c + i < K) row[c + i] = e[i];
+  }
+}
+
+// Codes and scale of the 16 threads' block; c is this thread's first column.
+__device__ __forceinline__ void quantise8(const QuantiseArgs& a, int row, int c, float (&v)[kPer], bool& bad) {
+  float amax = fp8::finite_max(v, bad);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const int e = fp8::block_exponent(amax);
+  const float inv = fp8::exp2i(-e);
+  if (c >= a.K) return;
+  const uint2 w = make_uint2(fp8::codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                             fp8::codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+  uint8_t* dst = a.codes + (long long)row * a.cs + c;
+  if (c + kPer <= a.K) {
+    *reinterpret_cast<uint2*>(dst) = w;
+  } else {
+    for (int i = 0; i < a.K - c; ++i) dst[i] = (uint8_t)((i < 4 ? w.x >> (8 * i) : w.y >> (8 * (i - 4))) & 0xffu);
+  }
+  if (c % kBlock == 0) a.scale[(long long)row * a.kblocks + c / kBlock] = fp8::exp2i(e);
+}
+
+// Without a norm: CTA (row, piece of the row).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) fp8_quantise_kernel(const QuantiseArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int row = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * kPer;
+  if (!fp8::valid_row(a.n_rows, a.T, row)) return;
+  float v[kPer];
+  load8<T, VEC>(static_cast<const T*>(a.x) + row * a.xs, c, a.K, v);
+  if (a.res) {
+    float r[kPer];
+    load8<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c, a.K, r);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = rounded(v[i] + r[i], (T*)nullptr);
+    store8<T, VEC>(static_cast<T*>(a.total) + row * a.ts, c, a.K, v);
+  }
+  bool bad = false;
+  quantise8(a, row, c, v, bad);
+  if (bad) flag_status(a.status, kDevNonfinite);
+}
+
+// With a norm: a CTA takes a row. HELD: the row's columns stay in registers (8 a thread); otherwise they are read again.
+template <typename T, bool VEC, bool HELD>
+__global__ void __launch_bounds__(1024) fp8_norm_quantise_kernel(const QuantiseArgs a) {
+  __shared__ float red[32];
+  pdl_trigger();
+  pdl_wait();
+  const int row = blockIdx.x, step = blockDim.x * kPer;
+  if (!fp8::valid_row(a.n_rows, a.T, row)) return;
+  const T* x = static_cast<const T*>(a.x) + row * a.xs;
+  T* total = static_cast<T*>(a.total) + row * a.ts;
+  float v[kPer], g[kPer], ss = 0.f;
+  if (HELD) load8<T, VEC>(static_cast<const T*>(a.gain), threadIdx.x * kPer, a.K, g);
+  for (int c = threadIdx.x * kPer; c < a.K || HELD; c += step) {
+    load8<T, VEC>(x, c, a.K, v);
+    if (a.res) {
+      float r[kPer];
+      load8<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c, a.K, r);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = rounded(v[i] + r[i], (T*)nullptr);
+      store8<T, VEC>(total, c, a.K, v);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) ss = fmaf(v[i], v[i], ss);
+    if (HELD) break;
+  }
+  const float inv = rsqrtf(block_sum(ss, red) / (float)a.K + a.eps);
+  bool bad = false;
+  // whole blocks of threads walk together: the maximum is taken by all lanes
+  for (int c = threadIdx.x * kPer; c - (int)(threadIdx.x * kPer) < a.K; c += step) {
+    if (!HELD) {
+      load8<T, VEC>(a.res ? total : x, c, a.K, v);  // this thread's own stores
+      load8<T, VEC>(static_cast<const T*>(a.gain), c, a.K, g);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = v[i] * inv * g[i];
+    quantise8(a, row, c, v, bad);
+  }
+  if (bad) flag_status(a.status, kDevNonfinite);
+}
+
+// A weight's block of 128 x 128: one CTA, two threads a row.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_weight_kernel(const T* w, long long ws, int N, int K, uint8_t* codes, long long cs, float* scale,
+                                                         int* status) {
+  __shared__ float red[8];
+  pdl_wait();
+  const int n = blockIdx.y * kBlock + (threadIdx.x >> 1), k0 = blockIdx.x * kBlock + (threadIdx.x & 1) * 64;
+  float amax = 0.f;
+  bool bad = false;
+  for (int k = k0; k < k0 + 64; ++k) {
+    if (n >= N || k >= K) break;
+    const float v = fabsf(to_f32(w[n * ws + k]));
+    if (v <= 3.402823466e38f)
+      amax = fmaxf(amax, v);
+    else
+      bad = true;
+  }
+  amax = warp_max(amax);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  __syncthreads();
+  amax = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) amax = fmaxf(amax, red[i]);
+  const int e = fp8::block_exponent(amax);
+  const float inv = fp8::exp2i(-e);
+  for (int k = k0; k < k0 + 64; ++k) {
+    if (n >= N || k >= K) break;
+    float v = to_f32(w[n * ws + k]);
+    v = fabsf(v) <= 3.402823466e38f ? v * inv : __uint_as_float(0x7fffffffu);
+    codes[n * cs + k] = (uint8_t)(fp8::codes4(v, 0.f, 0.f, 0.f) & 0xffu);
+  }
+  if (threadIdx.x == 0) scale[(long long)blockIdx.y * gridDim.x + blockIdx.x] = fp8::exp2i(e);
+  if (bad) flag_status(status, kDevNonfinite);
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_quantise(const QuantiseArgs& a, cudaStream_t s) {
+  const int threads = (a.K + kPer - 1) / kPer;
+  if (!a.gain) {
+    const int t = std::min(256, (threads + 31) / 32 * 32);
+    return launch_pdl(fp8_quantise_kernel<T, VEC>, dim3(a.rows, (threads + t - 1) / t), dim3(t), 0, s, a);
+  }
+  const int t = std::min(1024, (threads + 31) / 32 * 32);
+  return threads <= t ? launch_pdl(fp8_norm_quantise_kernel<T, VEC, true>, dim3(a.rows), dim3(t), 0, s, a)
+                      : launch_pdl(fp8_norm_quantise_kernel<T, VEC, false>, dim3(a.rows), dim3(t), 0, s, a);
+}
+
+}  // namespace
+}  // namespace dlite
+
+extern "C" int dlite_fp8_quantise(const dlite_fp8_quantise_args* g, dlite_stream_t stream) {
+  using namespace dlite;
+  if (!g || !g->x || !g->codes || !g->scale || (g->residual != nullptr) != (g->total != nullptr)) return DLITE_ERR_INVALID_ARG;
+  if (g->B < 1 || g->T < 1 || g->K < 1 || (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16)) return DLITE_ERR_INVALID_ARG;
+  if (g->gain && !(g->eps >= 0.f && g->eps <= 3.402823466e38f)) return DLITE_ERR_INVALID_ARG;
+  const int es = g->dtype == DLITE_F32 ? 4 : 2, V = 16 / es;
+  if (((uintptr_t)g->x | (uintptr_t)g->residual | (uintptr_t)g->total | (uintptr_t)g->gain) % es || !aligned4(g->scale, g->n_rows, g->status) ||
+      ((uintptr_t)g->codes & 15))
+    return DLITE_ERR_INVALID_ARG;
+  if (g->x_stride < g->K || g->codes_stride < g->K || g->codes_stride % 16) return DLITE_ERR_INVALID_ARG;
+  if (g->residual && (g->residual_stride < g->K || g->total_stride < g->K)) return DLITE_ERR_INVALID_ARG;
+  if ((g->total == g->residual && g->total_stride != g->residual_stride) || (g->total == g->x && g->total_stride != g->x_stride))
+    return DLITE_ERR_INVALID_ARG;
+  if ((long long)g->B * g->T > 0x7fffffffLL || g->K > DLITE_FP8_MAX_K) return DLITE_ERR_UNSUPPORTED_SHAPE;
+  QuantiseArgs a = {};
+  a.rows = g->B * g->T;
+  a.T = g->T;
+  a.K = g->K;
+  a.kblocks = fp8::blocks_of(g->K);
+  a.x = g->x;
+  a.xs = g->x_stride;
+  a.res = g->residual;
+  a.rs = g->residual_stride;
+  a.total = g->total;
+  a.ts = g->total_stride;
+  a.gain = g->gain;
+  a.eps = g->eps;
+  a.codes = g->codes;
+  a.cs = g->codes_stride;
+  a.scale = g->scale;
+  a.n_rows = g->n_rows;
+  a.status = g->status;
+  const bool vec = !(((uintptr_t)g->x | (uintptr_t)g->residual | (uintptr_t)g->total | (uintptr_t)g->gain) & 15) && g->K % kPer == 0 &&
+                   g->x_stride % V == 0 && (!g->residual || (g->residual_stride % V == 0 && g->total_stride % V == 0));
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (g->dtype == DLITE_F32)
+    return launch_status(vec ? launch_quantise<float, true>(a, s) : launch_quantise<float, false>(a, s));
+  return launch_status(vec ? launch_quantise<bf16, true>(a, s) : launch_quantise<bf16, false>(a, s));
+}
+
+extern "C" int dlite_fp8_weight(const dlite_fp8_weight_args* g, dlite_stream_t stream) {
+  using namespace dlite;
+  if (!g || !g->w || !g->codes || !g->scale || g->N < 1 || g->K < 1) return DLITE_ERR_INVALID_ARG;
+  if (g->dtype != DLITE_F32 && g->dtype != DLITE_BF16) return DLITE_ERR_INVALID_ARG;
+  if ((uintptr_t)g->w % (g->dtype == DLITE_F32 ? 4 : 2) || !aligned4(g->scale, g->status) || ((uintptr_t)g->codes & 15)) return DLITE_ERR_INVALID_ARG;
+  if (g->w_stride < g->K || g->codes_stride < g->K || g->codes_stride % 16) return DLITE_ERR_INVALID_ARG;
+  if (g->K > DLITE_FP8_MAX_K || g->N > DLITE_FP8_MAX_N) return DLITE_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid(fp8::blocks_of(g->K), fp8::blocks_of(g->N));
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (g->dtype == DLITE_F32)
+    return launch_status(launch_pdl(fp8_weight_kernel<float>, grid, dim3(256), 0, s, static_cast<const float*>(g->w), (long long)g->w_stride, g->N,
+                                    g->K, g->codes, (long long)g->codes_stride, g->scale, g->status));
+  return launch_status(launch_pdl(fp8_weight_kernel<bf16>, grid, dim3(256), 0, s, static_cast<const bf16*>(g->w), (long long)g->w_stride, g->N, g->K,
+                                  g->codes, (long long)g->codes_stride, g->scale, g->status));
+}

@@ -593,6 +593,97 @@ typedef struct {
 } dlite_logprobs_args;
 int dlite_token_logprobs(const dlite_logprobs_args *args, dlite_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Products with 8-bit weights: the projections and the gated feed-forward block of the target's rows, whose time at a verification
+ * block's sizes is the reading of the weights. The common rules of the target-side calls hold (rows, n_rows, status).
+ * Numbers are e4m3 codes with a scale per block of DLITE_FP8_BLOCK:
+ *   activations  codes [B, T, K] and scale [B T][ceil(K / 128)] float32, one per 128 columns of a row
+ *   weights      codes [N, K] and scale [ceil(N / 128)][ceil(K / 128)] float32 (any finite numbers), one per 128 x 128 elements
+ * A code's value is code x scale. Code rows start on 16 bytes: 16-byte aligned memory, strides (in bytes) a multiple of 16;
+ * bytes of a row past its columns are neither read into a result nor written. Scales are dense.
+ * Quantisation: scale = 2^e, the least with max |x| <= 448 2^e, e >= -126; code = e4m3(x 2^-e) to nearest, ties to even.
+ * The format holds no infinity: what is not finite becomes NaN, does not count for the maximum, and flags DLITE_DEV_NONFINITE; a
+ * NaN code makes the results of its row (of a weight: of its output) NaN and no others. Sums of a product are float32, each block's
+ * scaled by the float32 product of its two scales and added in order of the blocks (a few runs of blocks added in order where rows are few):
+ * the same bits run to run. */
+#define DLITE_FP8_BLOCK 128
+#define DLITE_FP8_MAX_K (1 << 20)
+#define DLITE_FP8_MAX_N (1 << 22)
+#define DLITE_FP8_MAX_ROWS (1 << 22) /* B T of a product */
+
+/* Rows into codes. With residual: total = x + residual, rounded to dtype, is stored and takes x's place below (total may be
+ * residual or x themselves, with their stride; otherwise they do not overlap). With gain [K]: y = x gain / sqrt(mean x^2 + eps) in float32 takes its
+ * place. Then codes and scale of it. Elements past float32's square root (1.8e19) overflow the norm's sum. */
+typedef struct {
+    int B, T, K;          /* K <= DLITE_FP8_MAX_K */
+    int dtype;            /* of x, residual, total and gain */
+    const void *x;        /* [B, T, K] */
+    int64_t x_stride;
+    const void *residual; /* [B, T, K] or NULL */
+    int64_t residual_stride;
+    void *total;          /* with residual, else NULL */
+    int64_t total_stride;
+    const void *gain;     /* [K] or NULL */
+    float eps;            /* >= 0, finite */
+    uint8_t *codes;       /* out */
+    int64_t codes_stride;
+    float *scale;         /* out */
+    const int32_t *n_rows;
+    int *status;
+} dlite_fp8_quantise_args;
+int dlite_fp8_quantise(const dlite_fp8_quantise_args *args, dlite_stream_t stream);
+
+/* A weight w [N, K] into codes and scales of 128 x 128 blocks (once, where a model is loaded). */
+typedef struct {
+    int N, K;             /* N <= DLITE_FP8_MAX_N */
+    int dtype;            /* of w */
+    const void *w;        /* [N, K] */
+    int64_t w_stride;
+    uint8_t *codes;       /* out */
+    int64_t codes_stride;
+    float *scale;         /* out */
+    int *status;
+} dlite_fp8_weight_args;
+int dlite_fp8_weight(const dlite_fp8_weight_args *args, dlite_stream_t stream);
+
+/* out[b, t, n] = sum_k x[b, t, k] w[n, k], rounded once to dtype. */
+typedef struct {
+    int B, T, K, N;
+    int dtype;            /* of out */
+    const uint8_t *codes; /* x */
+    int64_t codes_stride;
+    const float *scale;
+    const uint8_t *w;
+    int64_t w_stride;
+    const float *w_scale;
+    void *out;            /* [B, T, N] */
+    int64_t out_stride;
+    const int32_t *n_rows;
+    int *status;
+} dlite_fp8_linear_args;
+int dlite_fp8_linear(const dlite_fp8_linear_args *args, dlite_stream_t stream);
+
+/* The gated block's first half: a[b, t, f] = g / (1 + exp(-g)) u with g = x . gate[f], u = x . up[f], in float32, as codes and
+ * scales of a (what dlite_fp8_linear takes as x of the down projection). */
+typedef struct {
+    int B, T, K, F;
+    const uint8_t *codes; /* x */
+    int64_t codes_stride;
+    const float *scale;
+    const uint8_t *gate;  /* [F, K] */
+    int64_t gate_stride;
+    const float *gate_scale;
+    const uint8_t *up;    /* [F, K] */
+    int64_t up_stride;
+    const float *up_scale;
+    uint8_t *out_codes;   /* [B, T, F] */
+    int64_t out_stride;
+    float *out_scale;     /* [B T][ceil(F / 128)] */
+    const int32_t *n_rows;
+    int *status;
+} dlite_fp8_gated_args;
+int dlite_fp8_gated(const dlite_fp8_gated_args *args, dlite_stream_t stream);
+
 /* Read (and with clear != 0, reset) the sticky device status word.
  * Synchronises `stream`. *status_out gets DLITE_DEV_* bits. Returns
  * DLITE_ERR_DEVICE_TIMEOUT or DLITE_ERR_BOUNDS when those bits are set. */

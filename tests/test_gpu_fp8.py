@@ -1,0 +1,177 @@
+"""GPU: the products with 8-bit weights through the binding, against the CPU oracle in 64 bits. Codes and scales of given
+numbers are compared bit for bit; sums within what float32 sums may be off."""
+import numpy as np
+import pytest
+import torch
+
+from history_free_speculative_gb300 import binding
+from oracle import fp8_oracle as FO
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}     # a rounding's share of the value (bf16: eps / 2 = 2^-8)
+
+
+def _np(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _bytes(t):
+    return t.detach().cpu().contiguous().view(torch.uint8).numpy()
+
+
+def _input(B, T, K, dtype, seed, pad=0, offset=0):
+    """[B, T, K] of columns of different sizes, on the device: dense, or rows K + pad apart, or `offset` elements into its memory."""
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(B, T, K, generator=g) * torch.exp(torch.randn(K, generator=g))).to(DT[dtype])
+    buf = torch.zeros(offset + B * T * (K + pad), dtype=x.dtype, device=DEV)
+    y = buf[offset:].view(B, T, K + pad)[..., :K]
+    y.copy_(x)
+    return y
+
+
+def _weight(N, K, seed, pad=0):
+    """Random codes (no NaN) and scales of any sign and size; rows on 16 bytes, `pad` bytes between them."""
+    g = torch.Generator().manual_seed(seed)
+    pitch = -(-K // 16) * 16 + pad
+    c = torch.randn(N, pitch, generator=g).mul(30).to(torch.float8_e4m3fn).to(DEV)[:, :K]
+    s = (torch.randn(-(-N // 128), -(-K // 128), generator=g).exp() * 1e-2).to(DEV)
+    return c, s
+
+
+def _reach(x, w):
+    """Sum of the products' magnitudes: what a float32 sum's error is relative to."""
+    return np.abs(x) @ np.abs(w).T
+
+
+def _off(kblocks):
+    """What a product may be off, relative to its reach: 128 products of a block (exact) added in the tensor cores, an add cut off at one
+    step of 2^-23; the scales' product and one rounding add a block, up to 8 runs joined: half steps of 2^-24."""
+    return 128 * 2.0 ** -23 + (kblocks + 8 + 2) * 2.0 ** -24
+
+
+def _quantised(c, s, want, err):
+    """Codes and scales as a rounding of numbers within err of `want`: the scale is the rule's for one of them, the values are within half a
+    step."""
+    y, e = FO.blocked(want), FO.blocked(err)
+    hi, lo = np.max(np.abs(y) + e, -1), np.max(np.maximum(np.abs(y) - e, 0), -1)
+    assert np.all(s >= FO.block_scale(lo)) and np.all(s <= FO.block_scale(hi))
+    got = FO.blocked(FO.values(c, s))
+    size = np.maximum((np.abs(y) + e) / s[..., None], 2.0 ** -6)
+    step = 2.0 ** (np.floor(np.log2(size)) - 3) * s[..., None]
+    assert np.all(np.abs(got - y) <= step / 2 + e)
+
+
+# ---------------------------------------------------------------- quantisation
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,K,pad,offset", [(1, 1, 1, 0, 0), (1, 1, 4096, 0, 0), (2, 3, 128, 0, 0), (1, 5, 129, 0, 0), (3, 2, 1000, 0, 0), (2, 4, 777, 3, 0),
+                                              (1, 3, 2560, 64, 0), (2, 2, 512, 0, 1), (1, 2, 12288, 0, 0), (4, 1, 16, 8, 0), (1, 2, 20000, 0, 0)])
+def test_quantise(dtype, B, T, K, pad, offset):
+    x = _input(B, T, K, dtype, K + T, pad, offset)
+    x[0, 0] *= 1e-3
+    c, s = binding.fp8_quantise(x)
+    want, ws = FO.quantise(_np(x))
+    assert np.array_equal(_np(s), ws)
+    assert np.array_equal(_bytes(c), want)
+
+
+def test_quantise_borders():
+    """The scale's borders, zeros, subnormal numbers, the largest ones, ties of the codes."""
+    f = torch.finfo(torch.float32)
+    tops = [0.0, 448.0, float(np.nextafter(np.float32(448), np.float32(1e9))), 447.9, 224.0, 1e-45, f.tiny, 448 * 2.0 ** -126, 449 * 2.0 ** -126, f.max, 1.0, 2.0 ** -120]
+    grid = torch.from_numpy((FO.E4M3[:-1] + FO.E4M3[1:]) / 2).float()      # 126 ties
+    x = torch.zeros(1, len(tops), 128)
+    for i, t in enumerate(tops):
+        x[0, i, 1:127] = grid * (t / 448 if t > 1e-30 else 0.0)
+        x[0, i, 3::2] *= -1
+        x[0, i, 0] = t
+    c, s = binding.fp8_quantise(x.to(DEV))
+    want, ws = FO.quantise(x.double().numpy())
+    assert np.array_equal(_np(s), ws) and np.array_equal(_bytes(c), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [256, 1000, 9000])
+def test_quantise_of_what_is_not_finite(dtype, K):
+    x = _input(1, 3, K, dtype, 5)
+    x[0, 1, 3], x[0, 1, 130], x[0, 1, 131] = float("nan"), float("inf"), float("-inf")
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c, s = binding.fp8_quantise(x, status=st)
+    want, ws = FO.quantise(_np(x))
+    assert np.array_equal(_np(s), ws) and np.array_equal(_bytes(c) & 0x7F, want & 0x7F)
+    assert int(st.item()) == binding.DEV_NONFINITE
+    fin = np.isfinite(_np(x))
+    assert np.array_equal(_bytes(c)[fin], want[fin])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,K,pad", [(1, 1, 4096, 0), (2, 3, 1000, 0), (1, 4, 130, 6), (1, 2, 9728, 0), (1, 2, 8200, 8), (2, 1, 8, 0), (1, 1, 1, 0)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_and_quantise(dtype, B, T, K, pad, residual):
+    x, gain = _input(B, T, K, dtype, 1, pad), _input(1, 1, K, dtype, 2)[0, 0]
+    res = _input(B, T, K, dtype, 3, 2 * pad) if residual else None
+    total = torch.full((B, T, K), 7.0, dtype=DT[dtype], device=DEV) if residual else None
+    c, s = binding.fp8_quantise(x, gain=gain, eps=1e-5, residual=res, total=total)
+    v = _np(x)
+    if residual:
+        v = FO.total(v, _np(res), dtype)
+        assert np.array_equal(_np(total), v)
+    y = FO.norm(v, _np(gain), 1e-5)
+    # the sum of squares: 8 a thread and round, two rounds at most, ten joins; its root halves that; mean, eps; rsqrt 2 steps; two products
+    err = ((16 + 10) / 2 + 2 + 4 + 2) * 2.0 ** -24 * np.abs(y)
+    _quantised(_bytes(c), _np(s), y, err)
+    if residual:      # in place, and without the norm
+        keep = res.clone()
+        binding.fp8_quantise(x, gain=gain, eps=1e-5, residual=res)
+        assert torch.equal(res.contiguous(), total)
+        res.copy_(keep)
+        c, s = binding.fp8_quantise(x, residual=res, total=total)
+        want, ws = FO.quantise(v)
+        assert np.array_equal(_np(total), v) and np.array_equal(_np(s), ws) and np.array_equal(_bytes(c), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K,pad", [(128, 128, 0), (1, 1, 0), (130, 300, 0), (257, 1000, 5), (64, 129, 0)])
+def test_weight(dtype, N, K, pad):
+    w = _input(1, N, K, dtype, 9, pad)[0]
+    c, s = binding.fp8_weight(w)
+    want, ws = FO.quantise_weight(_np(w))
+    assert np.array_equal(_np(s), ws) and np.array_equal(_bytes(c), want)
+    assert c.stride(0) % 16 == 0
+
+
+# ---------------------------------------------------------------- products
+
+SHAPES = [(1, 1, 128, 128), (1, 1, 1, 1), (1, 1, 4096, 4096), (1, 8, 2560, 1000), (1, 7, 100, 129), (3, 3, 129, 64), (1, 33, 384, 200), (2, 64, 1000, 777),
+          (1, 129, 256, 130), (4, 75, 640, 384), (1, 65, 4100, 65), (16, 8, 9728, 256), (1, 200, 16, 5)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,K,N", SHAPES)
+def test_linear(B, T, K, N, out):
+    c, s = binding.fp8_quantise(_input(B, T, K, "f32", K + N))
+    w, ws = _weight(N, K, N)
+    y = binding.fp8_linear(c, s, w, ws, dtype=DT[out])
+    x, wv = FO.values(_bytes(c), _np(s)).reshape(B * T, K), FO.weight_values(_bytes(w), _np(ws))
+    want = x @ wv.T
+    tol = _off(-(-K // 128)) * _reach(x, wv) + HALF[out] * np.abs(want)
+    assert np.all(np.abs(_np(y).reshape(B * T, N) - want) <= tol * 1.0000001)
+    assert torch.equal(binding.fp8_linear(c, s, w, ws, dtype=DT[out]), y)
+
+
+@pytest.mark.parametrize("B,T,K,F", SHAPES)
+def test_gated(B, T, K, F):
+    c, s = binding.fp8_quantise(_input(B, T, K, "bf16", K + F))
+    (g, gs), (u, us) = _weight(F, K, F), _weight(F, K, F + 1, pad=16)
+    gs, us = gs * K ** -0.5, us * K ** -0.5
+    oc, os_ = binding.fp8_gated(c, s, g, gs, u, us)
+    x = FO.values(_bytes(c), _np(s)).reshape(B * T, K)
+    gv, uv = FO.weight_values(_bytes(g), _np(gs)), FO.weight_values(_bytes(u), _np(us))
+    gw, uw, off = x @ gv.T, x @ uv.T, _off(-(-K // 128))
+    ge, ue = off * _reach(x, gv), off * _reach(x, uv)
+    want = FO.silu(gw) * uw
+    # |silu'| < 1.1; exp within 2 steps of 2^-23 and the sum, quotient and product half a step each
+    err = 1.1 * ge * (np.abs(uw) + ue) + np.abs(FO.silu(gw)) * ue + (4 + 3) * 2.0 ** -24 * np.abs(want)
+    _quantised(_bytes(oc).reshape(B * T, F), _np(os_).reshape(B * T, -1), want, err)
