@@ -7,7 +7,7 @@
 
 #include <cuda.h>
 
-#include "internal.h"
+#include "tc_device.cuh"
 
 namespace dlite {
 namespace fp8 {
@@ -59,6 +59,13 @@ __device__ __forceinline__ bool valid_row(const int32_t* n_rows, int T, int row)
   return !n_rows || row % T < n_rows[row / T];
 }
 
+// Instruction descriptor, kind::f8f6f4: float32 sums, e4m3 on both sides, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// The gated activation of two sums.
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
 struct ProductArgs {
   int rows, T;            // rows = B T
   int K, kblocks;
@@ -78,6 +85,10 @@ struct ProductArgs {
 // Map of byte rows [rows, K] of `stride` bytes for boxes of box_rows x 128 bytes under the 128-byte swizzle; columns and rows
 // past the matrix read as 0.
 bool make_map(CUtensorMap* m, const void* base, long long rows, int K, long long stride, int box_rows);
+
+// The kernel for many rows (fp8_pair.cu): boxes of 128 rows of x, 128 (linear) or 64 (gated) weight rows.
+bool use_pairs(const ProductArgs& p, bool gated);
+cudaError_t launch_pairs(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, bool gated, bool f32, cudaStream_t s);
 
 }  // namespace fp8
 }  // namespace dlite

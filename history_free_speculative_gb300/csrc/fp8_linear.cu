@@ -28,10 +28,6 @@ constexpr uint32_t kCols = 256;            // tensor memory: two accumulators of
 constexpr int kPitch = 132;                // floats of a staged row (16-byte stores of a warp's lanes fall on different banks)
 constexpr size_t kSmem = 112 * 1024;       // two CTAs an SM
 
-// Instruction descriptor, kind::f8f6f4: float32 sums, e4m3 on both sides, both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
 __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -137,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
   } else if (live && warp == 1) {  // ---------------- products
-    constexpr uint32_t idesc = idesc_e4m3(128, 128);
+    constexpr uint32_t idesc = fp8::idesc_e4m3(128, 128);
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -230,8 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           g.x += a.x, g.y += a.y, g.z += a.z, g.w += a.w;
           u.x += b.x, u.y += b.y, u.z += b.z, u.w += b.w;
         }
-        float v[4] = {g.x / (1.f + expf(-g.x)) * u.x, g.y / (1.f + expf(-g.y)) * u.y, g.z / (1.f + expf(-g.z)) * u.z,
-                      g.w / (1.f + expf(-g.w)) * u.w};
+        float v[4] = {fp8::gated(g.x, u.x), fp8::gated(g.y, u.y), fp8::gated(g.z, u.z), fp8::gated(g.w, u.w)};
         bool bad = false;
         const float amax = warp_max(fp8::finite_max(v, bad));   // columns past N are 0
         const int e = fp8::block_exponent(amax);
@@ -316,6 +311,14 @@ cudaError_t launch_small(const CUtensorMap& x, const CUtensorMap& w0, const CUte
 template <bool GATED, typename OUT>
 int product(const ProductArgs& p, const void* x, long long x_stride, const void* w0, long long w0_stride, const void* w1, long long w1_stride,
             cudaStream_t s) {
+  if (fp8::use_pairs(p, GATED)) {
+    CUtensorMap mx, m0, m1;
+    const int wbox = GATED ? 64 : 128;
+    if (!fp8::make_map(&mx, x, p.rows, p.K, x_stride, 128) || !fp8::make_map(&m0, w0, p.N, p.K, w0_stride, wbox) ||
+        !fp8::make_map(&m1, w1, p.N, p.K, w1_stride, wbox))
+      return launch_status(cudaErrorInvalidValue);
+    return launch_status(fp8::launch_pairs(mx, m0, m1, p, GATED, sizeof(OUT) == 4, s));
+  }
   const SmallPlan pl = small_plan(p, GATED);
   CUtensorMap mx, m0, m1;
   const int wbox = GATED ? 64 : 128;

@@ -1,0 +1,351 @@
+// The block-scaled products (fp8_linear.cu) for many rows: CTA pairs, 2-SM MMAs.
+//
+// A cluster of two CTAs walks tiles of 256 rows x 256 weight rows. Per k block of 128 columns four tcgen05.mma.cta_group::2
+// kind::f8f6f4 (M = 256, N = 256, K = 32) write one of two accumulators in tensor memory (all its 512 columns); CTA c holds rows 128 c .. of x
+// and rows 128 c .. of the weights in its shared memory and gets its 128 rows over all 256 columns. Eight epilogue warps a CTA take an
+// accumulator times the block's scales into float32 sums in registers (lane = row, 128 columns a thread) while the
+// tensor cores work on the next, so that the scales cost the tensor pipe nothing as long as a block's sums (256 issue slots of
+// packed multiply-adds a scheduler) stay under its 512 cycles of products.
+// Gated: the 256 weight rows are [64 gate | 64 up] twice, so a thread holds 64 gate and 64 up columns of its row, and the two warps of a
+// row exchange one maximum for the scale of its 128 results.
+// Tiles go to the pairs row tiles first: the weights are read from HBM once, x stays in L2.
+#include <algorithm>
+
+#include "fp8.cuh"
+
+namespace dlite {
+namespace {
+
+using fp8::kBlock;
+using fp8::ProductArgs;
+
+constexpr int kThreads = 64 + 256;            // copy warp, MMA warp, eight epilogue warps
+constexpr int kStages = 5;
+constexpr uint32_t kTile = 128 * 128;         // 128 rows of one k block
+constexpr uint32_t kStage = 2 * kTile;        // this CTA's rows of x and of the weights
+constexpr int kPitch = 144;                   // bytes of a staged row: 128 and 16 that take its chunks to other banks
+constexpr uint32_t kStaging = 8 * 32 * kPitch;
+constexpr uint32_t kSmem = 1024 + 1024 + kStages * kStage + kStaging;
+static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
+// Whether one of the 256 rows from row0 on is valid. The whole warp asks.
+__device__ __forceinline__ bool live_tile(const ProductArgs& p, int row0) {
+  if (!p.n_rows) return true;
+  bool any = false;
+  for (int r = row0 + (int)(threadIdx.x & 31); r < min(row0 + 256, p.rows); r += 32) any |= fp8::valid_row(p.n_rows, p.T, r);
+  return __any_sync(0xffffffffu, any);
+}
+
+template <bool GATED, typename OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
+                    const ProductArgs p, const int row_tiles, const int tiles) {
+  // Shared memory: [barriers, row maxima | pad to 1 KB] [stage 0] .. [epilogue staging]; stage = [x tile][weight tile]
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = (uint64_t*)base;
+  const uint32_t full0 = tc::su32(bars), empty0 = full0 + 8 * kStages, accf0 = empty0 + 8 * kStages, acce0 = accf0 + 16, done = acce0 + 16;
+  uint32_t* tmem_holder = (uint32_t*)(bars + 2 * kStages + 5);
+  uint8_t* smem = base + 1024;
+  __shared__ float row_max[2][128];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(full0 + 8 * s, 1);
+      tc::mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(accf0 + 8 * b, 1);
+      tc::mbar_init(acce0 + 8 * b, 16);  // every epilogue warp of both CTAs
+    }
+    tc::mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tmem_holder)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync_all();  // both CTAs' barriers exist before any copy, commit or arrival reaches them
+  tc::fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == 0) {  // ---------------- copies (both CTAs; every one signals rank 0's full barrier)
+    const uint32_t full_leader = tc::map_to_rank(full0, 0);
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
+      if (!live_tile(p, row0)) continue;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (issued >= kStages) ok = tc::mbar_wait_warp(empty0 + 8 * s, ph ^ 1u, p.status);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t st = tc::su32(smem + s * kStage), bar = full_leader + 8 * s;
+          if (rank == 0) tc::mbar_expect_tx(full0 + 8 * s, 2 * kStage);
+          if (GATED) {
+            tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
+            tc::tma_load_2d_pair(st + kTile + kTile / 2, &mw1, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
+          } else {
+            tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 256 + (int)rank * 128);
+          }
+          tc::tma_load_2d_pair(st, &mx, bar, kb * kBlock, row0 + (int)rank * 128);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok && rank == 0)  // the copies in flight end (bounded) before the pair's memory is given back
+      for (int i = 0; i < kStages && i < issued; ++i) {
+        if (s == 0) {
+          s = kStages;
+          ph ^= 1u;
+        }
+        --s;
+        tc::mbar_wait_warp(full0 + 8 * s, ph, p.status);
+      }
+  } else if (warp == 1) {  // ---------------- products (rank 0)
+    if (rank == 0) {
+      constexpr uint32_t idesc = fp8::idesc_e4m3(256, 256);
+      const uint64_t desc0 = tc::sw128_desc(tc::su32(smem));
+      int s = 0, i = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        if (!live_tile(p, (t % row_tiles) * 256)) continue;
+        for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
+          const int b = i & 1;
+          if (i >= 2) ok = tc::mbar_wait_warp(acce0 + 8 * b, (uint32_t)((i >> 1) - 1) & 1u, p.status);
+          ok = ok && tc::mbar_wait_warp(full0 + 8 * s, ph, p.status);
+          if (!ok) break;
+          tc::fence_after();
+          if (lane == 0) {
+            const uint64_t a0 = desc0 + (uint64_t)(kStage >> 4) * s, b0 = a0 + (kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_e4m3_pair(tmem + 256 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
+            tc::umma_commit_pair(empty0 + 8 * s);
+            tc::umma_commit_pair(accf0 + 8 * b);
+          }
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // every product issued has finished before the pair's memory goes
+      if (lane == 0) tc::umma_commit_pair(done);
+      __syncwarp();
+      tc::mbar_wait_warp(done, 0, p.status);
+    }
+  } else {  // ---------------- sums: lane = row, 128 columns a thread
+    const int q = warp & 3, eg = (warp - 2) >> 2;
+    const uint32_t acce_leader = tc::map_to_rank(acce0, 0);
+    uint8_t* staged = smem + kStages * kStage + (warp - 2) * 32 * kPitch;
+    const int nb = fp8::blocks_of(p.N);
+    int i = 0;
+    for (int t = pair; t < tiles; t += pairs) {
+      const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
+      if (!live_tile(p, row0)) continue;
+      const int wrow0 = row0 + (int)rank * 128 + q * 32, row = wrow0 + lane;
+      const float* xs = p.xs + (long long)min(row, p.rows - 1) * p.kblocks;
+      const int wb = GATED ? n0 : min(2 * n0 + eg, nb - 1);      // a block past the last has no columns to write
+      const float* w0 = p.ws[0] + (long long)wb * p.kblocks;
+      const float* w1 = GATED ? p.ws[1] + (long long)wb * p.kblocks : w0;
+      uint64_t acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = 0;
+      float x_next = xs[0], w0_next = w0[0], w1_next = w1[0];
+      bool ok = true;
+      for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
+        const int b = i & 1;
+        const float s0 = x_next * w0_next, s1 = GATED ? x_next * w1_next : s0;
+        if (kb + 1 < p.kblocks) {
+          x_next = xs[kb + 1];
+          w0_next = w0[kb + 1];
+          if (GATED) w1_next = w1[kb + 1];
+        }
+        ok = tc::mbar_wait_warp(accf0 + 8 * b, (uint32_t)(i >> 1) & 1u, p.status);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + 256 * b + 128 * eg;
+        uint32_t v[2][16];
+        tc::tmem_ld16_nowait(t0, v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          tc::tmem_wait_ld();
+          if (c < 7) tc::tmem_ld16_nowait(t0 + 16 * (c + 1), v[(c + 1) & 1]);
+          const float sc = c < 4 ? s0 : s1;
+          const uint64_t sc2 = pack2f(sc, sc);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            acc[8 * c + j] = fma2(pack2f(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc2, acc[8 * c + j]);
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(acce_leader + 8 * b) : "memory");
+      }
+      // the sums leave through this warp's staging, so that neighbouring lanes store neighbouring columns
+      if constexpr (GATED) {
+        float a[64];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          a[2 * j] = fp8::gated(lo2f(acc[j]), lo2f(acc[32 + j]));
+          a[2 * j + 1] = fp8::gated(hi2f(acc[j]), hi2f(acc[32 + j]));
+        }
+        bool bad = false;
+        float amax = fp8::finite_max(a, bad);
+        row_max[eg][q * 32 + lane] = ok ? amax : -1.f;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+        const float other = row_max[eg ^ 1][q * 32 + lane];
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");  // read before the next tile's is written
+        if (!ok || other < 0.f) break;  // where one warp of a row gave up both leave, so that none waits for the other
+        amax = fmaxf(amax, other);
+        const int e = fp8::block_exponent(amax);
+        const float inv = fp8::exp2i(-e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 w;
+          w.x = fp8::codes4(a[16 * j] * inv, a[16 * j + 1] * inv, a[16 * j + 2] * inv, a[16 * j + 3] * inv);
+          w.y = fp8::codes4(a[16 * j + 4] * inv, a[16 * j + 5] * inv, a[16 * j + 6] * inv, a[16 * j + 7] * inv);
+          w.z = fp8::codes4(a[16 * j + 8] * inv, a[16 * j + 9] * inv, a[16 * j + 10] * inv, a[16 * j + 11] * inv);
+          w.w = fp8::codes4(a[16 * j + 12] * inv, a[16 * j + 13] * inv, a[16 * j + 14] * inv, a[16 * j + 15] * inv);
+          *reinterpret_cast<uint4*>(staged + lane * kPitch + 16 * j) = w;
+        }
+        const bool valid = row < p.rows && fp8::valid_row(p.n_rows, p.T, row);
+        if (valid && bad) flag_status(p.status, kDevNonfinite);
+        if (valid && eg == 0) p.scale[(long long)row * nb + n0] = fp8::exp2i(e);
+        const uint32_t valid_rows = __ballot_sync(0xffffffffu, valid);
+        const int n = n0 * 128 + eg * 64 + (lane & 3) * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 8 * j + (lane >> 2);
+          const uint4 w = *reinterpret_cast<const uint4*>(staged + r * kPitch + 16 * (lane & 3));
+          if (!(valid_rows >> r & 1)) continue;
+          uint8_t* dst = p.codes + (long long)(wrow0 + r) * p.cs + n;
+          if (n + 16 <= p.N) {
+            *reinterpret_cast<uint4*>(dst) = w;
+          } else {
+            const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (n + k < p.N) dst[k] = (uint8_t)(word[k >> 2] >> (8 * (k & 3)));
+          }
+        }
+        __syncwarp();
+      } else {
+        if (!ok) break;
+        constexpr int C = 128 / sizeof(OUT), E = 16 / sizeof(OUT);  // columns of a staged piece, of a 16-byte chunk
+        const uint32_t valid_rows = __ballot_sync(0xffffffffu, row < p.rows && fp8::valid_row(p.n_rows, p.T, row));
+#pragma unroll
+        for (int piece = 0; piece < 128 / C; ++piece) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint4 w;
+            const int a0 = (piece * C + j * E) / 2;
+            if constexpr (sizeof(OUT) == 2) {
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(lo2f(acc[a0 + k]), hi2f(acc[a0 + k]));
+                h[k] = *reinterpret_cast<const uint32_t*>(&two);
+              }
+              w = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+              w = make_uint4(__float_as_uint(lo2f(acc[a0])), __float_as_uint(hi2f(acc[a0])), __float_as_uint(lo2f(acc[a0 + 1])),
+                             __float_as_uint(hi2f(acc[a0 + 1])));
+            }
+            *reinterpret_cast<uint4*>(staged + lane * kPitch + 16 * j) = w;
+          }
+          __syncwarp();
+          const int n = n0 * 256 + eg * 128 + piece * C + (lane & 7) * E;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = 4 * j + (lane >> 3);
+            const uint4 w = *reinterpret_cast<const uint4*>(staged + r * kPitch + 16 * (lane & 7));
+            if (!(valid_rows >> r & 1)) continue;
+            OUT* dst = static_cast<OUT*>(p.out) + (long long)(wrow0 + r) * p.os + n;
+            if (p.vec && n + E <= p.N) {
+              *reinterpret_cast<uint4*>(dst) = w;
+            } else {
+              const OUT* e = reinterpret_cast<const OUT*>(&w);
+#pragma unroll
+              for (int k = 0; k < E; ++k)
+                if (n + k < p.N) dst[k] = e[k];
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync_all();  // no copy, commit, arrival or product of the pair is outstanding past this point
+  if (warp == 1) {
+    tc::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+template <bool GATED, typename OUT>
+cudaError_t launch(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, int row_tiles, int tiles, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<GATED, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * std::min(tiles, std::max(1, device_sms() / 2)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<GATED, OUT>, x, w0, w1, p, row_tiles, tiles);
+}
+
+}  // namespace
+
+namespace fp8 {
+
+bool use_pairs(const ProductArgs& p, bool gated) {
+  return p.rows > 256;
+}
+
+cudaError_t launch_pairs(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, bool gated, bool f32,
+                         cudaStream_t s) {
+  const int row_tiles = (p.rows + 255) / 256, tiles = row_tiles * (gated ? blocks_of(p.N) : (p.N + 255) / 256);
+  if (gated) return launch<true, float>(x, w0, w1, p, row_tiles, tiles, s);
+  return f32 ? launch<false, float>(x, w0, w1, p, row_tiles, tiles, s) : launch<false, bf16>(x, w0, w1, p, row_tiles, tiles, s);
+}
+
+}  // namespace fp8
+}  // namespace dlite

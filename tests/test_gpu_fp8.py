@@ -145,7 +145,8 @@ def test_weight(dtype, N, K, pad):
 # ---------------------------------------------------------------- products
 
 SHAPES = [(1, 1, 128, 128), (1, 1, 1, 1), (1, 1, 4096, 4096), (1, 8, 2560, 1000), (1, 7, 100, 129), (3, 3, 129, 64), (1, 33, 384, 200), (2, 64, 1000, 777),
-          (1, 129, 256, 130), (4, 75, 640, 384), (1, 65, 4100, 65), (16, 8, 9728, 256), (1, 200, 16, 5)]
+          (1, 129, 256, 130), (4, 75, 640, 384), (1, 65, 4100, 65), (16, 8, 9728, 256), (1, 200, 16, 5),
+          (1, 513, 1000, 777), (3, 171, 4100, 300), (1, 260, 16, 5), (1, 1025, 384, 2600)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -175,3 +176,97 @@ def test_gated(B, T, K, F):
     # |silu'| < 1.1; exp within 2 steps of 2^-23 and the sum, quotient and product half a step each
     err = 1.1 * ge * (np.abs(uw) + ue) + np.abs(FO.silu(gw)) * ue + (4 + 3) * 2.0 ** -24 * np.abs(want)
     _quantised(_bytes(oc).reshape(B * T, F), _np(os_).reshape(B * T, -1), want, err)
+
+
+# ---------------------------------------------------------------- rows of a ragged batch
+
+@pytest.mark.parametrize("B,T,K,N", [(3, 7, 300, 200), (5, 40, 1000, 130), (6, 90, 640, 520), (2, 700, 256, 256), (4, 1, 128, 64)])
+def test_rows_behind_a_requests_last(B, T, K, N):
+    """Rows t >= n_rows[b] hold anything, NaN codes and scales too: neither do they reach a result nor is one of theirs written."""
+    n = torch.tensor([(b * 5 * T // 7 + (b == 1) * 3) % (T + 1) if b else -4 for b in range(B)], dtype=torch.int32)
+    n[-1] = T + 9                                  # values outside [0, T] are taken to its ends
+    x = _input(B, T, K, "bf16", 1)
+    ok = torch.arange(T)[None] < n[:, None]
+    x[~ok.to(DEV)] = float("nan")
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kw = dict(n_rows=n.to(DEV), status=st)
+    codes = torch.full((B, T, -(-K // 16) * 16), 0x7F, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)[..., :K]
+    scale = torch.full((B, T, -(-K // 128)), float("nan"), device=DEV)
+    res, total = torch.ones_like(x), torch.full_like(x, 5.0)
+    binding.fp8_quantise(x, residual=res, total=total, codes=codes, scale=scale, **kw)
+    v = FO.total(np.where(ok.numpy()[..., None], _np(x), 0), _np(res), "bf16")
+    want, ws = FO.quantise(v)
+    m = ok.numpy()
+    assert np.array_equal(_bytes(codes)[m], want[m]) and np.array_equal(_np(scale)[m], ws[m]) and np.array_equal(_np(total)[m], v[m])
+    assert np.all(_bytes(codes)[~m] == 0x7F) and np.all(np.isnan(_np(scale)[~m])) and np.all(_np(total)[~m] == 5)
+    w, wsc = _weight(N, K, 3)
+    out = torch.full((B, T, N + 8), 3.0, device=DEV)[..., :N]
+    binding.fp8_linear(codes, scale, w, wsc, out=out, **kw)
+    xv, wv = np.where(m[..., None], FO.values(np.where(m[..., None], want, 0), ws), 0), FO.weight_values(_bytes(w), _np(wsc))
+    y = xv @ wv.T
+    tol = _off(-(-K // 128)) * (np.abs(xv) @ np.abs(wv).T) + HALF["f32"] * np.abs(y)
+    got = _np(out)
+    assert np.all(np.abs(got - y)[m] <= tol[m]) and np.all(got[~m] == 3) and bool((out.as_strided((B, T, 8), (T * (N + 8), N + 8, 1), N) == 3).all())
+    F = N
+    oc = torch.full((B, T, -(-F // 16) * 16 + 16), 0x55, dtype=torch.uint8, device=DEV)
+    os_ = torch.full((B, T, -(-F // 128)), 9.0, device=DEV)
+    binding.fp8_gated(codes, scale, w, wsc, w, wsc, out=oc.view(torch.float8_e4m3fn)[..., :F], out_scale=os_, **kw)
+    full, fs = binding.fp8_gated(*binding.fp8_quantise(torch.from_numpy(v).float().to(DEV)), w, wsc, w, wsc)
+    assert np.array_equal(_bytes(oc)[..., :F][m], _bytes(full)[m]) and np.array_equal(_np(os_)[m], _np(fs)[m])
+    assert np.all(_bytes(oc)[~m] == 0x55) and np.all(_bytes(oc)[..., F:] == 0x55) and np.all(_np(os_)[~m] == 9)
+    assert int(st.item()) == 0
+    assert bool((binding.fp8_linear(codes, scale, w, wsc, n_rows=kw["n_rows"])[~ok.to(DEV)] == 0).all())
+
+
+# ---------------------------------------------------------------- strides, alignment, what is not finite
+
+@pytest.mark.parametrize("rows,K,N", [(5, 200, 70), (300, 200, 333)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_strides_of_products(rows, K, N, out):
+    """Codes as a slice of wider rows, weights as a slice of wider ones, outputs off 16 bytes and as a slice: the results of dense ones."""
+    c, s = binding.fp8_quantise(_input(1, rows, K, "bf16", 4))
+    w, ws = _weight(N, K, 5, pad=48)
+    want = binding.fp8_linear(c, s, w, ws, dtype=DT[out])
+    wide = torch.zeros(1, rows, 400, dtype=torch.uint8, device=DEV).fill_(0x7F).view(torch.float8_e4m3fn)
+    cw = wide[..., 16:16 + K]
+    cw.view(torch.uint8).copy_(c.view(torch.uint8))
+    for off, pad in ((0, 0), (1, 0), (0, 3), (8, 16)):
+        buf = torch.full((off + rows * (N + pad),), 2.0, dtype=DT[out], device=DEV)
+        y = buf[off:].view(1, rows, N + pad)[..., :N]
+        assert binding.fp8_linear(cw, s, w, ws, out=y) is y and torch.equal(y, want)
+        assert bool((buf[:off] == 2).all()) and bool((buf[off:].view(rows, N + pad)[:, N:] == 2).all())
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_nan_codes_stay_in_their_row(rows):
+    K, N = 300, 260
+    c, s = binding.fp8_quantise(_input(1, rows, K, "bf16", 4))
+    w, ws = _weight(N, K, 5)
+    y0 = binding.fp8_linear(c, s, w, ws)
+    g0, gs0 = binding.fp8_gated(c, s, w, ws * 0.1, w, ws * 0.1)
+    c.view(torch.uint8)[0, 1, 290] = 0xFF
+    w.view(torch.uint8)[200, 7] = 0x7F
+    y = binding.fp8_linear(c, s, w, ws)
+    hit = torch.zeros(rows, N, dtype=torch.bool, device=DEV)
+    hit[1], hit[:, 200] = True, True
+    assert torch.equal(torch.isnan(y[0]), hit) and torch.equal(y[0][~hit], y0[0][~hit])
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    g, gs = binding.fp8_gated(c, s, w, ws * 0.1, w, ws * 0.1, status=st)
+    assert int(st.item()) == binding.DEV_NONFINITE
+    assert torch.equal((g.view(torch.uint8)[0] & 0x7F) == 0x7F, hit)
+    same = ~hit & (torch.arange(N, device=DEV) // 128 != 1)      # the block of column 200 may have lost its largest
+    assert torch.equal(g.view(torch.uint8)[0][same], g0.view(torch.uint8)[0][same])
+
+
+@pytest.mark.parametrize("rows", [2, 300])
+@pytest.mark.parametrize("size", [-100, -60, 60, 100])
+def test_far_scales(rows, size):
+    """Rows and weights of far sizes whose products are float32 numbers."""
+    K, N = 384, 140
+    x = _input(1, rows, K, "f32", 4)
+    c, s = binding.fp8_quantise(x * 2.0 ** size)
+    c0, s0 = binding.fp8_quantise(x)
+    w, ws = _weight(N, K, 5)
+    assert torch.equal(c.view(torch.uint8), c0.view(torch.uint8)) and torch.equal(s, s0 * 2.0 ** size)
+    y, y0 = (binding.fp8_linear(c, a, w, b, dtype=torch.float32) for a, b in ((s, ws * 2.0 ** -size), (s0, ws)))
+    assert torch.equal(y, y0)
