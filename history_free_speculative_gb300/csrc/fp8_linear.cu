@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         w0_next = w0[j + 1];
         if (GATED) w1_next = w1[j + 1];
       }
-      ok = tc::mbar_wait_warp(accf0 + 8 * b, (uint32_t)(j >> 1) & 1u, p.status);
+      ok = fp8::wait_all(accf0 + 8 * b, (uint32_t)(j >> 1) & 1u, p.status);
       if (!ok) break;
       tc::fence_after();
       const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + 128 * b;

@@ -19,7 +19,10 @@ namespace {
 using fp8::kBlock;
 using fp8::ProductArgs;
 
-constexpr int kThreads = 64 + 256;            // copy warp, MMA warp, eight epilogue warps
+constexpr int kThreads = 128 + 256;           // copy warp, MMA warp, two that only make up the warpgroup; eight epilogue warps
+// Registers a thread: the epilogue's sums (128) and two loads of 32 columns in flight need more than the launch's 168.
+// 128 x 56 + 256 x 224 = 384 x 168, what the CTA was launched with.
+constexpr int kRegsFew = 56, kRegsMany = 224;
 constexpr int kStages = 5;
 constexpr uint32_t kTile = 128 * 128;         // 128 rows of one k block
 constexpr uint32_t kStage = 2 * kTile;        // this CTA's rows of x and of the weights
@@ -86,83 +89,87 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   pdl_wait();
 
-  if (warp == 0) {  // ---------------- copies (both CTAs; every one signals rank 0's full barrier)
-    const uint32_t full_leader = tc::map_to_rank(full0, 0);
-    int s = 0, issued = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int t = pair; t < tiles && ok; t += pairs) {
-      const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
-      if (!live_tile(p, row0)) continue;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
-        if (issued >= kStages) ok = tc::mbar_wait_warp(empty0 + 8 * s, ph ^ 1u, p.status);
-        if (!ok) break;
-        if (lane == 0) {
-          const uint32_t st = tc::su32(smem + s * kStage), bar = full_leader + 8 * s;
-          if (rank == 0) tc::mbar_expect_tx(full0 + 8 * s, 2 * kStage);
-          if (GATED) {
-            tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
-            tc::tma_load_2d_pair(st + kTile + kTile / 2, &mw1, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
-          } else {
-            tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 256 + (int)rank * 128);
-          }
-          tc::tma_load_2d_pair(st, &mx, bar, kb * kBlock, row0 + (int)rank * 128);
-        }
-        __syncwarp();
-        ++issued;
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-    }
-    if (!ok && rank == 0)  // the copies in flight end (bounded) before the pair's memory is given back
-      for (int i = 0; i < kStages && i < issued; ++i) {
-        if (s == 0) {
-          s = kStages;
-          ph ^= 1u;
-        }
-        --s;
-        tc::mbar_wait_warp(full0 + 8 * s, ph, p.status);
-      }
-  } else if (warp == 1) {  // ---------------- products (rank 0)
-    if (rank == 0) {
-      constexpr uint32_t idesc = fp8::idesc_e4m3(256, 256);
-      const uint64_t desc0 = tc::sw128_desc(tc::su32(smem));
-      int s = 0, i = 0;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 0) {  // ---------------- copies (both CTAs; every one signals rank 0's full barrier)
+      const uint32_t full_leader = tc::map_to_rank(full0, 0);
+      int s = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs) {
-        if (!live_tile(p, (t % row_tiles) * 256)) continue;
-        for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
-          const int b = i & 1;
-          if (i >= 2) ok = tc::mbar_wait_warp(acce0 + 8 * b, (uint32_t)((i >> 1) - 1) & 1u, p.status);
-          ok = ok && tc::mbar_wait_warp(full0 + 8 * s, ph, p.status);
+        const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
+        if (!live_tile(p, row0)) continue;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (issued >= kStages) ok = tc::mbar_wait_warp(empty0 + 8 * s, ph ^ 1u, p.status);
           if (!ok) break;
-          tc::fence_after();
           if (lane == 0) {
-            const uint64_t a0 = desc0 + (uint64_t)(kStage >> 4) * s, b0 = a0 + (kTile >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_e4m3_pair(tmem + 256 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
-            tc::umma_commit_pair(empty0 + 8 * s);
-            tc::umma_commit_pair(accf0 + 8 * b);
+            const uint32_t st = tc::su32(smem + s * kStage), bar = full_leader + 8 * s;
+            if (rank == 0) tc::mbar_expect_tx(full0 + 8 * s, 2 * kStage);
+            if (GATED) {
+              tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
+              tc::tma_load_2d_pair(st + kTile + kTile / 2, &mw1, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
+            } else {
+              tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 256 + (int)rank * 128);
+            }
+            tc::tma_load_2d_pair(st, &mx, bar, kb * kBlock, row0 + (int)rank * 128);
           }
           __syncwarp();
+          ++issued;
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      // every product issued has finished before the pair's memory goes
-      if (lane == 0) tc::umma_commit_pair(done);
-      __syncwarp();
-      tc::mbar_wait_warp(done, 0, p.status);
+      if (!ok && rank == 0)  // the copies in flight end (bounded) before the pair's memory is given back
+        for (int i = 0; i < kStages && i < issued; ++i) {
+          if (s == 0) {
+            s = kStages;
+            ph ^= 1u;
+          }
+          --s;
+          tc::mbar_wait_warp(full0 + 8 * s, ph, p.status);
+        }
+    } else if (warp == 1) {  // ---------------- products (rank 0)
+      if (rank == 0) {
+        constexpr uint32_t idesc = fp8::idesc_e4m3(256, 256);
+        const uint64_t desc0 = tc::sw128_desc(tc::su32(smem));
+        int s = 0, i = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+          if (!live_tile(p, (t % row_tiles) * 256)) continue;
+          for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
+            const int b = i & 1;
+            if (i >= 2) ok = fp8::wait_all(acce0 + 8 * b, (uint32_t)((i >> 1) - 1) & 1u, p.status);
+            ok = ok && fp8::wait_all(full0 + 8 * s, ph, p.status);
+            if (!ok) break;
+            tc::fence_after();
+            if (lane == 0) {
+              const uint64_t a0 = desc0 + (uint64_t)(kStage >> 4) * s, b0 = a0 + (kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) umma_e4m3_pair(tmem + 256 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
+              tc::umma_commit_pair(empty0 + 8 * s);
+              tc::umma_commit_pair(accf0 + 8 * b);
+            }
+            __syncwarp();
+            if (++s == kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        // every product issued has finished before the pair's memory goes
+        if (lane == 0) tc::umma_commit_pair(done);
+        __syncwarp();
+        tc::mbar_wait_warp(done, 0, p.status);
+      }
     }
   } else {  // ---------------- sums: lane = row, 128 columns a thread
-    const int q = warp & 3, eg = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+    const int q = warp & 3, eg = (warp - 4) >> 2;
     const uint32_t acce_leader = tc::map_to_rank(acce0, 0);
-    uint8_t* staged = smem + kStages * kStage + (warp - 2) * 32 * kPitch;
+    uint8_t* staged = smem + kStages * kStage + (warp - 4) * 32 * kPitch;
     const int nb = fp8::blocks_of(p.N);
     int i = 0;
     for (int t = pair; t < tiles; t += pairs) {
@@ -186,26 +193,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           w0_next = w0[kb + 1];
           if (GATED) w1_next = w1[kb + 1];
         }
-        ok = tc::mbar_wait_warp(accf0 + 8 * b, (uint32_t)(i >> 1) & 1u, p.status);
+        ok = fp8::wait_all(accf0 + 8 * b, (uint32_t)(i >> 1) & 1u, p.status);
         if (!ok) break;
         tc::fence_after();
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + 256 * b + 128 * eg;
-        uint32_t v[2][16];
-        tc::tmem_ld16_nowait(t0, v[0]);
+        uint32_t v[2][32];
+        fp8::tmem_ld32(t0, v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
           tc::tmem_wait_ld();
-          if (c < 7) tc::tmem_ld16_nowait(t0 + 16 * (c + 1), v[(c + 1) & 1]);
-          const float sc = c < 4 ? s0 : s1;
+          if (c < 3) fp8::tmem_ld32(t0 + 32 * (c + 1), v[(c + 1) & 1]);
+          const float sc = c < 2 ? s0 : s1;
           const uint64_t sc2 = pack2f(sc, sc);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[8 * c + j] = fma2(pack2f(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc2, acc[8 * c + j]);
+          for (int j = 0; j < 16; ++j)
+            acc[16 * c + j] = fma2(pack2f(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc2, acc[16 * c + j]);
         }
         tc::fence_before();
         __syncwarp();
         if (lane == 0)
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(acce_leader + 8 * b) : "memory");
+          // what it hands over was read from tensor memory, which tcgen05.fence orders: a release of the generic memory, at
+          // the cluster's scope, doubled the kernel's time
+          asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(acce_leader + 8 * b) : "memory");
       }
       // the sums leave through this warp's staging, so that neighbouring lanes store neighbouring columns
       if constexpr (GATED) {
