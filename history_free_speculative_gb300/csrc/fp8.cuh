@@ -66,6 +66,29 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
 // The gated activation of two sums.
 __device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
+// One lane of a converged warp. Copies and products take their operands from uniform registers; in a branch on the lane's
+// number each of them took 100 clocks to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+// Whether a phase is over, without waiting for it.
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // 32 columns of tensor memory, not waited for.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* staged = (float*)smem;
 
   if (live && warp == 0) {  // ---------------- copies
-    if (lane == 0) {
+    if (fp8::elect_one()) {
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -133,33 +133,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
   } else if (live && warp == 1) {  // ---------------- products
-    constexpr uint32_t idesc = fp8::idesc_e4m3(128, 128);
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int j = 0; j < kn && ok; ++j) {
-      const int b = j & 1;
-      if (j >= 2) ok = tc::mbar_wait_warp(acce0 + 8 * b, (uint32_t)((j >> 1) - 1) & 1u, p.status);
-      ok = ok && tc::mbar_wait_warp(full0 + 8 * s, ph, p.status);
-      if (!ok) break;
-      tc::fence_after();
-      if (lane == 0) {
+    if (fp8::elect_one()) {
+      constexpr uint32_t idesc = fp8::idesc_e4m3(128, 128);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int j = 0; j < kn; ++j) {
+        const int b = j & 1;
+        if (j >= 2 && !tc::mbar_wait(acce0 + 8 * b, (uint32_t)((j >> 1) - 1) & 1u, p.status)) break;
+        if (!tc::mbar_wait(full0 + 8 * s, ph, p.status)) break;
+        tc::fence_after();
         const uint64_t a0 = tc::sw128_desc(tc::su32(smem + (size_t)s * stage_bytes)), b0 = a0 + (pl.a_bytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + 128 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
-        tc::umma_commit(empty0 + 8 * s);
         tc::umma_commit(accf0 + 8 * b);
+        tc::umma_commit(empty0 + 8 * s);
+        if (++s == pl.stages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      __syncwarp();
-      if (++s == pl.stages) {
-        s = 0;
-        ph ^= 1u;
-      }
+      // every product issued has finished before the stages and the tensor memory go
+      tc::umma_commit(done);
+      tc::mbar_wait(done, 0, p.status);
     }
-    // every product issued has finished before the stages and the tensor memory go
-    if (lane == 0) tc::umma_commit(done);
     __syncwarp();
-    tc::mbar_wait_warp(done, 0, p.status);
   } else if (live && (warp & 3) < quads) {  // ---------------- sums: lane = row
     const int q = warp & 3, r = q * 32 + lane;
     const float* xs = p.xs + (long long)(row0 + min(r, rows - 1)) * p.kblocks + kb0;

@@ -40,12 +40,17 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d, uint64_t a, uint64_t 
       : "memory");
 }
 
-// Whether one of the 256 rows from row0 on is valid. The whole warp asks.
+constexpr int kMaxRowTiles = DLITE_FP8_MAX_ROWS / 256;
+
+// Whether one of the 256 rows from row0 on is valid.
 __device__ __forceinline__ bool live_tile(const ProductArgs& p, int row0) {
-  if (!p.n_rows) return true;
-  bool any = false;
-  for (int r = row0 + (int)(threadIdx.x & 31); r < min(row0 + 256, p.rows); r += 32) any |= fp8::valid_row(p.n_rows, p.T, r);
-  return __any_sync(0xffffffffu, any);
+  const int end = min(row0 + 256, p.rows);
+  for (int r = row0; r < end;) {
+    const int b = r / p.T, t = r - b * p.T;
+    if (t < p.n_rows[b]) return true;
+    r += p.T - t;
+  }
+  return false;
 }
 
 template <bool GATED, typename OUT>
@@ -60,6 +65,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = (uint32_t*)(bars + 2 * kStages + 5);
   uint8_t* smem = base + 1024;
   __shared__ float row_max[2][128];
+  __shared__ uint32_t live[kMaxRowTiles / 32];  // row tiles with a valid row
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_rank();
@@ -88,32 +94,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_holder;
   pdl_trigger();
   pdl_wait();
+  if (p.n_rows) {
+    for (int i = threadIdx.x; i < (row_tiles + 31) / 32 * 32; i += kThreads) {  // whole warps
+      const uint32_t bits = __ballot_sync(0xffffffffu, i < row_tiles && live_tile(p, i * 256));
+      if (lane == 0) live[i >> 5] = bits;
+    }
+    __syncthreads();
+  }
+  auto skip = [&](int t) { return p.n_rows && !(live[(t % row_tiles) >> 5] >> ((t % row_tiles) & 31) & 1); };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
-    if (warp == 0) {  // ---------------- copies (both CTAs; every one signals rank 0's full barrier)
+    if (warp == 0 && fp8::elect_one()) {  // ---------------- copies (both CTAs; every one signals rank 0's full barrier)
       const uint32_t full_leader = tc::map_to_rank(full0, 0);
       int s = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs) {
         const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
-        if (!live_tile(p, row0)) continue;
+        if (skip(t)) continue;
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (issued >= kStages) ok = tc::mbar_wait_warp(empty0 + 8 * s, ph ^ 1u, p.status);
+          if (issued >= kStages) ok = tc::mbar_wait(empty0 + 8 * s, ph ^ 1u, p.status);
           if (!ok) break;
-          if (lane == 0) {
-            const uint32_t st = tc::su32(smem + s * kStage), bar = full_leader + 8 * s;
-            if (rank == 0) tc::mbar_expect_tx(full0 + 8 * s, 2 * kStage);
-            if (GATED) {
-              tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
-              tc::tma_load_2d_pair(st + kTile + kTile / 2, &mw1, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
-            } else {
-              tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 256 + (int)rank * 128);
-            }
-            tc::tma_load_2d_pair(st, &mx, bar, kb * kBlock, row0 + (int)rank * 128);
+          const uint32_t st = tc::su32(smem + s * kStage), bar = full_leader + 8 * s;
+          if (rank == 0) tc::mbar_expect_tx(full0 + 8 * s, 2 * kStage);
+          if (GATED) {
+            tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
+            tc::tma_load_2d_pair(st + kTile + kTile / 2, &mw1, bar, kb * kBlock, n0 * 128 + (int)rank * 64);
+          } else {
+            tc::tma_load_2d_pair(st + kTile, &mw0, bar, kb * kBlock, n0 * 256 + (int)rank * 128);
           }
-          __syncwarp();
+          tc::tma_load_2d_pair(st, &mx, bar, kb * kBlock, row0 + (int)rank * 128);
           ++issued;
           if (++s == kStages) {
             s = 0;
@@ -128,42 +139,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1u;
           }
           --s;
-          tc::mbar_wait_warp(full0 + 8 * s, ph, p.status);
+          tc::mbar_wait(full0 + 8 * s, ph, p.status);
         }
-    } else if (warp == 1) {  // ---------------- products (rank 0)
-      if (rank == 0) {
-        constexpr uint32_t idesc = fp8::idesc_e4m3(256, 256);
-        const uint64_t desc0 = tc::sw128_desc(tc::su32(smem));
-        int s = 0, i = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
-          if (!live_tile(p, (t % row_tiles) * 256)) continue;
-          for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
-            const int b = i & 1;
-            if (i >= 2) ok = fp8::wait_all(acce0 + 8 * b, (uint32_t)((i >> 1) - 1) & 1u, p.status);
-            ok = ok && fp8::wait_all(full0 + 8 * s, ph, p.status);
+    } else if (warp == 1 && rank == 0 && fp8::elect_one()) {  // ---------------- products
+      constexpr uint32_t idesc = fp8::idesc_e4m3(256, 256);
+      const uint64_t desc0 = tc::sw128_desc(tc::su32(smem));
+      // The tensor pipe stands still from the last product of a block to the first of the next if this lane is late: the barriers of
+      // the next block are looked at before the last product.
+      int s = 0, i = 0;
+      uint32_t ph = 0;
+      bool ok = true, ready = false;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        if (skip(t)) continue;
+        for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
+          const int b = i & 1;
+          if (!ready) {
+            ok = (i < 2 || tc::mbar_wait(acce0 + 8 * b, (uint32_t)((i >> 1) - 1) & 1u, p.status)) && tc::mbar_wait(full0 + 8 * s, ph, p.status);
             if (!ok) break;
-            tc::fence_after();
-            if (lane == 0) {
-              const uint64_t a0 = desc0 + (uint64_t)(kStage >> 4) * s, b0 = a0 + (kTile >> 4);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) umma_e4m3_pair(tmem + 256 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
-              tc::umma_commit_pair(empty0 + 8 * s);
-              tc::umma_commit_pair(accf0 + 8 * b);
-            }
-            __syncwarp();
-            if (++s == kStages) {
-              s = 0;
-              ph ^= 1u;
-            }
           }
+          tc::fence_after();
+          const uint64_t a0 = desc0 + (uint64_t)(kStage >> 4) * s, b0 = a0 + (kTile >> 4);
+          const uint32_t empty = empty0 + 8 * s;
+#pragma unroll
+          for (int kk = 0; kk < 3; ++kk) umma_e4m3_pair(tmem + 256 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+          ready = (i == 0 || fp8::mbar_peek(acce0 + 8 * (b ^ 1), (uint32_t)((i - 1) >> 1) & 1u)) && fp8::mbar_peek(full0 + 8 * s, ph);
+          umma_e4m3_pair(tmem + 256 * b, a0 + 6, b0 + 6, idesc, 1);
+          tc::umma_commit_pair(accf0 + 8 * b);
+          tc::umma_commit_pair(empty);
         }
-        // every product issued has finished before the pair's memory goes
-        if (lane == 0) tc::umma_commit_pair(done);
-        __syncwarp();
-        tc::mbar_wait_warp(done, 0, p.status);
       }
+      // every product issued has finished before the pair's memory goes
+      tc::umma_commit_pair(done);
+      tc::mbar_wait(done, 0, p.status);
     }
   } else {  // ---------------- sums: lane = row, 128 columns a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int i = 0;
     for (int t = pair; t < tiles; t += pairs) {
       const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
-      if (!live_tile(p, row0)) continue;
+      if (skip(t)) continue;
       const int wrow0 = row0 + (int)rank * 128 + q * 32, row = wrow0 + lane;
       const float* xs = p.xs + (long long)min(row, p.rows - 1) * p.kblocks;
       const int wb = GATED ? n0 : min(2 * n0 + eg, nb - 1);      // a block past the last has no columns to write
@@ -202,19 +213,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           tc::tmem_wait_ld();
-          if (c < 3) fp8::tmem_ld32(t0 + 32 * (c + 1), v[(c + 1) & 1]);
+          if (c < 3) {
+            fp8::tmem_ld32(t0 + 32 * (c + 1), v[(c + 1) & 1]);
+          } else {  // all read: the accumulator is the products' again
+            tc::fence_before();
+            __syncwarp();
+            // what this hands over was read from tensor memory, which tcgen05.fence orders: a release of the generic memory, at
+            // the cluster's scope, doubled the kernel's time
+            if (lane == 0)
+              asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(acce_leader + 8 * b) : "memory");
+          }
           const float sc = c < 2 ? s0 : s1;
           const uint64_t sc2 = pack2f(sc, sc);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             acc[16 * c + j] = fma2(pack2f(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc2, acc[16 * c + j]);
         }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0)
-          // what it hands over was read from tensor memory, which tcgen05.fence orders: a release of the generic memory, at
-          // the cluster's scope, doubled the kernel's time
-          asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(acce_leader + 8 * b) : "memory");
       }
       // the sums leave through this warp's staging, so that neighbouring lanes store neighbouring columns
       if constexpr (GATED) {
