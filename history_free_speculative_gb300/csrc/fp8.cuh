@@ -63,8 +63,25 @@ __device__ __forceinline__ bool valid_row(const int32_t* n_rows, int T, int row)
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// The gated activation of two sums.
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The gated activation g / (1 + exp(-g)) u of two sums. exp2 within 2^-22, its argument's rounding |g| 2^-23, the reciprocal within
+// 2^-23: far below the 2^-4 of the code that it becomes. (With expf and a division the 16,384 results of a tile cost the many-row kernel 4 us.)
+
+__device__ __forceinline__ float gated(float g, float u) {
+  return g * rcp_approx(1.f + tc::ex2_approx(g * -tc::kLog2e)) * u;
+}
 
 // One lane of a converged warp. Copies and products take their operands from uniform registers; in a branch on the lane's
 // number each of them took 100 clocks to issue.
@@ -100,9 +117,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[31])
       : "r"(taddr));
 }
-// Wait of a whole warp for an accumulator: every lane polls for itself (no vote in the polls), one vote at the end.
+// Wait of a whole warp for an accumulator: the lanes sleep (polling, eight warps took the issue slots and shared memory's queue from the lanes
+// that issue copies and products), one vote at the end.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, int* status) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status));
+  return __all_sync(0xffffffffu, tc::mbar_wait_hint(bar, parity, status));
 }
 
 struct ProductArgs {

@@ -28,14 +28,6 @@ constexpr uint32_t kCols = 256;            // tensor memory: two accumulators of
 constexpr int kPitch = 132;                // floats of a staged row (16-byte stores of a warp's lanes fall on different banks)
 constexpr size_t kSmem = 112 * 1024;       // two CTAs an SM
 
-__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accum)
-      : "memory");
-}
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
@@ -139,12 +131,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t ph = 0;
       for (int j = 0; j < kn; ++j) {
         const int b = j & 1;
-        if (j >= 2 && !tc::mbar_wait(acce0 + 8 * b, (uint32_t)((j >> 1) - 1) & 1u, p.status)) break;
-        if (!tc::mbar_wait(full0 + 8 * s, ph, p.status)) break;
+        if (j >= 2 && !tc::mbar_wait_hint(acce0 + 8 * b, (uint32_t)((j >> 1) - 1) & 1u, p.status)) break;
+        if (!tc::mbar_wait_hint(full0 + 8 * s, ph, p.status)) break;
         tc::fence_after();
         const uint64_t a0 = tc::sw128_desc(tc::su32(smem + (size_t)s * stage_bytes)), b0 = a0 + (pl.a_bytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + 128 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
+        for (int kk = 0; kk < 4; ++kk) fp8::umma_e4m3(tmem + 128 * b, a0 + 2 * kk, b0 + 2 * kk, idesc, kk > 0);
         tc::umma_commit(accf0 + 8 * b);
         tc::umma_commit(empty0 + 8 * s);
         if (++s == pl.stages) {
@@ -154,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // every product issued has finished before the stages and the tensor memory go
       tc::umma_commit(done);
-      tc::mbar_wait(done, 0, p.status);
+      tc::mbar_wait_hint(done, 0, p.status);
     }
     __syncwarp();
   } else if (live && (warp & 3) < quads) {  // ---------------- sums: lane = row
