@@ -117,10 +117,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[31])
       : "r"(taddr));
 }
-// Wait of a whole warp for an accumulator: the lanes sleep (polling, eight warps took the issue slots and shared memory's queue from the lanes
-// that issue copies and products), one vote at the end.
+// Wait of a whole warp for an accumulator: every lane polls for itself (no vote in the polls), one vote at the end.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, int* status) {
-  return __all_sync(0xffffffffu, tc::mbar_wait_hint(bar, parity, status));
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status));
+}
+// A box of the map into L2, without waiting for the kernel before: the weights' way from HBM begins while that one still runs.
+// (L2 is where all SMs' accesses meet: what the kernel before writes there afterwards is what the copy reads.)
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
 }
 
 struct ProductArgs {
@@ -144,7 +148,7 @@ struct ProductArgs {
 bool make_map(CUtensorMap* m, const void* base, long long rows, int K, long long stride, int box_rows);
 
 // The kernel for many rows (fp8_pair.cu): boxes of 128 rows of x, 128 (linear) or 64 (gated) weight rows.
-bool use_pairs(const ProductArgs& p, bool gated);
+double pairs_us(const ProductArgs& p, bool gated);  // an estimate of its time
 cudaError_t launch_pairs(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, bool gated, bool f32, cudaStream_t s);
 
 }  // namespace fp8

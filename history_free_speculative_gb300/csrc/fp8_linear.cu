@@ -22,10 +22,11 @@ namespace {
 using fp8::kBlock;
 using fp8::ProductArgs;
 
-constexpr int kThreads = 192;              // copy warp, MMA warp, four epilogue warps
+constexpr int kThreads = 320;              // copy warp, MMA warp, eight epilogue warps
 constexpr uint32_t kWTile = 128 * 128;     // a k block of the weights' 128 rows
 constexpr uint32_t kCols = 256;            // tensor memory: two accumulators of 128 columns
 constexpr int kPitch = 132;                // floats of a staged row (16-byte stores of a warp's lanes fall on different banks)
+constexpr int kAhead = 8;                  // k blocks of the weights asked into L2 before the kernel before has ended
 constexpr size_t kSmem = 112 * 1024;       // two CTAs an SM
 
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tile = blockIdx.x / cl;                              // 128 columns of the result
   const int row0 = blockIdx.y * 128, rows = min(128, p.rows - row0);
   const int kb0 = (int)((long long)z * p.kblocks / pl.splits), kn = (int)((long long)(z + 1) * p.kblocks / pl.splits) - kb0;
-  const int quads = (rows + 31) / 32;                            // epilogue warps with rows
+  const int quads = (rows + 31) / 32;                            // quarters of the accumulator's lanes that hold rows
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < pl.stages; ++s) {
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(accf0 + 8 * b, 1);
-      tc::mbar_init(acce0 + 8 * b, quads);
+      tc::mbar_init(acce0 + 8 * b, 2 * quads);
     }
     tc::mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -80,6 +81,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_trigger();
+  if (warp == 0 && fp8::elect_one())
+    for (int j = 0; j < min(kn, kAhead); ++j) {
+      const int k = (kb0 + j) * kBlock;
+      fp8::prefetch_2d(&mw0, k, tile * 128 + half * 64);
+      if (GATED) fp8::prefetch_2d(&mw1, k, tile * 128 + half * 64);
+    }
   pdl_wait();
   tc::fence_before();
   // a tile without a valid row (padding of a ragged batch) is left out by the whole cluster
@@ -149,48 +156,47 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc::mbar_wait_hint(done, 0, p.status);
     }
     __syncwarp();
-  } else if (live && (warp & 3) < quads) {  // ---------------- sums: lane = row
-    const int q = warp & 3, r = q * 32 + lane;
+  } else if (live && (warp & 3) < quads) {  // ---------------- sums: lane = row, 64 columns a thread
+    const int q = warp & 3, eg = (warp - 2) >> 2, r = q * 32 + lane;
     const float* xs = p.xs + (long long)(row0 + min(r, rows - 1)) * p.kblocks + kb0;
-    const float* w0 = p.ws[0] + (long long)tile * p.kblocks + kb0;
-    const float* w1 = GATED ? p.ws[1] + (long long)tile * p.kblocks + kb0 : w0;
-    uint64_t acc[64];
+    const float* ws = p.ws[GATED ? eg : 0] + (long long)tile * p.kblocks + kb0;
+    uint64_t acc[32];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) acc[i] = 0;
-    float x_next = xs[0], w0_next = w0[0], w1_next = w1[0];
+    for (int i = 0; i < 32; ++i) acc[i] = 0;
+    float x = xs[0], w = ws[0];
     bool ok = true;
     for (int j = 0; j < kn; ++j) {
       const int b = j & 1;
-      const float s0 = x_next * w0_next, s1 = GATED ? x_next * w1_next : s0;
+      const float sc = x * w;
+      const uint64_t sc2 = pack2f(sc, sc);
       if (j + 1 < kn) {
-        x_next = xs[j + 1];
-        w0_next = w0[j + 1];
-        if (GATED) w1_next = w1[j + 1];
+        x = xs[j + 1];
+        w = ws[j + 1];
       }
       ok = fp8::wait_all(accf0 + 8 * b, (uint32_t)(j >> 1) & 1u, p.status);
       if (!ok) break;
       tc::fence_after();
-      const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + 128 * b;
+      const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + 128 * b + 64 * eg;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t v[16];
         tc::tmem_ld16_nowait(t0 + 16 * c, v);
         tc::tmem_wait_ld();
-        const float sc = c < 4 ? s0 : s1;
-        const uint64_t sc2 = pack2f(sc, sc);
+        if (c == 3) {  // all read: the accumulator is the products' again
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(acce0 + 8 * b);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           acc[8 * c + i] = fma2(pack2f(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2, acc[8 * c + i]);
       }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(acce0 + 8 * b);
     }
     // the last accumulator is there, so every product has read its stage: their memory takes the sums
     if (ok && r < rows) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        *reinterpret_cast<float4*>(staged + r * kPitch + 4 * i) =
+      for (int i = 0; i < 16; ++i)
+        *reinterpret_cast<float4*>(staged + r * kPitch + 64 * eg + 4 * i) =
             make_float4(lo2f(acc[2 * i]), hi2f(acc[2 * i]), lo2f(acc[2 * i + 1]), hi2f(acc[2 * i + 1]));
     }
   }
@@ -262,15 +268,32 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ---------------------------------------------------------------- host side
 
-SmallPlan small_plan(const ProductArgs& p, bool gated) {
+// Splits of the k blocks: the least time of one CTA's run, where two CTAs on an SM take 8/5 of one's time a block (1 row, 4,096 x
+// 12,288: 4 splits, 128 CTAs, 12.7 us; 8 splits, 256 CTAs, 11.0; 32 rows, 6,144 x 4,096: 3 splits, 144 CTAs, 8.75, 4 splits, 192 CTAs, 8.85). At
+// least four blocks a CTA (340 rows, 1,024 x 2,176: 7.8 us, with two 10.0), and clusters of four and more leave an eighth of the places
+// free, since not every GPC has a multiple of them (gated 9,728 x 2,560, 8 rows: 152 CTAs in twos 14.2 us, 304 in fours 17.9).
+// us: an estimate of the call's time, to be compared with the many-row kernel's.
+SmallPlan small_plan(const ProductArgs& p, bool gated, double& us) {
   SmallPlan pl;
   pl.box = p.rows >= 128 ? 128 : (p.rows + 7) / 8 * 8;
   pl.a_bytes = (uint32_t)(pl.box * 128);
   pl.stages = std::min<int>(16, (int)((kSmem - 2048) / (pl.a_bytes + kWTile)));
-  const int halves = gated ? 2 : 1;
-  const long long ctas = (long long)fp8::blocks_of(p.N) * halves * ((p.rows + 127) / 128);
+  const int halves = gated ? 2 : 1, sms = device_sms();
+  const long long tiles = (long long)fp8::blocks_of(p.N) * halves * ((p.rows + 127) / 128);
   pl.splits = 1;
-  while (pl.splits * 2 * halves <= 8 && pl.splits * 2 <= p.kblocks && ctas * pl.splits * 2 <= 2LL * device_sms()) pl.splits *= 2;
+  double best = 0;
+  for (int s : {1, 2, 3, 4, 6, 8}) {
+    const long long ctas = tiles * s, places = halves * s >= 4 ? 2LL * sms * 7 / 8 : 2LL * sms;
+    const int run = (p.kblocks + s - 1) / s;
+    if (s > 1 && (halves * s > 8 || run < 4 || ctas > places)) break;
+    const double t = (double)((ctas + 2 * sms - 1) / (2 * sms)) * run * (ctas <= sms ? 5 : 8);
+    if (s == 1 || t < best) {
+      best = t;
+      pl.splits = s;
+    }
+  }
+  // full row tiles: 0.5 us a block alone on an SM, 0.6 two at a time for both; 4.5 us to start, join and end
+  us = 4.5 + best * (tiles * pl.splits <= sms ? 0.5 / 5 : 0.6 / 8);
   return pl;
 }
 
@@ -300,7 +323,9 @@ cudaError_t launch_small(const CUtensorMap& x, const CUtensorMap& w0, const CUte
 template <bool GATED, typename OUT>
 int product(const ProductArgs& p, const void* x, long long x_stride, const void* w0, long long w0_stride, const void* w1, long long w1_stride,
             cudaStream_t s) {
-  if (fp8::use_pairs(p, GATED)) {
+  double us;
+  const SmallPlan pl = small_plan(p, GATED, us);
+  if (fp8::pairs_us(p, GATED) < us) {
     CUtensorMap mx, m0, m1;
     const int wbox = GATED ? 64 : 128;
     if (!fp8::make_map(&mx, x, p.rows, p.K, x_stride, 128) || !fp8::make_map(&m0, w0, p.N, p.K, w0_stride, wbox) ||
@@ -308,7 +333,6 @@ int product(const ProductArgs& p, const void* x, long long x_stride, const void*
       return launch_status(cudaErrorInvalidValue);
     return launch_status(fp8::launch_pairs(mx, m0, m1, p, GATED, sizeof(OUT) == 4, s));
   }
-  const SmallPlan pl = small_plan(p, GATED);
   CUtensorMap mx, m0, m1;
   const int wbox = GATED ? 64 : 128;
   if (!fp8::make_map(&mx, x, p.rows, p.K, x_stride, pl.box) || !fp8::make_map(&m0, w0, p.N, p.K, w0_stride, wbox) ||

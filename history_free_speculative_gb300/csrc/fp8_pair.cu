@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
         if (skip(t)) continue;
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (issued >= kStages) ok = tc::mbar_wait_hint(empty0 + 8 * s, ph ^ 1u, p.status);
+          if (issued >= kStages) ok = tc::mbar_wait(empty0 + 8 * s, ph ^ 1u, p.status);
           if (!ok) break;
           const uint32_t st = tc::su32(smem + s * kStage), bar = full_leader + 8 * s;
           if (rank == 0) tc::mbar_expect_tx(full0 + 8 * s, 2 * kStage);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1u;
           }
           --s;
-          tc::mbar_wait_hint(full0 + 8 * s, ph, p.status);
+          tc::mbar_wait(full0 + 8 * s, ph, p.status);
         }
     } else if (warp == 1 && rank == 0 && fp8::elect_one()) {  // ---------------- products
       constexpr uint32_t idesc = fp8::idesc_e4m3(256, 256);
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
           const int b = i & 1;
           if (!ready) {
-            ok = (i < 2 || tc::mbar_wait_hint(acce0 + 8 * b, (uint32_t)((i >> 1) - 1) & 1u, p.status)) && tc::mbar_wait_hint(full0 + 8 * s, ph, p.status);
+            ok = (i < 2 || tc::mbar_wait(acce0 + 8 * b, (uint32_t)((i >> 1) - 1) & 1u, p.status)) && tc::mbar_wait(full0 + 8 * s, ph, p.status);
             if (!ok) break;
           }
           tc::fence_after();
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every product issued has finished before the pair's memory goes
       tc::umma_commit_pair(done);
-      tc::mbar_wait_hint(done, 0, p.status);
+      tc::mbar_wait(done, 0, p.status);
     }
   } else {  // ---------------- sums: lane = row, 128 columns a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
@@ -183,7 +183,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* staged = smem + kStages * kStage + (warp - 4) * 32 * kPitch;
     const int nb = fp8::blocks_of(p.N);
     int i = 0;
-    bool ready = false;  // the next accumulator was seen to be there
     for (int t = pair; t < tiles; t += pairs) {
       const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
       if (skip(t)) continue;
@@ -195,41 +194,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      float x = xs[0], wg = w0[0], wu = w1[0];
+      float x_next = xs[0], w0_next = w0[0], w1_next = w1[0];
       bool ok = true;
       for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
         const int b = i & 1;
-        const float s0 = x * wg, s1 = GATED ? x * wu : s0;
+        const float s0 = x_next * w0_next, s1 = GATED ? x_next * w1_next : s0;
         if (kb + 1 < p.kblocks) {
-          x = xs[kb + 1];
-          wg = w0[kb + 1];
-          if (GATED) wu = w1[kb + 1];
+          x_next = xs[kb + 1];
+          w0_next = w0[kb + 1];
+          if (GATED) w1_next = w1[kb + 1];
         }
-        if (!ready) ok = fp8::wait_all(accf0 + 8 * b, (uint32_t)(i >> 1) & 1u, p.status);
+        ok = fp8::wait_all(accf0 + 8 * b, (uint32_t)(i >> 1) & 1u, p.status);
         if (!ok) break;
         tc::fence_after();
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + 256 * b + 128 * eg;
+        uint32_t v[2][32];
+        fp8::tmem_ld32(t0, v[0]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          // 64 columns at a time: a wait is for all loads of a thread, and a load takes 100 clocks whatever its width
-          uint32_t v[2][32];
-          fp8::tmem_ld32(t0 + 64 * c, v[0]);
-          fp8::tmem_ld32(t0 + 64 * c + 32, v[1]);
+        for (int c = 0; c < 4; ++c) {
           tc::tmem_wait_ld();
-          if (c == 1) {  // all read: the accumulator is the products' again
+          if (c < 3) {
+            fp8::tmem_ld32(t0 + 32 * (c + 1), v[(c + 1) & 1]);
+          } else {  // all read: the accumulator is the products' again
             tc::fence_before();
             __syncwarp();
             // what this hands over was read from tensor memory, which tcgen05.fence orders: a release of the generic memory, at
             // the cluster's scope, doubled the kernel's time
             if (lane == 0)
               asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(acce_leader + 8 * b) : "memory");
-            ready = __all_sync(0xffffffffu, fp8::mbar_peek(accf0 + 8 * (b ^ 1), (uint32_t)((i + 1) >> 1) & 1u));
           }
-          const float sc = c == 0 ? s0 : s1;
+          const float sc = c < 2 ? s0 : s1;
           const uint64_t sc2 = pack2f(sc, sc);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            acc[32 * c + j] = fma2(pack2f(__uint_as_float(v[j >> 4][2 * (j & 15)]), __uint_as_float(v[j >> 4][2 * (j & 15) + 1])), sc2, acc[32 * c + j]);
+          for (int j = 0; j < 16; ++j)
+            acc[16 * c + j] = fma2(pack2f(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc2, acc[16 * c + j]);
         }
       }
       // the sums leave through this warp's staging, so that neighbouring lanes store neighbouring columns
@@ -361,8 +359,12 @@ cudaError_t launch(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMa
 
 namespace fp8 {
 
-bool use_pairs(const ProductArgs& p, bool gated) {
-  return p.rows > 256;
+// 0.43 us a k block of a tile, 3 us to start and end (512 rows: 6,144 x 4,096 16.9 us, 21.6 with the few-row kernel; 4,096 x 12,288 39.5 us, 33.0 with
+// it, since 32 tiles leave most SMs idle; gated 12,288 x 4,096, 256 rows: 35 us, 49 with it; 128 rows: 34 us, 29 with it).
+double pairs_us(const ProductArgs& p, bool gated) {
+  const int pairs = std::max(1, device_sms() / 2);
+  const long long tiles = (long long)((p.rows + 255) / 256) * (gated ? blocks_of(p.N) : (p.N + 255) / 256);
+  return 3.0 + 0.43 * (double)((tiles + pairs - 1) / pairs) * p.kblocks;
 }
 
 cudaError_t launch_pairs(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, bool gated, bool f32,
