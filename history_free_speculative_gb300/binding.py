@@ -650,9 +650,11 @@ def _weight_of(w, scale, K, what):
 
 
 def _new_codes(stream, B, T, C):
+    """(codes [B, T, C], bytes between their rows): rows on 16 bytes."""
     pitch = -(-C // 16) * 16
-    t = _new(stream, (B, T, pitch), _E4M3)
-    return t if pitch == C else t[:, :, :C]
+    if pitch == C:
+        return _new(stream, (B, T, C), _E4M3), C
+    return _new(stream, (B, T, pitch), _E4M3)[:, :, :C], pitch
 
 
 def fp8_quantise(x, gain=None, eps=1e-6, residual=None, total=None, n_rows=None, codes=None, scale=None, status=None, stream=None):
@@ -671,15 +673,18 @@ def fp8_quantise(x, gain=None, eps=1e-6, residual=None, total=None, n_rows=None,
         total = residual if total is None else total
         rs, ts = _like(residual, x, "residual"), _like(total, x, "total")
     if codes is None:
-        codes = _new_codes(s, B, T, K)
+        codes, cs = _new_codes(s, B, T, K)
     elif codes.shape != x.shape:
         raise ValueError(f"codes: {list(x.shape)} expected, got {list(codes.shape)}")
+    else:
+        cs = _codes_of(codes, "codes")[3]
     if scale is None:
         scale = _new(s, (B, T, -(-K // FP8_BLOCK)), torch.float32)
+    else:
+        _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale")
     a = Fp8QuantiseArgs(B, T, K, _dtype(x, "x"), x.data_ptr(), xs, None if residual is None else residual.data_ptr(), rs,
                         None if residual is None else total.data_ptr(), ts, _vec(gain, x.dtype, (K,), "gain"), eps, codes.data_ptr(),
-                        _codes_of(codes, "codes")[3], _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale"),
-                        _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
+                        cs, scale.data_ptr(), _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_fp8_quantise(ctypes.byref(a), ptr), "dlite_fp8_quantise")
     return codes, scale
 
@@ -694,9 +699,10 @@ def fp8_weight(w, status=None, stream=None):
     N, K = w.shape
     if (N | K) >> 31:
         _sizes("w", N, K)
-    codes = _new_codes(s, 1, N, K)[0]
+    codes, cs = _new_codes(s, 1, N, K)
+    codes = codes[0]
     scale = _new(s, (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)), torch.float32)
-    a = Fp8WeightArgs(N, K, _dtype(w, "w"), w.data_ptr(), w.stride(0) if N > 1 else K, codes.data_ptr(), -(-K // 16) * 16, scale.data_ptr(),
+    a = Fp8WeightArgs(N, K, _dtype(w, "w"), w.data_ptr(), w.stride(0) if N > 1 else K, codes.data_ptr(), cs, scale.data_ptr(),
                       _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_fp8_weight(ctypes.byref(a), ptr), "dlite_fp8_weight")
     return codes, scale
@@ -733,15 +739,18 @@ def fp8_gated(codes, scale, gate, gate_scale, up, up_scale, n_rows=None, out=Non
     if n != N:
         raise ValueError(f"up: the gate's {N} rows expected, got {n}")
     if out is None:
-        out = _new_codes(s, B, T, N)
+        out, ocs = _new_codes(s, B, T, N)
     elif tuple(out.shape) != (B, T, N):
         raise ValueError(f"out: {[B, T, N]} expected, got {list(out.shape)}")
+    else:
+        ocs = _codes_of(out, "out")[3]
     at = (B, T, -(-N // FP8_BLOCK))
     if out_scale is None:
         out_scale = _new(s, at, torch.float32)
+    else:
+        _vec(out_scale, torch.float32, at, "out_scale")
     a = Fp8GatedArgs(B, T, K, N, codes.data_ptr(), cs, _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale"), gp, gs, gsp, pp, ps, psp,
-                     out.data_ptr(), _codes_of(out, "out")[3], _vec(out_scale, torch.float32, at, "out_scale"),
-                     _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
+                     out.data_ptr(), ocs, out_scale.data_ptr(), _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_fp8_gated(ctypes.byref(a), ptr), "dlite_fp8_gated")
     return out, out_scale
 

@@ -2,7 +2,7 @@
 //
 // Rows: optionally total = x + residual (rounded to the stream's type and stored), then y = total / sqrt(mean total^2 + eps) gain, then the
 // codes of y. A thread holds eight neighbouring columns, so 16 neighbouring threads hold a block and its maximum is four shuffles.
-// With a norm a CTA takes a whole row (the sum of squares is over the row); without one the
+// With a norm a CTA takes whole rows (the sum of squares is over the row); without one the
 // row's pieces go to CTAs of their own.
 #include <algorithm>
 
@@ -12,6 +12,8 @@ namespace dlite {
 namespace {
 
 using fp8::kBlock;
+
+constexpr int kPer = 8;  // columns of a thread
 
 struct QuantiseArgs {
   int rows, T, K, kblocks;
@@ -30,27 +32,27 @@ struct QuantiseArgs {
   int* status;
 };
 
-constexpr int kPer = 8;  // columns of a thread
-
-// Columns [c, c + 8) of a row, zeros past K
+// Columns [c, c + 8) of a row as they are stored, zeros past K
+template <typename T>
+struct Eight {
+  T e[kPer];
+  __device__ __forceinline__ void to(float (&v)[kPer]) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = to_f32(e[i]);
+  }
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int c, int K, float (&v)[kPer]) {
+__device__ __forceinline__ Eight<T> load8(const T* row, int c, int K) {
+  Eight<T> r;
   if (VEC) {  // K is a multiple of 8 here
-    if (c < K) {
-      uint4 w[sizeof(T) / 2];
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(row + c)[i];
-      const T* e = reinterpret_cast<const T*>(w);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = to_f32(e[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = 0.f;
-    }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      reinterpret_cast<uint4*>(r.e)[i] = c < K ? reinterpret_cast<const uint4*>(row + c)[i] : make_uint4(0, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = c + i < K ? to_f32(row[c + i]) : 0.f;
+    for (int i = 0; i < kPer; ++i) r.e[i] = c + i < K ? row[c + i] : T(0.f);
   }
+  return r;
 }
 __device__ __forceinline__ float rounded(float v, float*) { return v; }
 __device__ __forceinline__ float rounded(float v, bf16*) { return round_bf16(v); }
@@ -94,60 +96,133 @@ __device__ __forceinline__ void quantise8(const QuantiseArgs& a, int row, int c,
   if (c % kBlock == 0) a.scale[(long long)row * a.kblocks + c / kBlock] = fp8::exp2i(e);
 }
 
-// Without a norm: CTA (row, piece of the row).
+// v = x + residual in the stream's type, stored
+template <typename T, bool VEC>
+__device__ __forceinline__ void add_residual(const QuantiseArgs& a, int row, int c, const Eight<T>& res, float (&v)[kPer]) {
+  float r[kPer];
+  res.to(r);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = rounded(v[i] + r[i], (T*)nullptr);
+  store8<T, VEC>(static_cast<T*>(a.total) + row * a.ts, c, a.K, v);
+}
+
+// Without a norm: CTA (row, piece of the row), two times eight columns a thread.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) fp8_quantise_kernel(const QuantiseArgs a) {
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * kPer;
+  const int row = blockIdx.x, step = blockDim.x * kPer, c0 = blockIdx.y * 2 * step + threadIdx.x * kPer;
   if (!fp8::valid_row(a.n_rows, a.T, row)) return;
-  float v[kPer];
-  load8<T, VEC>(static_cast<const T*>(a.x) + row * a.xs, c, a.K, v);
-  if (a.res) {
-    float r[kPer];
-    load8<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c, a.K, r);
+  Eight<T> x[2], r[2];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = rounded(v[i] + r[i], (T*)nullptr);
-    store8<T, VEC>(static_cast<T*>(a.total) + row * a.ts, c, a.K, v);
+  for (int i = 0; i < 2; ++i) {
+    x[i] = load8<T, VEC>(static_cast<const T*>(a.x) + row * a.xs, c0 + i * step, a.K);
+    if (a.res) r[i] = load8<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c0 + i * step, a.K);
   }
   bool bad = false;
-  quantise8(a, row, c, v, bad);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float v[kPer];
+    x[i].to(v);
+    if (a.res) add_residual<T, VEC>(a, row, c0 + i * step, r[i], v);
+    quantise8(a, row, c0 + i * step, v, bad);
+  }
   if (bad) flag_status(a.status, kDevNonfinite);
 }
 
-// With a norm: a CTA takes a row. HELD: the row's columns stay in registers (8 a thread); otherwise they are read again.
-template <typename T, bool VEC, bool HELD>
-__global__ void __launch_bounds__(1024) fp8_norm_quantise_kernel(const QuantiseArgs a) {
+// The block's sum of v, in every thread, in an order of its own size alone. red: 32 floats that nobody else reads before the next barrier but one.
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum((threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0.f);
+}
+
+// With a norm, rows on 16 bytes of up to 8 x 1,024 columns: a CTA takes rows in turn out of a ring in shared memory that bulk copies fill a
+// few rows ahead. What bounds it is the bytes on their way: 8,192 rows of 4,096 bf16 columns with the residual sum took 71 us with one row a
+// CTA and 69 with the next row's loads in registers, 32 KB an SM on their way in both.
+constexpr int kRing = 4;
+template <typename T>
+__global__ void __launch_bounds__(1024) fp8_norm_quantise_kernel(const QuantiseArgs a, const int slots) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[2][32];
+  __shared__ uint64_t full[kRing];
+  const int c = threadIdx.x * kPer, bytes = a.K * (int)sizeof(T), slot_bytes = a.res ? 2 * bytes : bytes;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < slots; ++i) tc::mbar_init(tc::su32(full + i), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_trigger();
+  pdl_wait();
+  const Eight<T> gain = load8<T, true>(static_cast<const T*>(a.gain), c, a.K);
+  auto next_row = [&](int row) {
+    while (row < a.rows && !fp8::valid_row(a.n_rows, a.T, row)) row += gridDim.x;
+    return row;
+  };
+  auto copy = [&](int row, int slot) {  // thread 0
+    const uint32_t dst = tc::su32(ring + (size_t)slot * slot_bytes), bar = tc::su32(full + slot);
+    tc::mbar_expect_tx(bar, slot_bytes);
+    tc::bulk_load(dst, static_cast<const T*>(a.x) + row * a.xs, bytes, bar);
+    if (a.res) tc::bulk_load(dst + bytes, static_cast<const T*>(a.res) + row * a.rs, bytes, bar);
+  };
+  int row = next_row(blockIdx.x), ahead = row, slot = 0, turn = 0;
+  uint32_t ph = 0;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < slots && ahead < a.rows; ++i, ahead = next_row(ahead + gridDim.x)) copy(ahead, i);
+  __syncthreads();  // the barriers are there
+  bool bad = false, ok = true;
+  while (row < a.rows) {
+    ok = tc::mbar_wait_hint(tc::su32(full + slot), ph, a.status) && ok;
+    const T* at = reinterpret_cast<const T*>(ring + (size_t)slot * slot_bytes);
+    float v[kPer], ss = 0.f;
+    load8<T, true>(at, c, a.K).to(v);
+    if (a.res) add_residual<T, true>(a, row, c, load8<T, true>(at + a.K, c, a.K), v);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) ss = fmaf(v[i], v[i], ss);
+    const float inv = rsqrtf(row_sum(ss, red[turn]) / (float)a.K + a.eps);
+    if (threadIdx.x == 0 && ahead < a.rows && ok) {  // the sum's barrier: the slot is read
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      copy(ahead, slot);
+      ahead = next_row(ahead + gridDim.x);
+    }
+    float g[kPer];
+    gain.to(g);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = v[i] * inv * g[i];
+    quantise8(a, row, c, v, bad);
+    turn ^= 1;
+    row = next_row(row + gridDim.x);
+    if (++slot == slots) {
+      slot = 0;
+      ph ^= 1u;
+    }
+  }
+  if (bad) flag_status(a.status, kDevNonfinite);
+}
+
+// With a norm, other rows: a CTA takes a row and reads its columns twice.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(1024) fp8_norm_quantise_wide_kernel(const QuantiseArgs a) {
   __shared__ float red[32];
   pdl_trigger();
   pdl_wait();
   const int row = blockIdx.x, step = blockDim.x * kPer;
   if (!fp8::valid_row(a.n_rows, a.T, row)) return;
   const T* x = static_cast<const T*>(a.x) + row * a.xs;
-  T* total = static_cast<T*>(a.total) + row * a.ts;
+  const T* total = static_cast<const T*>(a.total) + row * a.ts;
   float v[kPer], g[kPer], ss = 0.f;
-  if (HELD) load8<T, VEC>(static_cast<const T*>(a.gain), threadIdx.x * kPer, a.K, g);
-  for (int c = threadIdx.x * kPer; c < a.K || HELD; c += step) {
-    load8<T, VEC>(x, c, a.K, v);
-    if (a.res) {
-      float r[kPer];
-      load8<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c, a.K, r);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = rounded(v[i] + r[i], (T*)nullptr);
-      store8<T, VEC>(total, c, a.K, v);
-    }
+  for (int c = threadIdx.x * kPer; c < a.K; c += step) {
+    load8<T, VEC>(x, c, a.K).to(v);
+    if (a.res) add_residual<T, VEC>(a, row, c, load8<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c, a.K), v);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) ss = fmaf(v[i], v[i], ss);
-    if (HELD) break;
   }
-  const float inv = rsqrtf(block_sum(ss, red) / (float)a.K + a.eps);
+  const float inv = rsqrtf(row_sum(ss, red) / (float)a.K + a.eps);
   bool bad = false;
   // whole blocks of threads walk together: the maximum is taken by all lanes
-  for (int c = threadIdx.x * kPer; c - (int)(threadIdx.x * kPer) < a.K; c += step) {
-    if (!HELD) {
-      load8<T, VEC>(a.res ? total : x, c, a.K, v);  // this thread's own stores
-      load8<T, VEC>(static_cast<const T*>(a.gain), c, a.K, g);
-    }
+  for (int c = threadIdx.x * kPer; c - (int)threadIdx.x * kPer < a.K; c += step) {
+    load8<T, VEC>(a.res ? total : x, c, a.K).to(v);  // this thread's own stores
+    load8<T, VEC>(static_cast<const T*>(a.gain), c, a.K).to(g);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = v[i] * inv * g[i];
     quantise8(a, row, c, v, bad);
@@ -194,12 +269,20 @@ template <typename T, bool VEC>
 cudaError_t launch_quantise(const QuantiseArgs& a, cudaStream_t s) {
   const int threads = (a.K + kPer - 1) / kPer;
   if (!a.gain) {
-    const int t = std::min(256, (threads + 31) / 32 * 32);
-    return launch_pdl(fp8_quantise_kernel<T, VEC>, dim3(a.rows, (threads + t - 1) / t), dim3(t), 0, s, a);
+    const int t = std::min(256, (threads / 2 + 31) / 32 * 32 + (threads < 2) * 32);
+    return launch_pdl(fp8_quantise_kernel<T, VEC>, dim3(a.rows, (threads + 2 * t - 1) / (2 * t)), dim3(t), 0, s, a);
   }
-  const int t = std::min(1024, (threads + 31) / 32 * 32);
-  return threads <= t ? launch_pdl(fp8_norm_quantise_kernel<T, VEC, true>, dim3(a.rows), dim3(t), 0, s, a)
-                      : launch_pdl(fp8_norm_quantise_kernel<T, VEC, false>, dim3(a.rows), dim3(t), 0, s, a);
+  const int t = std::min(1024, (threads + 31) / 32 * 32), row_bytes = a.K * (int)sizeof(T) * (a.res ? 2 : 1);
+  if constexpr (VEC) {
+    if (threads <= t) {
+      constexpr int kMost = 200 * 1024;
+      const int ctas = std::min(16, std::max(1, 1536 / t)), slots = std::max(1, std::min(kRing, kMost / ctas / row_bytes));
+      cudaError_t e = cudaFuncSetAttribute(fp8_norm_quantise_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(fp8_norm_quantise_kernel<T>, dim3(std::min(a.rows, device_sms() * ctas)), dim3(t), (size_t)slots * row_bytes, s, a, slots);
+    }
+  }
+  return launch_pdl(fp8_norm_quantise_wide_kernel<T, VEC>, dim3(a.rows), dim3(t), 0, s, a);
 }
 
 }  // namespace
