@@ -143,13 +143,24 @@ struct ProductArgs {
   int* status;
 };
 
-// Map of byte rows [rows, K] of `stride` bytes for boxes of box_rows x 128 bytes under the 128-byte swizzle; columns and rows
-// past the matrix read as 0.
-bool make_map(CUtensorMap* m, const void* base, long long rows, int K, long long stride, int box_rows);
+// The products' operands in memory and their tensor maps: byte rows of K columns for boxes of 128 bytes under the 128-byte swizzle; columns and
+// rows past a matrix read as 0.
+struct Operands {
+  const void* x;
+  long long xs;
+  const void* w[2];
+  long long ws[2];
+};
+struct Maps {
+  CUtensorMap x, w0, w1;
+};
+// To be called after a call of the runtime that needs the device's context (a kernel's attribute): in a host thread that has made no CUDA call
+// yet the context is not current, and the encoder refuses.
+bool make_maps(Maps& m, const Operands& o, const ProductArgs& p, int x_box, int w_box);
 
 // The kernel for many rows (fp8_pair.cu): boxes of 128 rows of x, 128 (linear) or 64 (gated) weight rows.
 double pairs_us(const ProductArgs& p, bool gated);  // an estimate of its time
-cudaError_t launch_pairs(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, bool gated, bool f32, cudaStream_t s);
+cudaError_t launch_pairs(const Operands& o, const ProductArgs& p, bool gated, bool f32, cudaStream_t s);
 
 }  // namespace fp8
 }  // namespace dlite

@@ -335,9 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool GATED, typename OUT>
-cudaError_t launch(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, int row_tiles, int tiles, cudaStream_t s) {
+cudaError_t launch(const fp8::Operands& o, const ProductArgs& p, int row_tiles, int tiles, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<GATED, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
+  fp8::Maps m;
+  if (!fp8::make_maps(m, o, p, 128, GATED ? 64 : 128)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * std::min(tiles, std::max(1, device_sms() / 2)));
   cfg.blockDim = dim3(kThreads);
@@ -352,7 +354,7 @@ cudaError_t launch(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMa
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<GATED, OUT>, x, w0, w1, p, row_tiles, tiles);
+  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<GATED, OUT>, m.x, m.w0, m.w1, p, row_tiles, tiles);
 }
 
 }  // namespace
@@ -367,11 +369,10 @@ double pairs_us(const ProductArgs& p, bool gated) {
   return 3.0 + 0.43 * (double)((tiles + pairs - 1) / pairs) * p.kblocks;
 }
 
-cudaError_t launch_pairs(const CUtensorMap& x, const CUtensorMap& w0, const CUtensorMap& w1, const ProductArgs& p, bool gated, bool f32,
-                         cudaStream_t s) {
+cudaError_t launch_pairs(const Operands& o, const ProductArgs& p, bool gated, bool f32, cudaStream_t s) {
   const int row_tiles = (p.rows + 255) / 256, tiles = row_tiles * (gated ? blocks_of(p.N) : (p.N + 255) / 256);
-  if (gated) return launch<true, float>(x, w0, w1, p, row_tiles, tiles, s);
-  return f32 ? launch<false, float>(x, w0, w1, p, row_tiles, tiles, s) : launch<false, bf16>(x, w0, w1, p, row_tiles, tiles, s);
+  if (gated) return launch<true, float>(o, p, row_tiles, tiles, s);
+  return f32 ? launch<false, float>(o, p, row_tiles, tiles, s) : launch<false, bf16>(o, p, row_tiles, tiles, s);
 }
 
 }  // namespace fp8

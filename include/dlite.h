@@ -604,7 +604,7 @@ int dlite_token_logprobs(const dlite_logprobs_args *args, dlite_stream_t stream)
  * Quantisation: scale = 2^e, the least with max |x| <= 448 2^e, e >= -126; code = e4m3(x 2^-e) to nearest, ties to even.
  * The format holds no infinity: what is not finite becomes NaN, does not count for the maximum, and flags DLITE_DEV_NONFINITE; a
  * NaN code makes the results of its row (of a weight: of its output) NaN and no others. Sums of a product are float32, each block's
- * scaled by the float32 product of its two scales and added in order of the blocks (a few runs of blocks added in order where rows are few):
+ * scaled by the float32 product of its two scales (which has to be a number float32 holds) and added in order of the blocks (a few runs of blocks added in order where rows are few):
  * the same bits run to run. */
 #define DLITE_FP8_BLOCK 128
 #define DLITE_FP8_MAX_K (1 << 20)

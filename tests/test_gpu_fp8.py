@@ -119,8 +119,8 @@ def test_norm_and_quantise(dtype, B, T, K, pad, residual):
         v = FO.total(v, _np(res), dtype)
         assert np.array_equal(_np(total), v)
     y = FO.norm(v, _np(gain), 1e-5)
-    # the sum of squares: 8 a thread and round, two rounds at most, ten joins; its root halves that; mean, eps; rsqrt 2 steps; two products
-    err = ((16 + 10) / 2 + 2 + 4 + 2) * 2.0 ** -24 * np.abs(y)
+    # the sum of squares: 16 a thread (two rounds of them at most), ten joins; its root halves that and the mean's and the eps' steps; rsqrt 2 steps of 2^-23; two products
+    err = ((32 + 10 + 3) / 2 + 4 + 2) * 2.0 ** -24 * np.abs(y)
     _quantised(_bytes(c), _np(s), y, err)
     if residual:      # in place, and without the norm
         keep = res.clone()
