@@ -654,6 +654,8 @@ def _new_codes(stream, B, T, C):
     pitch = -(-C // 16) * 16
     if pitch == C:
         return _new(stream, (B, T, C), _E4M3), C
+    if stream is None:
+        return torch.empty_strided((B, T, C), (T * pitch, pitch, 1), dtype=_E4M3, device="cuda"), pitch
     return _new(stream, (B, T, pitch), _E4M3)[:, :, :C], pitch
 
 
