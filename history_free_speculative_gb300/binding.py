@@ -649,14 +649,19 @@ def _weight_of(w, scale, K, what):
     return N, w.data_ptr(), row, _vec(scale, torch.float32, (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)), what + "_scale")
 
 
+def _new_strided(stream, shape, strides, dtype):
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
 def _new_codes(stream, B, T, C):
     """(codes [B, T, C], bytes between their rows): rows on 16 bytes."""
     pitch = -(-C // 16) * 16
     if pitch == C:
         return _new(stream, (B, T, C), _E4M3), C
-    if stream is None:
-        return torch.empty_strided((B, T, C), (T * pitch, pitch, 1), dtype=_E4M3, device="cuda"), pitch
-    return _new(stream, (B, T, pitch), _E4M3)[:, :, :C], pitch
+    return _new_strided(stream, (B, T, C), (T * pitch, pitch, 1), _E4M3), pitch
 
 
 def fp8_quantise(x, gain=None, eps=1e-6, residual=None, total=None, n_rows=None, codes=None, scale=None, status=None, stream=None):

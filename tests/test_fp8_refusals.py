@@ -85,6 +85,7 @@ def closed(monkeypatch):
     monkeypatch.setattr(binding, "load", lambda: Closed())
     monkeypatch.setattr(binding, "_here", lambda stream, *t: (0, None))
     monkeypatch.setattr(binding, "_new", lambda s, shape, dtype, zero=False: torch.empty(shape, dtype=dtype, device="meta"))
+    monkeypatch.setattr(binding, "_new_strided", lambda s, shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="meta"))
 
 
 def _codes(*shape):
