@@ -638,6 +638,26 @@ def _codes_of(t, what):
     return B, T, C, row if B * T > 1 else -(-C // 16) * 16
 
 
+def _scale_of(t, B, T, C, what):
+    """Pointer of the scales [B, T, ceil(C / 128)] of rows, whose memory has the rows (b, t) of a block side by side."""
+    n = -(-C // FP8_BLOCK)
+    sb, st, sn = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.dtype != torch.float32 or t.shape != (B, T, n) or (n > 1 and sn != B * T) or (T > 1 and st != 1) or (B > 1 and sb != T):
+        raise ValueError(f"{what}: float32 {[B, T, n]} with strides {[T, 1, B * T]} expected, got {t.dtype} {list(t.shape)} with strides "
+                         f"{list(t.stride())}")
+    return t.data_ptr()
+
+
+def _new_scale(stream, B, T, C):
+    return _new_strided(stream, (B, T, -(-C // FP8_BLOCK)), (T, 1, B * T), torch.float32)
+
+
+def fp8_scale(B, T, C, stream=None):
+    """Memory for the scales of rows [B, T, C]: float32 [B, T, ceil(C / 128)] with strides (T, 1, B T), the rows (b, t) of a block side
+    by side. What fp8_quantise and fp8_gated make where none is given."""
+    return _new_scale(_here(stream)[1], _int(B, "B"), _int(T, "T"), _int(C, "C"))
+
+
 def _weight_of(w, scale, K, what):
     """(N, pointer, bytes between the rows, pointer of the scales) of codes [N, K] and their scales."""
     if w.dtype != _E4M3 or w.dim() != 2 or w.shape[1] != K or (K > 1 and w.stride(1) != 1):
@@ -666,7 +686,7 @@ def _new_codes(stream, B, T, C):
 
 def fp8_quantise(x, gain=None, eps=1e-6, residual=None, total=None, n_rows=None, codes=None, scale=None, status=None, stream=None):
     """x [B, T, K] as 8-bit codes (float8_e4m3fn [B, T, K]) and scales (float32 [B, T, ceil(K / 128)]), one per 128 columns
-    (dlite_fp8_quantise). With residual: total = x + residual is stored (total None: in residual's place) and takes x's place; with
+    (dlite_fp8_quantise); the scales' memory has the rows (b, t) of a block side by side (fp8_scale). With residual: total = x + residual is stored (total None: in residual's place) and takes x's place; with
     gain [K] it is normed by its root mean square. Rows t >= n_rows[b] are left as they were (in new outputs: anything).
     Returns (codes, scale)."""
     lib = load()
@@ -686,9 +706,9 @@ def fp8_quantise(x, gain=None, eps=1e-6, residual=None, total=None, n_rows=None,
     else:
         cs = _codes_of(codes, "codes")[3]
     if scale is None:
-        scale = _new(s, (B, T, -(-K // FP8_BLOCK)), torch.float32)
+        scale = _new_scale(s, B, T, K)
     else:
-        _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale")
+        _scale_of(scale, B, T, K, "scale")
     a = Fp8QuantiseArgs(B, T, K, _dtype(x, "x"), x.data_ptr(), xs, None if residual is None else residual.data_ptr(), rs,
                         None if residual is None else total.data_ptr(), ts, _vec(gain, x.dtype, (K,), "gain"), eps, codes.data_ptr(),
                         cs, scale.data_ptr(), _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
@@ -727,7 +747,7 @@ def fp8_linear(codes, scale, w, w_scale, dtype=torch.bfloat16, n_rows=None, out=
         out = _new(s, (B, T, N), dtype, zero=n_rows is not None)
     elif tuple(out.shape) != (B, T, N):
         raise ValueError(f"out: {[B, T, N]} expected, got {list(out.shape)}")
-    a = Fp8LinearArgs(B, T, K, N, _dtype(out, "out"), codes.data_ptr(), cs, _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale"),
+    a = Fp8LinearArgs(B, T, K, N, _dtype(out, "out"), codes.data_ptr(), cs, _scale_of(scale, B, T, K, "scale"),
                       wp, ws, wsp, out.data_ptr(), _rows_of(out, "out")[3], _vec(n_rows, torch.int32, (B,), "n_rows"),
                       _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_fp8_linear(ctypes.byref(a), ptr), "dlite_fp8_linear")
@@ -751,12 +771,11 @@ def fp8_gated(codes, scale, gate, gate_scale, up, up_scale, n_rows=None, out=Non
         raise ValueError(f"out: {[B, T, N]} expected, got {list(out.shape)}")
     else:
         ocs = _codes_of(out, "out")[3]
-    at = (B, T, -(-N // FP8_BLOCK))
     if out_scale is None:
-        out_scale = _new(s, at, torch.float32)
+        out_scale = _new_scale(s, B, T, N)
     else:
-        _vec(out_scale, torch.float32, at, "out_scale")
-    a = Fp8GatedArgs(B, T, K, N, codes.data_ptr(), cs, _vec(scale, torch.float32, (B, T, -(-K // FP8_BLOCK)), "scale"), gp, gs, gsp, pp, ps, psp,
+        _scale_of(out_scale, B, T, N, "out_scale")
+    a = Fp8GatedArgs(B, T, K, N, codes.data_ptr(), cs, _scale_of(scale, B, T, K, "scale"), gp, gs, gsp, pp, ps, psp,
                      out.data_ptr(), ocs, out_scale.data_ptr(), _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_fp8_gated(ctypes.byref(a), ptr), "dlite_fp8_gated")
     return out, out_scale

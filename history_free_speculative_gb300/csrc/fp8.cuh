@@ -132,13 +132,13 @@ struct ProductArgs {
   int K, kblocks;
   int N;                  // outputs (gated: columns of the activation)
   const int32_t* n_rows;
-  const float* xs;        // [rows][kblocks]
+  const float* xs;        // [kblocks][rows]: a warp, lane = row, reads a block's scales side by side
   const float* ws[2];     // [N / 128][kblocks]; gated: gate, up
   void* out;              // linear
   long long os;
   uint8_t* codes;         // gated
   long long cs;
-  float* scale;           // [rows][N / 128]
+  float* scale;           // [N / 128][rows]
   int vec;                // linear: rows of out on 16 bytes
   int* status;
 };

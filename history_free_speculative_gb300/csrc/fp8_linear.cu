@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else if (live && (warp & 3) < quads) {  // ---------------- sums: lane = row, 64 columns a thread
     const int q = warp & 3, eg = (warp - 2) >> 2, r = q * 32 + lane;
-    const float* xs = p.xs + (long long)(row0 + min(r, rows - 1)) * p.kblocks + kb0;
+    const float* xs = p.xs + (long long)kb0 * p.rows + row0 + min(r, rows - 1);
     const float* ws = (GATED && eg ? p.ws[1] : p.ws[0]) + (long long)tile * p.kblocks + kb0;
     uint64_t acc[32];
 #pragma unroll
@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float sc = x * w;
       const uint64_t sc2 = pack2f(sc, sc);
       if (j + 1 < kn) {
-        x = xs[j + 1];
+        xs += p.rows;
+        x = *xs;
         w = ws[j + 1];
       }
       ok = fp8::wait_all(accf0 + 8 * b, (uint32_t)(j >> 1) & 1u, p.status);
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           *reinterpret_cast<uint32_t*>(dst) = w;
         else
           for (int i = 0; i < p.N - n; ++i) dst[i] = (uint8_t)(w >> (8 * i));
-        if (lane == 0) p.scale[(long long)row * fp8::blocks_of(p.N) + tile] = fp8::exp2i(e);
+        if (lane == 0) p.scale[(long long)tile * p.rows + row] = fp8::exp2i(e);
         if (bad) flag_status(p.status, kDevNonfinite);
       } else {
         const int n = tile * 128 + lane * 4;

@@ -28,7 +28,11 @@ constexpr uint32_t kTile = 128 * 128;         // 128 rows of one k block
 constexpr uint32_t kStage = 2 * kTile;        // this CTA's rows of x and of the weights
 constexpr int kPitch = 144;                   // bytes of a staged row: 128 and 16 that take its chunks to other banks
 constexpr uint32_t kStaging = 8 * 32 * kPitch;
-constexpr uint32_t kSmem = 1024 + 1024 + kStages * kStage + kStaging;
+// A thread's own scales of the blocks to come go to shared memory a few blocks ahead of their use, without registers or barriers: the
+// thread that copies is the one that reads. (A load one block ahead was late wherever it missed the first cache: 8,192 rows of 4,096 x
+// 12,288 took 404 us so, 290 with the copies.)
+constexpr int kScalesAhead = 6, kScaleSlots = 8;
+constexpr uint32_t kSmem = 1024 + 1024 + kStages * kStage + kStaging + kScaleSlots * 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 
 __device__ __forceinline__ void umma_e4m3_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
@@ -38,6 +42,15 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d, uint64_t a, uint64_t 
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
+}
+
+__device__ __forceinline__ void copy_scale(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float own_scale(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
 }
 
 constexpr int kMaxRowTiles = DLITE_FP8_MAX_ROWS / 256;
@@ -182,25 +195,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t acce_leader = tc::map_to_rank(acce0, 0);
     uint8_t* staged = smem + kStages * kStage + (warp - 4) * 32 * kPitch;
     const int nb = fp8::blocks_of(p.N);
+    const uint32_t scales = tc::su32(smem + kStages * kStage + kStaging) + threadIdx.x * 4 - 512;  // this thread's word of slot 0
     int i = 0;
     for (int t = pair; t < tiles; t += pairs) {
       const int row0 = (t % row_tiles) * 256, n0 = t / row_tiles;
       if (skip(t)) continue;
       const int wrow0 = row0 + (int)rank * 128 + q * 32, row = wrow0 + lane;
-      const float* xs = p.xs + (long long)min(row, p.rows - 1) * p.kblocks;
+      const float* xs = p.xs + min(row, p.rows - 1);
+#pragma unroll
+      for (int k = 0; k < kScalesAhead; ++k) {
+        if (k < p.kblocks) copy_scale(scales + k * 1024, xs);
+        xs += p.rows;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
       const int wb = GATED ? n0 : min(2 * n0 + eg, nb - 1);      // a block past the last has no columns to write
       const float* w0 = p.ws[0] + (long long)wb * p.kblocks;
       const float* w1 = GATED ? p.ws[1] + (long long)wb * p.kblocks : w0;
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      float x_next = xs[0], w0_next = w0[0], w1_next = w1[0];
+      float w0_next = w0[0], w1_next = w1[0];
       bool ok = true;
       for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
         const int b = i & 1;
-        const float s0 = x_next * w0_next, s1 = GATED ? x_next * w1_next : s0;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kScalesAhead - 1) : "memory");
+        const float x = own_scale(scales + kb % kScaleSlots * 1024), s0 = x * w0_next, s1 = GATED ? x * w1_next : s0;
+        if (kb + kScalesAhead < p.kblocks) copy_scale(scales + (kb + kScalesAhead) % kScaleSlots * 1024, xs);
+        xs += p.rows;
+        asm volatile("cp.async.commit_group;" ::: "memory");
         if (kb + 1 < p.kblocks) {
-          x_next = xs[kb + 1];
           w0_next = w0[kb + 1];
           if (GATED) w1_next = w1[kb + 1];
         }
@@ -230,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc[16 * c + j] = fma2(pack2f(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])), sc2, acc[16 * c + j]);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // where a wait gave up: no copy is left on its way
       // the sums leave through this warp's staging, so that neighbouring lanes store neighbouring columns
       if constexpr (GATED) {
         float a[64];
@@ -259,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool valid = row < p.rows && fp8::valid_row(p.n_rows, p.T, row);
         if (valid && bad) flag_status(p.status, kDevNonfinite);
-        if (valid && eg == 0) p.scale[(long long)row * nb + n0] = fp8::exp2i(e);
+        if (valid && eg == 0) p.scale[(long long)n0 * p.rows + row] = fp8::exp2i(e);
         const uint32_t valid_rows = __ballot_sync(0xffffffffu, valid);
         const int n = n0 * 128 + eg * 64 + (lane & 3) * 16;
 #pragma unroll

@@ -18,7 +18,7 @@ using fp8::kBlock;
 constexpr int kPer = 16;  // columns of a thread
 
 struct QuantiseArgs {
-  int rows, T, K, kblocks;
+  int rows, T, K;
   const void* x;
   long long xs;
   const void* res;
@@ -100,7 +100,7 @@ __device__ __forceinline__ void quantise_piece(const QuantiseArgs& a, int row, i
     for (int i = 0; i < kPer; ++i)
       if (c + i < a.K) dst[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
-  if (c % kBlock == 0) a.scale[(long long)row * a.kblocks + c / kBlock] = fp8::exp2i(e);
+  if (c % kBlock == 0) a.scale[(long long)(c / kBlock) * a.rows + row] = fp8::exp2i(e);
 }
 
 // v = x + residual in the stream's type, stored
@@ -345,7 +345,6 @@ extern "C" int dlite_fp8_quantise(const dlite_fp8_quantise_args* g, dlite_stream
   a.rows = g->B * g->T;
   a.T = g->T;
   a.K = g->K;
-  a.kblocks = fp8::blocks_of(g->K);
   a.x = g->x;
   a.xs = g->x_stride;
   a.res = g->residual;

@@ -597,7 +597,7 @@ int dlite_token_logprobs(const dlite_logprobs_args *args, dlite_stream_t stream)
  * Products with 8-bit weights: the projections and the gated feed-forward block of the target's rows, whose time at a verification
  * block's sizes is the reading of the weights. The common rules of the target-side calls hold (rows, n_rows, status).
  * Numbers are e4m3 codes with a scale per block of DLITE_FP8_BLOCK:
- *   activations  codes [B, T, K] and scale [B T][ceil(K / 128)] float32, one per 128 columns of a row
+ *   activations  codes [B, T, K] and scale [ceil(K / 128)][B T] float32, one per 128 columns of a row (the rows of a block side by side)
  *   weights      codes [N, K] and scale [ceil(N / 128)][ceil(K / 128)] float32 (any finite numbers), one per 128 x 128 elements
  * A code's value is code x scale. Code rows start on 16 bytes: 16-byte aligned memory, strides (in bytes) a multiple of 16;
  * bytes of a row past its columns are neither read into a result nor written. Scales are dense.
@@ -678,7 +678,7 @@ typedef struct {
     const float *up_scale;
     uint8_t *out_codes;   /* [B, T, F] */
     int64_t out_stride;
-    float *out_scale;     /* [B T][ceil(F / 128)] */
+    float *out_scale;     /* [ceil(F / 128)][B T] */
     const int32_t *n_rows;
     int *status;
 } dlite_fp8_gated_args;

@@ -108,13 +108,14 @@ def test_sizes_outside_32_bits(closed, call):
 
 
 def test_the_bindings_checks(closed):
-    x, c, s, w, ws = _far(2, 3, 160), _codes(2, 3, 160), _far(2, 3, 2), _codes(50, 160), _far(1, 2)
+    x, c, s, w, ws = _far(2, 3, 160), _codes(2, 3, 160), torch.empty_strided((2, 3, 2), (3, 1, 6), device="meta"), _codes(50, 160), _far(1, 2)
     bad = [
         lambda: binding.fp8_quantise(x[0]), lambda: binding.fp8_quantise(x[:, :2]), lambda: binding.fp8_quantise(x[..., ::2]),
         lambda: binding.fp8_quantise(x.to(torch.float16)), lambda: binding.fp8_quantise(x, total=x), lambda: binding.fp8_quantise(x, residual=x[:, :1]),
         lambda: binding.fp8_quantise(x, residual=x.bfloat16()), lambda: binding.fp8_quantise(x, gain=x[0, 0, :100]),
         lambda: binding.fp8_quantise(x, gain=x[0, 0].bfloat16()), lambda: binding.fp8_quantise(x, codes=c[..., :100]),
         lambda: binding.fp8_quantise(x, codes=x), lambda: binding.fp8_quantise(x, scale=s[..., :1]), lambda: binding.fp8_quantise(x, scale=s.double()),
+        lambda: binding.fp8_quantise(x, scale=_far(2, 3, 2)), lambda: binding.fp8_linear(c, _far(2, 3, 2), w, ws),
         lambda: binding.fp8_quantise(x, n_rows=torch.zeros(3, dtype=torch.int32)), lambda: binding.fp8_quantise(x, n_rows=torch.zeros(2)),
         lambda: binding.fp8_quantise(x[:1].expand(2, 3, 160)),
         lambda: binding.fp8_weight(x), lambda: binding.fp8_weight(x[0].t()), lambda: binding.fp8_weight(x[0].double()),
@@ -123,7 +124,7 @@ def test_the_bindings_checks(closed):
         lambda: binding.fp8_linear(c, s, w, ws, out=_far(2, 3, 50).double()), lambda: binding.fp8_linear(c, s, w, ws, out=_far(2, 50, 3).transpose(1, 2)),
         lambda: binding.fp8_linear(c, s, w, ws, dtype=torch.float16),
         lambda: binding.fp8_gated(c, s, w, ws, w[:49], ws), lambda: binding.fp8_gated(c, s, w, ws, w, ws, out=_codes(2, 3, 49)),
-        lambda: binding.fp8_gated(c, s, w, ws, w, ws, out=_far(2, 3, 50)), lambda: binding.fp8_gated(c, s, w, ws, w, ws, out_scale=_far(2, 3, 2)),
+        lambda: binding.fp8_gated(c, s, w, ws, w, ws, out=_far(2, 3, 50)), lambda: binding.fp8_gated(c, s, w, ws, w, ws, out_scale=s),
         lambda: binding.fp8_gated(c, s, w, ws, w, ws.double()),
     ]
     for i, call in enumerate(bad):

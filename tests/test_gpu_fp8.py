@@ -192,7 +192,7 @@ def test_rows_behind_a_requests_last(B, T, K, N):
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     kw = dict(n_rows=n.to(DEV), status=st)
     codes = torch.full((B, T, -(-K // 16) * 16), 0x7F, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)[..., :K]
-    scale = torch.full((B, T, -(-K // 128)), float("nan"), device=DEV)
+    scale = binding.fp8_scale(B, T, K).fill_(float("nan"))
     res, total = torch.ones_like(x), torch.full_like(x, 5.0)
     binding.fp8_quantise(x, residual=res, total=total, codes=codes, scale=scale, **kw)
     v = FO.total(np.where(ok.numpy()[..., None], _np(x), 0), _np(res), "bf16")
@@ -210,7 +210,7 @@ def test_rows_behind_a_requests_last(B, T, K, N):
     assert np.all(np.abs(got - y)[m] <= tol[m]) and np.all(got[~m] == 3) and bool((out.as_strided((B, T, 8), (T * (N + 8), N + 8, 1), N) == 3).all())
     F = N
     oc = torch.full((B, T, -(-F // 16) * 16 + 16), 0x55, dtype=torch.uint8, device=DEV)
-    os_ = torch.full((B, T, -(-F // 128)), 9.0, device=DEV)
+    os_ = binding.fp8_scale(B, T, F).fill_(9.0)
     binding.fp8_gated(codes, scale, w, wsc, w, wsc, out=oc.view(torch.float8_e4m3fn)[..., :F], out_scale=os_, **kw)
     full, fs = binding.fp8_gated(*binding.fp8_quantise(torch.from_numpy(v).float().to(DEV)), w, wsc, w, wsc)
     assert np.array_equal(_bytes(oc)[..., :F][m], _bytes(full)[m]) and np.array_equal(_np(os_)[m], _np(fs)[m])
