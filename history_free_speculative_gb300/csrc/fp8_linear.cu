@@ -10,7 +10,9 @@
 // that are its own, in order, so results are the same run to run.
 // Gated: a tile has 64 gate rows and the 64 up rows of the same columns; two CTAs of a cluster make up the 128 columns
 // that share a scale.
-// Bound: the weights' bytes.
+// Bound: the weights' bytes, and 4 us to begin and end (the way of the first bytes, the join). A graph's call, weights from HBM: 1 row of 4,096 x
+// 4,096 6.4 us (floor 2.5), of 4,096 x 12,288 10.9 (7.4), 8 rows of 151,936 x 4,096 91 to 94 (91.8: 98% of the copy rate), gated 12,288 x
+// 4,096 20.4 (14.9). With full row tiles the way round of an accumulator counts: 256 rows of 6,144 x 4,096 13.6 us, 0.95 PFLOP/s.
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -272,9 +274,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---------------------------------------------------------------- host side
 
 // Splits of the k blocks: the least time of one CTA's run, where two CTAs on an SM take 8/5 of one's time a block (1 row, 4,096 x
-// 12,288: 4 splits, 128 CTAs, 12.7 us; 8 splits, 256 CTAs, 11.0; 32 rows, 6,144 x 4,096: 3 splits, 144 CTAs, 8.75, 4 splits, 192 CTAs, 8.85). At
-// least four blocks a CTA (340 rows, 1,024 x 2,176: 7.8 us, with two 10.0), and clusters of four and more leave an eighth of the places
-// free, since not every GPC has a multiple of them (gated 9,728 x 2,560, 8 rows: 152 CTAs in twos 14.2 us, 304 in fours 17.9).
+// 12,288: 4 splits, 128 CTAs, 12.1 us, 8 splits, 256 CTAs, 10.9; 32 rows, 6,144 x 4,096: 3 splits, 144 CTAs, 8.7, 4 splits, 192 CTAs, 9.0). At
+// least four blocks a CTA (340 rows, 1,024 x 2,176: 8.0 us with four, 9.7 with two), and clusters of four and more leave an eighth of the
+// places free, since not every GPC has a multiple of them (gated 9,728 x 2,560, 8 rows: 152 CTAs in twos 11.7 us, 304 in fours 16.5).
 // us: an estimate of the call's time, to be compared with the many-row kernel's.
 SmallPlan small_plan(const ProductArgs& p, bool gated, double& us) {
   SmallPlan pl;
@@ -328,7 +330,7 @@ template <bool GATED, typename OUT>
 int product(const ProductArgs& p, const fp8::Operands& o, cudaStream_t s) {
   double us;
   const SmallPlan pl = small_plan(p, GATED, us);
-  if (fp8::pairs_us(p, GATED) < us) return launch_status(fp8::launch_pairs(o, p, GATED, sizeof(OUT) == 4, s));
+  if (p.rows > 128 && fp8::pairs_us(p, GATED) < us) return launch_status(fp8::launch_pairs(o, p, GATED, sizeof(OUT) == 4, s));
   return launch_status(launch_small<GATED, OUT>(o, p, pl, s));
 }
 

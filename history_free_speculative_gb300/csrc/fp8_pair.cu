@@ -4,8 +4,13 @@
 // kind::f8f6f4 (M = 256, N = 256, K = 32) write one of two accumulators in tensor memory (all its 512 columns); CTA c holds rows 128 c .. of x
 // and rows 128 c .. of the weights in its shared memory and gets its 128 rows over all 256 columns. Eight epilogue warps a CTA take an
 // accumulator times the block's scales into float32 sums in registers (lane = row, 128 columns a thread) while the
-// tensor cores work on the next, so that the scales cost the tensor pipe nothing as long as a block's sums (256 issue slots of
-// packed multiply-adds a scheduler) stay under its 512 cycles of products.
+// tensor cores work on the next.
+// What bounds it: the way round of an accumulator (products 512 clocks, commit to both CTAs, reads, hand-over to the CTA that issues), 1,700
+// clocks for two blocks, and under load the power cap (1,300 W, 1.57 GHz): 8,192 rows of 6,144 x 4,096 153 to 183 us (2.3 to 2.7 PFLOP/s), of
+// 4,096 x 12,288 290 to 300 us, gated 12,288 x 4,096 571 us (2.9). The same kernel without reads and hand-overs takes 0.36 us a block instead of 0.43.
+// Tried: 128 weight rows a step and four accumulators (371 us for 4,096 x 12,288: twice the waits); one-CTA products of 128 x 256 handed over
+// inside the SM (309 us: an SM then takes in 48 KB a block where its way from L2 brings 64 bytes a clock); splits of the k blocks over clusters of
+// four to eight CTAs for few tiles (few such clusters of whole-SM CTAs are resident at once).
 // Gated: the 256 weight rows are [64 gate | 64 up] twice, so a thread holds 64 gate and 64 up columns of its row, and the two warps of a
 // row exchange one maximum for the scale of its 128 results.
 // Tiles go to the pairs row tiles first: the weights are read from HBM once, x stays in L2.
@@ -385,8 +390,9 @@ cudaError_t launch(const fp8::Operands& o, const ProductArgs& p, int row_tiles, 
 
 namespace fp8 {
 
-// 0.43 us a k block of a tile, 3 us to start and end (512 rows: 6,144 x 4,096 16.9 us, 21.6 with the few-row kernel; 4,096 x 12,288 39.5 us, 33.0 with
-// it, since 32 tiles leave most SMs idle; gated 12,288 x 4,096, 256 rows: 35 us, 49 with it; 128 rows: 34 us, 29 with it).
+// 0.43 us a k block of a tile, 3 us to start and end. 512 rows: 6,144 x 4,096 16.6 us, with the few-row kernel 19.4; 4,096 x 12,288 37.7 us, 28.0 with
+// it, since 32 tiles leave most SMs idle. Gated 12,288 x 4,096: 256 rows 32.9 us, 44.5 with it; 128 rows, which fill half of a tile, 34.5 and
+// 25.7: up to 128 rows this kernel is not asked.
 double pairs_us(const ProductArgs& p, bool gated) {
   const int pairs = std::max(1, device_sms() / 2);
   const long long tiles = (long long)((p.rows + 255) / 256) * (gated ? blocks_of(p.N) : (p.N + 255) / 256);
