@@ -635,16 +635,17 @@ def _codes_of(t, what):
     if t.dtype != _E4M3:
         raise ValueError(f"{what}: float8_e4m3fn expected, got {t.dtype}")
     B, T, C, row = _rows_of(t, what)
-    return B, T, C, row if B * T > 1 else -(-C // 16) * 16
+    return B, T, C, row if row != C or B * T > 1 else -(-C // 16) * 16
 
 
 def _scale_of(t, B, T, C, what):
     """Pointer of the scales [B, T, ceil(C / 128)] of rows, whose memory has the rows (b, t) of a block side by side."""
     n = -(-C // FP8_BLOCK)
-    sb, st, sn = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if t.dtype != torch.float32 or t.shape != (B, T, n) or (n > 1 and sn != B * T) or (T > 1 and st != 1) or (B > 1 and sb != T):
-        raise ValueError(f"{what}: float32 {[B, T, n]} with strides {[T, 1, B * T]} expected, got {t.dtype} {list(t.shape)} with strides "
-                         f"{list(t.stride())}")
+    if t.dtype != torch.float32 or t.shape != (B, T, n) or t.stride() != (T, 1, B * T):
+        sb, st, sn = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if t.dtype != torch.float32 or t.shape != (B, T, n) or (n > 1 and sn != B * T) or (T > 1 and st != 1) or (B > 1 and sb != T):
+            raise ValueError(f"{what}: float32 {[B, T, n]} with strides {[T, 1, B * T]} expected, got {t.dtype} {list(t.shape)} with strides "
+                             f"{list(t.stride())}")
     return t.data_ptr()
 
 
@@ -660,13 +661,20 @@ def fp8_scale(B, T, C, stream=None):
 
 def _weight_of(w, scale, K, what):
     """(N, pointer, bytes between the rows, pointer of the scales) of codes [N, K] and their scales."""
-    if w.dtype != _E4M3 or w.dim() != 2 or w.shape[1] != K or (K > 1 and w.stride(1) != 1):
-        raise ValueError(f"{what}: float8_e4m3fn [N, {K}] with dense rows expected, got {w.dtype} {list(w.shape)}")
+    if w.dtype != _E4M3 or w.dim() != 2 or w.shape[1] != K:
+        raise ValueError(f"{what}: float8_e4m3fn [N, {K}] expected, got {w.dtype} {list(w.shape)}")
     N = w.shape[0]
     if N >> 31:
         _sizes(what, N, K)
-    row = w.stride(0) if N > 1 else -(-K // 16) * 16
-    return N, w.data_ptr(), row, _vec(scale, torch.float32, (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)), what + "_scale")
+    row, col = w.stride()
+    if K > 1 and col != 1:
+        raise ValueError(f"{what}: the columns of a row have to be dense")
+    if N == 1:
+        row = -(-K // 16) * 16
+    if scale.dtype != torch.float32 or scale.shape != (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)) or not scale.is_contiguous():
+        raise ValueError(f"{what}_scale: contiguous float32 {[-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)]} expected, got {scale.dtype} "
+                         f"{list(scale.shape)}")
+    return N, w.data_ptr(), row, scale.data_ptr()
 
 
 def _new_strided(stream, shape, strides, dtype):
