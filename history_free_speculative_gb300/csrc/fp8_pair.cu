@@ -75,7 +75,7 @@ template <bool GATED, typename OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
                     const ProductArgs p, const int row_tiles, const int tiles) {
-  // Shared memory: [barriers, row maxima | pad to 1 KB] [stage 0] .. [epilogue staging]; stage = [x tile][weight tile]
+  // Shared memory: [barriers | pad to 1 KB] [stage 0] .. [epilogue staging] [scales]; stage = [x tile][weight tile]
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = (uint64_t*)base;
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc::fence_before();
   __syncthreads();
+  if (warp == 1 && rank == 1) tc::mbar_wait_warp(done, 0, p.status);  // the last commit's arrival, behind all others', before the barriers go
   tc::cluster_sync_all();  // no copy, commit, arrival or product of the pair is outstanding past this point
   if (warp == 1) {
     tc::fence_after();

@@ -142,6 +142,15 @@ def test_weight(dtype, N, K, pad):
     assert c.stride(0) % 16 == 0
 
 
+def test_weight_that_is_not_finite():
+    w = _input(1, 140, 300, "f32", 9)[0]
+    w[3, 4], w[130, 299] = float("nan"), float("-inf")
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c, s = binding.fp8_weight(w, status=st)
+    want, ws = FO.quantise_weight(_np(w))
+    assert np.array_equal(_np(s), ws) and np.array_equal(_bytes(c), want) and int(st.item()) == binding.DEV_NONFINITE
+
+
 # ---------------------------------------------------------------- products
 
 SHAPES = [(1, 1, 128, 128), (1, 1, 1, 1), (1, 1, 4096, 4096), (1, 8, 2560, 1000), (1, 7, 100, 129), (3, 3, 129, 64), (1, 33, 384, 200), (2, 64, 1000, 777),
@@ -177,6 +186,65 @@ def test_gated(B, T, K, F):
     # a result below 2^-120 may be 0 (the reciprocal's)
     err = 1.1 * ge * (np.abs(uw) + ue) + np.abs(FO.silu(gw)) * ue + (9 + 2 * np.abs(gw)) * 2.0 ** -24 * np.abs(want) + 2.0 ** -110 * np.abs(uw)
     _quantised(_bytes(oc).reshape(B * T, F), _np(os_).reshape(B * T, -1), want, err)
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+@pytest.mark.parametrize("size", [1e2, 1e5, 1e30])
+def test_gated_far(rows, size):
+    """Gates far from 0: exp(-g) from nothing to infinity. Results past float32 become NaN codes and flag the status."""
+    K, F = 256, 130
+    c, s = binding.fp8_quantise(_input(1, rows, K, "bf16", 8))
+    (g, gs), (u, us) = _weight(F, K, 9), _weight(F, K, 10)
+    gs = gs * size
+    us = us * (1e15 if size == 1e30 else 1)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    oc, os_ = binding.fp8_gated(c, s, g, gs, u, us, status=st)
+    x = FO.values(_bytes(c), _np(s))[0]
+    gv, uv = FO.weight_values(_bytes(g), _np(gs)), FO.weight_values(_bytes(u), _np(us))
+    gw, uw, off = x @ gv.T, x @ uv.T, _off(2)
+    ge, ue = off * _reach(x, gv), off * _reach(x, uv)
+    want, big = FO.silu(gw) * uw, 3.4e38
+    # as in test_gated; above 128 exp(-g) is nothing to 1, below -128 the result is less than 2^-110 of u
+    err = 1.1 * ge * (np.abs(uw) + ue) + np.abs(FO.silu(gw)) * ue + (9 + 2 * np.minimum(np.abs(gw), 128)) * 2.0 ** -24 * np.abs(want) + 2.0 ** -110 * np.abs(uw)
+    got, sure = _bytes(oc)[0], np.abs(want) - err > big
+    nan = (got & 0x7F) == 0x7F
+    assert np.all(nan[sure]) and not nan[np.abs(want) + err < big].any() and int(st.item()) == (binding.DEV_NONFINITE if nan.any() else 0)
+    assert nan.any() == (size == 1e30)
+    ok = ~FO.blocked(nan.astype(float)).any(-1)[..., None] & (FO.blocked(np.ones_like(want)) > 0)      # blocks without one
+    y, e, v = FO.blocked(want), FO.blocked(err), FO.blocked(FO.values(np.where(nan, 0, got), _np(os_)[0]))
+    sc = _np(os_)[0][..., None]
+    step = 2.0 ** (np.floor(np.log2(np.maximum((np.abs(y) + e) / sc, 2.0 ** -6))) - 3) * sc
+    assert np.all((np.abs(v - y) <= step / 2 + e)[ok])
+
+
+# ---------------------------------------------------------------- the largest sizes
+
+@pytest.mark.parametrize("B,T,K,N", [(1, 2, 1 << 20, 130), (1, 2, 16, 1 << 22), (1 << 11, 1 << 11, 16, 8), (1, 300, 1 << 18, 20)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_largest_sizes(B, T, K, N, ragged):
+    """The ends of K, N and rows, against products in 64 bits on the device."""
+    x = torch.randn(B, T, K, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    n = torch.arange(B, dtype=torch.int32, device=DEV) * 7 % (T + 1) if ragged else None
+    c, s = binding.fp8_quantise(x, n_rows=n)
+    c0, s0 = binding.fp8_quantise(x)
+    m = torch.arange(T, device=DEV)[None] < n[:, None] if ragged else torch.ones(B, T, dtype=torch.bool, device=DEV)
+    assert torch.equal(c.view(torch.uint8)[m], c0.view(torch.uint8)[m]) and torch.equal(s[m], s0[m])
+    w, ws = _weight(N, K, 2)
+    y = binding.fp8_linear(c, s, w, ws, dtype=torch.float32, n_rows=n)
+    oc, os_ = binding.fp8_gated(c, s, w, ws * K ** -0.5, w, ws * K ** -0.5, n_rows=n)
+    assert not bool(y[~m].any())
+    xv = (c0.double() * s0.double().repeat_interleave(128, -1)[..., :K]).view(B * T, K)
+    wv = w.double() * ws.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    want, reach = (xv @ wv.T).view(B, T, N), (xv.abs() @ wv.abs().T).view(B, T, N)
+    tol = _off(-(-K // 128)) * reach + HALF["f32"] * want.abs()
+    assert bool(((y.double() - want).abs() <= tol)[m].all())
+    g = want * K ** -0.5
+    a = g / (1 + torch.exp(-g)) * g
+    v = oc.double() * os_.double().repeat_interleave(128, -1)[..., :N]
+    # half a step of the value, of the least step where it is small, and the sums' error through the product: |d(silu(g) g)| < 2.2 |g| + 1 times it
+    e = tol * K ** -0.5
+    err = a.abs() / 16 + os_.double().repeat_interleave(128, -1)[..., :N] * 2.0 ** -10 + e * (2.2 * g.abs() + 1 + e) + (9 + 2 * g.abs()) * 2.0 ** -24 * a.abs()
+    assert bool(((v - a).abs() <= err * 1.07)[m].all())      # the step is that of the value with its error
 
 
 # ---------------------------------------------------------------- rows of a ragged batch
