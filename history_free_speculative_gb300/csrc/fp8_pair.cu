@@ -71,7 +71,44 @@ __device__ __forceinline__ bool live_tile(const ProductArgs& p, int row0) {
   return false;
 }
 
-template <bool GATED, typename OUT>
+// 32 staged rows of 128 bytes to rows off 16 bytes, lanes side by side, `cols` columns at most. 16 bytes a lane element by element, 770 rows of 260
+// and 26,226 bf16 columns took 110 us, side by side 40 (26,224 on 16 bytes: 23); 4,096 of 4,096 and 4,099 116 and 75. In a kernel of its own: with
+// both stores in one, rows on 16 bytes took 3 % more. (The few-row kernel keeps its scalar stores: 64 rows of 4,096 and 4,099 lose 0.25 us of 8.6 to
+// them, and lanes side by side there cost its other calls 0.1 to 0.9 us.)
+template <typename OUT>
+__device__ __noinline__ void store_rows(OUT* dst, long long stride, const uint8_t* staged, uint32_t valid_rows, int cols) {
+  constexpr int E = 4 / sizeof(OUT), kBatch = 8;
+  const int lane = threadIdx.x & 31, c = lane * E;
+  // 16 bits: a row on 4 bytes takes a lane's columns c and c + 1 as a word, any other row columns c + 1 and c + 2 and its first column alone
+  const bool word0 = c + E <= cols, half0 = c + 1 == cols, word1 = lane < 31 && c + 2 < cols, half1 = !word1 && c + 1 < cols,
+             first1 = lane == 0 && cols > 0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += kBatch) {
+    uint32_t w[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) w[i] = reinterpret_cast<const uint32_t*>(staged + (r0 + i) * kPitch)[lane];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i, dst += stride) {
+      const bool valid = valid_rows >> (r0 + i) & 1;
+      if constexpr (E == 1) {
+        if (valid && word0) dst[c] = __uint_as_float(w[i]);
+      } else {
+        uint16_t* d = reinterpret_cast<uint16_t*>(dst) + c;
+        if (((uintptr_t)dst & 3) == 0) {
+          if (valid && word0) *reinterpret_cast<uint32_t*>(d) = w[i];
+          if (valid && half0) d[0] = (uint16_t)w[i];
+        } else {
+          const uint32_t next = __shfl_down_sync(~0u, w[i], 1);
+          if (valid && word1) *reinterpret_cast<uint32_t*>(d + 1) = w[i] >> 16 | next << 16;
+          if (valid && half1) d[1] = (uint16_t)(w[i] >> 16);
+          if (valid && first1) d[0] = (uint16_t)w[i];
+        }
+      }
+    }
+  }
+}
+
+template <bool GATED, typename OUT, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw0, const __grid_constant__ CUtensorMap mw1,
                     const ProductArgs p, const int row_tiles, const int tiles) {
@@ -332,21 +369,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(staged + lane * kPitch + 16 * j) = w;
           }
           __syncwarp();
-          const int n = n0 * 256 + eg * 128 + piece * C + (lane & 7) * E;
+          const int n = n0 * 256 + eg * 128 + piece * C;
+          if constexpr (VEC) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = 4 * j + (lane >> 3);
-            const uint4 w = *reinterpret_cast<const uint4*>(staged + r * kPitch + 16 * (lane & 7));
-            if (!(valid_rows >> r & 1)) continue;
-            OUT* dst = static_cast<OUT*>(p.out) + (long long)(wrow0 + r) * p.os + n;
-            if (p.vec && n + E <= p.N) {
-              *reinterpret_cast<uint4*>(dst) = w;
-            } else {
-              const OUT* e = reinterpret_cast<const OUT*>(&w);
+            for (int j = 0; j < 8; ++j) {
+              const int r = 4 * j + (lane >> 3), m = n + (lane & 7) * E;
+              const uint4 w = *reinterpret_cast<const uint4*>(staged + r * kPitch + 16 * (lane & 7));
+              if (!(valid_rows >> r & 1)) continue;
+              OUT* dst = static_cast<OUT*>(p.out) + (long long)(wrow0 + r) * p.os + m;
+              if (m + E <= p.N) {
+                *reinterpret_cast<uint4*>(dst) = w;
+              } else {
+                const OUT* e = reinterpret_cast<const OUT*>(&w);
 #pragma unroll
-              for (int k = 0; k < E; ++k)
-                if (n + k < p.N) dst[k] = e[k];
+                for (int k = 0; k < E; ++k)
+                  if (m + k < p.N) dst[k] = e[k];
+              }
             }
+          } else {
+            store_rows(static_cast<OUT*>(p.out) + (long long)wrow0 * p.os + n, p.os, staged, valid_rows, p.N - n);
           }
           __syncwarp();
         }
@@ -364,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool GATED, typename OUT>
+template <bool GATED, typename OUT, bool VEC>
 cudaError_t launch(const fp8::Operands& o, const ProductArgs& p, int row_tiles, int tiles, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<GATED, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<GATED, OUT, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   fp8::Maps m;
   if (!fp8::make_maps(m, o, p, 128, GATED ? 64 : 128)) return cudaErrorInvalidValue;
@@ -384,7 +425,7 @@ cudaError_t launch(const fp8::Operands& o, const ProductArgs& p, int row_tiles, 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<GATED, OUT>, m.x, m.w0, m.w1, p, row_tiles, tiles);
+  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<GATED, OUT, VEC>, m.x, m.w0, m.w1, p, row_tiles, tiles);
 }
 
 }  // namespace
@@ -402,8 +443,9 @@ double pairs_us(const ProductArgs& p, bool gated) {
 
 cudaError_t launch_pairs(const Operands& o, const ProductArgs& p, bool gated, bool f32, cudaStream_t s) {
   const int row_tiles = (p.rows + 255) / 256, tiles = row_tiles * (gated ? blocks_of(p.N) : (p.N + 255) / 256);
-  if (gated) return launch<true, float>(o, p, row_tiles, tiles, s);
-  return f32 ? launch<false, float>(o, p, row_tiles, tiles, s) : launch<false, bf16>(o, p, row_tiles, tiles, s);
+  if (gated) return launch<true, float, true>(o, p, row_tiles, tiles, s);
+  if (!p.vec) return f32 ? launch<false, float, false>(o, p, row_tiles, tiles, s) : launch<false, bf16, false>(o, p, row_tiles, tiles, s);
+  return f32 ? launch<false, float, true>(o, p, row_tiles, tiles, s) : launch<false, bf16, true>(o, p, row_tiles, tiles, s);
 }
 
 }  // namespace fp8
