@@ -293,56 +293,86 @@ __global__ void __launch_bounds__(VEC ? 1024 : 512) fp8_norm_quantise_wide_kerne
   if (bad) flag_status(a.status, kDevNonfinite);
 }
 
-// A weight's block of 128 x 128: one CTA, 16 rows a warp, four columns a lane, read once and held in registers.
+// A weight's block of 128 x 128: one CTA, 16 rows a warp, four columns a lane, read once and held in registers. Magnitudes compare as integers; a
+// block that is not finite is found by its maximum and takes a second way. 151,936 x 4,096 took 305 us
+// from bf16 and 446 from float32, 6.1 and 7.0 TB/s (580 and 565 with a test of each element, at two CTAs an SM): HBM bounds it.
+template <typename T>
+using Word4 = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
+__device__ __forceinline__ uint32_t magnitudes(uint32_t m, uint4 w) {
+  return max(max(max(m, w.x & 0x7fffffffu), w.y & 0x7fffffffu), max(w.z & 0x7fffffffu, w.w & 0x7fffffffu));
+}
+__device__ __forceinline__ uint32_t magnitudes(uint32_t m, uint2 w) { return __vmaxu2(__vmaxu2(m, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu); }
+__device__ __forceinline__ void floats4(uint4 w, float (&v)[4]) {
+  v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void floats4(uint2 w, float (&v)[4]) {
+  v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+  v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+// The block's maximum, in every thread. red: 8 words that nobody else reads or writes.
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
+  m = __reduce_max_sync(~0u, m);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, red[i]);
+  return m;
+}
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) fp8_weight_kernel(const T* w, long long ws, int N, int K, uint8_t* codes, long long cs, float* scale,
-                                                         int* status) {
-  __shared__ float red[8];
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
+    fp8_weight_kernel(const T* w, long long ws, int N, int K, uint8_t* codes, long long cs, float* scale, int* status) {
+  __shared__ uint32_t red[2][8];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x * kBlock + 4 * lane;
-  T held[16][4];
+  Word4<T> held[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int n = blockIdx.y * kBlock + 8 * i + warp;
     const T* at = w + n * ws + k;
+    held[i] = Word4<T>{};
     if (VEC) {  // K is a multiple of 4, rows on 16 bytes
-      using Word = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
-      *reinterpret_cast<Word*>(held[i]) = n < N && k < K ? *reinterpret_cast<const Word*>(at) : Word{};
+      if (n < N && k < K) held[i] = *reinterpret_cast<const Word4<T>*>(at);
     } else {
+      T e[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) held[i][j] = n < N && k + j < K ? at[j] : T(0.f);
+      for (int j = 0; j < 4; ++j) e[j] = n < N && k + j < K ? at[j] : T(0.f);
+      memcpy(&held[i], e, sizeof(held[i]));
     }
   }
-  float amax = 0.f;
-  bool bad = false;
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 16; ++i) m = magnitudes(m, held[i]);
+  if (sizeof(T) == 2) m = max(m >> 16, m & 0xffffu) << 16;
+  m = block_max(m, red[0]);
+  const bool bad = m >= 0x7f800000u;
+  if (bad) {  // the largest finite one
+    m = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float v = fabsf(to_f32(held[i][j]));
-      if (v <= 3.402823466e38f)
-        amax = fmaxf(amax, v);
-      else
-        bad = true;
+    for (int i = 0; i < 16; ++i) {
+      float v[4];
+      floats4(held[i], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (fabsf(v[j]) <= 3.402823466e38f) m = max(m, __float_as_uint(fabsf(v[j])));
     }
-  amax = warp_max(amax);
-  if (lane == 0) red[warp] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, red[i]);
-  const int e = fp8::block_exponent(amax);
+    m = block_max(m, red[1]);
+  }
+  const int e = fp8::block_exponent(__uint_as_float(m));
   const float inv = fp8::exp2i(-e);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int n = blockIdx.y * kBlock + 8 * i + warp;
     if (n >= N) break;
     float v[4];
+    floats4(held[i], v);
+    if (bad) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = to_f32(held[i][j]);
-      v[j] = fabsf(v[j]) <= 3.402823466e38f ? v[j] * inv : __uint_as_float(0x7fffffffu);
+      for (int j = 0; j < 4; ++j)
+        if (!(fabsf(v[j]) <= 3.402823466e38f)) v[j] = __uint_as_float(0x7fffffffu);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= inv;
     const uint32_t c = fp8::codes4(v[0], v[1], v[2], v[3]);
     uint8_t* dst = codes + n * cs + k;
     if (k + 4 <= K) {
@@ -352,7 +382,7 @@ __global__ void __launch_bounds__(256) fp8_weight_kernel(const T* w, long long w
     }
   }
   if (threadIdx.x == 0) scale[(long long)blockIdx.y * gridDim.x + blockIdx.x] = fp8::exp2i(e);
-  if (bad) flag_status(status, kDevNonfinite);
+  if (bad && threadIdx.x == 0) flag_status(status, kDevNonfinite);
 }
 template <typename T>
 cudaError_t launch_weight(const dlite_fp8_weight_args& g, cudaStream_t s) {

@@ -151,6 +151,20 @@ def test_weight_that_is_not_finite():
     assert np.array_equal(_np(s), ws) and np.array_equal(_bytes(c), want) and int(st.item()) == binding.DEV_NONFINITE
 
 
+@pytest.mark.parametrize("dtype,K", [("bf16", 300), ("bf16", 304), ("f32", 304)])
+def test_weight_blocks_without_a_finite_element(dtype, K):
+    w = _input(1, 260, K, dtype, 19)[0]
+    w[:128, :128] = float("inf")
+    w[128:256, 128:256] = float("nan")
+    w[259, K - 1] = -float("inf")
+    w[5, 200] = torch.finfo(w.dtype).max  # the largest magnitude that counts
+    w[6, 201] = float("inf")
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c, s = binding.fp8_weight(w, status=st)
+    want, ws = FO.quantise_weight(_np(w))
+    assert np.array_equal(_np(s), ws) and np.array_equal(_bytes(c), want) and int(st.item()) == binding.DEV_NONFINITE
+
+
 # ---------------------------------------------------------------- products
 
 SHAPES = [(1, 1, 128, 128), (1, 1, 1, 1), (1, 1, 4096, 4096), (1, 8, 2560, 1000), (1, 7, 100, 129), (3, 3, 129, 64), (1, 33, 384, 200), (2, 64, 1000, 777),
