@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tmem_holder)), "r"(kCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    pdl_trigger();  // behind the allocation: a kernel after this one cannot take columns that it still waits for
   }
-  pdl_trigger();
   if (warp == 0 && fp8::elect_one())
     for (int j = 0; j < min(kn, kAhead); ++j) {
       const int k = (kb0 + j) * kBlock;
