@@ -429,7 +429,7 @@ extern "C" int dlite_fp8_quantise(const dlite_fp8_quantise_args* g, dlite_stream
   if (g->residual && (g->residual_stride < g->K || g->total_stride < g->K)) return DLITE_ERR_INVALID_ARG;
   if ((g->total == g->residual && g->total_stride != g->residual_stride) || (g->total == g->x && g->total_stride != g->x_stride))
     return DLITE_ERR_INVALID_ARG;
-  if ((long long)g->B * g->T > 0x7fffffffLL || g->K > DLITE_FP8_MAX_K) return DLITE_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)g->B * g->T > DLITE_FP8_MAX_ROWS || g->K > DLITE_FP8_MAX_K) return DLITE_ERR_UNSUPPORTED_SHAPE;
   QuantiseArgs a = {};
   a.rows = g->B * g->T;
   a.T = g->T;

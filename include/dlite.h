@@ -609,7 +609,7 @@ int dlite_token_logprobs(const dlite_logprobs_args *args, dlite_stream_t stream)
 #define DLITE_FP8_BLOCK 128
 #define DLITE_FP8_MAX_K (1 << 20)
 #define DLITE_FP8_MAX_N (1 << 22)
-#define DLITE_FP8_MAX_ROWS (1 << 22) /* B T of a product */
+#define DLITE_FP8_MAX_ROWS (1 << 22) /* B T */
 
 /* Rows into codes. With residual: total = x + residual, rounded to dtype, is stored and takes x's place below (total may be
  * residual or x themselves, with their stride; otherwise they do not overlap). With gain [K]: y = x gain / sqrt(mean x^2 + eps) in float32 takes its

@@ -28,7 +28,7 @@ BAD = {
                                   ({"residual": P + 4096, "total": P + 4096, "residual_stride": 200, "total_stride": 208}, INVALID),
                                   ({"residual": P + 4096, "total": P, "residual_stride": 200, "total_stride": 208}, INVALID),
                                   ({"gain": P, "eps": -1.0}, INVALID), ({"gain": P, "eps": NAN}, INVALID), ({"gain": P, "eps": INF}, INVALID),
-                                  ({"B": 1 << 30, "T": 4}, SHAPE)],
+                                  ({"B": 1 << 30, "T": 4}, SHAPE), ({"B": 1, "T": (1 << 31) - 1}, SHAPE), ({"B": (1 << 22) + 1, "T": 1}, SHAPE)],
     "dlite_fp8_weight": [({"N": 0}, INVALID), ({"K": 0}, INVALID), ({"w": None}, INVALID), ({"codes": None}, INVALID), ({"scale": None}, INVALID),
                          ({"dtype": -1}, INVALID), ({"w_stride": 199}, INVALID), ({"codes_stride": 200}, INVALID), ({"codes_stride": 192}, INVALID),
                          ({"N": (1 << 22) + 1}, SHAPE), ({"K": (1 << 20) + 1, "w_stride": 1 << 21, "codes_stride": 1 << 21}, SHAPE)],
