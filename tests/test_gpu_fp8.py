@@ -133,6 +133,28 @@ def test_norm_and_quantise(dtype, B, T, K, pad, residual):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,K,pad", [(3, 8193, 0), (2, 20001, 2), (5, 511, 0), (5, 514, 1), (2, 16385, 0)])
+def test_rows_off_16_bytes(dtype, T, K, pad):
+    """Widths and starts of every parity, sums over several rounds of a row; the stream in place."""
+    B = 2
+    x, gain = _input(B, T, K, dtype, 1, pad), _input(1, 1, K + 1, dtype, 2)[0, 0][1:]
+    res = torch.full((B, T, K + 5), 7.0, dtype=DT[dtype], device=DEV)
+    res[..., 3:3 + K] = _input(B, T, K, dtype, 3)
+    inner = res[..., 3:3 + K]
+    v = FO.total(_np(x), _np(inner), dtype)
+    n_rows = torch.tensor([T, T - 1], dtype=torch.int32, device=DEV)
+    m = (torch.arange(T, device=DEV)[None] < n_rows[:, None]).cpu().numpy()
+    old = _np(inner)
+    c, s = binding.fp8_quantise(x, gain=gain, eps=1e-5, residual=inner, n_rows=n_rows)
+    assert np.array_equal(_np(inner)[m], v[m]) and np.array_equal(_np(inner)[~m], old[~m])
+    assert bool((res[..., :3] == 7).all()) and bool((res[..., 3 + K:] == 7).all())
+    y = FO.norm(v, _np(gain), 1e-5)
+    # as in test_norm_and_quantise, with 16 numbers a thread and round of 8,192
+    err = ((16 * -(-K // 8192) + 10 + 3) / 2 + 4 + 2) * 2.0 ** -24 * np.abs(y)
+    _quantised(_bytes(c)[m][None], _np(s)[m][None], y[m][None], err[m][None])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,K,pad", [(128, 128, 0), (1, 1, 0), (130, 300, 0), (257, 1000, 5), (64, 129, 0)])
 def test_weight(dtype, N, K, pad):
     w = _input(1, N, K, dtype, 9, pad)[0]
@@ -318,6 +340,27 @@ def test_strides_of_products(rows, K, N, out):
         y = buf[off:].view(1, rows, N + pad)[..., :N]
         assert binding.fp8_linear(cw, s, w, ws, out=y) is y and torch.equal(y, want)
         assert bool((buf[:off] == 2).all()) and bool((buf[off:].view(rows, N + pad)[:, N:] == 2).all())
+
+
+@pytest.mark.parametrize("rows", [9, 300, 513])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 2, 3, 63, 65, 66, 127, 193, 258, 450])
+def test_outputs_of_odd_widths(rows, out, N):
+    """Rows of any width, begun anywhere: the bits of rows on 16 bytes, and nothing beside them."""
+    B, T, K = 3, rows // 3, 200
+    c, s = binding.fp8_quantise(_input(B, T, K, "bf16", 4))
+    w, ws = _weight(N, K, 5)
+    n_rows = torch.tensor([T, T - 1, 1], dtype=torch.int32, device=DEV)
+    m = torch.arange(T, device=DEV)[None] < n_rows[:, None]
+    want = torch.full((B, T, -(-N // 8) * 8), 2.0, dtype=DT[out], device=DEV)[..., :N]
+    binding.fp8_linear(c, s, w, ws, n_rows=n_rows, out=want)
+    for off, pad in ((0, 0), (1, 0), (0, 1), (1, 1), (2, 2), (3, 5)):
+        buf = torch.full((off + rows * (N + pad) + 8,), 2.0, dtype=DT[out], device=DEV)
+        y = buf[off:off + rows * (N + pad)].view(B, T, N + pad)[..., :N]
+        binding.fp8_linear(c, s, w, ws, n_rows=n_rows, out=y)
+        assert torch.equal(y, want) and bool((y[~m] == 2).all())
+        assert bool((buf[:off] == 2).all()) and bool((buf[-8:] == 2).all())
+        assert bool((buf[off:-8].view(rows, N + pad)[:, N:] == 2).all())
 
 
 @pytest.mark.parametrize("rows", [3, 300])
