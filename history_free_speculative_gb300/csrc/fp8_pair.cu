@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.w = fp8::codes4(a[16 * j + 12] * inv, a[16 * j + 13] * inv, a[16 * j + 14] * inv, a[16 * j + 15] * inv);
           *reinterpret_cast<uint4*>(staged + lane * kPitch + 16 * j) = w;
         }
+        __syncwarp();  // the lanes read each other's rows below
         const bool valid = row < p.rows && fp8::valid_row(p.n_rows, p.T, row);
         if (valid && bad) flag_status(p.status, kDevNonfinite);
         if (valid && eg == 0) p.scale[(long long)n0 * p.rows + row] = fp8::exp2i(e);
