@@ -194,6 +194,7 @@ _SIGS = {
     "dlite_fp8_linear": (_I, [ctypes.POINTER(Fp8LinearArgs), _P]),
     "dlite_fp8_gated": (_I, [ctypes.POINTER(Fp8GatedArgs), _P]),
     "dlite_selftest_wait": (_I, [_P, _U64, _P, _P]),
+    "dlite_selftest_ring": (_I, [_U64, _P, _P, _P]),
     "dlite_device_status": (_I, [_P, _I, ctypes.POINTER(_I), _P]),
     "dlite_status_string": (ctypes.c_char_p, [_I]),
     "dlite_last_cuda_error": (ctypes.c_char_p, []),
@@ -787,6 +788,14 @@ def fp8_gated(codes, scale, gate, gate_scale, up, up_scale, n_rows=None, out=Non
                      out.data_ptr(), ocs, out_scale.data_ptr(), _vec(n_rows, torch.int32, (B,), "n_rows"), _vec(status, torch.int32, (1,), "status"))
     _check(lib.dlite_fp8_gated(ctypes.byref(a), ptr), "dlite_fp8_gated")
     return out, out_scale
+
+
+def selftest_ring(limit_ns, status, result, stream=None):
+    """Probe of the bounded waits of rows over a ring of copies (dlite_selftest_ring): result is a device int32 [3, 4]."""
+    lib = load()
+    ptr, _ = _here(stream, status, result)
+    _check(lib.dlite_selftest_ring(int(limit_ns), _vec(status, torch.int32, (1,), "status"), _vec(result, torch.int32, (3, 4), "result"), ptr),
+           "dlite_selftest_ring")
 
 
 def config_struct(cfg, B_max):

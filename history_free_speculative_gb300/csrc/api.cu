@@ -1681,6 +1681,12 @@ int dlite_selftest_wait(dlite_handle* h, uint64_t limit_ns, int32_t* result, dli
   return DLITE_OK;
 }
 
+int dlite_selftest_ring(uint64_t limit_ns, int* status, int32_t* result, dlite_stream_t stream) {
+  if (!status || !result || !aligned4(status, result) || limit_ns < 1 || limit_ns > 1000000000ull) return DLITE_ERR_INVALID_ARG;
+  CK(launch_ring_probe(limit_ns, status, result, (cudaStream_t)stream));
+  return DLITE_OK;
+}
+
 int dlite_launch_count(dlite_handle* h, int B, float temperature) {
   if (!h || B < 1) return -1;
   (void)temperature;

@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "fp8.cuh"
+#include "row_ring.cuh"
 
 namespace dlite {
 namespace {
@@ -158,13 +159,16 @@ __device__ __forceinline__ void quantise_piece(const QuantiseArgs& a, int row, i
   if (c % kBlock == 0) a.scale[(long long)(c / kBlock) * a.rows + row] = fp8::exp2i(e);
 }
 
-// v = x + residual in the stream's type, stored
-template <typename T, bool VEC>
-__device__ __forceinline__ void add_residual(const QuantiseArgs& a, int row, int c, const Piece<T>& res, float (&v)[kPer], T* buf) {
+// v = x + residual in the stream's type
+template <typename T>
+__device__ __forceinline__ void add_residual(const Piece<T>& res, float (&v)[kPer]) {
   float r[kPer];
   res.to(r);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) v[i] = rounded(v[i] + r[i], (T*)nullptr);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_total(const QuantiseArgs& a, int row, int c, const float (&v)[kPer], T* buf) {
   store_piece<T, VEC>(static_cast<T*>(a.total) + row * a.ts, c, a.K, v, buf);
 }
 
@@ -182,7 +186,8 @@ __global__ void __launch_bounds__(256) fp8_quantise_kernel(const QuantiseArgs a)
   if (a.res) {
     const Piece<T> r = load_piece<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c, a.K, buf);
     x.to(v);
-    add_residual<T, VEC>(a, row, c, r, v, buf);
+    add_residual(r, v);
+    store_total<T, VEC>(a, row, c, v, buf);
   } else {
     x.to(v);
   }
@@ -208,9 +213,11 @@ __global__ void __launch_bounds__(1024) fp8_norm_quantise_kernel(const QuantiseA
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float red[2][32];
   __shared__ uint64_t full[kRing];
+  __shared__ int gave_up[2];
   const int c = threadIdx.x * kPer, bytes = a.K * (int)sizeof(T), slot_bytes = a.res ? 2 * bytes : bytes;
   if (threadIdx.x == 0) {
     for (int i = 0; i < slots; ++i) tc::mbar_init(tc::su32(full + i), 1);
+    gave_up[0] = gave_up[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_trigger();
@@ -226,38 +233,41 @@ __global__ void __launch_bounds__(1024) fp8_norm_quantise_kernel(const QuantiseA
     tc::bulk_load(dst, static_cast<const T*>(a.x) + row * a.xs, bytes, bar);
     if (a.res) tc::bulk_load(dst + bytes, static_cast<const T*>(a.res) + row * a.rs, bytes, bar);
   };
-  int row = next_row(blockIdx.x), ahead = row, slot = 0, turn = 0;
-  uint32_t ph = 0;
+  RowRing r = {tc::su32(full), slots, gave_up, a.status};
+  int row = next_row(blockIdx.x), ahead = row;
   if (threadIdx.x == 0)
-    for (int i = 0; i < slots && ahead < a.rows; ++i, ahead = next_row(ahead + gridDim.x)) copy(ahead, i);
+    for (; r.flying < slots && ahead < a.rows; ++r.flying, ahead = next_row(ahead + gridDim.x)) copy(ahead, r.flying);
   __syncthreads();  // the barriers are there
-  bool bad = false, ok = true;
+  bool bad = false;
   while (row < a.rows) {
-    ok = tc::mbar_wait_hint(tc::su32(full + slot), ph, a.status) && ok;
-    const T* at = reinterpret_cast<const T*>(ring + (size_t)slot * slot_bytes);
+    r.wait();
+    const T* at = reinterpret_cast<const T*>(ring + (size_t)r.slot * slot_bytes);
     float v[kPer], ss = 0.f;
     load_piece<T, true>(at, c, a.K, nullptr).to(v);
-    if (a.res) add_residual<T, true>(a, row, c, load_piece<T, true>(at + a.K, c, a.K, nullptr), v, nullptr);
+    if (a.res) add_residual(load_piece<T, true>(at + a.K, c, a.K, nullptr), v);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) ss = fmaf(v[i], v[i], ss);
-    const float inv = rsqrtf(fmaf(row_sum(ss, red[turn]), a.inv_k, a.eps));
-    if (threadIdx.x == 0 && ahead < a.rows && ok) {  // the sum's barrier: the slot is read
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      copy(ahead, slot);
-      ahead = next_row(ahead + gridDim.x);
+    const float inv = rsqrtf(fmaf(row_sum(ss, red[r.parity]), a.inv_k, a.eps));
+    if (r.late()) break;  // the slot may hold anything: nothing of this turn has left
+    if (threadIdx.x == 0) {  // the sum's barrier: the slot is read
+      if (ahead < a.rows) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        copy(ahead, r.slot);
+        ahead = next_row(ahead + gridDim.x);
+      } else {
+        r.used();
+      }
     }
+    if (a.res) store_total<T, true>(a, row, c, v, nullptr);
     float g[kPer];
     gain.to(g);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = v[i] * inv * g[i];
     quantise_piece(a, row, c, v, bad);
-    turn ^= 1;
+    r.next();
     row = next_row(row + gridDim.x);
-    if (++slot == slots) {
-      slot = 0;
-      ph ^= 1u;
-    }
   }
+  if (threadIdx.x == 0) r.drain();
   if (bad) flag_status(a.status, kDevNonfinite);
 }
 
@@ -277,7 +287,10 @@ __global__ void __launch_bounds__(VEC ? 1024 : 512) fp8_norm_quantise_wide_kerne
   // whole warps walk together: they load together, and a block's maximum is taken by all lanes
   for (int c = threadIdx.x * kPer; c - (int)threadIdx.x * kPer < a.K; c += step) {
     load_piece<T, VEC>(x, c, a.K, buf).to(v);
-    if (a.res) add_residual<T, VEC>(a, row, c, load_piece<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c, a.K, buf), v, buf);
+    if (a.res) {
+      add_residual(load_piece<T, VEC>(static_cast<const T*>(a.res) + row * a.rs, c, a.K, buf), v);
+      store_total<T, VEC>(a, row, c, v, buf);
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) ss = fmaf(v[i], v[i], ss);
   }

@@ -163,6 +163,7 @@ cudaError_t launch_advance(int B, const int32_t* n_commit, int64_t* pos, cudaStr
 // barrier nobody arrives at gave up after limit_ns (flagging the timeout bit in *status);
 // result[2] = 1 when a following kernel sees that bit at entry and skips its work.
 cudaError_t launch_wait_probe(uint64_t limit_ns, int* status, int32_t* result, cudaStream_t s);
+cudaError_t launch_ring_probe(uint64_t limit_ns, int* status, int32_t* result, cudaStream_t s);
 cudaError_t launch_shift_group(int B, int G, int K1, const int32_t* commits, const int32_t* n_commit,
                                int32_t* group, cudaStream_t s);
 cudaError_t launch_repack(const void* src, bool src_f32, int rows, int cols, int src_ld,

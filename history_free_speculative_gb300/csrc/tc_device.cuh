@@ -56,7 +56,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* st
 }
 // The same with a suspend hint: a waiting thread sleeps instead of polling, which leaves the issue slots to the
 // other warps of a kernel that has many kinds of them waiting for each other.
-__device__ __forceinline__ bool mbar_wait_hint(uint32_t bar, uint32_t parity, int* status) {
+__device__ __forceinline__ bool mbar_wait_hint(uint32_t bar, uint32_t parity, int* status,
+                                               uint64_t limit_ns = kTimeoutNs) {
   uint64_t t0 = 0;
   while (true) {
     uint32_t ok;
@@ -70,7 +71,7 @@ __device__ __forceinline__ bool mbar_wait_hint(uint32_t bar, uint32_t parity, in
     if (ok) return true;
     const uint64_t t = gtimer();
     if (t0 == 0) t0 = t;
-    if (t - t0 > kTimeoutNs) {
+    if (t - t0 > limit_ns) {
       flag_status(status, kDevTimeout);
       return false;
     }

@@ -384,6 +384,13 @@ int dlite_synthetic_target(int B, int K, int V, const int32_t *candidates, const
  * the flag if asked). Errors: INVALID_ARG, CUDA. */
 int dlite_selftest_wait(dlite_handle *h, uint64_t limit_ns, int32_t *result, dlite_stream_t stream);
 
+/* The same for the rows that a CTA takes in turn out of a ring of copies (dlite_fp8_quantise): three CTAs walk up to 1,000 rows over a
+ * ring of three, with limit_ns (1 ns .. 1 s) in place of its 2 s. CTA 0: no row arrives; CTA 1: rows 0 to 4 arrive; CTA 2: all arrive,
+ * and one thread takes itself for late in row 7. result [3][4] device int32 (out), per CTA: rows done, 1 if all threads left the loop behind
+ * the same row, copies not waited for at the end, whole limits that passed. status (device int32) receives DLITE_DEV_TIMEOUT.
+ * Errors: INVALID_ARG, CUDA. */
+int dlite_selftest_ring(uint64_t limit_ns, int *status, int32_t *result, dlite_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Target-side operators of the round. Between the draft and its verification
  * the target runs one causal forward over [a, d_1..d_K] ([P1] §"一次因果前向评估整条候选"):
