@@ -76,11 +76,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// The gated activation g / (1 + exp(-g)) u of two sums. exp2 within 2^-22, its argument's rounding |g| 2^-23, the reciprocal within
+// The gated activation g / (1 + exp(-g)) u, of two pairs of sums at once. exp2 within 2^-22, its argument's rounding |g| 2^-23, the reciprocal within
 // 2^-23: far below the 2^-4 of the code that it becomes. (With expf and a division the 16,384 results of a tile cost the many-row kernel 4 us.)
-
-__device__ __forceinline__ float gated(float g, float u) {
-  return g * rcp_approx(1.f + tc::ex2_approx(g * -tc::kLog2e)) * u;
+// As 1/4 over (1 + exp(-g)) / 4: the reciprocal instruction takes what is below 2^-126 to 0, where exp(-g) is still a float32
+// number (g from -88.72 to -87.34); of the quarter it is above that. Past them exp(-g) is infinite and the result 0, as in float32.
+__device__ __forceinline__ uint64_t gated2(uint64_t g, uint64_t u) {
+  const uint64_t quarter = pack2f(0.25f, 0.25f), t = fma2(g, pack2f(-tc::kLog2e, -tc::kLog2e), pack2f(-2.f, -2.f));
+  const uint64_t d = add2(quarter, pack2f(tc::ex2_approx(lo2f(t)), tc::ex2_approx(hi2f(t))));
+  return mul2(mul2(g, mul2(quarter, pack2f(rcp_approx(lo2f(d)), rcp_approx(hi2f(d))))), u);
 }
 
 // One lane of a converged warp. Copies and products take their operands from uniform registers; in a branch on the lane's

@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           g.x += a.x, g.y += a.y, g.z += a.z, g.w += a.w;
           u.x += b.x, u.y += b.y, u.z += b.z, u.w += b.w;
         }
-        float v[4] = {fp8::gated(g.x, u.x), fp8::gated(g.y, u.y), fp8::gated(g.z, u.z), fp8::gated(g.w, u.w)};
+        const uint64_t a0 = fp8::gated2(pack2f(g.x, g.y), pack2f(u.x, u.y)), a1 = fp8::gated2(pack2f(g.z, g.w), pack2f(u.z, u.w));
+        float v[4] = {lo2f(a0), hi2f(a0), lo2f(a1), hi2f(a1)};
         bool bad = false;
         const float amax = warp_max(fp8::finite_max(v, bad));   // columns past N are 0
         const int e = fp8::block_exponent(amax);

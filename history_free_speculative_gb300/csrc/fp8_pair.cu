@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float a[64];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          a[2 * j] = fp8::gated(lo2f(acc[j]), lo2f(acc[32 + j]));
-          a[2 * j + 1] = fp8::gated(hi2f(acc[j]), hi2f(acc[32 + j]));
+          const uint64_t two = fp8::gated2(acc[j], acc[32 + j]);
+          a[2 * j] = lo2f(two);
+          a[2 * j + 1] = hi2f(two);
         }
         bool bad = false;
         float amax = fp8::finite_max(a, bad);

@@ -671,7 +671,8 @@ typedef struct {
 int dlite_fp8_linear(const dlite_fp8_linear_args *args, dlite_stream_t stream);
 
 /* The gated block's first half: a[b, t, f] = g / (1 + exp(-g)) u with g = x . gate[f], u = x . up[f], in float32, as codes and
- * scales of a (what dlite_fp8_linear takes as x of the down projection). */
+ * scales of a (what dlite_fp8_linear takes as x of the down projection). exp(-g) past float32 (g below -88.7) makes a 0, where it is
+ * 2.7e-37 |u| at most. */
 typedef struct {
     int B, T, K, F;
     const uint8_t *codes; /* x */
