@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(VEC ? 1024 : 512) fp8_norm_quantise_wide_kerne
 // A weight's block of 128 x 128: one CTA, 16 rows a warp, four columns a lane, read once and held in registers. Magnitudes compare as integers; a
 // block that is not finite is found by its maximum and takes a second way. 151,936 x 4,096 took 305 us
 // from bf16 and 446 from float32, 6.1 and 7.0 TB/s (580 and 565 with a test of each element, at two CTAs an SM): HBM bounds it.
+// From bf16 rows off 16 bytes four CTAs an SM cost three registers spilled, and are the faster all the same: 151,936 x 4,095 356 us, 381 at three.
 template <typename T>
 using Word4 = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
 __device__ __forceinline__ uint32_t magnitudes(uint32_t m, uint4 w) {
