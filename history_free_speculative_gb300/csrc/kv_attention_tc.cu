@@ -771,18 +771,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int N>
-cudaError_t launch(const CUtensorMap& map, const AttnArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t s) {
+  // First a call that needs the device's context: in a host thread without one yet the map's encoder refuses.
   const cudaError_t e = cudaFuncSetAttribute(kv_attention_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N>::BYTES);
-  return e != cudaSuccess ? e : launch_pdl(kv_attention_tc_kernel<N>, dim3(grid), dim3(kThreads), Smem<N>::BYTES, s, map, a);
+  if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!tc::make_record_map(&map, a.pages, kRecRows, (long long)a.n_pages * a.n_kv)) return cudaErrorInvalidValue;
+  return launch_pdl(kv_attention_tc_kernel<N>, dim3(grid), dim3(kThreads), Smem<N>::BYTES, s, map, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_tc(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-  CUtensorMap map;
-  const long long records = (long long)a.n_pages * a.n_kv;
-  if (!tc::make_record_map(&map, a.pages, kRecRows, records)) return cudaErrorInvalidValue;
-  return p.rows == 16 ? launch<16>(map, a, p.grid, s) : launch<32>(map, a, p.grid, s);
+  return p.rows == 16 ? launch<16>(a, p.grid, s) : launch<32>(a, p.grid, s);
 }
 
 }  // namespace kv
