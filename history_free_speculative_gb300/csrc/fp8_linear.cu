@@ -373,6 +373,8 @@ int check_product(int B, int T, int K, int N, const void* codes, int64_t codes_s
   if ((long long)B * T > DLITE_FP8_MAX_ROWS || K > DLITE_FP8_MAX_K || N > DLITE_FP8_MAX_N || codes_stride >= (1LL << 40)) return DLITE_ERR_UNSUPPORTED_SHAPE;
   return DLITE_OK;
 }
+// The scales of `rows` rows (of a weight: of blocks of rows) of K columns, which are dense
+dlite::Rows scales(const float* at, int rows, int K) { return {at, 1, 0, 4LL * rows * dlite::fp8::blocks_of(K)}; }
 int check_weight(const void* w, int64_t stride, const float* scale, int K) {
   if (!w || !scale || ((uintptr_t)w & 15) || stride < K || stride % 16 || ((uintptr_t)scale & 3)) return DLITE_ERR_INVALID_ARG;
   return stride >= (1LL << 40) ? DLITE_ERR_UNSUPPORTED_SHAPE : DLITE_OK;
@@ -402,6 +404,9 @@ extern "C" int dlite_fp8_linear(const dlite_fp8_linear_args* g, dlite_stream_t s
   p.vec = !((uintptr_t)g->out & 15) && g->out_stride % (16 / es) == 0;
   p.status = g->status;
   const cudaStream_t s = (cudaStream_t)stream;
+  if (!apart_of(Rows{p.out, p.rows, p.os * es, (long long)p.N * es}, Rows{g->codes, p.rows, g->codes_stride, p.K}, scales(p.xs, p.rows, p.K),
+                Rows{g->w, p.N, g->w_stride, p.K}, scales(p.ws[0], fp8::blocks_of(p.N), p.K)))
+    return DLITE_ERR_INVALID_ARG;
   const fp8::Operands o = {g->codes, g->codes_stride, {g->w, nullptr}, {g->w_stride, 0}};
   return g->dtype == DLITE_F32 ? product<false, float>(p, o, s) : product<false, bf16>(p, o, s);
 }
@@ -428,6 +433,12 @@ extern "C" int dlite_fp8_gated(const dlite_fp8_gated_args* g, dlite_stream_t str
   p.cs = g->out_stride;
   p.scale = g->out_scale;
   p.status = g->status;
+  const Rows codes = {p.codes, p.rows, p.cs, p.N}, scale = scales(p.scale, p.rows, p.N);
+  for (const Rows& out : {codes, scale})
+    if (!apart_of(out, Rows{g->codes, p.rows, g->codes_stride, p.K}, scales(p.xs, p.rows, p.K), Rows{g->gate, p.N, g->gate_stride, p.K},
+                  scales(p.ws[0], fp8::blocks_of(p.N), p.K), Rows{g->up, p.N, g->up_stride, p.K}, scales(p.ws[1], fp8::blocks_of(p.N), p.K)))
+      return DLITE_ERR_INVALID_ARG;
+  if (!apart(codes, scale)) return DLITE_ERR_INVALID_ARG;
   const fp8::Operands o = {g->codes, g->codes_stride, {g->gate, g->up}, {g->gate_stride, g->up_stride}};
   return product<true, float>(p, o, (cudaStream_t)stream);
 }

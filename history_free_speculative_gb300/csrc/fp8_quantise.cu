@@ -462,6 +462,12 @@ extern "C" int dlite_fp8_quantise(const dlite_fp8_quantise_args* g, dlite_stream
   a.scale = g->scale;
   a.n_rows = g->n_rows;
   a.status = g->status;
+  const Rows x = {g->x, a.rows, a.xs * es, (long long)a.K * es}, res = {g->residual, a.rows, a.rs * es, x.width},
+             total = {g->total, a.rows, a.ts * es, x.width}, gain = {g->gain, 1, 0, x.width}, codes = {g->codes, a.rows, a.cs, a.K},
+             scale = {g->scale, 1, 0, 4LL * a.rows * fp8::blocks_of(a.K)};
+  if (!apart_of(codes, x, res, total, gain, scale) || !apart_of(scale, x, res, total, gain) || !apart(total, gain) ||
+      (total.at != x.at && !apart(total, x)) || (total.at != res.at && !apart(total, res)))
+    return DLITE_ERR_INVALID_ARG;
   const bool vec = !(((uintptr_t)g->x | (uintptr_t)g->residual | (uintptr_t)g->total | (uintptr_t)g->gain) & 15) && g->K % 8 == 0 &&
                    g->x_stride % V == 0 && (!g->residual || (g->residual_stride % V == 0 && g->total_stride % V == 0));
   const cudaStream_t s = (cudaStream_t)stream;
@@ -477,6 +483,10 @@ extern "C" int dlite_fp8_weight(const dlite_fp8_weight_args* g, dlite_stream_t s
   if ((uintptr_t)g->w % (g->dtype == DLITE_F32 ? 4 : 2) || !aligned4(g->scale, g->status) || ((uintptr_t)g->codes & 15)) return DLITE_ERR_INVALID_ARG;
   if (g->w_stride < g->K || g->codes_stride < g->K || g->codes_stride % 16) return DLITE_ERR_INVALID_ARG;
   if (g->K > DLITE_FP8_MAX_K || g->N > DLITE_FP8_MAX_N) return DLITE_ERR_UNSUPPORTED_SHAPE;
+  const int es = g->dtype == DLITE_F32 ? 4 : 2;
+  const Rows w = {g->w, g->N, g->w_stride * es, (long long)g->K * es}, codes = {g->codes, g->N, g->codes_stride, g->K},
+             scale = {g->scale, 1, 0, 4LL * fp8::blocks_of(g->N) * fp8::blocks_of(g->K)};
+  if (!apart_of(codes, w, scale) || !apart(scale, w)) return DLITE_ERR_INVALID_ARG;
   const cudaStream_t s = (cudaStream_t)stream;
   return launch_status(g->dtype == DLITE_F32 ? launch_weight<float>(*g, s) : launch_weight<bf16>(*g, s));
 }

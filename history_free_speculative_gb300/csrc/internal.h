@@ -32,6 +32,27 @@ inline bool aligned4(const P*... p) {
   return ((0 | ... | (uintptr_t)p) & 3) == 0;
 }
 
+// Rows in memory, in bytes. n == 1: the stride does not count. at NULL: nothing.
+struct Rows {
+  const void* at;
+  long long n, stride, width;
+};
+// Whether no byte belongs to both. Rows of one stride may lie beside each other in wider ones; of other strides, their whole ranges are looked at.
+inline bool apart(const Rows& a, const Rows& b) {
+  if (!a.at || !b.at) return true;
+  typedef unsigned __int128 Wide;
+  const Wide pa = (uintptr_t)a.at, pb = (uintptr_t)b.at;
+  if (pa + (Wide)(a.n - 1) * a.stride + a.width <= pb || pb + (Wide)(b.n - 1) * b.stride + b.width <= pa) return true;
+  if (a.n > 1 && b.n > 1 && a.stride != b.stride) return false;
+  if (a.n == 1 && b.n == 1) return false;
+  const Wide s = a.n > 1 ? a.stride : b.stride, d = pb >= pa ? (pb - pa) % s : (s - (pa - pb) % s) % s;  // b's columns behind a's, around a row
+  return d >= (Wide)a.width && d + b.width <= s;
+}
+template <typename... R>
+inline bool apart_of(const Rows& a, const R&... others) {
+  return (apart(a, others) && ...);
+}
+
 // Status code of a launch; an error is kept for dlite_last_cuda_error (api.cu).
 int launch_status(cudaError_t e);
 

@@ -607,7 +607,8 @@ int dlite_token_logprobs(const dlite_logprobs_args *args, dlite_stream_t stream)
  *   activations  codes [B, T, K] and scale [ceil(K / 128)][B T] float32, one per 128 columns of a row (the rows of a block side by side)
  *   weights      codes [N, K] and scale [ceil(N / 128)][ceil(K / 128)] float32 (any finite numbers), one per 128 x 128 elements
  * A code's value is code x scale. Code rows start on 16 bytes: 16-byte aligned memory, strides (in bytes) a multiple of 16;
- * bytes of a row past its columns are neither read into a result nor written. Scales are dense.
+ * bytes of a row past its columns are neither read into a result nor written. Scales are dense. No byte of an output belongs to an
+ * input or another output (INVALID_ARG; total below excepted): rows of one stride may lie beside each other in wider ones.
  * Quantisation: scale = 2^e, the least with max |x| <= 448 2^e, e >= -126; code = e4m3(x 2^-e) to nearest, ties to even.
  * The format holds no infinity: what is not finite becomes NaN, does not count for the maximum, and flags DLITE_DEV_NONFINITE; a
  * NaN code makes the results of its row (of a weight: of its output) NaN and no others. Sums of a product are float32, each block's
@@ -619,7 +620,7 @@ int dlite_token_logprobs(const dlite_logprobs_args *args, dlite_stream_t stream)
 #define DLITE_FP8_MAX_ROWS (1 << 22) /* B T */
 
 /* Rows into codes. With residual: total = x + residual, rounded to dtype, is stored and takes x's place below (total may be
- * residual or x themselves, with their stride; otherwise they do not overlap). With gain [K]: y = x gain / sqrt(mean x^2 + eps) in float32 takes its
+ * residual or x themselves, with their stride). With gain [K]: y = x gain / sqrt(mean x^2 + eps) in float32 takes its
  * place. Then codes and scale of it. Elements past float32's square root (1.8e19) overflow the norm's sum. */
 typedef struct {
     int B, T, K;          /* K <= DLITE_FP8_MAX_K */
