@@ -240,15 +240,19 @@ __global__ void __launch_bounds__(1024) fp8_norm_quantise_kernel(const QuantiseA
   __syncthreads();  // the barriers are there
   bool bad = false;
   while (row < a.rows) {
-    r.wait();
+    const bool there = r.wait();
     const T* at = reinterpret_cast<const T*>(ring + (size_t)r.slot * slot_bytes);
     float v[kPer], ss = 0.f;
     load_piece<T, true>(at, c, a.K, nullptr).to(v);
-    if (a.res) add_residual(load_piece<T, true>(at + a.K, c, a.K, nullptr), v);
+    if (a.res) {
+      add_residual(load_piece<T, true>(at + a.K, c, a.K, nullptr), v);
+      // ahead of the barrier: 8,192 rows of 12,288 take 118 us so, 130 with the stores behind it
+      if (there) store_total<T, true>(a, row, c, v, nullptr);
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) ss = fmaf(v[i], v[i], ss);
     const float inv = rsqrtf(fmaf(row_sum(ss, red[r.parity]), a.inv_k, a.eps));
-    if (r.late()) break;  // the slot may hold anything: nothing of this turn has left
+    if (r.late()) break;  // a slot that was not filled holds anything
     if (threadIdx.x == 0) {  // the sum's barrier: the slot is read
       if (ahead < a.rows) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -258,7 +262,6 @@ __global__ void __launch_bounds__(1024) fp8_norm_quantise_kernel(const QuantiseA
         r.used();
       }
     }
-    if (a.res) store_total<T, true>(a, row, c, v, nullptr);
     float g[kPer];
     gain.to(g);
 #pragma unroll

@@ -2,8 +2,8 @@
 //
 //   thread 0 fills slots and counts them in `flying`
 //   while rows are left:
-//     wait()               every thread, for the turn's slot
-//     .. reads it, stores nothing outside the CTA ..
+//     wait()               every thread, for the turn's slot; true: the row is there, whatever other threads say
+//     .. reads it; a thread whose wait ran out stores nothing outside the CTA ..
 //     a barrier of the CTA
 //     if (late()) break    the same answer in every thread
 //     thread 0: refill(), or used() where no row is left to copy
@@ -11,7 +11,7 @@
 //     next()
 //   thread 0: drain()
 //
-// A wait that runs out (status flagged) takes the whole CTA out of the loop in the same turn, before that turn's stores; then the
+// A wait that runs out (status flagged) takes the whole CTA out of the loop in the same turn, at its barrier; then the
 // copies in flight have one more limit, all of them together. So a CTA ends within two limits, however many rows it had.
 #pragma once
 
@@ -29,8 +29,10 @@ struct RowRing {
   uint32_t phase = 0;
 
   __device__ __forceinline__ uint32_t bar(int s) const { return full + 8 * s; }
-  __device__ __forceinline__ void wait() {
-    if (!tc::mbar_wait_hint(bar(slot), phase, status, limit_ns)) gave_up[parity] = 1;
+  __device__ __forceinline__ bool wait() {
+    const bool there = tc::mbar_wait_hint(bar(slot), phase, status, limit_ns);
+    if (!there) gave_up[parity] = 1;
+    return there;
   }
   __device__ __forceinline__ bool late() const { return gave_up[parity] != 0; }
   __device__ __forceinline__ void used() { --flying; }
@@ -42,6 +44,7 @@ struct RowRing {
     }
   }
   __device__ __forceinline__ void drain() {
+    if (flying <= 0) return;
     const uint64_t t0 = tc::gtimer();
     for (; flying > 0; --flying, next()) {
       const uint64_t spent = tc::gtimer() - t0;
