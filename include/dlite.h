@@ -621,7 +621,8 @@ int dlite_token_logprobs(const dlite_logprobs_args *args, dlite_stream_t stream)
 
 /* Rows into codes. With residual: total = x + residual, rounded to dtype, is stored and takes x's place below (total may be
  * residual or x themselves, with their stride). With gain [K]: y = x gain / sqrt(mean x^2 + eps) in float32 takes its
- * place. Then codes and scale of it. Elements past float32's square root (1.8e19) overflow the norm's sum. */
+ * place. Then codes and scale of it. Elements past float32's square root (1.8e19) overflow the norm's sum; with eps
+ * below 1e-30, rows of nothing above 1e-18 lose their squares to underflow (a row of zeros is NaN with eps 0). */
 typedef struct {
     int B, T, K;          /* K <= DLITE_FP8_MAX_K */
     int dtype;            /* of x, residual, total and gain */

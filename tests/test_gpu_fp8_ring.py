@@ -78,3 +78,17 @@ def test_norm_over_a_ring_of_rows(dtype, B, T, K, pad, total, slots, ragged):
     # the sum of squares: 16 a thread, ten joins; its root halves that and the mean's and the eps' steps; rsqrt 2 steps of 2^-23; two products
     err = ((16 + 10 + 3) / 2 + 4 + 2) * 2.0 ** -24 * np.abs(y)
     _quantised(_bytes(codes)[..., :K][m], _np(scale)[m], y, err)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,K", [(3, 512), (3, 513), (2500, 512)])      # read twice, off 16 bytes, over the ring
+def test_rows_of_zeros(dtype, rows, K):
+    """With eps a row of zeros has codes of 0; without, it is 0 / 0: NaN, flagged, in its row."""
+    x = _input(1, rows, K, dtype, 4)
+    x[0, 1] = 0
+    gain, st = _input(1, 1, K, dtype, 5)[0, 0], torch.zeros(1, dtype=torch.int32, device=DEV)
+    c, s = binding.fp8_quantise(x, gain=gain, eps=1e-6, status=st)
+    assert int(st.item()) == 0 and np.all(_bytes(c)[0, 1] & 0x7F == 0) and np.all(_np(s)[0, 1] == 2.0 ** -126)
+    c, s = binding.fp8_quantise(x, gain=gain, eps=0.0, status=st)
+    nan = (_bytes(c)[0] & 0x7F) == 0x7F
+    assert int(st.item()) == binding.DEV_NONFINITE and nan[1].all() and not nan[0].any() and not nan[2:].any()
