@@ -5,9 +5,11 @@
 // and rows 128 c .. of the weights in its shared memory and gets its 128 rows over all 256 columns. Eight epilogue warps a CTA take an
 // accumulator times the block's scales into float32 sums in registers (lane = row, 128 columns a thread) while the
 // tensor cores work on the next.
-// What bounds it: the way round of an accumulator (products 512 clocks, commit to both CTAs, reads, hand-over to the CTA that issues), 1,700
-// clocks for two blocks, and under load the power cap (1,300 W, 1.57 GHz): 8,192 rows of 6,144 x 4,096 153 to 183 us (2.3 to 2.7 PFLOP/s), of
-// 4,096 x 12,288 290 to 300 us, gated 12,288 x 4,096 571 us (2.9). The same kernel without reads and hand-overs takes 0.36 us a block instead of 0.43.
+// What bounds it: the way round of an accumulator (products 512 clocks, commit to both CTAs, reads, hand-over to the CTA that issues), 1,600 to
+// 1,800 clocks for two blocks, and under load the power cap (1,350 W). 8,192 rows over and over, with the clock that held: 6,144 x 4,096 168 to 171 us
+// at 1.87 to 1.92 GHz (2.4 PFLOP/s), 4,096 x 12,288 345 to 349 us at 1.53 GHz (2.4), gated 12,288 x 4,096 630 to 658 us at 1.67 to 1.81 GHz (2.5 to 2.6);
+// six calls behind a pause 169 to 185, 306 to 317 and 594 to 602 us. Without the reads, the hand-overs kept, the last two take 298 us at 2.06 GHz
+// and 624 at 1.97; with the weights copied five times alone besides, 288 and 588: at full clock about 900 clocks a block stay, the hand-over's.
 // Tried: 128 weight rows a step and four accumulators (371 us for 4,096 x 12,288: twice the waits); one-CTA products of 128 x 256 handed over
 // inside the SM (309 us: an SM then takes in 48 KB a block where its way from L2 brings 64 bytes a clock); splits of the k blocks over clusters of
 // four to eight CTAs for few tiles (few such clusters of whole-SM CTAs are resident at once).
