@@ -6,13 +6,13 @@
 //     .. reads it; a thread whose wait ran out stores nothing outside the CTA ..
 //     a barrier of the CTA
 //     if (late()) break    the same answer in every thread
-//     thread 0: refill(), or used() where no row is left to copy
+//     thread 0: copies the next row into the slot, or used() where none is left
 //     .. stores ..
 //     next()
 //   thread 0: drain()
 //
 // A wait that runs out (status flagged) takes the whole CTA out of the loop in the same turn, at its barrier; then the
-// copies in flight have one more limit, all of them together. So a CTA ends within two limits, however many rows it had.
+// copies in flight have one more limit, all of them together. So a CTA ends within two limits of a row that does not come, however many it had left.
 #pragma once
 
 #include "tc_device.cuh"
